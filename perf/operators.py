@@ -204,7 +204,7 @@ def _plain_route(s):
         score = 1.0 / (1.0 + torch.exp(-x))
     rank = x if s["bias_t"] is None else score + s["bias_t"]
     if G > 1:
-        best2 = rank.view(T, G, E // G).sort(2, descending=True).values[:, :, : min(2, E // G)].sum(2)
+        best2 = (score if s["bias_t"] is None else rank).view(T, G, E // G).sort(2, descending=True).values[:, :, : min(2, E // G)].sum(2)
         keep = best2.sort(dim=1, descending=True, stable=True).indices[:, : s["top_groups"]]
         closed = torch.ones((T, G), dtype=torch.bool, device=x.device).scatter_(1, keep, False)
         rank = rank.masked_fill(closed.repeat_interleave(E // G, dim=1), -math.inf)
@@ -362,7 +362,7 @@ def exact(case, seed):
         score = torch.softmax(x, 1) if case["score"] == "softmax" else torch.sigmoid(x)
         rank = x if s["bias_t"] is None else score + s["bias_t"].double()
         if G > 1:
-            best = rank.view(T, G, E // G).topk(min(2, E // G), dim=2).values.sum(2)
+            best = (score if s["bias_t"] is None else rank).view(T, G, E // G).topk(min(2, E // G), dim=2).values.sum(2)
             kept = best.argsort(dim=1, descending=True, stable=True)[:, : case["top_groups"]]
             mine = (torch.arange(E, device=DEV) // (E // G)).view(1, E, 1)
             rank = torch.where((mine == kept.unsqueeze(1)).any(2), rank, -math.inf)
