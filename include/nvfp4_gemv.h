@@ -375,6 +375,229 @@ typedef struct {
 nvfp4_status_t nvfp4_gemv_plan(int64_t M, int64_t K, int64_t L, int sf_layout, int kernel,
                                int num_sms, int ctas_per_sm, nvfp4_gemv_plan_t* out);
 
+/* ------------------------------------------------------------------------
+ * Layer operators: what a program that serves a model calls around the
+ * product.  Rows of activations are quantised on the GPU, multiplied with
+ * quantised weights for any number of rows, and, in layers whose feed-forward
+ * part is a set of experts, routed to the experts and summed back.
+ *
+ * The rules of the calls above hold: device pointers owned by the caller, no
+ * allocation, no synchronisation, everything on `stream`, stream-capturable,
+ * arguments validated before anything is launched.  Results are bitwise
+ * reproducible run to run (no atomics on values).  There are no gradients: the
+ * weights are 4-bit codes.
+ *
+ * Scales: these products read a scale code as an unsigned magnitude (bit 7 is
+ * ignored; 0x7F and 0xFF are NaN), unlike the GEMV calls, which take signed
+ * codes.  nvfp4_quantize never writes a code with bit 7 set.  Weights whose
+ * scales have signs are made unsigned once with nvfp4_fold_scale_signs.
+ * ------------------------------------------------------------------------ */
+
+typedef enum {
+  NVFP4_DTYPE_FP16 = 0,
+  NVFP4_DTYPE_BF16 = 1,
+  NVFP4_DTYPE_FP32 = 2
+} nvfp4_dtype_t;
+
+/*
+ * Quantise rows to NVFP4.  With y = fp32(x * encode_scale), for each block of
+ * 16 consecutive elements of a row:
+ *   s    = E4M3(max|y| / 6)   to nearest even, at most 448
+ *   code = E2M1(y / s)        to nearest even, at most 6 in magnitude
+ * s = 0 gives zero codes; a block with an infinity or a NaN in y has the scale
+ * code 0x7F (NaN) and zero codes.  x stands for code * s / encode_scale: a
+ * product's alpha takes 1 / encode_scale.
+ *   x       : [L][rows] rows of K elements of x_dtype (nvfp4_dtype_t), x_row_stride
+ *             elements apart (0 = K); element aligned (16-byte aligned rows load faster)
+ *   q       : uint8 [L][rows][K/2], 8-byte aligned
+ *   sf      : uint8 scales in sf_layout, 4-byte aligned; the permuted layout's padding
+ *             is written as 0x00
+ *   row_map : NULL, or int32 [rows][copies] (then L = 1, copies <= 32): row r is
+ *             written to the rows row_map[r][0..copies-1] of q and sf instead, which
+ *             hold q_rows rows; entries outside [0, q_rows) are skipped, rows that no
+ *             entry names are left as they are (their scales too), and two
+ *             entries must not name one row.  copies and q_rows are ignored without it.
+ * Shapes: K % 16 == 0; rows, K or L of 0 is a no-op.  encode_scale is finite and > 0.
+ */
+nvfp4_status_t nvfp4_quantize(const void* x, int x_dtype, int64_t x_row_stride, int64_t rows, int64_t K,
+                              int64_t L, float encode_scale, void* q, void* sf, int sf_layout,
+                              const int32_t* row_map, int copies, int64_t q_rows,
+                              struct CUstream_st* stream);
+
+/*
+ * The values of quantised rows: x = x_dtype(fp32(E2M1 * E4M3) * scale), the product
+ * of code and scale exact, signed scale codes accepted.  Arguments as for
+ * nvfp4_quantize; q 8-byte aligned.
+ */
+nvfp4_status_t nvfp4_dequantize(const void* q, const void* sf, int sf_layout, int64_t rows, int64_t K,
+                                int64_t L, float scale, void* x, int x_dtype, int64_t x_row_stride,
+                                struct CUstream_st* stream);
+
+/*
+ * Make the scales of a quantised matrix unsigned, in place: every scale code with
+ * bit 7 set has it cleared, and the sign bits of the 16 elements it scales are
+ * flipped.  The values stay the same (NaN stays NaN).  a 8-byte aligned.
+ */
+nvfp4_status_t nvfp4_fold_scale_signs(void* a, void* sf, int sf_layout, int64_t rows, int64_t K, int64_t L,
+                                      struct CUstream_st* stream);
+
+/*
+ * Options of nvfp4_gemm.  NULL = {1.0f, NULL, NVFP4_ACT_NONE, NVFP4_DTYPE_FP16, 0}.
+ *   alpha        : fp32 output scale
+ *   bias         : NULL, or fp32 [L][M], added after the scaling
+ *   activation   : nvfp4_activation_t, applied last
+ *   c_dtype      : nvfp4_dtype_t of c
+ *   c_row_stride : elements from row n to n+1 of c; 0 = M
+ */
+typedef struct {
+  float alpha;
+  const float* bias;
+  int32_t activation;
+  int32_t c_dtype;
+  int64_t c_row_stride;
+} nvfp4_gemm_options_t;
+
+/*
+ * NVFP4 product for any number of rows: for each batch l, row n < N of b and row
+ * m < M of a,
+ *   c[l][n][m] = c_dtype(act(alpha * sum_k a[l][m][k] * b[l][n][k] + bias[l][m])),
+ * a and b the values of their codes and (unsigned) scales.
+ *   a : uint8 [L][M][K/2]; sfa its scales in the 128x4 layout
+ *   b : uint8 [L][N][K/2]; sfb its scales in the 128x4 layout (per batch, ceil(N/128) atom rows)
+ *   c : [L][N] rows of M elements, c_row_stride apart
+ * Shapes: K % 32 == 0 (rows of 16-byte multiples; K = 0 gives act(bias)), any M and
+ * N; an empty c is a no-op.  a, b, sfa, sfb 16-byte aligned; c element aligned.
+ * Accuracy: fp32 sums in the tensor cores' order, one rounding to c_dtype.
+ */
+nvfp4_status_t nvfp4_gemm(const void* a, const void* b, const void* sfa, const void* sfb, void* c,
+                          int64_t M, int64_t N, int64_t K, int64_t L,
+                          const nvfp4_gemm_options_t* options, struct CUstream_st* stream);
+
+typedef enum {
+  NVFP4_SCORE_SOFTMAX = 0, /* over all E experts */
+  NVFP4_SCORE_SIGMOID = 1
+} nvfp4_score_t;
+
+/*
+ * Options of nvfp4_route.  NULL = {NVFP4_SCORE_SOFTMAX, NULL, 1, 1, 1, 1.0f}.
+ *   score        : nvfp4_score_t
+ *   bias         : NULL, or fp32 [E]: added to the scores to choose, not to weigh
+ *   groups       : the E experts are cut into this many equal runs (<= 32)
+ *   top_groups   : runs that stay open, those with the largest sum of their two
+ *                  largest score + bias (of one, if only one is not masked)
+ *   renormalize  : weights are divided by their sum
+ *   weight_scale : and then multiplied by this
+ */
+typedef struct {
+  int32_t score;
+  const float* bias;
+  int32_t groups;
+  int32_t top_groups;
+  int32_t renormalize;
+  float weight_scale;
+} nvfp4_route_options_t;
+
+/*
+ * Choose top_k experts for each of T tokens.  logits: [T] rows of E values of dtype,
+ * row_stride elements apart (0 = E).  Scores are computed in fp32; experts are
+ * ranked by score + bias, or without a bias by the logit (the same order,
+ * without the scores' rounding), ties to the lower index.
+ *   ids     : int32 [T][top_k], best first
+ *   weights : fp32 [T][top_k], the scores of the chosen
+ * A logit that is -inf or NaN, or a bias that makes the rank so, masks the expert:
+ * it is never chosen.  Where fewer than top_k are left, the remaining ids are -1 and
+ * their weights 0.  Logits of +inf share the softmax evenly.
+ * Limits: E <= 1024, top_k <= 32 and <= E, E % groups == 0.
+ */
+nvfp4_status_t nvfp4_route(const void* logits, int dtype, int64_t row_stride, int64_t T, int64_t E,
+                           int top_k, const nvfp4_route_options_t* options, int32_t* ids, float* weights,
+                           struct CUstream_st* stream);
+
+/*
+ * The experts' rows.  T tokens with top_k choices each are sorted by expert into a
+ * buffer of row_capacity rows: an expert's choices, in the order of the tokens,
+ * fill tiles of tile_rows rows, each tile starting on a row that is a multiple of
+ * 128 (a scale atom).  The capacity, the tile and the size of the plan (what the sort
+ * tells the products, opaque) follow from T, top_k and E alone.
+ * Limits: E <= 1024, top_k <= 32 and <= E, T * top_k <= 2^24.
+ */
+typedef struct {
+  int32_t tile_rows;
+  int64_t row_capacity;
+  size_t plan_bytes;
+} nvfp4_moe_shape_t;
+nvfp4_status_t nvfp4_moe_shape(int64_t T, int64_t top_k, int64_t E, nvfp4_moe_shape_t* out);
+
+/*
+ * Sort the choices ids int32 [T][top_k]; an id outside [0, E) is no choice.
+ *   rows   : int32 [T][top_k], the row of each choice, -1 for none
+ *   counts : int32 [E], choices per expert
+ *   starts : int32 [E], first row of each expert
+ *   plan   : plan_bytes bytes, 16-byte aligned
+ */
+nvfp4_status_t nvfp4_moe_sort(const int32_t* ids, int64_t T, int64_t top_k, int64_t E, int32_t* rows,
+                              int32_t* counts, int32_t* starts, void* plan, struct CUstream_st* stream);
+
+/*
+ * Products of the experts' rows, for a plan of the same T, top_k and E.
+ *   a, sfa : weights uint8 [E][M][K/2] and their 128x4 scales
+ *   b, sfb : rows uint8 [row_capacity][K/2] and their 128x4 scales (nvfp4_quantize with
+ *            row_map = rows, or the gated product)
+ *   alpha  : fp32 [E] on the device, or NULL (1)
+ * nvfp4_moe_gemm: c[row][m] = c_dtype(act(alpha[e] * sum_k a[e][m][k] * b[row][k])).
+ * nvfp4_moe_gated_gemm: a has M = 2F rows per expert, row 2f the gate and row 2f+1 the
+ * input of output f; h = act(alpha gate) * (alpha input) in fp32 is quantised with
+ * encode_scale as nvfp4_quantize does: q uint8 [row_capacity][F/2], sf 128x4 scales
+ * (both 16-byte aligned).
+ * Rows of the buffers that hold no choice are neither read into a result nor written.
+ * Shapes: K % 32 == 0, K > 0; F % 32 == 0.  Alignment as for nvfp4_gemm.
+ */
+nvfp4_status_t nvfp4_moe_gemm(const void* a, const void* sfa, const void* b, const void* sfb,
+                              const void* plan, int64_t T, int64_t top_k, int64_t E, int64_t M, int64_t K,
+                              const float* alpha, int activation, void* c, int c_dtype,
+                              struct CUstream_st* stream);
+nvfp4_status_t nvfp4_moe_gated_gemm(const void* a, const void* sfa, const void* b, const void* sfb,
+                                    const void* plan, int64_t T, int64_t top_k, int64_t E, int64_t F,
+                                    int64_t K, const float* alpha, int activation, float encode_scale,
+                                    void* q, void* sf, struct CUstream_st* stream);
+
+/*
+ * out[t][m] = dtype(sum_j weights[t][j] * y[rows[t][j]][m]), fp32 sums in the order
+ * of j, choices with row -1 left out.  y: [row_capacity][M], out: [T][M], fp16 or bf16,
+ * 16-byte aligned; M % 8 == 0.
+ */
+nvfp4_status_t nvfp4_moe_combine(const void* y, int dtype, const int32_t* rows, const float* weights,
+                                 int64_t T, int64_t top_k, int64_t M, void* out,
+                                 struct CUstream_st* stream);
+
+/*
+ * The whole routed feed-forward layer: sort, quantise, gated product, product, sum.
+ *   x       : [T] rows of D fp16 or bf16 elements, x_row_stride apart (0 = D)
+ *   ids, weights : [T][top_k], as nvfp4_route writes them
+ *   w1, sf1 : [E][2F][D/2], gate and input rows interleaved (see above), 128x4 scales
+ *   w2, sf2 : [E][D][F/2], 128x4 scales
+ *   out     : [T][D], the type of x, 16-byte aligned
+ * Options (NULL = {NULL, NULL, 1, 1, NVFP4_ACT_SILU}): alpha1 and alpha2 scale the two
+ * products per expert (fp32 [E] on the device; NULL = 1), encode_x and encode_h the
+ * values before they are quantised, activation is the gate's.  An expert's output is
+ * rounded to the type of x before the weighted sum.
+ * workspace: nvfp4_moe_ffn_workspace_bytes bytes (0 for sizes that are not supported),
+ * 256-byte aligned; its contents need not be kept.  Shapes: D and F > 0, multiples of 32.
+ */
+typedef struct {
+  const float* alpha1;
+  const float* alpha2;
+  float encode_x;
+  float encode_h;
+  int32_t activation;
+} nvfp4_moe_options_t;
+size_t nvfp4_moe_ffn_workspace_bytes(int64_t T, int64_t top_k, int64_t E, int64_t D, int64_t F);
+nvfp4_status_t nvfp4_moe_ffn(const void* x, int dtype, int64_t x_row_stride, const int32_t* ids,
+                             const float* weights, const void* w1, const void* sf1, const void* w2,
+                             const void* sf2, int64_t T, int64_t top_k, int64_t E, int64_t D, int64_t F,
+                             const nvfp4_moe_options_t* options, void* out, void* workspace,
+                             size_t workspace_bytes, struct CUstream_st* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -42,6 +42,18 @@ EXPORTS = (
     "nvfp4_gemm_small_n",
     "nvfp4_gemm_small_n_explicit",
     "nvfp4_gemm_small_n_plan",
+    "nvfp4_quantize",
+    "nvfp4_dequantize",
+    "nvfp4_fold_scale_signs",
+    "nvfp4_gemm",
+    "nvfp4_route",
+    "nvfp4_moe_shape",
+    "nvfp4_moe_sort",
+    "nvfp4_moe_gemm",
+    "nvfp4_moe_gated_gemm",
+    "nvfp4_moe_combine",
+    "nvfp4_moe_ffn",
+    "nvfp4_moe_ffn_workspace_bytes",
 )
 
 
@@ -120,6 +132,8 @@ def library() -> ctypes.CDLL:
     lib.nvfp4_selftest_bounded_wait.argtypes = [ctypes.POINTER(I), ctypes.POINTER(I),
                                                 ctypes.POINTER(I), ctypes.POINTER(I64), P]
     lib.nvfp4_selftest_bounded_wait.restype = I
+    from . import layer
+    layer.declare(lib)
     _lib = lib
     return lib
 
@@ -309,3 +323,12 @@ def repack_scales(src, dst=None, stream=None):
         nvfp4_repack_scales(src.data_ptr(), dst.data_ptr(), rows, K, L,
                             _stream_handle(stream, src.device))
     return dst
+
+
+# The layer operators (quantise, product, routing, experts).
+from .layer import (  # noqa: E402
+    DTYPE_BF16, DTYPE_FP16, DTYPE_FP32, SCORE_SIGMOID, SCORE_SOFTMAX, dequantize, fold_scale_signs, gemm,
+    moe_combine, moe_ffn, moe_gated_gemm, moe_gemm, moe_sort, nvfp4_dequantize, nvfp4_fold_scale_signs,
+    nvfp4_gemm, nvfp4_moe_combine, nvfp4_moe_ffn, nvfp4_moe_ffn_workspace_bytes, nvfp4_moe_gated_gemm,
+    nvfp4_moe_gemm, nvfp4_moe_shape, nvfp4_moe_sort, nvfp4_quantize, nvfp4_route, quantize, quantize_rows,
+    route)

@@ -5,6 +5,7 @@
 #include <cstdint>
 
 #include "internal.h"
+#include "layer.h"
 #include "nvfp4_gemv.h"
 #include "selftest.h"
 
@@ -30,8 +31,7 @@ constexpr int64_t kMaxM = (int64_t(1) << 31) - 1;
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 nvfp4_status_t cuda_failure(cudaError_t err) {
-  g_last_cuda_error = (int)err;
-  (void)cudaGetLastError();  // clear a non-sticky launch error
+  record_cuda_error(err);
   return NVFP4_ERR_CUDA;
 }
 
@@ -598,6 +598,11 @@ bool plan_gemv(int64_t M, int64_t K, int64_t L, bool permuted, int kernel, int n
 
 }  // namespace nvfp4
 
+void nvfp4::record_cuda_error(cudaError_t err) {
+  g_last_cuda_error = (int)err;
+  (void)cudaGetLastError();  // clear a non-sticky launch error
+}
+
 using namespace nvfp4;
 
 extern "C" {
@@ -808,15 +813,16 @@ nvfp4_status_t nvfp4_gemm_small_n_plan(int64_t M, int64_t N, int64_t K, int64_t 
 int nvfp4_last_cuda_error(void) { return g_last_cuda_error; }
 
 int nvfp4_tensor_wait_timeouts(int reset) {
-  int v = 0, w = 0;
+  int v = 0, w = 0, g = 0;
   cudaError_t err = tc_wait_timeouts(reset, &v);
   if (err == cudaSuccess) err = blockdot_wait_timeouts(reset, &w);
+  if (err == cudaSuccess) err = gemm_wait_timeouts(reset, &g);
   if (err != cudaSuccess) {
     g_last_cuda_error = (int)err;
     (void)cudaGetLastError();
     return -1;
   }
-  return v + w;
+  return v + w + g;
 }
 
 nvfp4_status_t nvfp4_selftest_bounded_wait(int* completed, int* gave_up, int* timeouts,

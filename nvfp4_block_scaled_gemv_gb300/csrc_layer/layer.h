@@ -1,0 +1,150 @@
+// Host/device interface of the layer operators: quantise, the product for any
+// number of rows, routing, and the routed experts.
+#pragma once
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+namespace nvfp4 {
+
+enum DataType { kF16 = 0, kBF16 = 1, kF32 = 2 };  // nvfp4_dtype_t
+
+// Remembers a failed runtime call for nvfp4_last_cuda_error and clears a
+// non-sticky launch error (api.cu).
+void record_cuda_error(cudaError_t err);
+
+// Launch with programmatic stream serialization (the kernel waits for the
+// preceding work itself, with pdl_wait, before it touches memory).
+template <typename P>
+inline cudaError_t launch_pdl(void (*kern)(P), dim3 grid, dim3 block, size_t smem,
+                              cudaStream_t stream, const P& p, int cluster = 1) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+// ---- quantise / dequantise (quantize.cu) ----
+
+struct QuantizeParams {
+  const void* x;      // [L][rows] rows of x_stride elements
+  uint8_t* q;         // [L][rows][K/2], or with row_map [q_rows][K/2]
+  uint8_t* sf;        // scales of those rows
+  const int32_t* row_map;  // [rows][copies]: rows of q that a row of x goes to, or null
+  int64_t q_rows;     // rows of q with a row_map (entries outside [0, q_rows) are skipped)
+  int64_t rows, rows_pad, x_stride;
+  int64_t grid_rows, grid_blocks;  // set by the launcher
+  float encode;
+  int32_t copies, half_k, blocks, rest_k;
+};
+cudaError_t launch_quantize(QuantizeParams p, int dtype, bool permuted, int64_t L, int sms,
+                            cudaStream_t stream);
+
+struct DequantizeParams {
+  const uint8_t* q;
+  const uint8_t* sf;
+  void* x;
+  int64_t rows, L, x_stride;
+  float scale;
+  int32_t half_k, blocks, rest_k;
+  bool permuted;
+};
+cudaError_t launch_dequantize(const DequantizeParams& p, int dtype, int sms, cudaStream_t stream);
+
+struct FoldParams {
+  uint8_t* a;
+  uint8_t* sf;
+  int64_t rows, L;
+  int32_t half_k, blocks, rest_k;
+  bool permuted;
+};
+cudaError_t launch_fold_signs(const FoldParams& p, int sms, cudaStream_t stream);
+
+// ---- the product (gemm_tc.cu) ----
+
+// Dense (groups = batches) or grouped (groups = experts, token tiles from a
+// device table).
+struct GemmArgs {
+  const uint8_t* a;    // [G][M][K/2]
+  const uint8_t* sfa;  // 128x4 atoms per group
+  const uint8_t* b;    // dense [L][N][K/2]; grouped [rows][K/2]
+  const uint8_t* sfb;  // 128x4 atoms (grouped: of all rows)
+  int64_t M, N, K, G;  // N: rows of b per batch; grouped: all rows of b
+  // grouped: tiles of token rows {expert, first row, rows, 0} and their number, on the device
+  const int4* tiles;
+  const int32_t* tile_count;
+  int64_t max_tiles;   // upper bound of *tile_count
+  int tile_rows;       // rows of a grouped tile (the kernel's N tile)
+  // epilogue
+  void* c;             // [G or 1][N][c_stride], or null with a quantised output
+  int c_dtype;
+  int64_t c_stride;
+  const float* bias;   // [G][M] or null
+  const float* alphas; // [G] or null
+  float alpha;
+  int activation;
+  // quantised gated output: rows of K = M/2
+  uint8_t* q;
+  uint8_t* qsf;
+  float encode;
+};
+cudaError_t launch_gemm(const GemmArgs& g, int sms, cudaStream_t stream);
+cudaError_t gemm_wait_timeouts(int reset, int* out);
+// Rows of b per tile that the dense product uses for N rows.
+int gemm_tile_rows(int64_t M, int64_t N, int64_t L, int sms);
+
+// ---- routing and the experts' rows (route.cu, moe.cu) ----
+
+struct RouteParams {
+  const void* logits;  // [T] rows of stride elements
+  const float* bias;   // [E] or null
+  int32_t* ids;        // [T][k]
+  float* weights;      // [T][k]
+  int64_t T, stride;
+  float scale;
+  int32_t E, k, groups, top_groups, sigmoid, renormalize;
+};
+constexpr int kMaxExperts = 1024;
+constexpr int kMaxTopK = 32;
+constexpr int kMaxGroups = 32;
+cudaError_t launch_route(const RouteParams& p, int dtype, int sms, cudaStream_t stream);
+
+// Where the sort leaves its results: counts [E], tiles and their number, and
+// each choice's row.
+struct SortParams {
+  const int32_t* ids;  // [T*k]; outside [0, E): no expert
+  int32_t* rows;       // [T*k]: row of the choice, or -1
+  int32_t* counts;     // [E]
+  int32_t* starts;     // [E]: first row
+  int4* tiles;
+  int32_t* tile_count;
+  int32_t* chunk_counts;  // [chunks][E] scratch
+  int64_t n;           // T*k
+  int32_t E, tile_rows, pitch;  // a tile's rows, and rows from one tile to the next
+};
+constexpr int kSortThreads = 512;
+constexpr int kSortChunk = 4096;  // choices per CTA
+cudaError_t launch_sort(const SortParams& p, cudaStream_t stream);
+
+struct CombineParams {
+  const void* y;       // [rows][M] 16-bit values
+  const int32_t* rows; // [T][k]
+  const float* weights;
+  void* out;           // [T][M]
+  int64_t T, M;
+  int32_t k;
+};
+cudaError_t launch_combine(const CombineParams& p, int dtype, int sms, cudaStream_t stream);
+
+}  // namespace nvfp4

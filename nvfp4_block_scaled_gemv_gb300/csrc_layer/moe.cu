@@ -1,0 +1,225 @@
+// The experts' rows (sm_103a): a stable sort of the routed choices by expert,
+// and the weighted sum of a token's expert outputs.
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "layer.h"
+#include "ptx.cuh"
+
+namespace nvfp4 {
+
+namespace {
+
+constexpr int kSortWarps = kSortThreads / 32;
+
+// A warp's choices of its CTA's chunk are consecutive, 32 at a time; within 32
+// of them the ones with the same expert find each other by a match, so ranks
+// follow the order of the choices and nothing depends on timing.
+__device__ __forceinline__ int32_t choice(const SortParams& p, int64_t i, int64_t end) {
+  if (i >= end) return -1;
+  const int32_t e = p.ids[i];
+  return e >= 0 && e < p.E ? e : -1;
+}
+
+// Choices per expert of each chunk.
+__global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const SortParams p) {
+  extern __shared__ int32_t hist[];  // [E]
+  pdl_launch_dependents();
+  for (int e = threadIdx.x; e < p.E; e += kSortThreads) hist[e] = 0;
+  pdl_wait();
+  __syncthreads();
+  const int64_t begin = (int64_t)blockIdx.x * kSortChunk;
+  const int64_t end = begin + kSortChunk < p.n ? begin + kSortChunk : p.n;
+  for (int64_t i = begin + threadIdx.x; i < end; i += kSortThreads) {
+    const int32_t e = choice(p, i, end);
+    if (e >= 0) atomicAdd(&hist[e], 1);  // (a count: the order does not show)
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.E; e += kSortThreads)
+    p.chunk_counts[(int64_t)blockIdx.x * p.E + e] = hist[e];
+}
+
+// Inclusive scan over the CTA (kSortThreads values).
+__device__ __forceinline__ int32_t scan_cta(int32_t v, int32_t* part) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int32_t o = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += o;
+  }
+  if (lane == 31) part[warp] = v;
+  __syncthreads();
+  int32_t before = 0;
+  for (int w = 0; w < warp; ++w) before += part[w];
+  __syncthreads();
+  return v + before;
+}
+
+// Every choice's row: the expert's first row, plus the rank of the choice among
+// the expert's.  With one chunk the counts come from the chunk itself (ONE).
+template <bool ONE>
+__global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortParams p) {
+  extern __shared__ int32_t place[];  // [warps][E] offsets, then [E] counts, [E] first tile
+  __shared__ int32_t part[kSortWarps];
+  int32_t* const counts = place + kSortWarps * p.E;
+  int32_t* const first = counts + p.E;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_launch_dependents();
+  for (int i = threadIdx.x; i < kSortWarps * p.E; i += kSortThreads) place[i] = 0;
+  pdl_wait();
+  __syncthreads();
+  const int64_t begin = (int64_t)blockIdx.x * kSortChunk;
+  const int64_t end = begin + kSortChunk < p.n ? begin + kSortChunk : p.n;
+  const int64_t wbegin = begin + (int64_t)warp * (kSortChunk / kSortWarps);
+  // the warps' own counts
+  for (int s = 0; s < kSortChunk / kSortWarps; s += 32) {
+    if (wbegin + s >= end) break;
+    const int32_t e = choice(p, wbegin + s + lane, end);
+    const uint32_t same = __match_any_sync(0xffffffffu, e);
+    if (e >= 0 && lane == __ffs((int)same) - 1) place[warp * p.E + e] += __popc(same);
+    __syncwarp();
+  }
+  __syncthreads();
+  // before this chunk, and in all
+  for (int e = threadIdx.x; e < p.E; e += kSortThreads) {
+    int32_t all = 0, before = 0;
+    if (ONE) {
+      for (int w = 0; w < kSortWarps; ++w) all += place[w * p.E + e];
+    } else {
+      const int chunks = (int)gridDim.x;
+      for (int c = 0; c < chunks; ++c) {
+        if (c == (int)blockIdx.x) before = all;
+        all += p.chunk_counts[(int64_t)c * p.E + e];
+      }
+    }
+    counts[e] = all;
+    for (int w = 0; w < kSortWarps; ++w) {
+      const int32_t own = place[w * p.E + e];
+      place[w * p.E + e] = before;
+      before += own;
+    }
+  }
+  __syncthreads();
+  // tiles before each expert
+  int32_t carry = 0;
+  for (int e0 = 0; e0 < p.E; e0 += kSortThreads) {
+    const int e = e0 + (int)threadIdx.x;
+    const int32_t tiles = e < p.E ? (counts[e] + p.tile_rows - 1) / p.tile_rows : 0;
+    const int32_t up_to = scan_cta(tiles, part) + carry;
+    if (e < p.E) first[e] = up_to - tiles;
+    if (threadIdx.x == kSortThreads - 1) part[0] = up_to;
+    __syncthreads();
+    carry = part[0];
+    __syncthreads();
+  }
+  if (blockIdx.x == 0) {
+    if (threadIdx.x == 0) *p.tile_count = carry;
+    for (int e = threadIdx.x; e < p.E; e += kSortThreads) {
+      p.counts[e] = counts[e];
+      p.starts[e] = first[e] * p.pitch;
+      for (int i = 0, left = counts[e]; left > 0; ++i, left -= p.tile_rows)
+        p.tiles[first[e] + i] = make_int4(e, (first[e] + i) * p.pitch, min(left, p.tile_rows), 0);
+    }
+  }
+  // the choices' rows
+  for (int s = 0; s < kSortChunk / kSortWarps; s += 32) {
+    if (wbegin + s >= end) break;
+    const int64_t i = wbegin + s + lane;
+    const int32_t e = choice(p, i, end);
+    const uint32_t same = __match_any_sync(0xffffffffu, e);
+    if (i < end) {
+      int32_t row = -1;
+      if (e >= 0) {
+        const int32_t rank = place[warp * p.E + e] + __popc(same & ((1u << lane) - 1u));
+        const int32_t tile = rank / p.tile_rows;
+        row = (first[e] + tile) * p.pitch + rank - tile * p.tile_rows;
+      }
+      p.rows[i] = row;
+    }
+    __syncwarp();
+    if (e >= 0 && lane == __ffs((int)same) - 1) place[warp * p.E + e] += __popc(same);
+    __syncwarp();
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ float2 two_floats(uint32_t v);
+template <>
+__device__ __forceinline__ float2 two_floats<__half>(uint32_t v) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+template <>
+__device__ __forceinline__ float2 two_floats<__nv_bfloat16>(uint32_t v) {
+  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v));
+}
+template <typename T>
+__device__ __forceinline__ uint32_t two_rounded(float2 v);
+template <>
+__device__ __forceinline__ uint32_t two_rounded<__half>(float2 v) {
+  const __half2 h = __float22half2_rn(v);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t two_rounded<__nv_bfloat16>(float2 v) {
+  const __nv_bfloat162 h = __float22bfloat162_rn(v);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+constexpr int kCombineThreads = 256;
+
+// out[t] = sum_j weights[t][j] * y[rows[t][j]] in fp32, in the order of j; 8
+// values per thread.  M % 8 == 0.
+template <typename T>
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t chunks = p.M / 8, total = p.T * chunks;
+  for (int64_t i = (int64_t)blockIdx.x * kCombineThreads + threadIdx.x; i < total;
+       i += (int64_t)gridDim.x * kCombineThreads) {
+    const int64_t t = i / chunks, ch = i - t * chunks;
+    float2 sum[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
+    for (int j = 0; j < p.k; ++j) {
+      const int32_t row = p.rows[t * p.k + j];
+      if (row < 0) continue;
+      const float w = p.weights[t * p.k + j];
+      const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.y) + row * p.M + ch * 8);
+      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float2 f = two_floats<T>(u[c]);
+        sum[c].x = fmaf(w, f.x, sum[c].x);
+        sum[c].y = fmaf(w, f.y, sum[c].y);
+      }
+    }
+    *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + t * p.M + ch * 8) =
+        make_uint4(two_rounded<T>(sum[0]), two_rounded<T>(sum[1]), two_rounded<T>(sum[2]),
+                   two_rounded<T>(sum[3]));
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_sort(const SortParams& p, cudaStream_t stream) {
+  const int64_t chunks = (p.n + kSortChunk - 1) / kSortChunk;
+  const size_t smem = sizeof(int32_t) * (size_t)p.E * (kSortWarps + 2);
+  if (chunks > 1) {
+    cudaError_t err = launch_pdl(sort_count_kernel, dim3((unsigned)chunks), dim3(kSortThreads),
+                                 sizeof(int32_t) * (size_t)p.E, stream, p);
+    if (err != cudaSuccess) return err;
+  }
+  auto kern = chunks > 1 ? sort_place_kernel<false> : sort_place_kernel<true>;
+  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (err != cudaSuccess) return err;
+  return launch_pdl(kern, dim3((unsigned)(chunks < 1 ? 1 : chunks)), dim3(kSortThreads), smem, stream, p);
+}
+
+cudaError_t launch_combine(const CombineParams& p, int dtype, int sms, cudaStream_t stream) {
+  int64_t ctas = (p.T * (p.M / 8) + kCombineThreads - 1) / kCombineThreads;
+  if (ctas > 64ll * sms) ctas = 64ll * sms;
+  auto kern = dtype == kBF16 ? combine_kernel<__nv_bfloat16> : combine_kernel<__half>;
+  return launch_pdl(kern, dim3((unsigned)ctas), dim3(kCombineThreads), 0, stream, p);
+}
+
+}  // namespace nvfp4
