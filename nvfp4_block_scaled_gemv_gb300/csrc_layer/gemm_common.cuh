@@ -1,0 +1,269 @@
+// What the product kernels share: parameters, tiles, and the epilogue.
+#pragma once
+#include <cstdint>
+
+#include "epilogue.cuh"
+#include "layer.h"
+#include "quantize.cuh"
+#include "tc_ptx.cuh"
+
+namespace nvfp4 {
+namespace gemm {
+
+constexpr uint32_t kABytes = 128 * 128;   // 128 rows x 256 elements
+constexpr uint32_t kAtoms = 4 * 512;      // a stage's scale atoms of 128 rows
+constexpr int kTransposePitch = 33;       // floats between columns of a warp's transpose buffer
+constexpr int kUnit = 16;                 // columns an epilogue warp takes at once
+constexpr uint32_t kTransposeBytes = kUnit * kTransposePitch * 4;  // per epilogue warp
+
+enum Epilogue { kStore = 0, kGatedQuantize = 1 };
+
+struct GemmParams {
+  CUtensorMap tmap_a;    // uint8 {K/2, M, G}, box {128, 128, 1}, 128-byte swizzle
+  CUtensorMap tmap_b;    // uint8 {K/2, N, L}, box {128, rows, 1}, 128-byte swizzle
+  CUtensorMap tmap_sfa;  // pair kernel: the atoms as uint64 {rest_k * 64, G * rest_m}, box {256, 1}
+  CUtensorMap tmap_sfb;  // pair kernel: {rest_k * 64, L * rest_n}, box {256, 2}
+  const uint8_t* sfa;    // [G][rest_m][rest_k][512]
+  const uint8_t* sfb;    // [L][rest_n][rest_k][512]
+  const int4* tiles;     // grouped: {expert, first row, rows, 0}
+  const int32_t* tile_count;
+  void* c;
+  const float* bias;
+  const float* alphas;
+  uint8_t* q;
+  uint8_t* qsf;
+  int64_t M, N, c_stride;
+  float alpha, encode;
+  int32_t c_dtype, activation;
+  int32_t paired;        // c takes stores of two adjacent elements
+  int32_t rest_m, rest_n, rest_k, kstages;
+  int32_t tiles_m;       // tiles of A per group
+  int32_t tiles_n;       // dense: N tiles per batch
+  int32_t total;         // dense: tiles
+  int64_t rows;          // dense: rows of c in all batches
+};
+
+// One output tile: the mt-th tile of group g's A against rows n0..n0+rows-1 of b.
+struct Tile {
+  int32_t g;     // batch or expert
+  int32_t mt;
+  int64_t n0;    // first row of b (within the batch)
+  int32_t rows;
+};
+
+template <int BN, bool GROUPED>
+__device__ __forceinline__ Tile tile_at(const GemmParams& p, int32_t t) {
+  Tile o;
+  const int32_t nt = t / p.tiles_m;
+  o.mt = t - nt * p.tiles_m;
+  if constexpr (GROUPED) {
+    const int4 e = p.tiles[nt];
+    o.g = e.x;
+    o.n0 = e.y;
+    o.rows = e.z;
+  } else {
+    o.g = nt / p.tiles_n;
+    o.n0 = (int64_t)(nt - o.g * p.tiles_n) * BN;
+    o.rows = (int32_t)(p.N - o.n0 < BN ? p.N - o.n0 : BN);
+  }
+  return o;
+}
+
+// True on one lane of a converged warp.  The tcgen05 instructions take their
+// descriptors from uniform registers: issued by an elected lane inside control
+// flow that the whole warp follows they are one instruction each, while under a
+// `lane == 0` branch a 256-row stage's 17 instructions took ~1500 cycles of the
+// issuing thread, 4 times the MMAs' own time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t is;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(is));
+  return is != 0;
+}
+
+__device__ __forceinline__ uint32_t pack2(__half, float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack2(__nv_bfloat16, float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float round_to(float, float v) { return v; }
+__device__ __forceinline__ __half round_to(__half, float v) { return __float2half_rn(v); }
+__device__ __forceinline__ __nv_bfloat16 round_to(__nv_bfloat16, float v) { return __float2bfloat16_rn(v); }
+
+// Columns i and i+1 of this lane's row (a, b), turned with the neighbouring
+// lane's into two adjacent rows of one column: column i on even lanes, i+1 on
+// odd ones.
+template <typename T>
+struct Turned;
+template <typename T>
+struct Turned16 {
+  using Store = uint32_t;
+  static __device__ __forceinline__ Store turn(float a, float b, bool odd) {
+    const uint32_t own = pack2(T(), a, b);
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, own, 1);
+    return __byte_perm(own, got, odd ? 0x3276 : 0x5410);
+  }
+};
+template <>
+struct Turned<__half> : Turned16<__half> {};
+template <>
+struct Turned<__nv_bfloat16> : Turned16<__nv_bfloat16> {};
+template <>
+struct Turned<float> {
+  using Store = float2;
+  static __device__ __forceinline__ Store turn(float a, float b, bool odd) {
+    const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+    return make_float2(odd ? got : a, odd ? b : got);
+  }
+};
+
+// Two fp32 fused multiply-adds in one instruction.
+__device__ __forceinline__ void fma2(float& x, float& y, float a, float b) {
+  asm("{\n\t.reg .b64 v, m, c;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 m, {%2, %2};\n\tmov.b64 c, {%3, %3};\n\t"
+      "fma.rn.f32x2 v, v, m, c;\n\tmov.b64 {%0, %1}, v;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
+
+// Columns 0..15 at a TMEM address, without waiting for them.
+__device__ __forceinline__ void tmem_load_16(uint32_t taddr, float (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15}, [%16];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]),
+        "=f"(v[15])
+      : "r"(taddr));
+}
+// Wait for the loads; v is theirs (so that nothing uses it before).
+__device__ __forceinline__ void tmem_wait(float (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]),
+                 "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]),
+                 "+f"(v[14]), "+f"(v[15])::"memory");
+}
+
+// A warp's place in a tile: lane i has the row m of A, all lanes the same
+// columns (rows of b).
+struct Place {
+  int64_t m, row0;   // row of A; row of c or q of the tile's column 0
+  int32_t rows;      // columns of the tile
+  int64_t block;     // quantised output: the scale block of the warp's 32 rows
+  float alpha, bias;
+  float* transpose;  // the warp's buffer, for the quantised output
+};
+
+// Columns n..n+kUnit-1 of the lanes' rows: column i goes to c[(row0 + n + i) * stride + m].
+// Neighbouring lanes swap values, so that each stores two adjacent elements of
+// one column: half the store instructions.
+template <typename T>
+__device__ __forceinline__ void store_columns(const GemmParams& p, const Place& w, int n,
+                                              const float (&v)[kUnit]) {
+  T* at = static_cast<T*>(p.c) + (w.row0 + n) * p.c_stride;
+  if (p.paired) {
+    const bool odd = (threadIdx.x & 1) != 0;  // (m is the lane plus a multiple of 32)
+    at += (odd ? p.c_stride : 0) + (w.m & ~int64_t(1));
+    const int64_t step = 2 * p.c_stride;
+    const bool whole = n + kUnit <= w.rows && (w.m | 31) < p.M;  // the same for the whole warp
+    const int left = w.m < p.M ? w.rows - n - (odd ? 1 : 0) : 0;
+#pragma unroll
+    for (int i = 0; i < kUnit; i += 2) {
+      const typename Turned<T>::Store two = Turned<T>::turn(v[i], v[i + 1], odd);
+      if (whole || i < left) *reinterpret_cast<typename Turned<T>::Store*>(at) = two;
+      at += step;
+    }
+  } else if (w.m < p.M) {
+    at += w.m;
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i) {
+      if (n + i < w.rows) *at = round_to(T(), v[i]);
+      at += p.c_stride;
+    }
+  }
+}
+
+// The epilogue of columns n..n+kUnit-1 (sums v) of a warp's 32 rows.
+template <int EPI>
+__device__ __forceinline__ void finish_columns(const GemmParams& p, const Place& w, int n, float (&v)[kUnit]) {
+  if constexpr (EPI == kStore) {
+#pragma unroll
+    for (int i = 0; i < kUnit; i += 2) fma2(v[i], v[i + 1], w.alpha, w.bias);
+    if (p.activation != 0) {
+#pragma unroll
+      for (int i = 0; i < kUnit; ++i) v[i] = activate(v[i], p.activation);
+    }
+    if (p.c_dtype == kBF16)
+      store_columns<__nv_bfloat16>(p, w, n, v);
+    else if (p.c_dtype == kF16)
+      store_columns<__half>(p, w, n, v);
+    else
+      store_columns<float>(p, w, n, v);
+  } else {
+    // the 32 rows are gate and input of 16 outputs: one scale block.  Transposed
+    // through shared memory, two lanes take a column, 8 outputs each.
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i) w.transpose[i * kTransposePitch + lane] = v[i];
+    __syncwarp();
+    const int col = lane >> 1, half = lane & 1;
+    float h[8];
+    float amax = 0.f;
+    bool finite = true;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float gate = w.transpose[col * kTransposePitch + half * 16 + 2 * i] * w.alpha;
+      const float in = w.transpose[col * kTransposePitch + half * 16 + 2 * i + 1] * w.alpha;
+      // (SiLU: the fast exponential and division are good to a few fp32 ulps, and
+      // the exact forms' instructions would outlast the tile's MMAs)
+      const float a = p.activation == 2 ? __fdividef(gate, 1.f + __expf(-gate)) : activate(gate, p.activation);
+      h[i] = a * in * p.encode;
+      const float mag = fabsf(h[i]);
+      finite = finite && mag < __int_as_float(0x7f800000);
+      amax = fmaxf(amax, mag);
+    }
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    finite = __shfl_xor_sync(0xffffffffu, finite ? 1 : 0, 1) != 0 && finite;
+    uint32_t code = 0x7Fu, q = 0;
+    if (finite) {
+      float s;
+      code = block_scale_code(amax, s);
+      if (s > 0.f) q = quantize_8(h, s, 1.0f / s);
+    }
+    const int64_t row = w.row0 + n + col;
+    const int64_t blocks = p.M / 32, rest = (p.M / 2 + 63) / 64;
+    if (n + col < w.rows) {
+      if (w.block < blocks) *reinterpret_cast<uint32_t*>(p.q + row * (p.M / 4) + w.block * 8 + 4 * half) = q;
+      // (blocks past the last one pad the last atom column with zero scales)
+      if (half == 0 && w.block < 4 * rest)
+        p.qsf[atom_offset(row, w.block, rest)] = w.block < blocks ? (uint8_t)code : (uint8_t)0;
+    }
+  }
+}
+
+template <int EPI, bool GROUPED>
+__device__ __forceinline__ Place place_of(const GemmParams& p, const Tile& t, int64_t row_tile, int quarter,
+                                          float* transpose) {
+  Place w;
+  w.m = row_tile * 128 + 32 * quarter + (int)(threadIdx.x & 31);
+  w.row0 = (GROUPED ? 0 : (int64_t)t.g * p.N) + t.n0;
+  w.rows = t.rows;
+  w.block = row_tile * 4 + quarter;
+  w.alpha = p.alphas ? p.alphas[t.g] : p.alpha;
+  w.bias = EPI == kStore && p.bias && w.m < p.M ? p.bias[(int64_t)t.g * p.M + w.m] : 0.f;
+  w.transpose = transpose;
+  return w;
+}
+
+}  // namespace gemm
+
+
+// The pair kernel (gemm_pair.cu); p complete but for its tensor maps' boxes.
+cudaError_t launch_gemm_pair(const gemm::GemmParams& p, int epi, bool grouped, int64_t max_tiles, int sms,
+                             cudaStream_t stream);
+cudaError_t gemm_pair_wait_timeouts(int reset, int* out);
+
+}  // namespace nvfp4

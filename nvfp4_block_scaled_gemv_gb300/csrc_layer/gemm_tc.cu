@@ -19,6 +19,7 @@
 //   warp 1     allocates tensor memory; one lane issues TMEM copies and MMAs
 //   warps 2-5  read the accumulator (a TMEM lane quarter each) and store c, or
 //              quantise the gated activation
+// Tiles of 256 rows of B run on pairs of SMs instead (gemm_pair.cu).
 //
 // Scale codes are unsigned magnitudes (the MMA ignores bit 7).
 //
@@ -27,10 +28,7 @@
 #include <cstdint>
 #include <cstring>
 
-#include "epilogue.cuh"
-#include "layer.h"
-#include "quantize.cuh"
-#include "tc_ptx.cuh"
+#include "gemm_common.cuh"
 
 namespace nvfp4 {
 
@@ -38,86 +36,29 @@ __device__ int g_gemm_timeouts;
 
 namespace {
 
+using namespace gemm;
+
 constexpr int kGemmThreads = 192;
-constexpr uint32_t kABytes = 128 * 128;
-constexpr uint32_t kAtoms = 4 * 512;  // a stage's scale atoms of 128 rows
-constexpr int kTransposePitch = 33;   // floats between columns of a warp's transpose buffer
-constexpr int kTransposeCols = 16;
 
-enum Epilogue { kStore = 0, kGatedQuantize = 1 };
-
-__host__ __device__ constexpr uint32_t stage_bytes(int bn) {
-  return kABytes + (uint32_t)bn * 128u + kAtoms + (bn > 128 ? 2u : 1u) * kAtoms;
-}
-__host__ __device__ constexpr int stages_for(int bn) { return bn > 128 ? 4 : bn == 128 ? 5 : 6; }
+__host__ __device__ constexpr uint32_t stage_bytes(int bn) { return kABytes + (uint32_t)bn * 128u + 2 * kAtoms; }
+__host__ __device__ constexpr int stages_for(int bn) { return bn == 128 ? 5 : 6; }
 __host__ __device__ constexpr uint32_t gemm_smem_bytes(int bn, int epi) {
   return (uint32_t)stages_for(bn) * stage_bytes(bn) + 1024u +
-         (epi == kGatedQuantize ? 4u * kTransposeCols * kTransposePitch * 4u : 0u);
+         (epi == kGatedQuantize ? 4u * kTransposeBytes : 0u);
 }
 
-struct GemmParams {
-  CUtensorMap tmap_a;  // uint8 {K/2, M, G}, box {128, 128, 1}, 128-byte swizzle
-  CUtensorMap tmap_b;  // uint8 {K/2, N, L}, box {128, BN, 1}, 128-byte swizzle
-  const uint8_t* sfa;  // [G][rest_m][rest_k][512]
-  const uint8_t* sfb;  // [L][rest_n][rest_k][512]
-  const int4* tiles;   // grouped: {expert, first row, rows, 0}
-  const int32_t* tile_count;
-  void* c;
-  const float* bias;
-  const float* alphas;
-  uint8_t* q;
-  uint8_t* qsf;
-  int64_t M, N, c_stride;
-  float alpha, encode;
-  int32_t c_dtype, activation;
-  int32_t rest_m, rest_n, rest_k, kstages;
-  int32_t tiles_n;     // dense: N tiles per batch
-  int64_t total;       // dense: tiles
-};
-
-// One output tile: rows m0.. of group g's A against rows n0..n0+rows-1 of b.
-struct Tile {
-  int32_t g;           // batch or expert
-  int32_t mt;          // 128-row tile of A
-  int64_t n0;          // first row of b (within the batch)
-  int32_t rows;        // rows of b in the tile
-};
-
-template <int BN, bool GROUPED>
-__device__ __forceinline__ Tile tile_at(const GemmParams& p, int64_t t) {
-  Tile o;
-  const int64_t nt = t / p.rest_m;
-  o.mt = (int32_t)(t - nt * p.rest_m);
-  if constexpr (GROUPED) {
-    const int4 e = p.tiles[nt];
-    o.g = e.x;
-    o.n0 = e.y;
-    o.rows = e.z;
-  } else {
-    o.g = (int32_t)(nt / p.tiles_n);
-    o.n0 = (nt - (int64_t)o.g * p.tiles_n) * BN;
-    o.rows = (int32_t)(p.N - o.n0 < BN ? p.N - o.n0 : BN);
-  }
-  return o;
-}
-
-__device__ __forceinline__ void store_c(const GemmParams& p, int64_t idx, float v) {
-  if (p.c_dtype == kF32)
-    static_cast<float*>(p.c)[idx] = v;
-  else if (p.c_dtype == kBF16)
-    static_cast<__nv_bfloat16*>(p.c)[idx] = __float2bfloat16_rn(v);
-  else
-    static_cast<__half*>(p.c)[idx] = __float2half_rn(v);
+template <typename T>
+__device__ __forceinline__ void store_one(const GemmParams& p, int64_t idx, float v) {
+  static_cast<T*>(p.c)[idx] = round_to(T(), v);
 }
 
 template <int BN, int EPI, bool GROUPED>
 __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_constant__ GemmParams p) {
   constexpr int S = stages_for(BN);
-  constexpr int kAcc = BN > 128 ? 1 : 2;            // accumulators in tensor memory
-  constexpr uint32_t kSfbAtomRows = BN > 128 ? 2 : 1;
-  constexpr uint32_t kSfaCol = kAcc * (BN < 32 ? 32 : BN);
+  constexpr int kAcc = 2;  // accumulators in tensor memory
+  constexpr uint32_t kSfaCol = kAcc * BN;
   constexpr uint32_t kSfbCol = kSfaCol + 16 * S;
-  static_assert(kSfbCol + 16 * kSfbAtomRows * S <= 512, "TMEM columns");
+  static_assert(kSfbCol + 16 * S <= 512, "TMEM columns");
   extern __shared__ uint8_t gemm_smem[];
   __shared__ __align__(8) uint64_t bars[2 * S + 2 * kAcc + 1];
   __shared__ uint32_t tmem_slot;
@@ -127,8 +68,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
   const uint32_t b_s = a_s + S * kABytes;
   const uint32_t sfa_s = b_s + S * BN * 128u;
   const uint32_t sfb_s = sfa_s + S * kAtoms;
-  const uint32_t tr_s = sfb_s + S * kSfbAtomRows * kAtoms;
-  uint8_t* const gen = gemm_smem - raw;
+  const uint32_t tr_s = sfb_s + S * kAtoms;
   const uint32_t bar0 = smem_u32(bars);
   auto full_bar = [&](int st) { return bar0 + 8u * st; };
   auto empty_bar = [&](int st) { return bar0 + 8u * (S + st); };
@@ -136,7 +76,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
   auto dempty_bar = [&](int i) { return bar0 + 8u * (2 * S + kAcc + i); };
   const uint32_t drain_bar = bar0 + 8u * (2 * S + 2 * kAcc);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int st = 0; st < S; ++st) {
       tc::mbar_init(full_bar(st), 1);
@@ -144,7 +84,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
     }
     for (int i = 0; i < kAcc; ++i) {
       tc::mbar_init(dfull_bar(i), 1);
-      tc::mbar_init(dempty_bar(i), 128);
+      tc::mbar_init(dempty_bar(i), 4);
     }
     tc::mbar_init(drain_bar, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -158,161 +98,117 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
   __syncthreads();
   tc::fence_after();
   pdl_launch_dependents();
-  const uint32_t tmem = tmem_slot;
-  const int64_t total = GROUPED ? (int64_t)*p.tile_count * p.rest_m : p.total;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
+  const int32_t total = GROUPED ? __shfl_sync(0xffffffffu, *p.tile_count, 0) * p.tiles_m : p.total;
   bool ok = true;
 
   if (warp == 0) {
-    if (lane == 0) {
-      int pos = 0, issued = 0;
-      uint32_t ph = 0;
-      for (int64_t t = blockIdx.x; t < total; t += gridDim.x) {
-        const Tile tile = tile_at<BN, GROUPED>(p, t);
-        const int64_t batch = GROUPED ? 0 : tile.g;
-        const uint8_t* sa = p.sfa + ((int64_t)tile.g * p.rest_m + tile.mt) * p.rest_k * 512;
-        const uint8_t* sb = p.sfb + (batch * p.rest_n + tile.n0 / 128) * p.rest_k * 512;
-        const bool second = BN > 128 && tile.rows > 128;  // the tile has rows in a second atom
-        for (int s = 0; s < p.kstages; ++s) {
-          const uint32_t nb = (uint32_t)min(4, p.rest_k - 4 * s) * 512u;
-          if (tc::mbar_wait<false>(empty_bar(pos), ph ^ 1u, ok, &g_gemm_timeouts)) {
-            const uint32_t fb = full_bar(pos);
-            tc::mbar_expect_tx(fb, kABytes + BN * 128u + nb * (second ? 3u : 2u));
+    int pos = 0, issued = 0;
+    uint32_t ph = 0;
+    for (int32_t t = (int32_t)blockIdx.x; t < total; t += (int32_t)gridDim.x) {
+      const Tile tile = tile_at<BN, GROUPED>(p, t);
+      const int64_t batch = GROUPED ? 0 : tile.g;
+      const uint8_t* sa = p.sfa + ((int64_t)tile.g * p.rest_m + tile.mt) * p.rest_k * 512;
+      const uint8_t* sb = p.sfb + (batch * p.rest_n + tile.n0 / 128) * p.rest_k * 512;
+      for (int s = 0; s < p.kstages; ++s) {
+        const uint32_t nb = (uint32_t)min(4, p.rest_k - 4 * s) * 512u;
+        tc::mbar_wait<false>(empty_bar(pos), ph ^ 1u, ok, &g_gemm_timeouts);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) {
+          const uint32_t fb = full_bar(pos);
+          if (elect_one()) {
+            tc::mbar_expect_tx(fb, kABytes + BN * 128u + 2u * nb);
             tc::tma_load_3d(a_s + pos * kABytes, &p.tmap_a, s * 128, tile.mt * 128, tile.g, fb);
             tc::tma_load_3d(b_s + pos * BN * 128u, &p.tmap_b, s * 128, (int)tile.n0, (int)batch, fb);
             tc::bulk_load(sfa_s + pos * kAtoms, sa + (int64_t)s * kAtoms, nb, fb);
-            tc::bulk_load(sfb_s + pos * kSfbAtomRows * kAtoms, sb + (int64_t)s * kAtoms, nb, fb);
-            if (second)
-              tc::bulk_load(sfb_s + pos * kSfbAtomRows * kAtoms + kAtoms,
-                            sb + ((int64_t)p.rest_k + 4 * s) * 512, nb, fb);
-            ++issued;
+            tc::bulk_load(sfb_s + pos * kAtoms, sb + (int64_t)s * kAtoms, nb, fb);
           }
-          if (++pos == S) {
-            pos = 0;
-            ph ^= 1u;
-          }
+          __syncwarp();
+          ++issued;
         }
-      }
-      // copies still in flight land before the CTA can exit
-      bool drain_ok = true;
-      for (int k = 0; k < S && k < issued; ++k) {
-        const int i = issued - 1 - k;
-        tc::mbar_wait<false>(full_bar(i % S), (uint32_t)((i / S) & 1), drain_ok, &g_gemm_timeouts);
+        if (++pos == S) {
+          pos = 0;
+          ph ^= 1u;
+        }
       }
     }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t idesc = tc::mxf4nvf4_idesc(BN);
-      int pos = 0, j = 0;
-      uint32_t ph = 0;
-      for (int64_t t = blockIdx.x; t < total; t += gridDim.x, ++j) {
-        const int acc = j % kAcc;
-        const uint32_t d = tmem + acc * BN;
-        tc::mbar_wait<false>(dempty_bar(acc), ((uint32_t)(j / kAcc) & 1u) ^ 1u, ok, &g_gemm_timeouts);
-        for (int s = 0; s < p.kstages; ++s) {
-          const int nk = min(4, p.rest_k - 4 * s);
-          if (tc::mbar_wait<false>(full_bar(pos), ph, ok, &g_gemm_timeouts)) {
-            tc::fence_after();
-            const uint32_t ca = tmem + kSfaCol + 16u * pos, cb = tmem + kSfbCol + 16u * kSfbAtomRows * pos;
-            const uint32_t sa = sfa_s + pos * kAtoms, sb = sfb_s + pos * kSfbAtomRows * kAtoms;
-            for (int kk = 0; kk < nk; ++kk) {
-              tc::copy_atom(ca + 4u * kk, tc::desc_atom(sa + 512u * kk));
-              tc::copy_atom(cb + 4u * kSfbAtomRows * kk, tc::desc_atom(sb + 512u * kk));
-              if constexpr (BN > 128)
-                tc::copy_atom(cb + 8u * kk + 4u, tc::desc_atom(sb + kAtoms + 512u * kk));
-            }
-            for (int kk = 0; kk < nk; ++kk)
-              tc::mma(d, tc::desc_sw128(a_s + pos * kABytes + 32u * kk),
-                      tc::desc_sw128(b_s + pos * BN * 128u + 32u * kk), idesc, ca + 4u * kk,
-                      cb + 4u * kSfbAtomRows * kk, s > 0 || kk > 0);
-            tc::commit(empty_bar(pos));
-          }
-          if (++pos == S) {
-            pos = 0;
-            ph ^= 1u;
-          }
-        }
-        if (ok) tc::commit(dfull_bar(acc));
-      }
-      // every MMA and TMEM copy has finished before TMEM is released
-      tc::commit(drain_bar);
-      bool drain_ok = true;
-      tc::mbar_wait<false>(drain_bar, 0, drain_ok, &g_gemm_timeouts);
+    // copies still in flight land before the CTA can exit
+    bool drain_ok = true;
+    for (int k = 0; k < S && k < issued; ++k) {
+      const int i = issued - 1 - k;
+      tc::mbar_wait<false>(full_bar(i % S), (uint32_t)((i / S) & 1), drain_ok, &g_gemm_timeouts);
     }
     __syncwarp();
+  } else if (warp == 1) {
+    constexpr uint32_t idesc = tc::mxf4nvf4_idesc(BN);
+    int pos = 0, j = 0;
+    uint32_t ph = 0;
+    for (int32_t t = (int32_t)blockIdx.x; t < total; t += (int32_t)gridDim.x, ++j) {
+      const int acc = j % kAcc;
+      const uint32_t d = tmem + acc * BN;
+      tc::mbar_wait<false>(dempty_bar(acc), ((uint32_t)(j / kAcc) & 1u) ^ 1u, ok, &g_gemm_timeouts);
+      for (int s = 0; s < p.kstages; ++s) {
+        const int nk = min(4, p.rest_k - 4 * s);
+        tc::mbar_wait<false>(full_bar(pos), ph, ok, &g_gemm_timeouts);
+        ok = __all_sync(0xffffffffu, ok);
+        tc::fence_after();
+        if (ok) {
+          const uint32_t ca = tmem + kSfaCol + 16u * pos, cb = tmem + kSfbCol + 16u * pos;
+          const uint64_t da = tc::desc_sw128(a_s + pos * kABytes), db = tc::desc_sw128(b_s + pos * BN * 128u);
+          const uint64_t dsa = tc::desc_atom(sfa_s + pos * kAtoms);
+          const uint64_t dsb = tc::desc_atom(sfb_s + pos * kAtoms);
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              if (kk < nk) {
+                // (a descriptor counts addresses in units of 16 bytes)
+                tc::copy_atom(ca + 4u * kk, dsa + 32u * kk);
+                tc::copy_atom(cb + 4u * kk, dsb + 32u * kk);
+              }
+            }
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              if (kk < nk)
+                tc::mma(d, da + 2u * kk, db + 2u * kk, idesc, ca + 4u * kk, cb + 4u * kk, s > 0 || kk > 0);
+            }
+            tc::commit(empty_bar(pos));
+          }
+          __syncwarp();
+        }
+        if (++pos == S) {
+          pos = 0;
+          ph ^= 1u;
+        }
+      }
+      if (ok && elect_one()) tc::commit(dfull_bar(acc));
+      __syncwarp();
+    }
+    // every MMA and TMEM copy has finished before TMEM is released
+    if (elect_one()) tc::commit(drain_bar);
+    bool drain_ok = true;
+    tc::mbar_wait<false>(drain_bar, 0, drain_ok, &g_gemm_timeouts);
+    __syncwarp();
   } else {
-    const uint32_t quarter = (uint32_t)(warp & 3);
-    float* const tr = reinterpret_cast<float*>(gen + tr_s) + (warp - 2) * kTransposeCols * kTransposePitch;
+    const int quarter = warp & 3;
+    float* const tr =
+        reinterpret_cast<float*>(gemm_smem + (tr_s - raw)) + (warp - 2) * (int)(kTransposeBytes / 4);
     int j = 0;
-    for (int64_t t = blockIdx.x; t < total; t += gridDim.x, ++j) {
+    for (int32_t t = (int32_t)blockIdx.x; t < total; t += (int32_t)gridDim.x, ++j) {
       const int acc = j % kAcc;
       const Tile tile = tile_at<BN, GROUPED>(p, t);
-      const int64_t m = (int64_t)tile.mt * 128 + 32 * quarter + lane;
-      const float alpha = p.alphas ? p.alphas[tile.g] : p.alpha;
-      const float bias = p.bias && m < p.M ? p.bias[(int64_t)tile.g * p.M + m] : 0.f;
+      const Place w = place_of<EPI, GROUPED>(p, tile, tile.mt, quarter, tr);
       if (lane == 0) tc::mbar_wait<false>(dfull_bar(acc), (uint32_t)(j / kAcc) & 1u, ok, &g_gemm_timeouts);
       __syncwarp();
       ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-      constexpr int kCols = EPI == kGatedQuantize ? kTransposeCols : BN < 32 ? 16 : 32;
-      if (ok) {
-        tc::fence_after();
-        for (int n = 0; n < tile.rows; n += kCols) {
-          float v[kCols];
-          tc::tmem_load_cols<kCols>(tmem + acc * BN + n + ((32u * quarter) << 16), v);
-          if constexpr (EPI == kStore) {
-            const int64_t row0 = (GROUPED ? 0 : (int64_t)tile.g * p.N) + tile.n0 + n;
-            if (m < p.M) {
-#pragma unroll
-              for (int i = 0; i < kCols; ++i) {
-                if (n + i < tile.rows) {
-                  float y = fmaf(v[i], alpha, bias);
-                  if (p.activation != 0) y = activate(y, p.activation);
-                  store_c(p, (row0 + i) * p.c_stride + m, y);
-                }
-              }
-            }
-          } else {
-            // the quarter's 32 rows are gate and up of 16 outputs: one scale
-            // block.  Two lanes take a token, 8 outputs each.
-#pragma unroll
-            for (int i = 0; i < kCols; ++i) tr[i * kTransposePitch + lane] = v[i];
-            __syncwarp();
-            const int col = lane >> 1, half = lane & 1;
-            float h[8];
-            float amax = 0.f;
-            bool finite = true;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float gate = tr[col * kTransposePitch + half * 16 + 2 * i] * alpha;
-              const float up = tr[col * kTransposePitch + half * 16 + 2 * i + 1] * alpha;
-              const float a = p.activation == 2 ? gate / (1.f + expf(-gate)) : activate(gate, p.activation);
-              h[i] = a * up * p.encode;
-              const float mag = fabsf(h[i]);
-              finite = finite && mag < __int_as_float(0x7f800000);
-              amax = fmaxf(amax, mag);
-            }
-            __syncwarp();
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-            finite = __shfl_xor_sync(0xffffffffu, finite ? 1 : 0, 1) != 0 && finite;
-            uint32_t code = 0x7Fu, q = 0;
-            if (finite) {
-              float s;
-              code = block_scale_code(amax, s);
-              if (s > 0.f) q = quantize_8(h, s, 1.0f / s);
-            }
-            const int64_t row = tile.n0 + n + col;
-            const int64_t kb = (int64_t)tile.mt * 4 + quarter;  // scale block of the output row
-            const int64_t blocks = p.M / 32, rest = (p.M / 2 + 63) / 64;
-            if (n + col < tile.rows) {
-              if (kb < blocks)
-                *reinterpret_cast<uint32_t*>(p.q + row * (p.M / 4) + kb * 8 + 4 * half) = q;
-              if (half == 0 && kb < 4 * rest)
-                p.qsf[atom_offset(row, kb, rest)] = kb < blocks ? (uint8_t)code : (uint8_t)0;
-            }
-          }
-        }
+      tc::fence_after();
+      for (int n = 0; ok && n < tile.rows; n += kUnit) {
+        float v[kUnit];
+        tc::tmem_load_cols<kUnit>(tmem + acc * BN + n + ((uint32_t)(32 * quarter) << 16), v);
+        finish_columns<EPI>(p, w, n, v);
       }
       tc::fence_before();
-      tc::mbar_arrive(dempty_bar(acc));
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(dempty_bar(acc));
     }
   }
 
@@ -328,12 +224,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
 __global__ void __launch_bounds__(256) gemm_no_k_kernel(const GemmParams p) {
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t total = p.total * p.M;  // rows of all batches * M
+  const int64_t total = p.rows * p.M;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
     const int64_t row = i / p.M, m = i - row * p.M;
     float y = p.bias ? p.bias[row / p.N * p.M + m] : 0.f;
     if (p.activation != 0) y = activate(y, p.activation);
-    store_c(p, row * p.c_stride + m, y);
+    if (p.c_dtype == kF32)
+      store_one<float>(p, row * p.c_stride + m, y);
+    else if (p.c_dtype == kBF16)
+      store_one<__nv_bfloat16>(p, row * p.c_stride + m, y);
+    else
+      store_one<__half>(p, row * p.c_stride + m, y);
   }
 }
 
@@ -354,7 +255,7 @@ cudaError_t launch_bn(int bn, const GemmParams& p, int64_t max_tiles, int sms, c
     case 32: return launch_variant<32, EPI, GROUPED>(p, max_tiles, sms, stream);
     case 64: return launch_variant<64, EPI, GROUPED>(p, max_tiles, sms, stream);
     case 128: return launch_variant<128, EPI, GROUPED>(p, max_tiles, sms, stream);
-    case 256: return launch_variant<256, EPI, GROUPED>(p, max_tiles, sms, stream);
+    case 256: return launch_gemm_pair(p, EPI, GROUPED, max_tiles, sms, stream);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -367,6 +268,18 @@ bool encode_rows(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, con
   const cuuint32_t estr[3] = {1, 1, 1};
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(base), dims, strides, box,
                 estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Rows of scale atoms as 8-byte elements: a stage's 2 KB of a row is one box row.
+bool encode_atoms(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, const uint8_t* base,
+                  int64_t rest_k, int64_t rows, uint32_t box_rows) {
+  const cuuint64_t dims[2] = {(cuuint64_t)(rest_k * 64), (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)(rest_k * 512)};
+  const cuuint32_t box[2] = {256, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT64, 2, const_cast<uint8_t*>(base), dims, strides, box,
+                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -397,35 +310,46 @@ cudaError_t launch_gemm(const GemmArgs& g, int sms, cudaStream_t stream) {
   p.encode = g.encode;
   p.c_dtype = g.c_dtype;
   p.activation = g.activation;
+  const uintptr_t two = g.c_dtype == kF32 ? 8 : 4;
+  p.paired = reinterpret_cast<uintptr_t>(g.c) % two == 0 && g.c_stride % 2 == 0 && g.M % 2 == 0;
   p.rest_m = (int32_t)((g.M + 127) / 128);
   p.rest_n = (int32_t)((g.N + 127) / 128);
   p.rest_k = (int32_t)((g.K + 63) / 64);
   p.kstages = (p.rest_k + 3) / 4;
   if (g.K == 0) {
-    p.total = g.G * g.N;
-    const int64_t ctas = (p.total * g.M + 255) / 256;
+    p.rows = g.G * g.N;
+    const int64_t ctas = (p.rows * g.M + 255) / 256;
     return launch_pdl(gemm_no_k_kernel, dim3((unsigned)(ctas < 16 * sms ? ctas : 16 * sms)), dim3(256),
                       0, stream, p);
   }
   const int bn = grouped ? g.tile_rows : gemm_tile_rows(g.M, g.N, g.G, sms);
+  const bool pair = bn == 256;
+  const int64_t batches = grouped ? 1 : g.G;
   PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
   if (encode == nullptr) return cudaErrorNotSupported;
   const int64_t half_k = g.K / 2;
   if (!encode_rows(encode, &p.tmap_a, g.a, half_k, g.M, g.G, 128) ||
-      !encode_rows(encode, &p.tmap_b, g.b, half_k, g.N, grouped ? 1 : g.G, (uint32_t)bn))
+      !encode_rows(encode, &p.tmap_b, g.b, half_k, g.N, batches, pair ? 128u : (uint32_t)bn))
     return cudaErrorInvalidValue;
+  if (pair && (!encode_atoms(encode, &p.tmap_sfa, g.sfa, p.rest_k, g.G * p.rest_m, 1) ||
+               !encode_atoms(encode, &p.tmap_sfb, g.sfb, p.rest_k, batches * p.rest_n, 2)))
+    return cudaErrorInvalidValue;
+  p.tiles_m = pair ? (p.rest_m + 1) / 2 : p.rest_m;
   if (grouped) {
-    const int64_t max_tiles = g.max_tiles * p.rest_m;
+    const int64_t max_tiles = g.max_tiles * p.tiles_m;
     return g.q ? launch_bn<kGatedQuantize, true>(bn, p, max_tiles, sms, stream)
                : launch_bn<kStore, true>(bn, p, max_tiles, sms, stream);
   }
   p.tiles_n = (int32_t)((g.N + bn - 1) / bn);
-  p.total = g.G * p.tiles_n * p.rest_m;
+  p.total = (int32_t)(g.G * p.tiles_n * p.tiles_m);
   return launch_bn<kStore, false>(bn, p, p.total, sms, stream);
 }
 
 cudaError_t gemm_wait_timeouts(int reset, int* out) {
-  cudaError_t err = cudaMemcpyFromSymbol(out, g_gemm_timeouts, sizeof(int));
+  int own = 0, pairs = 0;
+  cudaError_t err = cudaMemcpyFromSymbol(&own, g_gemm_timeouts, sizeof(int));
+  if (err == cudaSuccess) err = gemm_pair_wait_timeouts(reset, &pairs);
+  *out = own + pairs;
   if (err != cudaSuccess || !reset) return err;
   const int zero = 0;
   return cudaMemcpyToSymbol(g_gemm_timeouts, &zero, sizeof(int));
