@@ -327,9 +327,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_pair_kernel(const __grid
 
 template <int EPI, bool GROUPED>
 cudaError_t launch_variant(const GemmParams& p, int64_t max_tiles, int sms, cudaStream_t stream) {
-  auto kern = gemm_pair_kernel<EPI, GROUPED>;
-  const uint32_t smem = pair_smem_bytes(EPI);
-  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  constexpr auto kern = gemm_pair_kernel<EPI, GROUPED>;
+  constexpr uint32_t smem = pair_smem_bytes(EPI);
+  cudaError_t err = allow_smem<kern>(smem);
   if (err != cudaSuccess) return err;
   const int64_t pairs = max_tiles < sms / 2 ? max_tiles : sms / 2;
   return launch_pdl(kern, dim3((unsigned)(2 * pairs)), dim3(kPairThreads), smem, stream, p, 2);

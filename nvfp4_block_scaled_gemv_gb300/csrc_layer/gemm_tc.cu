@@ -240,9 +240,9 @@ __global__ void __launch_bounds__(256) gemm_no_k_kernel(const GemmParams p) {
 
 template <int BN, int EPI, bool GROUPED>
 cudaError_t launch_variant(const GemmParams& p, int64_t max_tiles, int sms, cudaStream_t stream) {
-  auto kern = gemm_kernel<BN, EPI, GROUPED>;
-  const uint32_t smem = gemm_smem_bytes(BN, EPI);
-  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  constexpr auto kern = gemm_kernel<BN, EPI, GROUPED>;
+  constexpr uint32_t smem = gemm_smem_bytes(BN, EPI);
+  cudaError_t err = allow_smem<kern>(smem);
   if (err != cudaSuccess) return err;
   const int64_t ctas = max_tiles < sms ? max_tiles : sms;
   return launch_pdl(kern, dim3((unsigned)ctas), dim3(kGemmThreads), smem, stream, p);

@@ -1,6 +1,7 @@
 // Host/device interface of the layer operators: quantise, the product for any
 // number of rows, routing, and the routed experts.
 #pragma once
+#include <atomic>
 #include <cstdint>
 
 #include <cuda_runtime.h>
@@ -33,6 +34,22 @@ inline cudaError_t launch_pdl(void (*kern)(P), dim3 grid, dim3 block, size_t sme
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+// Allows the kernel its dynamic shared memory, once per device (each kernel
+// asks for one size only).
+template <auto KERN>
+inline cudaError_t allow_smem(size_t bytes) {
+  static std::atomic<uint64_t> done[2];  // a bit per device (of the first 128)
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev < 0 || dev >= 128) return cudaErrorInvalidDevice;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (done[dev >> 6].load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  err = cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (err == cudaSuccess) done[dev >> 6].fetch_or(bit, std::memory_order_relaxed);
+  return err;
 }
 
 // ---- quantise / dequantise (quantize.cu) ----

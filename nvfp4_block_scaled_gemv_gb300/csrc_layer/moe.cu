@@ -209,10 +209,11 @@ cudaError_t launch_sort(const SortParams& p, cudaStream_t stream) {
                                  sizeof(int32_t) * (size_t)p.E, stream, p);
     if (err != cudaSuccess) return err;
   }
-  auto kern = chunks > 1 ? sort_place_kernel<false> : sort_place_kernel<true>;
-  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  constexpr size_t most = sizeof(int32_t) * (size_t)kMaxExperts * (kSortWarps + 2);
+  cudaError_t err = chunks > 1 ? allow_smem<sort_place_kernel<false>>(most) : allow_smem<sort_place_kernel<true>>(most);
   if (err != cudaSuccess) return err;
-  return launch_pdl(kern, dim3((unsigned)(chunks < 1 ? 1 : chunks)), dim3(kSortThreads), smem, stream, p);
+  return launch_pdl(chunks > 1 ? sort_place_kernel<false> : sort_place_kernel<true>,
+                    dim3((unsigned)(chunks < 1 ? 1 : chunks)), dim3(kSortThreads), smem, stream, p);
 }
 
 cudaError_t launch_combine(const CombineParams& p, int dtype, int sms, cudaStream_t stream) {

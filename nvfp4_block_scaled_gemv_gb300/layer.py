@@ -9,8 +9,7 @@ from __future__ import annotations
 
 import ctypes
 
-from . import (ACT_NONE, ACT_SILU, SF_PERMUTED_128x4, SF_PLAIN, _check, _need, _on_device, _stream_handle,
-               library, nvfp4_permuted_scale_bytes)
+from . import (ACT_NONE, ACT_SILU, SF_PERMUTED_128x4, SF_PLAIN, _check, _need, _stream_handle, library)
 
 DTYPE_FP16, DTYPE_BF16, DTYPE_FP32 = 0, 1, 2
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
@@ -155,106 +154,134 @@ def nvfp4_moe_ffn(x: int, dtype: int, ids: int, weights: int, w1: int, sf1: int,
 # ---------------------------------------------------------------------------
 # torch tensors
 # ---------------------------------------------------------------------------
+# A call that decodes one token spends more time here than on the GPU, so these
+# make their checks in few steps: _ptr looks at everything _need looks at and
+# leaves the message to it, and _enqueue enters a device context only when
+# another device is current.
 
-def _dtype_code(dtype, name, allowed=("float16", "bfloat16", "float32")) -> int:
-    import torch
-
-    codes = {torch.float16: DTYPE_FP16, torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_FP32}
-    if dtype not in codes or str(dtype).split(".")[-1] not in allowed:
-        raise TypeError(f"{name} must be one of {', '.join(allowed)}, got {dtype}")
-    return codes[dtype]
+_torch = None
+_codes = {}
 
 
-def _need_rows(x, name):
-    """A matrix whose rows are contiguous; returns its row stride."""
-    import torch
+def _load():
+    """torch, imported at the first call (the device-pointer functions do without)."""
+    global _torch
+    if _torch is None:
+        import torch
 
-    if not isinstance(x, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
+        _codes.update({torch.float16: DTYPE_FP16, torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_FP32})
+        _torch = torch
+    return _torch
+
+
+def _ptr(t, name, dtype, numel, device) -> int:
+    """The address of a contiguous tensor of this type, size and device."""
+    try:
+        if t.dtype is dtype and t.numel() == numel and t.is_contiguous() and (t.device == device or not numel):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _need(t, name, dtype, numel, device)
+    return t.data_ptr()
+
+
+def _dtype_code(x, name, fp32=True) -> int:
+    code = _codes.get(getattr(x, "dtype", x))
+    if code is None or (code == DTYPE_FP32 and not fp32):
+        allowed = "float16, bfloat16 or float32" if fp32 else "float16 or bfloat16"
+        raise TypeError(f"{name} must be {allowed}, got {getattr(x, 'dtype', x)}")
+    return code
+
+
+def _rows(x, name):
+    """A matrix whose rows are contiguous: rows, columns, row stride."""
     if x.dim() != 2:
         raise ValueError(f"{name} must have 2 dimensions, has {x.dim()}")
-    if x.shape[1] > 1 and x.stride(1) != 1:
+    n, k = x.shape
+    stride, step = x.stride()
+    if k > 1 and step != 1:
         raise ValueError(f"{name} must have contiguous rows")
-    if x.shape[0] > 1 and x.stride(0) < x.shape[1]:
+    if n > 1 and stride < k:
         raise ValueError(f"{name} must have rows that do not overlap")
-    return x.stride(0) if x.shape[0] > 1 else x.shape[1]
+    return n, k, stride if n > 1 else k
 
 
-def _on_gpu(device):
-    """_on_device for a call that reads tensors: they have to be on a GPU."""
-    if device.type != "cuda":
+def _enqueue(where, device, stream, *args) -> None:
+    """The library's call `where` on args and the stream, with `device` current."""
+    index = device.index
+    if index is None:
         raise ValueError(f"the tensors are on {device}, expected a CUDA device")
-    return _on_device(device)
+    handle = _torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream_handle(stream, device)
+    call = getattr(library(), where)
+    if index == _torch._C._cuda_getDevice():
+        status = call(*args, handle)
+    else:
+        with _torch.cuda.device(index):
+            status = call(*args, handle)
+    if status:
+        _check(status, where)
 
 
 def _scale_bytes(layout, rows, K, L):
-    return L * rows * (K // 16) if layout == SF_PLAIN else nvfp4_permuted_scale_bytes(rows, K, L)
+    if layout == SF_PLAIN:
+        return L * rows * (K // 16)
+    return L * ((rows + 127) // 128) * ((K + 63) // 64) * 512
 
 
 def quantize(x, encode_scale: float = 1.0, sf_layout: int = SF_PERMUTED_128x4, q=None, sf=None, stream=None):
     """(q uint8 [rows, K//2], sf uint8 flat) of x [rows, K] (fp16, bf16 or fp32, rows may be
     strided); a 3-d contiguous x [L, rows, K] gives q [L, rows, K//2] and scales per batch."""
-    import torch
-
-    code = _dtype_code(getattr(x, "dtype", None), "x")
+    torch = _torch or _load()
+    code = _dtype_code(x, "x")
     if x.dim() == 3:
-        _need(x, "x", x.dtype, x.numel(), x.device)
+        _ptr(x, "x", x.dtype, x.numel(), x.device)
         (L, rows, K), stride = x.shape, 0
     else:
-        stride = _need_rows(x, "x")
-        L, (rows, K) = 1, x.shape
+        L, (rows, K, stride) = 1, _rows(x, "x")
     if K % 16:
         raise ValueError(f"x has rows of {K} elements, expected a multiple of 16")
-    n = _scale_bytes(sf_layout, rows, K, L)
+    n, dev, u8 = _scale_bytes(sf_layout, rows, K, L), x.device, torch.uint8
     if q is None:
-        q = torch.empty((*x.shape[:-1], K // 2), dtype=torch.uint8, device=x.device)
+        q = torch.empty((*x.shape[:-1], K // 2), dtype=u8, device=dev)
     if sf is None:
-        sf = torch.empty(n, dtype=torch.uint8, device=x.device)
-    _need(q, "q", torch.uint8, L * rows * (K // 2), x.device)
-    _need(sf, "sf", torch.uint8, n, x.device)
-    with _on_gpu(x.device):
-        nvfp4_quantize(x.data_ptr(), code, rows, K, L, q.data_ptr(), sf.data_ptr(), sf_layout, encode_scale,
-                       stride, stream=_stream_handle(stream, x.device))
+        sf = torch.empty(n, dtype=u8, device=dev)
+    _enqueue("nvfp4_quantize", dev, stream, x.data_ptr(), code, stride, rows, K, L, encode_scale,
+             _ptr(q, "q", u8, L * rows * (K // 2), dev), _ptr(sf, "sf", u8, n, dev), sf_layout, None, 0, 0)
     return q, sf
 
 
 def dequantize(q, sf, scale: float = 1.0, dtype=None, sf_layout: int = SF_PERMUTED_128x4, x=None, stream=None):
     """The values of q [..., rows, K//2] and sf, times scale, as dtype (default float32)."""
-    import torch
-
+    torch = _torch or _load()
     if q.dim() not in (2, 3):
         raise ValueError("q must be [rows, K//2] or [L, rows, K//2]")
-    L = q.shape[0] if q.dim() == 3 else 1
-    rows, K = q.shape[-2], 2 * q.shape[-1]
+    shape, dev, u8 = q.shape, q.device, torch.uint8
+    L = shape[0] if len(shape) == 3 else 1
+    rows, K = shape[-2], 2 * shape[-1]
     if K % 16:
         raise ValueError(f"q has rows of {K} elements, expected a multiple of 16")
-    dtype = dtype or (torch.float32 if x is None else x.dtype)
+    if dtype is None:
+        dtype = torch.float32 if x is None else x.dtype
     code = _dtype_code(dtype, "dtype")
-    _need(q, "q", torch.uint8, L * rows * (K // 2), q.device)
-    _need(sf, "sf", torch.uint8, _scale_bytes(sf_layout, rows, K, L), q.device)
+    qp = _ptr(q, "q", u8, L * rows * (K // 2), dev)
+    sp = _ptr(sf, "sf", u8, _scale_bytes(sf_layout, rows, K, L), dev)
     if x is None:
-        x = torch.empty((*q.shape[:-1], K), dtype=dtype, device=q.device)
-    _need(x, "x", dtype, L * rows * K, q.device)
-    with _on_gpu(q.device):
-        nvfp4_dequantize(q.data_ptr(), sf.data_ptr(), rows, K, L, x.data_ptr(), code, sf_layout, scale,
-                         stream=_stream_handle(stream, q.device))
+        x = torch.empty((*shape[:-1], K), dtype=dtype, device=dev)
+    _enqueue("nvfp4_dequantize", dev, stream, qp, sp, sf_layout, rows, K, L, scale,
+             _ptr(x, "x", dtype, L * rows * K, dev), code, 0)
     return x
 
 
 def fold_scale_signs(a, sf, sf_layout: int = SF_PERMUTED_128x4, stream=None):
     """Make the scales of a [L, rows, K//2] unsigned, in place; returns (a, sf)."""
-    import torch
-
+    torch = _torch or _load()
     if a.dim() != 3:
         raise ValueError("a must be [L, rows, K//2]")
     L, rows, K = a.shape[0], a.shape[1], 2 * a.shape[2]
     if K % 16:
         raise ValueError(f"a has rows of {K} elements, expected a multiple of 16")
-    _need(a, "a", torch.uint8, a.numel(), a.device)
-    _need(sf, "sf", torch.uint8, _scale_bytes(sf_layout, rows, K, L), a.device)
-    with _on_gpu(a.device):
-        nvfp4_fold_scale_signs(a.data_ptr(), sf.data_ptr(), rows, K, L, sf_layout,
-                               _stream_handle(stream, a.device))
+    _enqueue("nvfp4_fold_scale_signs", a.device, stream, _ptr(a, "a", torch.uint8, a.numel(), a.device),
+             _ptr(sf, "sf", torch.uint8, _scale_bytes(sf_layout, rows, K, L), a.device), sf_layout, rows, K, L)
     return a, sf
 
 
@@ -262,136 +289,114 @@ def gemm(a, b, sfa, sfb, alpha: float = 1.0, bias=None, activation: int = ACT_NO
          stream=None):
     """c [L, N, M] = act(alpha * b a^T + bias) from a [L, M, K//2], b [L, N, K//2] (uint8) and their
     permuted scales (flat uint8); bias fp32 [L, M]; dtype float16 (default), bfloat16 or float32."""
-    import torch
-
+    torch = _torch or _load()
     if a.dim() != 3 or b.dim() != 3 or a.shape[0] != b.shape[0] or a.shape[2] != b.shape[2]:
         raise ValueError("a must be [L, M, K//2] and b [L, N, K//2]")
     L, M, half_k = a.shape
-    N, K, dev = b.shape[1], 2 * half_k, a.device
+    N, K, dev, u8 = b.shape[1], 2 * half_k, a.device, torch.uint8
     if K % 16:
         raise ValueError(f"a has rows of {K} elements, expected a multiple of 16")
-    _need(a, "a", torch.uint8, L * M * half_k, dev)
-    _need(b, "b", torch.uint8, L * N * half_k, dev)
-    _need(sfa, "sfa", torch.uint8, nvfp4_permuted_scale_bytes(M, K, L), dev)
-    _need(sfb, "sfb", torch.uint8, nvfp4_permuted_scale_bytes(N, K, L), dev)
-    if bias is not None:
-        _need(bias, "bias", torch.float32, L * M, dev)
-    dtype = dtype or (torch.float16 if c is None else c.dtype)
+    ap, bp = _ptr(a, "a", u8, L * M * half_k, dev), _ptr(b, "b", u8, L * N * half_k, dev)
+    sap = _ptr(sfa, "sfa", u8, _scale_bytes(SF_PERMUTED_128x4, M, K, L), dev)
+    sbp = _ptr(sfb, "sfb", u8, _scale_bytes(SF_PERMUTED_128x4, N, K, L), dev)
+    bias_p = None if bias is None else _ptr(bias, "bias", torch.float32, L * M, dev)
+    if dtype is None:
+        dtype = torch.float16 if c is None else c.dtype
     code = _dtype_code(dtype, "dtype")
     if c is None:
         c = torch.empty((L, N, M), dtype=dtype, device=dev)
-    _need(c, "c", dtype, L * N * M, dev)
-    with _on_gpu(dev):
-        nvfp4_gemm(a.data_ptr(), b.data_ptr(), sfa.data_ptr(), sfb.data_ptr(), c.data_ptr(), M, N, K, L, alpha,
-                   bias.data_ptr() if bias is not None else 0, activation, code,
-                   stream=_stream_handle(stream, dev))
+    _enqueue("nvfp4_gemm", dev, stream, ap, bp, sap, sbp, _ptr(c, "c", dtype, L * N * M, dev), M, N, K, L,
+             ctypes.byref(_GemmOptions(alpha, bias_p, activation, code, 0)))
     return c
 
 
 def route(logits, top_k: int, score: int = SCORE_SOFTMAX, bias=None, groups: int = 1, top_groups: int = 1,
           renormalize: bool = True, weight_scale: float = 1.0, stream=None):
     """(ids int32 [T, top_k], weights fp32 [T, top_k]) of logits [T, E]."""
-    import torch
-
-    code = _dtype_code(getattr(logits, "dtype", None), "logits")
-    stride = _need_rows(logits, "logits")
-    (T, E), dev = logits.shape, logits.device
-    if bias is not None:
-        _need(bias, "bias", torch.float32, E, dev)
+    torch = _torch or _load()
+    code = _dtype_code(logits, "logits")
+    T, E, stride = _rows(logits, "logits")
+    dev = logits.device
+    bias_p = None if bias is None else _ptr(bias, "bias", torch.float32, E, dev)
     ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
     weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
-    with _on_gpu(dev):
-        nvfp4_route(logits.data_ptr(), code, T, E, top_k, ids.data_ptr(), weights.data_ptr(), score,
-                    bias.data_ptr() if bias is not None else 0, groups, top_groups, renormalize, weight_scale,
-                    stride, _stream_handle(stream, dev))
+    _enqueue("nvfp4_route", dev, stream, logits.data_ptr(), code, stride, T, E, top_k,
+             ctypes.byref(_RouteOptions(score, bias_p, groups, top_groups, 1 if renormalize else 0, weight_scale)),
+             ids.data_ptr(), weights.data_ptr())
     return ids, weights
 
 
 def moe_sort(ids, E: int, stream=None) -> dict:
     """Sort the choices ids [T, top_k] (int32) by expert: rows [T, top_k], counts [E], starts [E],
     the plan of the products and the capacity and tile of the experts' rows."""
-    import torch
-
+    torch = _torch or _load()
     if ids.dim() != 2:
         raise ValueError("ids must be [T, top_k]")
-    T, k = ids.shape
-    dev = ids.device
-    _need(ids, "ids", torch.int32, T * k, dev)
+    (T, k), dev, i32 = ids.shape, ids.device, torch.int32
+    p = _ptr(ids, "ids", i32, T * k, dev)
     shape = nvfp4_moe_shape(T, k, E)
-    out = {"rows": torch.empty((T, k), dtype=torch.int32, device=dev),
-           "counts": torch.empty(E, dtype=torch.int32, device=dev),
-           "starts": torch.empty(E, dtype=torch.int32, device=dev),
+    out = {"rows": torch.empty((T, k), dtype=i32, device=dev), "counts": torch.empty(E, dtype=i32, device=dev),
+           "starts": torch.empty(E, dtype=i32, device=dev),
            "plan": torch.empty(shape["plan_bytes"], dtype=torch.uint8, device=dev),
            "row_capacity": shape["row_capacity"], "tile_rows": shape["tile_rows"], "experts": E}
-    with _on_gpu(dev):
-        nvfp4_moe_sort(ids.data_ptr(), T, k, E, out["rows"].data_ptr(), out["counts"].data_ptr(),
-                       out["starts"].data_ptr(), out["plan"].data_ptr(), _stream_handle(stream, dev))
+    _enqueue("nvfp4_moe_sort", dev, stream, p, T, k, E, out["rows"].data_ptr(), out["counts"].data_ptr(),
+             out["starts"].data_ptr(), out["plan"].data_ptr())
     return out
 
 
 def _need_sorted(order, b, sfb, dev):
-    import torch
-
+    torch = _torch or _load()
     T, k = order["rows"].shape
     E, rows = order["experts"], order["row_capacity"]
-    shape = nvfp4_moe_shape(T, k, E)
-    _need(order["plan"], "plan", torch.uint8, shape["plan_bytes"], dev)
+    _need(order["plan"], "plan", torch.uint8, nvfp4_moe_shape(T, k, E)["plan_bytes"], dev)
     if b.dim() != 2:
         raise ValueError("b must be [row_capacity, K//2]")
     K = 2 * b.shape[1]
     if K % 32:
         raise ValueError(f"b has rows of {K} elements, expected a multiple of 32")
     _need(b, "b", torch.uint8, rows * (K // 2), dev)
-    _need(sfb, "sfb", torch.uint8, nvfp4_permuted_scale_bytes(rows, K, 1), dev)
+    _need(sfb, "sfb", torch.uint8, _scale_bytes(SF_PERMUTED_128x4, rows, K, 1), dev)
     return T, k, E, rows, K
 
 
 def _need_experts(a, sfa, alpha, E, K, dev):
-    import torch
-
+    """(M, and the addresses of the weights, their scales and alpha)."""
+    torch = _torch or _load()
     if a.dim() != 3 or a.shape[0] != E or 2 * a.shape[2] != K:
         raise ValueError(f"the weights must be [{E}, M, {K // 2}]")
     M = a.shape[1]
-    _need(a, "weights", torch.uint8, a.numel(), dev)
-    _need(sfa, "weight scales", torch.uint8, nvfp4_permuted_scale_bytes(M, K, E), dev)
-    if alpha is not None:
-        _need(alpha, "alpha", torch.float32, E, dev)
-    return M
+    return (M, _ptr(a, "weights", torch.uint8, E * M * (K // 2), dev),
+            _ptr(sfa, "weight scales", torch.uint8, _scale_bytes(SF_PERMUTED_128x4, M, K, E), dev),
+            None if alpha is None else _ptr(alpha, "alpha", torch.float32, E, dev))
 
 
 def quantize_rows(x, order, encode_scale: float = 1.0, stream=None):
     """Quantise the tokens x [T, K] into the experts' rows of a moe_sort."""
-    import torch
-
-    code = _dtype_code(getattr(x, "dtype", None), "x")
-    stride = _need_rows(x, "x")
-    (T, K), dev, rows = x.shape, x.device, order["row_capacity"]
-    k = order["rows"].shape[1]
+    torch = _torch or _load()
+    code = _dtype_code(x, "x")
+    T, K, stride = _rows(x, "x")
+    dev, rows, k = x.device, order["row_capacity"], order["rows"].shape[1]
     if K % 16:
         raise ValueError(f"x has rows of {K} elements, expected a multiple of 16")
-    _need(order["rows"], "rows", torch.int32, T * k, dev)
+    to = _ptr(order["rows"], "rows", torch.int32, T * k, dev)
     q = torch.empty((rows, K // 2), dtype=torch.uint8, device=dev)
-    sf = torch.empty(nvfp4_permuted_scale_bytes(rows, K, 1), dtype=torch.uint8, device=dev)
-    with _on_gpu(dev):
-        nvfp4_quantize(x.data_ptr(), code, T, K, 1, q.data_ptr(), sf.data_ptr(), SF_PERMUTED_128x4, encode_scale,
-                       stride, order["rows"].data_ptr(), k, rows, _stream_handle(stream, dev))
+    sf = torch.empty(_scale_bytes(SF_PERMUTED_128x4, rows, K, 1), dtype=torch.uint8, device=dev)
+    _enqueue("nvfp4_quantize", dev, stream, x.data_ptr(), code, stride, T, K, 1, encode_scale, q.data_ptr(),
+             sf.data_ptr(), SF_PERMUTED_128x4, to, k, rows)
     return q, sf
 
 
 def moe_gemm(a, sfa, b, sfb, order, alpha=None, activation: int = ACT_NONE, dtype=None, stream=None):
     """c [row_capacity, M] = act(alpha[e] * b a[e]^T) for the experts' rows b of a moe_sort."""
-    import torch
-
+    torch = _torch or _load()
     dev = a.device
     T, k, E, rows, K = _need_sorted(order, b, sfb, dev)
-    M = _need_experts(a, sfa, alpha, E, K, dev)
+    M, ap, sp, alpha_p = _need_experts(a, sfa, alpha, E, K, dev)
     dtype = dtype or torch.float16
     code = _dtype_code(dtype, "dtype")
     c = torch.empty((rows, M), dtype=dtype, device=dev)
-    with _on_gpu(dev):
-        nvfp4_moe_gemm(a.data_ptr(), sfa.data_ptr(), b.data_ptr(), sfb.data_ptr(), order["plan"].data_ptr(), T,
-                       k, E, M, K, c.data_ptr(), code, alpha.data_ptr() if alpha is not None else 0, activation,
-                       _stream_handle(stream, dev))
+    _enqueue("nvfp4_moe_gemm", dev, stream, ap, sp, b.data_ptr(), sfb.data_ptr(), order["plan"].data_ptr(), T, k,
+             E, M, K, alpha_p, activation, c.data_ptr(), code)
     return c
 
 
@@ -399,39 +404,32 @@ def moe_gated_gemm(a, sfa, b, sfb, order, alpha=None, activation: int = ACT_SILU
                    stream=None):
     """(q [row_capacity, F//2], sf) of act(gate) * input, gate and input the even and odd rows of
     a [E, 2F, K//2], for the experts' rows b of a moe_sort."""
-    import torch
-
+    torch = _torch or _load()
     dev = a.device
     T, k, E, rows, K = _need_sorted(order, b, sfb, dev)
-    M = _need_experts(a, sfa, alpha, E, K, dev)
+    M, ap, sp, alpha_p = _need_experts(a, sfa, alpha, E, K, dev)
     if M % 64:
         raise ValueError(f"the weights have {M} rows, expected a multiple of 64")
     F = M // 2
     q = torch.empty((rows, F // 2), dtype=torch.uint8, device=dev)
-    sf = torch.empty(nvfp4_permuted_scale_bytes(rows, F, 1), dtype=torch.uint8, device=dev)
-    with _on_gpu(dev):
-        nvfp4_moe_gated_gemm(a.data_ptr(), sfa.data_ptr(), b.data_ptr(), sfb.data_ptr(),
-                             order["plan"].data_ptr(), T, k, E, F, K, q.data_ptr(), sf.data_ptr(),
-                             alpha.data_ptr() if alpha is not None else 0, activation, encode_scale,
-                             _stream_handle(stream, dev))
+    sf = torch.empty(_scale_bytes(SF_PERMUTED_128x4, rows, F, 1), dtype=torch.uint8, device=dev)
+    _enqueue("nvfp4_moe_gated_gemm", dev, stream, ap, sp, b.data_ptr(), sfb.data_ptr(), order["plan"].data_ptr(),
+             T, k, E, F, K, alpha_p, activation, encode_scale, q.data_ptr(), sf.data_ptr())
     return q, sf
 
 
 def moe_combine(y, order, weights, stream=None):
     """out [T, M] = sum_j weights[t, j] * y[rows[t, j]] (y fp16 or bf16)."""
-    import torch
-
-    code = _dtype_code(getattr(y, "dtype", None), "y", ("float16", "bfloat16"))
+    torch = _torch or _load()
+    code = _dtype_code(y, "y", fp32=False)
     if y.dim() != 2:
         raise ValueError("y must be [row_capacity, M]")
     T, k = order["rows"].shape
     M, dev = y.shape[1], y.device
-    _need(y, "y", y.dtype, order["row_capacity"] * M, dev)
-    _need(weights, "weights", torch.float32, T * k, dev)
+    yp = _ptr(y, "y", y.dtype, order["row_capacity"] * M, dev)
+    wp = _ptr(weights, "weights", torch.float32, T * k, dev)
     out = torch.empty((T, M), dtype=y.dtype, device=dev)
-    with _on_gpu(dev):
-        nvfp4_moe_combine(y.data_ptr(), code, order["rows"].data_ptr(), weights.data_ptr(), T, k, M,
-                          out.data_ptr(), _stream_handle(stream, dev))
+    _enqueue("nvfp4_moe_combine", dev, stream, yp, code, order["rows"].data_ptr(), wp, T, k, M, out.data_ptr())
     return out
 
 
@@ -440,37 +438,32 @@ def moe_ffn(x, ids, weights, w1, sf1, w2, sf2, alpha1=None, alpha2=None, encode_
     """The routed feed-forward layer: out [T, D] from x [T, D] (fp16 or bf16), ids and weights
     [T, top_k], w1 [E, 2F, D//2] (gate and input rows interleaved), w2 [E, D, F//2] and their
     permuted scales.  workspace: a uint8 tensor of nvfp4_moe_ffn_workspace_bytes, or None."""
-    import torch
-
-    code = _dtype_code(getattr(x, "dtype", None), "x", ("float16", "bfloat16"))
-    stride = _need_rows(x, "x")
-    (T, D), dev = x.shape, x.device
+    torch = _torch or _load()
+    code = _dtype_code(x, "x", fp32=False)
+    T, D, stride = _rows(x, "x")
+    dev = x.device
     if ids.dim() != 2:
         raise ValueError("ids must be [T, top_k]")
     k = ids.shape[1]
-    _need(ids, "ids", torch.int32, T * k, dev)
-    _need(weights, "weights", torch.float32, T * k, dev)
-    if w1.dim() != 3 or w2.dim() != 3 or 2 * w1.shape[2] != D:
+    idp = _ptr(ids, "ids", torch.int32, T * k, dev)
+    wp = _ptr(weights, "weights", torch.float32, T * k, dev)
+    if w1.dim() != 3 or w2.dim() != 3:
         raise ValueError("w1 must be [E, 2F, D//2] and w2 [E, D, F//2]")
     E, F = w1.shape[0], 2 * w2.shape[2]
-    if w1.shape[1] != 2 * F or tuple(w2.shape) != (E, D, F // 2) or D % 32 or F % 32:
+    if w1.shape[1] != 2 * F or w2.shape[1] != D or D % 32 or F % 32:
         raise ValueError("w1 must be [E, 2F, D//2] and w2 [E, D, F//2], D and F multiples of 32")
-    _need_experts(w1, sf1, alpha1, E, D, dev)
-    _need_experts(w2, sf2, alpha2, E, F, dev)
+    _, p1, s1, a1 = _need_experts(w1, sf1, alpha1, E, D, dev)
+    _, p2, s2, a2 = _need_experts(w2, sf2, alpha2, E, F, dev)
     if out is None:
         out = torch.empty((T, D), dtype=x.dtype, device=dev)
-    _need(out, "out", x.dtype, T * D, dev)
+    outp = _ptr(out, "out", x.dtype, T * D, dev)
     need = nvfp4_moe_ffn_workspace_bytes(T, k, E, D, F)
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.numel() < need:
-        raise ValueError(f"workspace must be {need} contiguous bytes (uint8)")
-    if need and workspace.device != dev:
-        raise ValueError(f"workspace is on {workspace.device}, expected {dev}")
-    with _on_gpu(dev):
-        nvfp4_moe_ffn(x.data_ptr(), code, ids.data_ptr(), weights.data_ptr(), w1.data_ptr(), sf1.data_ptr(),
-                      w2.data_ptr(), sf2.data_ptr(), T, k, E, D, F, out.data_ptr(), workspace.data_ptr(),
-                      workspace.numel(), alpha1.data_ptr() if alpha1 is not None else 0,
-                      alpha2.data_ptr() if alpha2 is not None else 0, encode_x, encode_h, activation, stride,
-                      _stream_handle(stream, dev))
+    size = workspace.numel()
+    if size < need:
+        raise ValueError(f"workspace has {size} bytes, expected {need}")
+    _enqueue("nvfp4_moe_ffn", dev, stream, x.data_ptr(), code, stride, idp, wp, p1, s1, p2, s2, T, k, E, D, F,
+             ctypes.byref(_MoeOptions(a1, a2, encode_x, encode_h, activation)), outp,
+             _ptr(workspace, "workspace", torch.uint8, size, dev), size)
     return out
