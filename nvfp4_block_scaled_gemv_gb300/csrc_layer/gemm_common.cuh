@@ -120,14 +120,6 @@ struct Turned<float> {
   }
 };
 
-// Two fp32 fused multiply-adds in one instruction.
-__device__ __forceinline__ void fma2(float& x, float& y, float a, float b) {
-  asm("{\n\t.reg .b64 v, m, c;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 m, {%2, %2};\n\tmov.b64 c, {%3, %3};\n\t"
-      "fma.rn.f32x2 v, v, m, c;\n\tmov.b64 {%0, %1}, v;\n\t}"
-      : "+f"(x), "+f"(y)
-      : "f"(a), "f"(b));
-}
-
 // Columns 0..15 at a TMEM address, without waiting for them.
 __device__ __forceinline__ void tmem_load_16(uint32_t taddr, float (&v)[16]) {
   asm volatile(
@@ -190,7 +182,12 @@ template <int EPI>
 __device__ __forceinline__ void finish_columns(const GemmParams& p, const Place& w, int n, float (&v)[kUnit]) {
   if constexpr (EPI == kStore) {
 #pragma unroll
-    for (int i = 0; i < kUnit; i += 2) fma2(v[i], v[i + 1], w.alpha, w.bias);
+    for (int i = 0; i < kUnit; i += 2) {
+      const float2 y = unpack_f32x2(fma2(pack_f32x2(v[i], v[i + 1]), pack_f32x2(w.alpha, w.alpha),
+                                         pack_f32x2(w.bias, w.bias)));
+      v[i] = y.x;
+      v[i + 1] = y.y;
+    }
     if (p.activation != 0) {
 #pragma unroll
       for (int i = 0; i < kUnit; ++i) v[i] = activate(v[i], p.activation);
@@ -210,28 +207,31 @@ __device__ __forceinline__ void finish_columns(const GemmParams& p, const Place&
     for (int i = 0; i < kUnit; ++i) w.transpose[i * kTransposePitch + lane] = v[i];
     __syncwarp();
     const int col = lane >> 1, half = lane & 1;
-    float h[8];
+    uint64_t h[4];
     float amax = 0.f;
-    bool finite = true;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float gate = w.transpose[col * kTransposePitch + half * 16 + 2 * i] * w.alpha;
-      const float in = w.transpose[col * kTransposePitch + half * 16 + 2 * i + 1] * w.alpha;
-      // (SiLU: the fast exponential and division are good to a few fp32 ulps, and
-      // the exact forms' instructions would outlast the tile's MMAs)
+    const float* const mine = w.transpose + col * kTransposePitch + half * 16;
+    // (SiLU: the fast exponential and division are good to a few fp32 ulps, and the
+    // exact forms' instructions would outlast the tile's MMAs)
+    auto gated = [&](float gate, float in) {
+      gate *= w.alpha;
       const float a = p.activation == 2 ? __fdividef(gate, 1.f + __expf(-gate)) : activate(gate, p.activation);
-      h[i] = a * in * p.encode;
-      const float mag = fabsf(h[i]);
-      finite = finite && mag < __int_as_float(0x7f800000);
-      amax = fmaxf(amax, mag);
+      return a * (in * w.alpha) * p.encode;
+    };
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float x = gated(mine[4 * i], mine[4 * i + 1]), y = gated(mine[4 * i + 2], mine[4 * i + 3]);
+      amax = abs_max(amax, x, y);
+      h[i] = pack_f32x2(x, y);
     }
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    finite = __shfl_xor_sync(0xffffffffu, finite ? 1 : 0, 1) != 0 && finite;
+    amax = abs_max(amax, __shfl_xor_sync(0xffffffffu, amax, 1), 0.f);  // (none is negative)
     uint32_t code = 0x7Fu, q = 0;
-    if (finite) {
+    if (is_finite_max(amax)) {
       float s;
       code = block_scale_code(amax, s);
-      if (s > 0.f) q = quantize_8(h, s, 1.0f / s);
+      if (s > 0.f) {
+        const float r = scale_reciprocal(s);
+        q = quantize_8(h, pack_f32x2(-s, -s), pack_f32x2(r, r));
+      }
     }
     const int64_t row = w.row0 + n + col;
     const int64_t blocks = p.M / 32, rest = (p.M / 2 + 63) / 64;

@@ -61,9 +61,9 @@ struct QuantizeParams {
   const int32_t* row_map;  // [rows][copies]: rows of q that a row of x goes to, or null
   int64_t q_rows;     // rows of q with a row_map (entries outside [0, q_rows) are skipped)
   int64_t rows, rows_pad, x_stride;
-  int64_t grid_rows, grid_blocks;  // set by the launcher
+  int64_t places;     // set by the launcher
   float encode;
-  int32_t copies, half_k, blocks, rest_k;
+  int32_t copies, half_k, blocks, rest_k, one_batch, chunks;
 };
 cudaError_t launch_quantize(QuantizeParams p, int dtype, bool permuted, int64_t L, int sms,
                             cudaStream_t stream);
@@ -73,11 +73,12 @@ struct DequantizeParams {
   const uint8_t* sf;
   void* x;
   int64_t rows, L, x_stride;
+  int64_t places;     // set by the launcher
   float scale;
-  int32_t half_k, blocks, rest_k;
+  int32_t half_k, blocks, rest_k, chunks;
   bool permuted;
 };
-cudaError_t launch_dequantize(const DequantizeParams& p, int dtype, int sms, cudaStream_t stream);
+cudaError_t launch_dequantize(DequantizeParams p, int dtype, int sms, cudaStream_t stream);
 
 struct FoldParams {
   uint8_t* a;
@@ -131,11 +132,12 @@ struct RouteParams {
   int64_t T, stride;
   float scale;
   int32_t E, k, groups, top_groups, sigmoid, renormalize;
+  int32_t aligned;     // alignment of the rows, up to 16 (set by the launcher)
 };
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 32;
 constexpr int kMaxGroups = 32;
-cudaError_t launch_route(const RouteParams& p, int dtype, int sms, cudaStream_t stream);
+cudaError_t launch_route(RouteParams p, int dtype, int sms, cudaStream_t stream);
 
 // Where the sort leaves its results: counts [E], tiles and their number, and
 // each choice's row.

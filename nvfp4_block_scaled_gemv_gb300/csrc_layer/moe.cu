@@ -72,9 +72,11 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortPara
   __syncthreads();
   const int64_t begin = (int64_t)blockIdx.x * kSortChunk;
   const int64_t end = begin + kSortChunk < p.n ? begin + kSortChunk : p.n;
-  const int64_t wbegin = begin + (int64_t)warp * (kSortChunk / kSortWarps);
+  // a warp's share: consecutive choices, whole steps of 32, all warps at work
+  const int share = ((int)(end - begin) + kSortThreads - 1) / kSortThreads * 32;
+  const int64_t wbegin = begin + (int64_t)warp * share;
   // the warps' own counts
-  for (int s = 0; s < kSortChunk / kSortWarps; s += 32) {
+  for (int s = 0; s < share; s += 32) {
     if (wbegin + s >= end) break;
     const int32_t e = choice(p, wbegin + s + lane, end);
     const uint32_t same = __match_any_sync(0xffffffffu, e);
@@ -124,7 +126,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortPara
     }
   }
   // the choices' rows
-  for (int s = 0; s < kSortChunk / kSortWarps; s += 32) {
+  for (int s = 0; s < share; s += 32) {
     if (wbegin + s >= end) break;
     const int64_t i = wbegin + s + lane;
     const int32_t e = choice(p, i, end);

@@ -12,9 +12,15 @@
 // NaN, is masked: it is never chosen, and a token with fewer than k experts
 // left has id -1 and weight 0 in the remaining places.
 //
-// One warp per token; lane i holds the experts i, i + 32, ...  A round of the
-// top k is a warp maximum over (rank, lowest index), done on the ranks as
-// ordered integers with the warp-wide reduction instructions.
+// One warp per token; lane i holds the NV consecutive experts from NV*i (one
+// vector load where the rows' alignment allows), NV the power of two that covers
+// E with 32 lanes.  A lane's experts lie in one group when NV divides the group's
+// size: the lane finds its two largest, and the group's lanes merge theirs by
+// shuffles (a power of two of them) or through shared memory.  Ranks are compared as
+// ordered integers, so that a round of the top k is one warp-wide maximum, a
+// vote, and an update on the lane that wins; the lowest such lane has the lowest
+// index.  The exponential and the division are the exact ones: a rank's last bit
+// decides between experts that are nearly level.
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -46,26 +52,65 @@ __device__ __forceinline__ float load_logit(const void* p, int64_t i, int dtype)
   return __half2float(static_cast<const __half*>(p)[i]);
 }
 
+// The two largest of (a1 >= b1) and (a2 >= b2).
+__device__ __forceinline__ void merge_two(uint32_t& a, uint32_t& b, uint32_t a2, uint32_t b2) {
+  b = max(min(a, a2), max(b, b2));
+  a = max(a, a2);
+}
+
+template <int NV, int DT>
+__device__ __forceinline__ void load_logits(const RouteParams& p, int64_t t, int lane, float (&x)[NV]) {
+  constexpr int kSize = DT == kF32 ? 4 : 2, kBytes = NV * kSize;
+  constexpr int kVec = kBytes < 16 ? kBytes : 16;  // bytes of a load
+  const int e0 = lane * NV;
+  if (kVec >= 4 && p.aligned % kVec == 0 && e0 + NV <= p.E) {
+    const char* const src = static_cast<const char*>(p.logits) + (t * p.stride + e0) * kSize;
+#pragma unroll
+    for (int i = 0; i < kBytes; i += kVec) {
+      uint32_t w[4];
+      if constexpr (kVec == 16) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(src + i));
+        w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+      } else if constexpr (kVec == 8) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(src + i));
+        w[0] = v.x; w[1] = v.y;
+      } else if constexpr (kVec == 4) {
+        w[0] = __ldg(reinterpret_cast<const uint32_t*>(src + i));
+      }
+#pragma unroll
+      for (int j = 0; j < kVec / kSize; ++j) {
+        const uint32_t u = DT == kF32 ? w[j] : j % 2 ? w[j / 2] >> 16 : w[j / 2] & 0xffffu;
+        x[i / kSize + j] = DT == kF32    ? __uint_as_float(u)
+                           : DT == kBF16 ? __uint_as_float(u << 16)
+                                         : __half2float(__ushort_as_half((unsigned short)u));
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      x[i] = e0 + i < p.E ? load_logit(p.logits, t * p.stride + e0 + i, DT) : -__int_as_float(0x7f800000);
+  }
+}
+
 template <int NV, int DT>
 __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams p) {
   __shared__ uint32_t group_keys[kRouteThreads / 32][NV * 32];
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int e0 = lane * NV;
   const float inf = __int_as_float(0x7f800000);
   for (int64_t t = (int64_t)blockIdx.x * (kRouteThreads / 32) + warp; t < p.T;
        t += (int64_t)gridDim.x * (kRouteThreads / 32)) {
     float x[NV];
+    load_logits<NV, DT>(p, t, lane, x);
     float top = -inf;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int e = lane + 32 * i;
-      x[i] = e < p.E ? load_logit(p.logits, t * p.stride + e, DT) : -inf;
       if (x[i] != x[i]) x[i] = -inf;  // NaN: masked
       top = fmaxf(top, x[i]);
     }
     float score[NV];
-    float total = 1.f;
     if (p.sigmoid) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) score[i] = 1.f / (1.f + expf(-x[i]));
@@ -81,81 +126,100 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams 
       }
 #pragma unroll
       for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-      total = sum;
-      if (total > 0.f)
+      if (sum > 0.f)
 #pragma unroll
-        for (int i = 0; i < NV; ++i) score[i] = score[i] / total;
+        for (int i = 0; i < NV; ++i) score[i] = score[i] / sum;
     }
     uint32_t key[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int e = lane + 32 * i;
       float r = x[i];
-      if (p.bias != nullptr && e < p.E) r = x[i] == -inf ? -inf : score[i] + p.bias[e];
+      if (p.bias != nullptr && e0 + i < p.E) r = x[i] == -inf ? -inf : score[i] + p.bias[e0 + i];
       key[i] = r == r && r != -inf ? ordered(r) : kMasked;
     }
     if (p.groups > 1) {
-      // lane g scores group g from shared memory
-      uint32_t* const keys = group_keys[warp];
+      const int per = p.E / p.groups;  // experts of a group
+      auto group_key = [&](int i) {
+        return p.bias != nullptr || key[i] == kMasked ? key[i] : ordered(score[i]);
+      };
+      uint32_t a = kMasked, b = kMasked;  // the two largest
+      const int lanes = per / NV;         // lanes of a group, if whole
+      const bool whole = per % NV == 0 && (lanes & (lanes - 1)) == 0;
+      int mine;                           // the group whose key this lane has, or -1
+      if (whole) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        keys[lane + 32 * i] = p.bias != nullptr || key[i] == kMasked ? key[i] : ordered(score[i]);
-      __syncwarp();
-      const int per = p.E / p.groups;
-      uint32_t gkey = kMasked;
-      if (lane < p.groups) {
-        uint32_t a = kMasked, b = kMasked;  // the two largest
-        for (int i = 0; i < per; ++i) {
-          const uint32_t k = keys[lane * per + i];
-          b = max(b, min(a, k));
-          a = max(a, k);
-        }
-        if (a != kMasked) gkey = ordered(b != kMasked ? from_ordered(a) + from_ordered(b) : from_ordered(a));
+        for (int i = 0; i < NV; ++i) merge_two(a, b, group_key(i), kMasked);
+        for (int d = 1; d < lanes; d <<= 1)
+          merge_two(a, b, __shfl_xor_sync(0xffffffffu, a, d), __shfl_xor_sync(0xffffffffu, b, d));
+        // (lanes past the last expert are past the last group)
+        mine = e0 < p.E && lane % lanes == 0 ? lane / lanes : -1;
+      } else {
+        uint32_t* const keys = group_keys[warp];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) keys[e0 + i] = group_key(i);
+        __syncwarp();
+        mine = lane < p.groups ? lane : -1;
+        if (mine >= 0)
+          for (int i = 0; i < per; ++i) merge_two(a, b, keys[mine * per + i], kMasked);
+        __syncwarp();
       }
-      __syncwarp();
+      uint32_t gkey = kMasked;
+      if (mine >= 0 && a != kMasked)
+        gkey = ordered(b != kMasked ? from_ordered(a) + from_ordered(b) : from_ordered(a));
       uint32_t open = 0;  // bit g: group g stays
       for (int j = 0; j < p.top_groups; ++j) {
         const uint32_t best = __reduce_max_sync(0xffffffffu, gkey);
         if (best == kMasked) break;
-        const uint32_t who = __ballot_sync(0xffffffffu, gkey == best);
-        const int g = __ffs((int)who) - 1;
-        open |= 1u << g;
-        if (lane == g) gkey = kMasked;
+        // (the lanes that have a group's key are in the order of the groups)
+        const int who = __ffs((int)__ballot_sync(0xffffffffu, gkey == best)) - 1;
+        open |= 1u << (whole ? who / lanes : who);
+        if (lane == who) gkey = kMasked;
       }
+      if (whole) {
+        if (!((open >> (lane / lanes)) & 1u))
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int e = lane + 32 * i;
-        if (e < p.E && !((open >> (e / per)) & 1u)) key[i] = kMasked;
+          for (int i = 0; i < NV; ++i) key[i] = kMasked;
+      } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if (e0 + i < p.E && !((open >> ((e0 + i) / per)) & 1u)) key[i] = kMasked;
       }
     }
     // the top k, best first; lane j keeps the j-th
-    int my_id = -1;
-    float my_score = 0.f;
-    for (int j = 0; j < p.k; ++j) {
-      uint32_t best = kMasked;
+    int my_lane = -1, my_at = 0;  // where the j-th is held
+    uint32_t best = kMasked;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) best = max(best, key[i]);
+    for (int i = 0; i < NV; ++i) best = max(best, key[i]);
+    for (int j = 0; j < p.k; ++j) {
       const uint32_t all = __reduce_max_sync(0xffffffffu, best);
       if (all == kMasked) break;
-      uint32_t e = 0xffffffffu;
+      const int who = __ffs((int)__ballot_sync(0xffffffffu, best == all)) - 1;
+      int at = 0;
+      if (lane == who) {
+        // this lane's first expert with that rank, and its next best
 #pragma unroll
-      for (int i = NV - 1; i >= 0; --i)
-        if (key[i] == all) e = (uint32_t)(lane + 32 * i);
-      e = __reduce_min_sync(0xffffffffu, e);
-      float mine = 0.f;
+        for (int i = NV - 1; i >= 0; --i)
+          if (key[i] == all) at = i;
+        best = kMasked;
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if ((uint32_t)(lane + 32 * i) == e) {
-          key[i] = kMasked;
-          mine = score[i];
+        for (int i = 0; i < NV; ++i) {
+          if (i == at) key[i] = kMasked;
+          best = max(best, key[i]);
         }
-      mine = __shfl_sync(0xffffffffu, mine, (int)(e & 31u));
+      }
+      at = __shfl_sync(0xffffffffu, at, who);
       if (lane == j) {
-        my_id = (int)e;
-        my_score = mine;
+        my_lane = who;
+        my_at = at;
       }
     }
-    float w = my_score;
+    float w = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const float s = __shfl_sync(0xffffffffu, score[i], my_lane & 31);
+      if (my_at == i) w = s;
+    }
+    if (my_lane < 0) w = 0.f;
     if (p.renormalize) {
       float sum = w;
 #pragma unroll
@@ -163,7 +227,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams 
       w = sum > 0.f ? w / sum : 0.f;
     }
     if (lane < p.k) {
-      p.ids[t * p.k + lane] = my_id;
+      p.ids[t * p.k + lane] = my_lane < 0 ? -1 : my_lane * NV + my_at;
       p.weights[t * p.k + lane] = w * p.scale;
     }
   }
@@ -181,7 +245,11 @@ void (*route_for(int E))(const RouteParams) {
 
 }  // namespace
 
-cudaError_t launch_route(const RouteParams& p, int dtype, int sms, cudaStream_t stream) {
+cudaError_t launch_route(RouteParams p, int dtype, int sms, cudaStream_t stream) {
+  // the largest power of two that divides every row's address (0 counts as all)
+  const uint64_t bits =
+      (uint64_t)reinterpret_cast<uintptr_t>(p.logits) | (uint64_t)(p.stride * (dtype == kF32 ? 4 : 2)) | 16u;
+  p.aligned = (int32_t)(bits & (~bits + 1));
   auto kern = dtype == kF32 ? route_for<kF32>(p.E) : dtype == kBF16 ? route_for<kBF16>(p.E) : route_for<kF16>(p.E);
   const int64_t warps = kRouteThreads / 32;
   int64_t ctas = (p.T + warps - 1) / warps;
