@@ -8,9 +8,11 @@
 // other half from the peer: 38 KB per stage for the same MMAs.
 //
 // The CTAs of a pair (a cluster of 2) each load their own rows of A and B and
-// their scales with TMA, all completing on the leader's barrier; one lane of the
-// leader issues the TMEM copies and MMAs for both.  Each CTA's accumulator (its
-// 128 rows, 256 columns) is in its own tensor memory, and 8 epilogue warps of
+// their scales with TMA, all completing on the leader's barrier; a warp of the
+// leader issues the MMAs and another the TMEM copies of the scales, for both CTAs.
+// (The 16 instructions of a stage take one issuing thread longer than their
+// execution, and more while epilogue warps run beside it.)  Each CTA's accumulator
+// (its 128 rows, 256 columns) is in its own tensor memory, and 8 epilogue warps of
 // each CTA read it.
 //
 // Tensor memory.  Two accumulators of 256 columns and the scales exceed its 512,
@@ -33,7 +35,8 @@ namespace {
 
 using namespace gemm;
 
-constexpr int kPairThreads = 320;  // producer, MMA, 8 epilogue warps
+constexpr int kPairThreads = 352;  // producer, MMA, scale copies, 8 epilogue warps
+constexpr int kEpilogueWarp = 3;   // the first of them
 constexpr int kStages = 5;
 constexpr uint32_t kBHalf = 128 * 128;
 constexpr uint32_t kStageBytes = kABytes + kBHalf + 3 * kAtoms;
@@ -115,7 +118,7 @@ template <int EPI, bool GROUPED>
 __global__ void __launch_bounds__(kPairThreads, 1) gemm_pair_kernel(const __grid_constant__ GemmParams p) {
   constexpr int S = kStages;
   extern __shared__ uint8_t pair_smem[];
-  __shared__ __align__(8) uint64_t bars[2 * S + 3];
+  __shared__ __align__(8) uint64_t bars[2 * S + 6];
   __shared__ uint32_t tmem_slot;
 
   const uint32_t raw = smem_u32(pair_smem);
@@ -130,6 +133,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_pair_kernel(const __grid
   const uint32_t dfull_bar = bar0 + 8u * (2 * S);                  // each CTA's
   const uint32_t dempty_bar = bar0 + 8u * (2 * S + 1);             // leader's
   const uint32_t drain_bar = bar0 + 8u * (2 * S + 2);              // leader's
+  auto scale_bar = [&](int i) { return bar0 + 8u * (2 * S + 3 + i); };  // leader's [3]
 
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t rank = tc::cluster_rank();
@@ -142,6 +146,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_pair_kernel(const __grid
     tc::mbar_init(dfull_bar, 1);
     tc::mbar_init(dempty_bar, 16);  // the epilogue warps of both CTAs
     tc::mbar_init(drain_bar, 1);
+    for (int i = 0; i < 3; ++i) tc::mbar_init(scale_bar(i), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   // the preceding kernels have ended before tensor memory is taken, and the next
@@ -154,7 +159,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_pair_kernel(const __grid
   tc::cluster_sync();
   tc::fence_after();
   pdl_launch_dependents();
-  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
+  constexpr uint32_t tmem = 0;  // (an allocation of all 512 columns starts at the first)
   const int32_t total = GROUPED ? __shfl_sync(0xffffffffu, *p.tile_count, 0) * p.tiles_m : p.total;
   bool ok = true;
 
@@ -201,41 +206,24 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_pair_kernel(const __grid
     __syncwarp();
   } else if (warp == 1) {
     if (rank == 0) {
-      // This thread's own instructions bound the stage rate while the epilogue
-      // warps run beside it, so the loop keeps to what it needs: descriptors that
-      // differ in their low words only, and no vote per stage (a lane that gave up
-      // waiting issues nothing).
       const uint64_t da0 = tc::desc_sw128(a_s), db0 = tc::desc_sw128(b_s);
-      const uint64_t dsa0 = tc::desc_atom(sfa_s), dsb0 = tc::desc_atom(sfb_s);
-      int pos = 0, j = 0;
-      uint32_t ph = 0;
-      int old = -3;            // the slot and phase of the stage three before this one
-      uint32_t old_ph = 0;
-      uint32_t sf = kSfCol;    // scale buffer of this stage
+      int pos = 0, j = 0, sf = 0;  // ring slot, tile, scale buffer
+      uint32_t ph = 0, sf_ph = 0;
       for (int32_t t = pair; t < total; t += pairs, ++j) {
         const uint32_t d = tmem + ((j & 1) ? kSecondCol : 0u);
         // the columns that this tile shares with the one before it have been read
         tc::mbar_wait<false>(dempty_bar, ((uint32_t)j & 1u) ^ 1u, ok, &g_gemm_pair_timeouts);
         for (int s = 0; s < p.kstages; ++s) {
-          // the stage's data is here, and its scale buffer, last read by the stage
-          // three before this one, is free (both barriers asked at once)
-          if (old >= 0)
-            tc::mbar_wait2(full_bar(pos), ph, empty_bar(old), old_ph, ok, &g_gemm_pair_timeouts);
-          else
-            tc::mbar_wait<false>(full_bar(pos), ph, ok, &g_gemm_pair_timeouts);
+          // the stage's data is here and its scales are in tensor memory
+          tc::mbar_wait2(full_bar(pos), ph, scale_bar(sf), sf_ph, ok, &g_gemm_pair_timeouts);
           tc::fence_after();
-          const uint32_t ca = tmem + sf, cb = ca + 16u;
+          const uint32_t ca = tmem + kSfCol + (uint32_t)sf * kSfCols, cb = ca + 16u;
           // (a descriptor counts addresses in units of 16 bytes)
           const uint64_t da = da0 + (uint32_t)pos * (kABytes / 16), db = db0 + (uint32_t)pos * (kBHalf / 16);
-          const uint64_t dsa = dsa0 + (uint32_t)pos * (kAtoms / 16), dsb = dsb0 + (uint32_t)pos * (2 * kAtoms / 16);
           const int nk = p.rest_k - 4 * s;
           __syncwarp();
           if (elect_one() && ok) {
-            // an MMA's own copies just before it measured faster than all copies first
             auto step = [&](int kk, bool accumulate) {
-              pair_copy_atom(ca + 4u * kk, dsa + 32u * kk);
-              pair_copy_atom(cb + 8u * kk, dsb + 32u * kk);
-              pair_copy_atom(cb + 8u * kk + 4u, dsb + kAtoms / 16 + 32u * kk);
               pair_mma(d, da + 2u * kk, db + 2u * kk, ca + 4u * kk, cb + 8u * kk, accumulate);
             };
             step(0, s > 0);
@@ -250,11 +238,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_pair_kernel(const __grid
             pair_commit_both(empty_bar(pos));
           }
           __syncwarp();
-          if (++old == S) {
-            old = 0;
-            old_ph ^= 1u;
+          if (++sf == 3) {
+            sf = 0;
+            sf_ph ^= 1u;
           }
-          sf = sf == kSfCol + 2 * kSfCols ? kSfCol : sf + kSfCols;
           if (++pos == S) {
             pos = 0;
             ph ^= 1u;
@@ -269,10 +256,59 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_pair_kernel(const __grid
       tc::mbar_wait<false>(drain_bar, 0, drain_ok, &g_gemm_pair_timeouts);
       __syncwarp();
     }
+  } else if (warp == 2) {
+    if (rank == 0) {
+      const uint64_t dsa0 = tc::desc_atom(sfa_s), dsb0 = tc::desc_atom(sfb_s);
+      int pos = 0, sf = 0;
+      uint32_t ph = 0, old_ph = 0;
+      int old = -3;  // the slot and phase of the stage three before this one
+      for (int32_t t = pair; t < total; t += pairs) {
+        for (int s = 0; s < p.kstages; ++s) {
+          // the stage's data is here, and its buffer, last read by the stage three
+          // before this one, is free (both barriers asked at once)
+          if (old >= 0)
+            tc::mbar_wait2(full_bar(pos), ph, empty_bar(old), old_ph, ok, &g_gemm_pair_timeouts);
+          else
+            tc::mbar_wait<false>(full_bar(pos), ph, ok, &g_gemm_pair_timeouts);
+          tc::fence_after();
+          const uint32_t ca = tmem + kSfCol + (uint32_t)sf * kSfCols;
+          const uint64_t dsa = dsa0 + (uint32_t)pos * (kAtoms / 16), dsb = dsb0 + (uint32_t)pos * (2 * kAtoms / 16);
+          const int nk = p.rest_k - 4 * s;
+          __syncwarp();
+          if (elect_one() && ok) {
+            auto step = [&](int kk) {
+              pair_copy_atom(ca + 4u * kk, dsa + 32u * kk);
+              pair_copy_atom(ca + 16u + 8u * kk, dsb + 32u * kk);
+              pair_copy_atom(ca + 20u + 8u * kk, dsb + kAtoms / 16 + 32u * kk);
+            };
+            step(0);
+            if (nk >= 4) {
+              step(1);
+              step(2);
+              step(3);
+            } else {
+              if (nk > 1) step(1);
+              if (nk > 2) step(2);
+            }
+            pair_commit(scale_bar(sf));
+          }
+          __syncwarp();
+          if (++old == S) {
+            old = 0;
+            old_ph ^= 1u;
+          }
+          if (++sf == 3) sf = 0;
+          if (++pos == S) {
+            pos = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+    }
   } else {
-    const int quarter = warp & 3, group = (warp - 2) >> 2;
-    float* const tr =
-        reinterpret_cast<float*>(pair_smem + (tr_s - raw)) + (warp - 2) * (int)(kTransposeBytes / 4);
+    const int quarter = warp & 3, group = (warp - kEpilogueWarp) >> 2;
+    float* const tr = reinterpret_cast<float*>(pair_smem + (tr_s - raw)) +
+                      (warp - kEpilogueWarp) * (int)(kTransposeBytes / 4);
     const uint32_t release = tc::map_rank(dempty_bar, 0);
     int j = 0;
     for (int32_t t = pair; t < total; t += pairs, ++j) {
