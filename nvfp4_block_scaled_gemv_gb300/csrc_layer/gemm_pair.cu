@@ -15,6 +15,9 @@
 // (its 128 rows, 256 columns) is in its own tensor memory, and 8 epilogue warps of
 // each CTA read it.
 //
+// A tile of at most 128 rows of B (the last of an expert, often) runs MMAs of
+// N = 128, half the time.
+//
 // Tensor memory.  Two accumulators of 256 columns and the scales exceed its 512,
 // so the accumulators overlap: tile j has columns 0..255 when j is even and
 // 112..367 when it is odd.  The epilogue first brings the shared 144 columns into
@@ -53,8 +56,10 @@ constexpr uint32_t pair_smem_bytes(int epi) {
   return kStages * kStageBytes + 1024u + (epi == kGatedQuantize ? 8u * kTransposeBytes : 0u);
 }
 
-// M = 256 over the pair, N = 256 (see tc::mxf4nvf4_idesc for the fields).
-constexpr uint32_t kIdesc = (1u << 7) | (1u << 10) | ((256u >> 3) << 17) | ((256u >> 7) << 27);
+// M = 256 over the pair, N = n (see tc::mxf4nvf4_idesc for the fields).
+constexpr uint32_t pair_idesc(uint32_t n) {
+  return (1u << 7) | (1u << 10) | ((n >> 3) << 17) | ((256u >> 7) << 27);
+}
 
 // TMA loads into this CTA's shared memory that complete on a barrier of either
 // CTA of the pair.
@@ -78,13 +83,13 @@ __device__ __forceinline__ void pair_load_2d(uint32_t dst, const CUtensorMap* ma
 __device__ __forceinline__ void pair_copy_atom(uint32_t taddr, uint64_t desc) {
   asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
-__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t sfa,
-                                         uint32_t sfb, bool accumulate) {
+__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t sfa, uint32_t sfb, bool accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%5], "
       "[%6], p;\n\t}" ::"r"(d),
-      "l"(adesc), "l"(bdesc), "r"(kIdesc), "r"((uint32_t)accumulate), "r"(sfa), "r"(sfb)
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"((uint32_t)accumulate), "r"(sfa), "r"(sfb)
       : "memory");
 }
 // Arrive on this barrier of the leader, or of both CTAs, once everything issued
@@ -112,6 +117,12 @@ __device__ __forceinline__ void pair_alloc(uint32_t slot) {
 }
 __device__ __forceinline__ void pair_dealloc(uint32_t taddr) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(taddr) : "memory");
+}
+
+// Rows of b in tile t (0 past the last tile), the same on every lane.
+template <bool GROUPED>
+__device__ __forceinline__ int32_t tile_rows_at(const GemmParams& p, int32_t t, int32_t total) {
+  return t < total ? __shfl_sync(0xffffffffu, tile_at<kBN, GROUPED>(p, t).rows, 0) : 0;
 }
 
 template <int EPI, bool GROUPED>
@@ -169,7 +180,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_pair_kernel(const __grid
     for (int32_t t = pair; t < total; t += pairs) {
       const Tile tile = tile_at<kBN, GROUPED>(p, t);
       const int batch = GROUPED ? 0 : tile.g;
-      const int m0 = tile.mt * 256 + (int)rank * 128, n0 = (int)tile.n0 + (int)rank * 128;
+      // the peer's rows of b follow the leader's 128, or 64 in a tile of at most 128
+      const int m0 = tile.mt * 256 + (int)rank * 128;
+      const int n0 = (int)tile.n0 + (int)rank * (tile.rows > 128 ? 128 : 64);
       // a row tile past the last one reads rows of zeros; its atoms are another's
       const int sa = min(tile.mt * 2 + (int)rank, p.rest_m - 1) + tile.g * p.rest_m;
       const int sb = batch * p.rest_n + (int)(tile.n0 / 128);
@@ -209,8 +222,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_pair_kernel(const __grid
       const uint64_t da0 = tc::desc_sw128(a_s), db0 = tc::desc_sw128(b_s);
       int pos = 0, j = 0, sf = 0;  // ring slot, tile, scale buffer
       uint32_t ph = 0, sf_ph = 0;
+      int32_t rows = tile_rows_at<GROUPED>(p, pair, total);
       for (int32_t t = pair; t < total; t += pairs, ++j) {
         const uint32_t d = tmem + ((j & 1) ? kSecondCol : 0u);
+        const uint32_t idesc = rows > 128 ? pair_idesc(256) : pair_idesc(128);
+        rows = tile_rows_at<GROUPED>(p, t + pairs, total);  // (the next tile's, ahead of its need)
         // the columns that this tile shares with the one before it have been read
         tc::mbar_wait<false>(dempty_bar, ((uint32_t)j & 1u) ^ 1u, ok, &g_gemm_pair_timeouts);
         for (int s = 0; s < p.kstages; ++s) {
@@ -224,7 +240,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_pair_kernel(const __grid
           __syncwarp();
           if (elect_one() && ok) {
             auto step = [&](int kk, bool accumulate) {
-              pair_mma(d, da + 2u * kk, db + 2u * kk, ca + 4u * kk, cb + 8u * kk, accumulate);
+              pair_mma(d, da + 2u * kk, db + 2u * kk, idesc, ca + 4u * kk, cb + 8u * kk, accumulate);
             };
             step(0, s > 0);
             if (nk >= 4) {
@@ -262,7 +278,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_pair_kernel(const __grid
       int pos = 0, sf = 0;
       uint32_t ph = 0, old_ph = 0;
       int old = -3;  // the slot and phase of the stage three before this one
+      int32_t rows = tile_rows_at<GROUPED>(p, pair, total);
       for (int32_t t = pair; t < total; t += pairs) {
+        const bool wide = rows > 128;  // scales of a second atom row
+        rows = tile_rows_at<GROUPED>(p, t + pairs, total);
         for (int s = 0; s < p.kstages; ++s) {
           // the stage's data is here, and its buffer, last read by the stage three
           // before this one, is free (both barriers asked at once)
@@ -279,7 +298,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_pair_kernel(const __grid
             auto step = [&](int kk) {
               pair_copy_atom(ca + 4u * kk, dsa + 32u * kk);
               pair_copy_atom(ca + 16u + 8u * kk, dsb + 32u * kk);
-              pair_copy_atom(ca + 20u + 8u * kk, dsb + kAtoms / 16 + 32u * kk);
+              if (wide) pair_copy_atom(ca + 20u + 8u * kk, dsb + kAtoms / 16 + 32u * kk);
             };
             step(0);
             if (nk >= 4) {
