@@ -177,7 +177,8 @@ def _load():
 def _ptr(t, name, dtype, numel, device) -> int:
     """The address of a contiguous tensor of this type, size and device."""
     try:
-        if t.dtype is dtype and t.numel() == numel and t.is_contiguous() and (t.device == device or not numel):
+        if t.dtype is dtype and t.numel() == numel and t.is_contiguous() and (
+                t.get_device() == device.index or not numel):
             return t.data_ptr()
     except AttributeError:
         pass
@@ -242,22 +243,26 @@ def quantize(x, encode_scale: float = 1.0, sf_layout: int = SF_PERMUTED_128x4, q
         raise ValueError(f"x has rows of {K} elements, expected a multiple of 16")
     n, dev, u8 = _scale_bytes(sf_layout, rows, K, L), x.device, torch.uint8
     if q is None:
-        q = torch.empty((*x.shape[:-1], K // 2), dtype=u8, device=dev)
+        q = torch.empty((rows, K // 2) if x.dim() == 2 else (L, rows, K // 2), dtype=u8, device=dev)
+    else:
+        _ptr(q, "q", u8, L * rows * (K // 2), dev)
     if sf is None:
         sf = torch.empty(n, dtype=u8, device=dev)
-    _enqueue("nvfp4_quantize", dev, stream, x.data_ptr(), code, stride, rows, K, L, encode_scale,
-             _ptr(q, "q", u8, L * rows * (K // 2), dev), _ptr(sf, "sf", u8, n, dev), sf_layout, None, 0, 0)
+    else:
+        _ptr(sf, "sf", u8, n, dev)
+    _enqueue("nvfp4_quantize", dev, stream, x.data_ptr(), code, stride, rows, K, L, encode_scale, q.data_ptr(),
+             sf.data_ptr(), sf_layout, None, 0, 0)
     return q, sf
 
 
 def dequantize(q, sf, scale: float = 1.0, dtype=None, sf_layout: int = SF_PERMUTED_128x4, x=None, stream=None):
     """The values of q [..., rows, K//2] and sf, times scale, as dtype (default float32)."""
     torch = _torch or _load()
-    if q.dim() not in (2, 3):
-        raise ValueError("q must be [rows, K//2] or [L, rows, K//2]")
     shape, dev, u8 = q.shape, q.device, torch.uint8
-    L = shape[0] if len(shape) == 3 else 1
-    rows, K = shape[-2], 2 * shape[-1]
+    if len(shape) not in (2, 3):
+        raise ValueError("q must be [rows, K//2] or [L, rows, K//2]")
+    L, rows, half = shape if len(shape) == 3 else (1, *shape)
+    K = 2 * half
     if K % 16:
         raise ValueError(f"q has rows of {K} elements, expected a multiple of 16")
     if dtype is None:
@@ -266,9 +271,10 @@ def dequantize(q, sf, scale: float = 1.0, dtype=None, sf_layout: int = SF_PERMUT
     qp = _ptr(q, "q", u8, L * rows * (K // 2), dev)
     sp = _ptr(sf, "sf", u8, _scale_bytes(sf_layout, rows, K, L), dev)
     if x is None:
-        x = torch.empty((*shape[:-1], K), dtype=dtype, device=dev)
-    _enqueue("nvfp4_dequantize", dev, stream, qp, sp, sf_layout, rows, K, L, scale,
-             _ptr(x, "x", dtype, L * rows * K, dev), code, 0)
+        x = torch.empty((rows, K) if len(shape) == 2 else (L, rows, K), dtype=dtype, device=dev)
+    else:
+        _ptr(x, "x", dtype, L * rows * K, dev)
+    _enqueue("nvfp4_dequantize", dev, stream, qp, sp, sf_layout, rows, K, L, scale, x.data_ptr(), code, 0)
     return x
 
 
@@ -290,10 +296,11 @@ def gemm(a, b, sfa, sfb, alpha: float = 1.0, bias=None, activation: int = ACT_NO
     """c [L, N, M] = act(alpha * b a^T + bias) from a [L, M, K//2], b [L, N, K//2] (uint8) and their
     permuted scales (flat uint8); bias fp32 [L, M]; dtype float16 (default), bfloat16 or float32."""
     torch = _torch or _load()
-    if a.dim() != 3 or b.dim() != 3 or a.shape[0] != b.shape[0] or a.shape[2] != b.shape[2]:
+    ashape, bshape = a.shape, b.shape
+    if len(ashape) != 3 or len(bshape) != 3 or ashape[0] != bshape[0] or ashape[2] != bshape[2]:
         raise ValueError("a must be [L, M, K//2] and b [L, N, K//2]")
-    L, M, half_k = a.shape
-    N, K, dev, u8 = b.shape[1], 2 * half_k, a.device, torch.uint8
+    L, M, half_k = ashape
+    N, K, dev, u8 = bshape[1], 2 * half_k, a.device, torch.uint8
     if K % 16:
         raise ValueError(f"a has rows of {K} elements, expected a multiple of 16")
     ap, bp = _ptr(a, "a", u8, L * M * half_k, dev), _ptr(b, "b", u8, L * N * half_k, dev)
@@ -305,7 +312,9 @@ def gemm(a, b, sfa, sfb, alpha: float = 1.0, bias=None, activation: int = ACT_NO
     code = _dtype_code(dtype, "dtype")
     if c is None:
         c = torch.empty((L, N, M), dtype=dtype, device=dev)
-    _enqueue("nvfp4_gemm", dev, stream, ap, bp, sap, sbp, _ptr(c, "c", dtype, L * N * M, dev), M, N, K, L,
+    else:
+        _ptr(c, "c", dtype, L * N * M, dev)
+    _enqueue("nvfp4_gemm", dev, stream, ap, bp, sap, sbp, c.data_ptr(), M, N, K, L,
              ctypes.byref(_GemmOptions(alpha, bias_p, activation, code, 0)))
     return c
 
@@ -447,23 +456,31 @@ def moe_ffn(x, ids, weights, w1, sf1, w2, sf2, alpha1=None, alpha2=None, encode_
     k = ids.shape[1]
     idp = _ptr(ids, "ids", torch.int32, T * k, dev)
     wp = _ptr(weights, "weights", torch.float32, T * k, dev)
-    if w1.dim() != 3 or w2.dim() != 3:
+    shape1, shape2 = w1.shape, w2.shape
+    if len(shape1) != 3 or len(shape2) != 3:
         raise ValueError("w1 must be [E, 2F, D//2] and w2 [E, D, F//2]")
-    E, F = w1.shape[0], 2 * w2.shape[2]
-    if w1.shape[1] != 2 * F or w2.shape[1] != D or D % 32 or F % 32:
+    E, F = shape1[0], 2 * shape2[2]
+    if shape1 != (E, 2 * F, D // 2) or shape2 != (E, D, F // 2) or D % 32 or F % 32:
         raise ValueError("w1 must be [E, 2F, D//2] and w2 [E, D, F//2], D and F multiples of 32")
-    _, p1, s1, a1 = _need_experts(w1, sf1, alpha1, E, D, dev)
-    _, p2, s2, a2 = _need_experts(w2, sf2, alpha2, E, F, dev)
+    u8, f32 = torch.uint8, torch.float32
+    p1, p2 = _ptr(w1, "w1", u8, E * F * D, dev), _ptr(w2, "w2", u8, E * D * (F // 2), dev)
+    s1 = _ptr(sf1, "sf1", u8, _scale_bytes(SF_PERMUTED_128x4, 2 * F, D, E), dev)
+    s2 = _ptr(sf2, "sf2", u8, _scale_bytes(SF_PERMUTED_128x4, D, F, E), dev)
+    a1 = None if alpha1 is None else _ptr(alpha1, "alpha1", f32, E, dev)
+    a2 = None if alpha2 is None else _ptr(alpha2, "alpha2", f32, E, dev)
     if out is None:
         out = torch.empty((T, D), dtype=x.dtype, device=dev)
-    outp = _ptr(out, "out", x.dtype, T * D, dev)
-    need = nvfp4_moe_ffn_workspace_bytes(T, k, E, D, F)
+    else:
+        _ptr(out, "out", x.dtype, T * D, dev)
+    need = library().nvfp4_moe_ffn_workspace_bytes(T, k, E, D, F)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    size = workspace.numel()
-    if size < need:
-        raise ValueError(f"workspace has {size} bytes, expected {need}")
+        workspace, size = torch.empty(need, dtype=u8, device=dev), need
+    else:
+        size = workspace.numel()
+        if size < need:
+            raise ValueError(f"workspace has {size} bytes, expected {need}")
+        _ptr(workspace, "workspace", u8, size, dev)
     _enqueue("nvfp4_moe_ffn", dev, stream, x.data_ptr(), code, stride, idp, wp, p1, s1, p2, s2, T, k, E, D, F,
-             ctypes.byref(_MoeOptions(a1, a2, encode_x, encode_h, activation)), outp,
-             _ptr(workspace, "workspace", torch.uint8, size, dev), size)
+             ctypes.byref(_MoeOptions(a1, a2, encode_x, encode_h, activation)), out.data_ptr(),
+             workspace.data_ptr(), size)
     return out
