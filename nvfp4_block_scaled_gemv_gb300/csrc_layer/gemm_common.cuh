@@ -120,6 +120,35 @@ struct Turned<float> {
   }
 };
 
+// y / (1 + exp(-x)) to a few fp32 ulps: the hardware's base-2 exponential of x log2(e),
+// whose product's rounding is put back, and its fast division.
+__device__ __forceinline__ float times_sigmoid(float y, float x) {
+  constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+  const float t = -x * kLog2e;
+  const float rest = fmaf(-x, kLog2e, -t);  // exact
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+  if (t < 127.f) e = fmaf(e, rest * kLn2, e);  // (beyond, e may be infinite already)
+  return __fdividef(y, 1.0f + e);
+}
+
+// act(y) as in epilogue.cuh, in line for the activations whose instructions matter
+// here (the ones made of a sigmoid, in terms of it).
+template <int ACT>
+__device__ __forceinline__ float activate_inline(float y) {
+  if constexpr (ACT == 1) return y > 0.f ? y : (y != y ? y : 0.f);
+  if constexpr (ACT == 2) return times_sigmoid(y, y);
+  // GELU, tanh form: 1 + tanh(u) = 2 / (1 + exp(-2u))
+  if constexpr (ACT == 3) return times_sigmoid(y, 1.5957691216057308f * fmaf(0.044715f * y, y * y, y));
+  if constexpr (ACT == 4) return activate(y, 4);
+  return y;
+}
+
+template <int A>
+struct Act {
+  static constexpr int value = A;
+};
+
 // Columns 0..15 at a TMEM address, without waiting for them.
 __device__ __forceinline__ void tmem_load_16(uint32_t taddr, float (&v)[16]) {
   asm volatile(
@@ -188,9 +217,16 @@ __device__ __forceinline__ void finish_columns(const GemmParams& p, const Place&
       v[i] = y.x;
       v[i + 1] = y.y;
     }
-    if (p.activation != 0) {
+    auto each = [&](auto act) {
 #pragma unroll
-      for (int i = 0; i < kUnit; ++i) v[i] = activate(v[i], p.activation);
+      for (int i = 0; i < kUnit; ++i) v[i] = activate_inline<decltype(act)::value>(v[i]);
+    };
+    switch (p.activation) {
+      case 1: each(Act<1>()); break;
+      case 2: each(Act<2>()); break;
+      case 3: each(Act<3>()); break;
+      case 4: each(Act<4>()); break;
+      default: break;
     }
     if (p.c_dtype == kBF16)
       store_columns<__nv_bfloat16>(p, w, n, v);
@@ -210,18 +246,23 @@ __device__ __forceinline__ void finish_columns(const GemmParams& p, const Place&
     uint64_t h[4];
     float amax = 0.f;
     const float* const mine = w.transpose + col * kTransposePitch + half * 16;
-    // (SiLU: the fast exponential and division are good to a few fp32 ulps, and the
-    // exact forms' instructions would outlast the tile's MMAs)
-    auto gated = [&](float gate, float in) {
-      gate *= w.alpha;
-      const float a = p.activation == 2 ? __fdividef(gate, 1.f + __expf(-gate)) : activate(gate, p.activation);
-      return a * (in * w.alpha) * p.encode;
-    };
+    auto gated = [&](auto act) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float x = gated(mine[4 * i], mine[4 * i + 1]), y = gated(mine[4 * i + 2], mine[4 * i + 3]);
-      amax = abs_max(amax, x, y);
-      h[i] = pack_f32x2(x, y);
+      for (int i = 0; i < 4; ++i) {
+        const float x = activate_inline<decltype(act)::value>(mine[4 * i] * w.alpha) *
+                        (mine[4 * i + 1] * w.alpha) * p.encode;
+        const float y = activate_inline<decltype(act)::value>(mine[4 * i + 2] * w.alpha) *
+                        (mine[4 * i + 3] * w.alpha) * p.encode;
+        amax = abs_max(amax, x, y);
+        h[i] = pack_f32x2(x, y);
+      }
+    };
+    switch (p.activation) {
+      case 1: gated(Act<1>()); break;
+      case 2: gated(Act<2>()); break;
+      case 3: gated(Act<3>()); break;
+      case 4: gated(Act<4>()); break;
+      default: gated(Act<0>()); break;
     }
     amax = abs_max(amax, __shfl_xor_sync(0xffffffffu, amax, 1), 0.f);  // (none is negative)
     uint32_t code = 0x7Fu, q = 0;
