@@ -52,7 +52,21 @@ __device__ __forceinline__ void store_one(const GemmParams& p, int64_t idx, floa
   static_cast<T*>(p.c)[idx] = round_to(T(), v);
 }
 
-template <int BN, int EPI, bool GROUPED>
+// NC floats at p of the CTA of the given cluster rank, added to v.
+__device__ __forceinline__ void add_remote(uint32_t saddr, uint32_t rank, float (&v)[kUnit]) {
+  const uint32_t at = tc::map_rank(saddr, rank);
+#pragma unroll
+  for (int i = 0; i < kUnit; ++i) {
+    float f;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(at + 512u * i) : "memory");
+    v[i] += f;
+  }
+}
+
+// SPLIT: the CTAs of a cluster take one tile, a part of its K stages each; the
+// others leave their sums in their own shared memory (the ring's, no longer in use)
+// and rank 0 adds them in rank order.
+template <int BN, int EPI, bool GROUPED, bool SPLIT>
 __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_constant__ GemmParams p) {
   constexpr int S = stages_for(BN);
   constexpr int kAcc = 2;  // accumulators in tensor memory
@@ -101,16 +115,22 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
   const int32_t total = GROUPED ? __shfl_sync(0xffffffffu, *p.tile_count, 0) * p.tiles_m : p.total;
   bool ok = true;
+  const int ks = SPLIT ? (int)tc::cluster_size() : 1, rank = SPLIT ? (int)tc::cluster_rank() : 0;
+  const int32_t first = (int32_t)blockIdx.x / ks, step = (int32_t)gridDim.x / ks;
+  // this CTA's stages of a tile (with SPLIT every rank has some)
+  const int s_begin = SPLIT ? p.kstages * rank / ks : 0;
+  const int s_end = SPLIT ? p.kstages * (rank + 1) / ks : p.kstages;
+  static_assert(!SPLIT || (uint32_t)BN * 128 * 4 <= S * kABytes, "the sums fit the ring");
 
   if (warp == 0) {
     int pos = 0, issued = 0;
     uint32_t ph = 0;
-    for (int32_t t = (int32_t)blockIdx.x; t < total; t += (int32_t)gridDim.x) {
+    for (int32_t t = first; t < total; t += step) {
       const Tile tile = tile_at<BN, GROUPED>(p, t);
       const int64_t batch = GROUPED ? 0 : tile.g;
       const uint8_t* sa = p.sfa + ((int64_t)tile.g * p.rest_m + tile.mt) * p.rest_k * 512;
       const uint8_t* sb = p.sfb + (batch * p.rest_n + tile.n0 / 128) * p.rest_k * 512;
-      for (int s = 0; s < p.kstages; ++s) {
+      for (int s = s_begin; s < s_end; ++s) {
         const uint32_t nb = (uint32_t)min(4, p.rest_k - 4 * s) * 512u;
         tc::mbar_wait<false>(empty_bar(pos), ph ^ 1u, ok, &g_gemm_timeouts);
         ok = __all_sync(0xffffffffu, ok);
@@ -143,11 +163,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
     constexpr uint32_t idesc = tc::mxf4nvf4_idesc(BN);
     int pos = 0, j = 0;
     uint32_t ph = 0;
-    for (int32_t t = (int32_t)blockIdx.x; t < total; t += (int32_t)gridDim.x, ++j) {
+    for (int32_t t = first; t < total; t += step, ++j) {
       const int acc = j % kAcc;
       const uint32_t d = tmem + acc * BN;
       tc::mbar_wait<false>(dempty_bar(acc), ((uint32_t)(j / kAcc) & 1u) ^ 1u, ok, &g_gemm_timeouts);
-      for (int s = 0; s < p.kstages; ++s) {
+      for (int s = s_begin; s < s_end; ++s) {
         const int nk = min(4, p.rest_k - 4 * s);
         tc::mbar_wait<false>(full_bar(pos), ph, ok, &g_gemm_timeouts);
         ok = __all_sync(0xffffffffu, ok);
@@ -169,7 +189,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
               if (kk < nk)
-                tc::mma(d, da + 2u * kk, db + 2u * kk, idesc, ca + 4u * kk, cb + 4u * kk, s > 0 || kk > 0);
+                tc::mma(d, da + 2u * kk, db + 2u * kk, idesc, ca + 4u * kk, cb + 4u * kk, s > s_begin || kk > 0);
             }
             tc::commit(empty_bar(pos));
           }
@@ -193,7 +213,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
     float* const tr =
         reinterpret_cast<float*>(gemm_smem + (tr_s - raw)) + (warp - 2) * (int)(kTransposeBytes / 4);
     int j = 0;
-    for (int32_t t = (int32_t)blockIdx.x; t < total; t += (int32_t)gridDim.x, ++j) {
+    for (int32_t t = first; t < total; t += step, ++j) {
       const int acc = j % kAcc;
       const Tile tile = tile_at<BN, GROUPED>(p, t);
       const Place w = place_of<EPI, GROUPED>(p, tile, tile.mt, quarter, tr);
@@ -201,10 +221,27 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
       __syncwarp();
       ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       tc::fence_after();
-      for (int n = 0; ok && n < tile.rows; n += kUnit) {
-        float v[kUnit];
-        tc::tmem_load_cols<kUnit>(tmem + acc * BN + n + ((uint32_t)(32 * quarter) << 16), v);
-        finish_columns<EPI>(p, w, n, v);
+      const uint32_t d = acc * BN + ((uint32_t)(32 * quarter) << 16);
+      // [column][row] sums of the other ranks
+      const uint32_t sums = a_s + 4u * (uint32_t)(32 * quarter + lane);
+      if (SPLIT && rank > 0) {
+        float* const mine = reinterpret_cast<float*>(gemm_smem + (sums - raw));
+        for (int n = 0; ok && n < tile.rows; n += kUnit) {
+          float v[kUnit];
+          tc::tmem_load_cols<kUnit>(tmem + d + n, v);
+#pragma unroll
+          for (int i = 0; i < kUnit; ++i) mine[(n + i) * 128] = v[i];
+        }
+      }
+      if constexpr (SPLIT) tc::cluster_sync();  // (one tile per cluster; the other warps meet it below)
+      if (rank == 0) {
+        for (int n = 0; ok && n < tile.rows; n += kUnit) {
+          float v[kUnit];
+          tc::tmem_load_cols<kUnit>(tmem + d + n, v);
+          if constexpr (SPLIT)
+            for (int r = 1; r < ks; ++r) add_remote(sums + 512u * n, (uint32_t)r, v);
+          finish_columns<EPI>(p, w, n, v);
+        }
       }
       tc::fence_before();
       __syncwarp();
@@ -212,6 +249,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
     }
   }
 
+  if constexpr (SPLIT) {
+    if (warp < 2) tc::cluster_sync();
+    tc::cluster_sync();  // rank 0 has read the others' sums
+  }
   tc::fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -238,23 +279,29 @@ __global__ void __launch_bounds__(256) gemm_no_k_kernel(const GemmParams p) {
   }
 }
 
-template <int BN, int EPI, bool GROUPED>
-cudaError_t launch_variant(const GemmParams& p, int64_t max_tiles, int sms, cudaStream_t stream) {
-  constexpr auto kern = gemm_kernel<BN, EPI, GROUPED>;
+template <int BN, int EPI, bool GROUPED, bool SPLIT = false>
+cudaError_t launch_variant(const GemmParams& p, int64_t ctas, int ks, cudaStream_t stream) {
+  constexpr auto kern = gemm_kernel<BN, EPI, GROUPED, SPLIT>;
   constexpr uint32_t smem = gemm_smem_bytes(BN, EPI);
   cudaError_t err = allow_smem<kern>(smem);
   if (err != cudaSuccess) return err;
-  const int64_t ctas = max_tiles < sms ? max_tiles : sms;
-  return launch_pdl(kern, dim3((unsigned)ctas), dim3(kGemmThreads), smem, stream, p);
+  return launch_pdl(kern, dim3((unsigned)ctas), dim3(kGemmThreads), smem, stream, p, ks);
+}
+
+template <int BN, int EPI, bool GROUPED>
+cudaError_t launch_bn(const GemmParams& p, int64_t max_tiles, int ks, int sms, cudaStream_t stream) {
+  if constexpr (EPI == kStore && !GROUPED)
+    if (ks > 1) return launch_variant<BN, EPI, false, true>(p, max_tiles * ks, ks, stream);
+  return launch_variant<BN, EPI, GROUPED>(p, max_tiles < sms ? max_tiles : sms, 1, stream);
 }
 
 template <int EPI, bool GROUPED>
-cudaError_t launch_bn(int bn, const GemmParams& p, int64_t max_tiles, int sms, cudaStream_t stream) {
+cudaError_t launch_for(int bn, const GemmParams& p, int64_t max_tiles, int ks, int sms, cudaStream_t stream) {
   switch (bn) {
-    case 16: return launch_variant<16, EPI, GROUPED>(p, max_tiles, sms, stream);
-    case 32: return launch_variant<32, EPI, GROUPED>(p, max_tiles, sms, stream);
-    case 64: return launch_variant<64, EPI, GROUPED>(p, max_tiles, sms, stream);
-    case 128: return launch_variant<128, EPI, GROUPED>(p, max_tiles, sms, stream);
+    case 16: return launch_bn<16, EPI, GROUPED>(p, max_tiles, ks, sms, stream);
+    case 32: return launch_bn<32, EPI, GROUPED>(p, max_tiles, ks, sms, stream);
+    case 64: return launch_bn<64, EPI, GROUPED>(p, max_tiles, ks, sms, stream);
+    case 128: return launch_bn<128, EPI, GROUPED>(p, max_tiles, ks, sms, stream);
     case 256: return launch_gemm_pair(p, EPI, GROUPED, max_tiles, sms, stream);
     default: return cudaErrorInvalidValue;
   }
@@ -285,9 +332,41 @@ bool encode_atoms(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, co
 
 }  // namespace
 
-int gemm_tile_rows(int64_t M, int64_t N, int64_t L, int sms) {
-  (void)M; (void)L; (void)sms;
-  return N <= 16 ? 16 : N <= 32 ? 32 : N <= 64 ? 64 : N <= 128 ? 128 : 256;
+// The dense product's tile and K split, by the time that each would take: rounds of
+// tiles over the SMs (or pairs), each its stages and its epilogue, in us as measured
+// on GB300.  A stage of a 128 x bn tile is bound by its bytes into shared memory; rows
+// that do not start on 128-byte lines (K % 256 != 0) bring 1.6 times as many.  Checked
+// on 14 shapes from 1024x1000x8192 to 8192x1024x1024: the choice was the faster of bn
+// = 128 and 256 on all.
+GemmChoice choose_gemm(int64_t M, int64_t N, int64_t K, int64_t L, int sms) {
+  const double lines = K % 256 == 0 ? 1.0 : 1.6;
+  const int64_t stages = (K + 255) / 256, rest_m = (M + 127) / 128;
+  struct Kind {
+    int bn;
+    double stage, tile;
+  };
+  static constexpr Kind kKinds[] = {{16, 0.20, 0.3}, {32, 0.21, 0.3}, {64, 0.22, 0.5}, {128, 0.29, 0.4}};
+  GemmChoice best = {256, 1};
+  const int64_t pair_tiles = L * ((rest_m + 1) / 2) * ((N + 255) / 256), pairs = sms / 2;
+  const double pair_stage = 0.24 * lines > 0.334 ? 0.24 * lines : 0.334;
+  double least = (double)((pair_tiles + pairs - 1) / pairs) * ((double)stages * pair_stage + 1.5) + 1.5;
+  for (const Kind& k : kKinds) {
+    if (k.bn < 128 && N > k.bn) continue;  // a tile starts on a scale atom
+    const int64_t tiles = L * rest_m * ((N + k.bn - 1) / k.bn);
+    for (int ks = 1; ks <= 4; ks *= 2) {
+      // a split needs room for all its CTAs at once, and two stages for each (clusters of
+      // 8 start late: 2048x16x8192 took 11.3 us with them, 6.4 with 4, 11.3 without)
+      if (ks > 1 && (tiles * ks > sms || stages < 2 * ks)) break;
+      const int64_t rounds = (tiles * ks + sms - 1) / sms, own = (stages + ks - 1) / ks;
+      const double time = (double)rounds * ((double)own * k.stage * lines + k.tile) +
+                          (ks > 1 ? 0.8 + 0.02 * k.bn * (ks - 1) : 0.0);
+      if (time < least) {
+        least = time;
+        best = {k.bn, ks};
+      }
+    }
+  }
+  return best;
 }
 
 cudaError_t launch_gemm(const GemmArgs& g, int sms, cudaStream_t stream) {
@@ -322,7 +401,8 @@ cudaError_t launch_gemm(const GemmArgs& g, int sms, cudaStream_t stream) {
     return launch_pdl(gemm_no_k_kernel, dim3((unsigned)(ctas < 16 * sms ? ctas : 16 * sms)), dim3(256),
                       0, stream, p);
   }
-  const int bn = grouped ? g.tile_rows : gemm_tile_rows(g.M, g.N, g.G, sms);
+  const GemmChoice choice = grouped ? GemmChoice{g.tile_rows, 1} : choose_gemm(g.M, g.N, g.K, g.G, sms);
+  const int bn = choice.bn;
   const bool pair = bn == 256;
   const int64_t batches = grouped ? 1 : g.G;
   PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
@@ -337,12 +417,12 @@ cudaError_t launch_gemm(const GemmArgs& g, int sms, cudaStream_t stream) {
   p.tiles_m = pair ? (p.rest_m + 1) / 2 : p.rest_m;
   if (grouped) {
     const int64_t max_tiles = g.max_tiles * p.tiles_m;
-    return g.q ? launch_bn<kGatedQuantize, true>(bn, p, max_tiles, sms, stream)
-               : launch_bn<kStore, true>(bn, p, max_tiles, sms, stream);
+    return g.q ? launch_for<kGatedQuantize, true>(bn, p, max_tiles, 1, sms, stream)
+               : launch_for<kStore, true>(bn, p, max_tiles, 1, sms, stream);
   }
   p.tiles_n = (int32_t)((g.N + bn - 1) / bn);
   p.total = (int32_t)(g.G * p.tiles_n * p.tiles_m);
-  return launch_bn<kStore, false>(bn, p, p.total, sms, stream);
+  return launch_for<kStore, false>(bn, p, p.total, choice.ks, sms, stream);
 }
 
 cudaError_t gemm_wait_timeouts(int reset, int* out) {

@@ -119,8 +119,11 @@ struct GemmArgs {
 };
 cudaError_t launch_gemm(const GemmArgs& g, int sms, cudaStream_t stream);
 cudaError_t gemm_wait_timeouts(int reset, int* out);
-// Rows of b per tile that the dense product uses for N rows.
-int gemm_tile_rows(int64_t M, int64_t N, int64_t L, int sms);
+// The dense product's rows of b per tile and CTAs that split a tile's K.
+struct GemmChoice {
+  int bn, ks;
+};
+GemmChoice choose_gemm(int64_t M, int64_t N, int64_t K, int64_t L, int sms);
 
 // ---- routing and the experts' rows (route.cu, moe.cu) ----
 
@@ -132,7 +135,9 @@ struct RouteParams {
   int64_t T, stride;
   float scale;
   int32_t E, k, groups, top_groups, sigmoid, renormalize;
-  int32_t aligned;     // alignment of the rows, up to 16 (set by the launcher)
+  // set by the launcher: the rows' alignment (up to 16), a group's experts, and the lanes
+  // that hold them as a power of two (-1: they do not fill lanes of their own)
+  int32_t aligned, per_group, lanes_log2;
 };
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 32;

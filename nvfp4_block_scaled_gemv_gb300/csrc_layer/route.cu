@@ -17,9 +17,9 @@
 // E with 32 lanes.  A lane's experts lie in one group when NV divides the group's
 // size: the lane finds its two largest, and the group's lanes merge theirs by
 // shuffles (a power of two of them) or through shared memory.  Ranks are compared as
-// ordered integers, so that a round of the top k is one warp-wide maximum, a
-// vote, and an update on the lane that wins; the lowest such lane has the lowest
-// index.  The exponential and the division are the exact ones: a rank's last bit
+// ordered integers.  Each lane puts its own in order once, in shared memory, so that
+// a round of the top k is one warp-wide maximum, a vote, and a step down the list of
+// the lane that wins; the lowest such lane has the lowest index.  The exponential and the division are the exact ones: a rank's last bit
 // decides between experts that are nearly level.
 #include <cstdint>
 
@@ -94,16 +94,26 @@ __device__ __forceinline__ void load_logits(const RouteParams& p, int64_t t, int
 
 template <int NV, int DT>
 __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams p) {
-  __shared__ uint32_t group_keys[kRouteThreads / 32][NV * 32];
+  __shared__ uint32_t sorted[kRouteThreads / 32][NV][32];  // [.][rank][lane] keys
+  __shared__ float scores[kRouteThreads / 32][NV][32];
+  __shared__ uint8_t place[kRouteThreads / 32][NV][32];
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int e0 = lane * NV;
   const float inf = __int_as_float(0x7f800000);
-  for (int64_t t = (int64_t)blockIdx.x * (kRouteThreads / 32) + warp; t < p.T;
-       t += (int64_t)gridDim.x * (kRouteThreads / 32)) {
+  float bias[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) bias[i] = p.bias != nullptr && e0 + i < p.E ? p.bias[e0 + i] : 0.f;
+  const int64_t step = (int64_t)gridDim.x * (kRouteThreads / 32);
+  int64_t t = (int64_t)blockIdx.x * (kRouteThreads / 32) + warp;
+  float next[NV];
+  if (t < p.T) load_logits<NV, DT>(p, t, lane, next);
+  for (; t < p.T; t += step) {
     float x[NV];
-    load_logits<NV, DT>(p, t, lane, x);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) x[i] = next[i];
+    if (t + step < p.T) load_logits<NV, DT>(p, t + step, lane, next);  // (ahead of its need)
     float top = -inf;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -134,17 +144,16 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams 
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float r = x[i];
-      if (p.bias != nullptr && e0 + i < p.E) r = x[i] == -inf ? -inf : score[i] + p.bias[e0 + i];
+      if (p.bias != nullptr) r = x[i] == -inf ? -inf : score[i] + bias[i];
       key[i] = r == r && r != -inf ? ordered(r) : kMasked;
     }
     if (p.groups > 1) {
-      const int per = p.E / p.groups;  // experts of a group
+      const int per = p.per_group, lanes = 1 << p.lanes_log2;  // a group's experts, and lanes if whole
+      const bool whole = p.lanes_log2 >= 0;
       auto group_key = [&](int i) {
         return p.bias != nullptr || key[i] == kMasked ? key[i] : ordered(score[i]);
       };
       uint32_t a = kMasked, b = kMasked;  // the two largest
-      const int lanes = per / NV;         // lanes of a group, if whole
-      const bool whole = per % NV == 0 && (lanes & (lanes - 1)) == 0;
       int mine;                           // the group whose key this lane has, or -1
       if (whole) {
 #pragma unroll
@@ -152,9 +161,10 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams 
         for (int d = 1; d < lanes; d <<= 1)
           merge_two(a, b, __shfl_xor_sync(0xffffffffu, a, d), __shfl_xor_sync(0xffffffffu, b, d));
         // (lanes past the last expert are past the last group)
-        mine = e0 < p.E && lane % lanes == 0 ? lane / lanes : -1;
+        mine = e0 < p.E && (lane & (lanes - 1)) == 0 ? lane >> p.lanes_log2 : -1;
       } else {
-        uint32_t* const keys = group_keys[warp];
+        uint32_t* const keys = &sorted[warp][0][0];
+        __syncwarp();
 #pragma unroll
         for (int i = 0; i < NV; ++i) keys[e0 + i] = group_key(i);
         __syncwarp();
@@ -172,11 +182,11 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams 
         if (best == kMasked) break;
         // (the lanes that have a group's key are in the order of the groups)
         const int who = __ffs((int)__ballot_sync(0xffffffffu, gkey == best)) - 1;
-        open |= 1u << (whole ? who / lanes : who);
+        open |= 1u << (whole ? who >> p.lanes_log2 : who);
         if (lane == who) gkey = kMasked;
       }
       if (whole) {
-        if (!((open >> (lane / lanes)) & 1u))
+        if (!((open >> (lane >> p.lanes_log2)) & 1u))
 #pragma unroll
           for (int i = 0; i < NV; ++i) key[i] = kMasked;
       } else {
@@ -185,41 +195,49 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams 
           if (e0 + i < p.E && !((open >> ((e0 + i) / per)) & 1u)) key[i] = kMasked;
       }
     }
-    // the top k, best first; lane j keeps the j-th
-    int my_lane = -1, my_at = 0;  // where the j-th is held
-    uint32_t best = kMasked;
+    // the lane's keys in order, equal ones by index: each to its rank among them
+    int rank[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) best = max(best, key[i]);
+    for (int i = 0; i < NV; ++i) rank[i] = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = i + 1; j < NV; ++j) {
+        const bool later = key[j] > key[i];
+        rank[i] += later ? 1 : 0;
+        rank[j] += later ? 0 : 1;
+      }
+    __syncwarp();  // (the last token's are read)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      sorted[warp][rank[i]][lane] = key[i];
+      place[warp][rank[i]][lane] = (uint8_t)i;
+      scores[warp][i][lane] = score[i];
+    }
+    __syncwarp();
+    // the top k, best first; lane j keeps where the j-th is
+    int my_lane = -1, my_head = 0, head = 0;
+    uint32_t best = sorted[warp][0][lane];
     for (int j = 0; j < p.k; ++j) {
       const uint32_t all = __reduce_max_sync(0xffffffffu, best);
       if (all == kMasked) break;
       const int who = __ffs((int)__ballot_sync(0xffffffffu, best == all)) - 1;
-      int at = 0;
+      const int at = __shfl_sync(0xffffffffu, head, who);
       if (lane == who) {
-        // this lane's first expert with that rank, and its next best
-#pragma unroll
-        for (int i = NV - 1; i >= 0; --i)
-          if (key[i] == all) at = i;
-        best = kMasked;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          if (i == at) key[i] = kMasked;
-          best = max(best, key[i]);
-        }
+        ++head;
+        best = head < NV ? sorted[warp][head][lane] : kMasked;
       }
-      at = __shfl_sync(0xffffffffu, at, who);
       if (lane == j) {
         my_lane = who;
-        my_at = at;
+        my_head = at;
       }
     }
+    int my_at = 0;
     float w = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const float s = __shfl_sync(0xffffffffu, score[i], my_lane & 31);
-      if (my_at == i) w = s;
+    if (my_lane >= 0) {
+      my_at = place[warp][my_head][my_lane];
+      w = scores[warp][my_at][my_lane];
     }
-    if (my_lane < 0) w = 0.f;
     if (p.renormalize) {
       float sum = w;
 #pragma unroll
@@ -234,26 +252,34 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams 
 }
 
 template <int DT>
-void (*route_for(int E))(const RouteParams) {
-  if (E <= 32) return route_kernel<1, DT>;
-  if (E <= 64) return route_kernel<2, DT>;
-  if (E <= 128) return route_kernel<4, DT>;
-  if (E <= 256) return route_kernel<8, DT>;
-  if (E <= 512) return route_kernel<16, DT>;
-  return route_kernel<32, DT>;
+void (*route_for(int nv))(const RouteParams) {
+  switch (nv) {
+    case 1: return route_kernel<1, DT>;
+    case 2: return route_kernel<2, DT>;
+    case 4: return route_kernel<4, DT>;
+    case 8: return route_kernel<8, DT>;
+    case 16: return route_kernel<16, DT>;
+    default: return route_kernel<32, DT>;
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_route(RouteParams p, int dtype, int sms, cudaStream_t stream) {
-  // the largest power of two that divides every row's address (0 counts as all)
+  // the largest power of two that divides every row's address (up to 16)
   const uint64_t bits =
       (uint64_t)reinterpret_cast<uintptr_t>(p.logits) | (uint64_t)(p.stride * (dtype == kF32 ? 4 : 2)) | 16u;
   p.aligned = (int32_t)(bits & (~bits + 1));
-  auto kern = dtype == kF32 ? route_for<kF32>(p.E) : dtype == kBF16 ? route_for<kBF16>(p.E) : route_for<kF16>(p.E);
+  int nv = 1;
+  while (32 * nv < p.E) nv *= 2;
+  p.per_group = p.E / p.groups;
+  p.lanes_log2 = -1;
+  for (int i = 0; i <= 5; ++i)
+    if (p.per_group == nv << i) p.lanes_log2 = i;
+  auto kern = dtype == kF32 ? route_for<kF32>(nv) : dtype == kBF16 ? route_for<kBF16>(nv) : route_for<kF16>(nv);
   const int64_t warps = kRouteThreads / 32;
   int64_t ctas = (p.T + warps - 1) / warps;
-  if (ctas > 64ll * sms) ctas = 64ll * sms;
+  if (ctas > 8ll * sms) ctas = 8ll * sms;  // about what is resident: the bias is loaded once per warp
   return launch_pdl(kern, dim3((unsigned)ctas), dim3(kRouteThreads), 0, stream, p);
 }
 
