@@ -161,6 +161,15 @@ constexpr int kSortThreads = 512;
 constexpr int kSortChunk = 4096;  // choices per CTA
 cudaError_t launch_sort(const SortParams& p, cudaStream_t stream);
 
+// The sort and the quantisation into the experts' rows of few choices in one launch
+// (quantize.cu): sort.n = T * quantize.copies <= kPlaceMost, 16-bit x.
+constexpr int kPlaceMost = 1024;
+struct PlaceParams {
+  SortParams sort;
+  QuantizeParams quantize;
+};
+cudaError_t launch_place(const PlaceParams& p, int dtype, int64_t T, cudaStream_t stream);
+
 struct CombineParams {
   const void* y;       // [rows][M] 16-bit values
   const int32_t* rows; // [T][k]

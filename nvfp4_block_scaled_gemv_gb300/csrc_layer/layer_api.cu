@@ -476,12 +476,29 @@ nvfp4_status_t nvfp4_moe_ffn(const void* x, int dtype, int64_t x_row_stride, con
     return NVFP4_ERR_MISALIGNED;
   uint8_t* const base = static_cast<uint8_t*>(workspace);
   int32_t* const rows = reinterpret_cast<int32_t*>(base + w.rows);
-  st = nvfp4_moe_sort(ids, T, top_k, E, rows, reinterpret_cast<int32_t*>(base + w.counts),
-                      reinterpret_cast<int32_t*>(base + w.starts), base + w.plan, stream);
-  if (st != NVFP4_OK) return st;
-  st = nvfp4_quantize(x, dtype, x_row_stride, T, D, 1, opt.encode_x, base + w.xq, base + w.xsf,
-                      NVFP4_SF_PERMUTED_128x4, rows, (int)top_k, s.rows, stream);
-  if (st != NVFP4_OK) return st;
+  int32_t* const counts = reinterpret_cast<int32_t*>(base + w.counts);
+  int32_t* const starts = reinterpret_cast<int32_t*>(base + w.starts);
+  if (s.choices <= kPlaceMost) {
+    PlaceParams p = {};
+    p.sort = sort_params(ids, s, E, rows, counts, starts, base + w.plan);
+    p.quantize.x = x;
+    p.quantize.q = base + w.xq;
+    p.quantize.sf = base + w.xsf;
+    p.quantize.x_stride = x_row_stride ? x_row_stride : D;
+    p.quantize.encode = opt.encode_x;
+    p.quantize.copies = (int32_t)top_k;
+    p.quantize.half_k = (int32_t)(D / 2);
+    p.quantize.blocks = (int32_t)(D / 16);
+    p.quantize.rest_k = (int32_t)ceil_div(D, 64);
+    st = result(launch_place(p, dtype, T, (cudaStream_t)stream));
+    if (st != NVFP4_OK) return st;
+  } else {
+    st = nvfp4_moe_sort(ids, T, top_k, E, rows, counts, starts, base + w.plan, stream);
+    if (st != NVFP4_OK) return st;
+    st = nvfp4_quantize(x, dtype, x_row_stride, T, D, 1, opt.encode_x, base + w.xq, base + w.xsf,
+                        NVFP4_SF_PERMUTED_128x4, rows, (int)top_k, s.rows, stream);
+    if (st != NVFP4_OK) return st;
+  }
   st = nvfp4_moe_gated_gemm(w1, sf1, base + w.xq, base + w.xsf, base + w.plan, T, top_k, E, F, D, opt.alpha1,
                             opt.activation, opt.encode_h, base + w.hq, base + w.hsf, stream);
   if (st != NVFP4_OK) return st;

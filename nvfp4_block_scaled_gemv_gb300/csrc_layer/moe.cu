@@ -75,10 +75,16 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortPara
   // a warp's share: consecutive choices, whole steps of 32, all warps at work
   const int share = ((int)(end - begin) + kSortThreads - 1) / kSortThreads * 32;
   const int64_t wbegin = begin + (int64_t)warp * share;
+  // the warp's choices, all loads at once
+  constexpr int kSteps = kSortChunk / kSortThreads;
+  int32_t ids[kSteps];
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) ids[s] = 32 * s < share ? choice(p, wbegin + 32 * s + lane, end) : -1;
   // the warps' own counts
-  for (int s = 0; s < share; s += 32) {
-    if (wbegin + s >= end) break;
-    const int32_t e = choice(p, wbegin + s + lane, end);
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) {
+    if (32 * s >= share) break;
+    const int32_t e = ids[s];
     const uint32_t same = __match_any_sync(0xffffffffu, e);
     if (e >= 0 && lane == __ffs((int)same) - 1) place[warp * p.E + e] += __popc(same);
     __syncwarp();
@@ -126,10 +132,11 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortPara
     }
   }
   // the choices' rows
-  for (int s = 0; s < share; s += 32) {
-    if (wbegin + s >= end) break;
-    const int64_t i = wbegin + s + lane;
-    const int32_t e = choice(p, i, end);
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) {
+    if (32 * s >= share) break;
+    const int64_t i = wbegin + 32 * s + lane;
+    const int32_t e = ids[s];
     const uint32_t same = __match_any_sync(0xffffffffu, e);
     if (i < end) {
       int32_t row = -1;

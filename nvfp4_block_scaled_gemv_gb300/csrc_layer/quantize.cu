@@ -195,6 +195,92 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantizeParams
   }
 }
 
+// The sort of few choices (at most kPlaceMost) and the quantisation of the tokens into
+// the experts' rows, in one launch: a CTA per token, which sorts all the choices for
+// itself (a count of every expert's, and for its own token's the ones before them)
+// instead of waiting for another kernel to have done so.  The first CTA leaves the
+// sort's results for the products.
+template <typename T, int ALIGN>
+__global__ void __launch_bounds__(kThreads) place_kernel(const PlaceParams p) {
+  __shared__ int32_t ids[kPlaceMost];
+  __shared__ int32_t counts[kMaxExperts], first[kMaxExperts];  // choices; tiles before the expert's
+  __shared__ int32_t part[kThreads / 32];
+  __shared__ int32_t rows[kMaxTopK];
+  pdl_launch_dependents();
+  const SortParams& s = p.sort;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int n = (int)s.n, k = p.quantize.copies;
+  for (int e = threadIdx.x; e < s.E; e += kThreads) counts[e] = 0;
+  pdl_wait();
+  // the first block of x while the sort goes on
+  const T* const x = static_cast<const T*>(p.quantize.x) + (int64_t)blockIdx.x * p.quantize.x_stride;
+  RawBlock<T> raw;
+  if ((int)threadIdx.x < p.quantize.blocks) load_raw<T, ALIGN>(x + 16 * threadIdx.x, raw);
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const int32_t e = s.ids[i];
+    ids[i] = e >= 0 && e < s.E ? e : -1;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kThreads)
+    if (ids[i] >= 0) atomicAdd(&counts[ids[i]], 1);  // (a count: the order does not show)
+  __syncthreads();
+  // tiles before each expert: every thread has some consecutive experts
+  const int per = (s.E + kThreads - 1) / kThreads, e0 = threadIdx.x * per;
+  int32_t mine = 0;
+  for (int e = e0; e < e0 + per && e < s.E; ++e) mine += (counts[e] + s.tile_rows - 1) / s.tile_rows;
+  int32_t upto = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int32_t o = __shfl_up_sync(0xffffffffu, upto, d);
+    if (lane >= d) upto += o;
+  }
+  if (lane == 31) part[warp] = upto;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) upto += part[w];
+  int32_t at = upto - mine;
+  for (int e = e0; e < e0 + per && e < s.E; ++e) {
+    first[e] = at;
+    at += (counts[e] + s.tile_rows - 1) / s.tile_rows;
+  }
+  __syncthreads();
+  // the rows of this token's choices: a warp counts the ones before
+  for (int j = warp; j < k; j += kThreads / 32) {
+    const int i = (int)blockIdx.x * k + j;
+    const int32_t e = ids[i];
+    int32_t before = 0;
+    for (int b = lane; b < i; b += 32) before += ids[b] == e ? 1 : 0;
+    before = __reduce_add_sync(0xffffffffu, before);
+    const int32_t tile = before / s.tile_rows;
+    const int32_t row = e < 0 ? -1 : (first[e] + tile) * s.pitch + before - tile * s.tile_rows;
+    if (lane == 0) {
+      rows[j] = row;
+      s.rows[i] = row;
+    }
+  }
+  if (blockIdx.x == 0) {
+    if (threadIdx.x == kThreads - 1) *s.tile_count = upto;
+    for (int e = threadIdx.x; e < s.E; e += kThreads) {
+      s.counts[e] = counts[e];
+      s.starts[e] = first[e] * s.pitch;
+      for (int i = 0, left = counts[e]; left > 0; ++i, left -= s.tile_rows)
+        s.tiles[first[e] + i] = make_int4(e, (first[e] + i) * s.pitch, min(left, s.tile_rows), 0);
+    }
+  }
+  __syncthreads();
+  const QuantizeParams& z = p.quantize;
+  for (int kb = threadIdx.x; kb < 4 * z.rest_k; kb += kThreads) {
+    if (kb >= kThreads && kb < z.blocks) load_raw<T, ALIGN>(x + 16 * kb, raw);
+    uint2 q = make_uint2(0u, 0u);
+    const uint32_t code = kb < z.blocks ? quantize_block<T>(raw, z.encode, q) : 0u;
+    for (int j = 0; j < k; ++j) {
+      const int64_t dst = rows[j];
+      if (dst < 0) continue;
+      if (kb < z.blocks) *(reinterpret_cast<uint2*>(z.q + dst * z.half_k) + kb) = q;
+      z.sf[atom_offset(dst, kb, z.rest_k)] = (uint8_t)code;
+    }
+  }
+}
+
 // Two fp32 values rounded to the output type.
 __device__ __forceinline__ uint32_t pack_two(float2 v, __half) {
   const __half2 h = __float22half2_rn(v);
@@ -357,6 +443,17 @@ cudaError_t launch_quantize(QuantizeParams p, int dtype, bool permuted, int64_t 
                                : quantize_for<__half>(align, permuted, map, u);
   const int64_t per_cta = kThreads / 32, need = (p.places + per_cta - 1) / per_cta;
   return launch_pdl(kern, dim3((unsigned)(need < kMaxCtas ? need : kMaxCtas)), dim3(kThreads), 0, stream, p);
+}
+
+template <typename T>
+void (*place_for(int align))(const PlaceParams) {
+  return align == 32 ? place_kernel<T, 32> : align == 16 ? place_kernel<T, 16> : place_kernel<T, 1>;
+}
+
+cudaError_t launch_place(const PlaceParams& p, int dtype, int64_t T, cudaStream_t stream) {
+  const int align = row_alignment(p.quantize.x, p.quantize.x_stride * 2);
+  auto kern = dtype == kBF16 ? place_for<__nv_bfloat16>(align) : place_for<__half>(align);
+  return launch_pdl(kern, dim3((unsigned)T), dim3(kThreads), 0, stream, p);
 }
 
 cudaError_t launch_fold_signs(const FoldParams& p, int sms, cudaStream_t stream) {
