@@ -563,11 +563,11 @@ nvfp4_status_t nvfp4_moe_gated_gemm(const void* a, const void* sfa, const void* 
 
 /*
  * out[t][m] = dtype(sum_j weights[t][j] * y[rows[t][j]][m]), fp32 sums in the order
- * of j, choices with row -1 left out.  y: [row_capacity][M], out: [T][M], fp16 or bf16,
- * 16-byte aligned; M % 8 == 0.
+ * of j, choices with row -1 left out.  y: [row_capacity][M], of dtype or fp32 (y_dtype);
+ * out: [T][M], dtype fp16 or bf16; both 16-byte aligned; M % 8 == 0.
  */
-nvfp4_status_t nvfp4_moe_combine(const void* y, int dtype, const int32_t* rows, const float* weights,
-                                 int64_t T, int64_t top_k, int64_t M, void* out,
+nvfp4_status_t nvfp4_moe_combine(const void* y, int y_dtype, const int32_t* rows, const float* weights,
+                                 int64_t T, int64_t top_k, int64_t M, void* out, int dtype,
                                  struct CUstream_st* stream);
 
 /*
@@ -580,7 +580,8 @@ nvfp4_status_t nvfp4_moe_combine(const void* y, int dtype, const int32_t* rows, 
  * Options (NULL = {NULL, NULL, 1, 1, NVFP4_ACT_SILU}): alpha1 and alpha2 scale the two
  * products per expert (fp32 [E] on the device; NULL = 1), encode_x and encode_h the
  * values before they are quantised, activation is the gate's.  An expert's output is
- * rounded to the type of x before the weighted sum.
+ * fp32 before the weighted sum up to 1024 choices (T * top_k), and rounded to the type
+ * of x beyond.
  * workspace: nvfp4_moe_ffn_workspace_bytes bytes (0 for sizes that are not supported),
  * 256-byte aligned; its contents need not be kept.  Shapes: D and F > 0, multiples of 32.
  */

@@ -171,13 +171,13 @@ struct PlaceParams {
 cudaError_t launch_place(const PlaceParams& p, int dtype, int64_t T, cudaStream_t stream);
 
 struct CombineParams {
-  const void* y;       // [rows][M] 16-bit values
+  const void* y;       // [rows][M], fp32 or the type of out
   const int32_t* rows; // [T][k]
   const float* weights;
   void* out;           // [T][M]
   int64_t T, M;
   int32_t k;
 };
-cudaError_t launch_combine(const CombineParams& p, int dtype, int sms, cudaStream_t stream);
+cudaError_t launch_combine(const CombineParams& p, int y_dtype, int dtype, int sms, cudaStream_t stream);
 
 }  // namespace nvfp4

@@ -144,6 +144,11 @@ GemmArgs moe_gemm_args(const void* a, const void* sfa, const void* b, const void
   return g;
 }
 
+// An expert's output before the weighted sum: fp32 for few choices, where it costs
+// nothing; with many its bytes are most of what the last two steps move, and it is
+// rounded to the type of x (which the sum is rounded to in the end as well).
+int ffn_y_dtype(const MoeShape& s, int dtype) { return s.choices <= kPlaceMost ? NVFP4_DTYPE_FP32 : dtype; }
+
 // Byte offsets of moe_ffn's workspace.
 struct FfnSpace {
   int64_t rows, counts, starts, plan, xq, xsf, hq, hsf, y, bytes;
@@ -165,7 +170,7 @@ FfnSpace ffn_space(const MoeShape& s, int64_t E, int64_t D, int64_t F) {
   w.xsf = take(s.rows / 128 * ceil_div(D, 64) * 512);
   w.hq = take(s.rows * (F / 2));
   w.hsf = take(s.rows / 128 * ceil_div(F, 64) * 512);
-  w.y = take(s.rows * D * 2);
+  w.y = take(s.rows * D * (s.choices <= kPlaceMost ? 4 : 2));
   w.bytes = at;
   return w;
 }
@@ -415,10 +420,11 @@ nvfp4_status_t nvfp4_moe_gated_gemm(const void* a, const void* sfa, const void* 
   return result(launch_gemm(g, sms, (cudaStream_t)stream));
 }
 
-nvfp4_status_t nvfp4_moe_combine(const void* y, int dtype, const int32_t* rows, const float* weights,
-                                 int64_t T, int64_t top_k, int64_t M, void* out,
+nvfp4_status_t nvfp4_moe_combine(const void* y, int y_dtype, const int32_t* rows, const float* weights,
+                                 int64_t T, int64_t top_k, int64_t M, void* out, int dtype,
                                  struct CUstream_st* stream) {
-  if ((dtype != NVFP4_DTYPE_FP16 && dtype != NVFP4_DTYPE_BF16) || T < 0 || top_k < 1 || M < 0)
+  if ((dtype != NVFP4_DTYPE_FP16 && dtype != NVFP4_DTYPE_BF16) ||
+      (y_dtype != dtype && y_dtype != NVFP4_DTYPE_FP32) || T < 0 || top_k < 1 || M < 0)
     return NVFP4_ERR_INVALID_VALUE;
   if (M % 8 != 0 || M > kMaxK || top_k > kMaxTopK || T > kMaxChoices) return NVFP4_ERR_UNSUPPORTED_SHAPE;
   if (T == 0 || M == 0) return NVFP4_OK;
@@ -436,7 +442,7 @@ nvfp4_status_t nvfp4_moe_combine(const void* y, int dtype, const int32_t* rows, 
   p.T = T;
   p.M = M;
   p.k = (int32_t)top_k;
-  return result(launch_combine(p, dtype, sms, (cudaStream_t)stream));
+  return result(launch_combine(p, y_dtype, dtype, sms, (cudaStream_t)stream));
 }
 
 size_t nvfp4_moe_ffn_workspace_bytes(int64_t T, int64_t top_k, int64_t E, int64_t D, int64_t F) {
@@ -502,10 +508,11 @@ nvfp4_status_t nvfp4_moe_ffn(const void* x, int dtype, int64_t x_row_stride, con
   st = nvfp4_moe_gated_gemm(w1, sf1, base + w.xq, base + w.xsf, base + w.plan, T, top_k, E, F, D, opt.alpha1,
                             opt.activation, opt.encode_h, base + w.hq, base + w.hsf, stream);
   if (st != NVFP4_OK) return st;
+  const int y_dtype = ffn_y_dtype(s, dtype);
   st = nvfp4_moe_gemm(w2, sf2, base + w.hq, base + w.hsf, base + w.plan, T, top_k, E, D, F, opt.alpha2,
-                      NVFP4_ACT_NONE, base + w.y, dtype, stream);
+                      NVFP4_ACT_NONE, base + w.y, y_dtype, stream);
   if (st != NVFP4_OK) return st;
-  return nvfp4_moe_combine(base + w.y, dtype, rows, weights, T, top_k, D, out, stream);
+  return nvfp4_moe_combine(base + w.y, y_dtype, rows, weights, T, top_k, D, out, dtype, stream);
 }
 
 }  // extern "C"

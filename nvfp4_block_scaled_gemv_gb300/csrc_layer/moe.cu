@@ -153,15 +153,27 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortPara
   }
 }
 
-template <typename T>
-__device__ __forceinline__ float2 two_floats(uint32_t v);
-template <>
-__device__ __forceinline__ float2 two_floats<__half>(uint32_t v) {
+// Eight consecutive values.
+__device__ __forceinline__ void load_eight(const float* src, float2 (&v)[4]) {
+  const float4 a = reinterpret_cast<const float4*>(src)[0], b = reinterpret_cast<const float4*>(src)[1];
+  v[0] = make_float2(a.x, a.y);
+  v[1] = make_float2(a.z, a.w);
+  v[2] = make_float2(b.x, b.y);
+  v[3] = make_float2(b.z, b.w);
+}
+__device__ __forceinline__ float2 two_floats(uint32_t v, __half) {
   return __half22float2(*reinterpret_cast<const __half2*>(&v));
 }
-template <>
-__device__ __forceinline__ float2 two_floats<__nv_bfloat16>(uint32_t v) {
+__device__ __forceinline__ float2 two_floats(uint32_t v, __nv_bfloat16) {
   return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v));
+}
+template <typename T>
+__device__ __forceinline__ void load_eight(const T* src, float2 (&v)[4]) {
+  const uint4 u = *reinterpret_cast<const uint4*>(src);
+  v[0] = two_floats(u.x, T());
+  v[1] = two_floats(u.y, T());
+  v[2] = two_floats(u.z, T());
+  v[3] = two_floats(u.w, T());
 }
 template <typename T>
 __device__ __forceinline__ uint32_t two_rounded(float2 v);
@@ -180,7 +192,7 @@ constexpr int kCombineThreads = 256;
 
 // out[t] = sum_j weights[t][j] * y[rows[t][j]] in fp32, in the order of j; 8
 // values per thread.  M % 8 == 0.
-template <typename T>
+template <typename Y, typename T>
 __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineParams p) {
   pdl_launch_dependents();
   pdl_wait();
@@ -193,13 +205,12 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineP
       const int32_t row = p.rows[t * p.k + j];
       if (row < 0) continue;
       const float w = p.weights[t * p.k + j];
-      const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.y) + row * p.M + ch * 8);
-      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+      float2 v[4];
+      load_eight(static_cast<const Y*>(p.y) + row * p.M + ch * 8, v);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const float2 f = two_floats<T>(u[c]);
-        sum[c].x = fmaf(w, f.x, sum[c].x);
-        sum[c].y = fmaf(w, f.y, sum[c].y);
+        sum[c].x = fmaf(w, v[c].x, sum[c].x);
+        sum[c].y = fmaf(w, v[c].y, sum[c].y);
       }
     }
     *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + t * p.M + ch * 8) =
@@ -225,10 +236,12 @@ cudaError_t launch_sort(const SortParams& p, cudaStream_t stream) {
                     dim3((unsigned)(chunks < 1 ? 1 : chunks)), dim3(kSortThreads), smem, stream, p);
 }
 
-cudaError_t launch_combine(const CombineParams& p, int dtype, int sms, cudaStream_t stream) {
+cudaError_t launch_combine(const CombineParams& p, int y_dtype, int dtype, int sms, cudaStream_t stream) {
   int64_t ctas = (p.T * (p.M / 8) + kCombineThreads - 1) / kCombineThreads;
   if (ctas > 64ll * sms) ctas = 64ll * sms;
-  auto kern = dtype == kBF16 ? combine_kernel<__nv_bfloat16> : combine_kernel<__half>;
+  auto kern = y_dtype == kF32
+                  ? (dtype == kBF16 ? combine_kernel<float, __nv_bfloat16> : combine_kernel<float, __half>)
+                  : (dtype == kBF16 ? combine_kernel<__nv_bfloat16, __nv_bfloat16> : combine_kernel<__half, __half>);
   return launch_pdl(kern, dim3((unsigned)ctas), dim3(kCombineThreads), 0, stream, p);
 }
 

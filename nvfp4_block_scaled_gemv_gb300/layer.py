@@ -50,7 +50,7 @@ def declare(lib: ctypes.CDLL) -> None:
             ("nvfp4_moe_sort", [P, I64, I64, I64, P, P, P, P, P]),
             ("nvfp4_moe_gemm", [P, P, P, P, P, I64, I64, I64, I64, I64, P, I, P, I, P]),
             ("nvfp4_moe_gated_gemm", [P, P, P, P, P, I64, I64, I64, I64, I64, P, I, F, P, P, P]),
-            ("nvfp4_moe_combine", [P, I, P, P, I64, I64, I64, P, P]),
+            ("nvfp4_moe_combine", [P, I, P, P, I64, I64, I64, P, I, P]),
             ("nvfp4_moe_ffn", [P, I, I64, P, P, P, P, P, P, I64, I64, I64, I64, I64, R(_MoeOptions), P, P, Z, P])):
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = I
@@ -130,10 +130,11 @@ def nvfp4_moe_gated_gemm(a: int, sfa: int, b: int, sfb: int, plan: int, T: int, 
                                           encode_scale, q, sf, stream), "nvfp4_moe_gated_gemm")
 
 
-def nvfp4_moe_combine(y: int, dtype: int, rows: int, weights: int, T: int, top_k: int, M: int, out: int,
-                      stream: int = 0) -> None:
+def nvfp4_moe_combine(y: int, y_dtype: int, rows: int, weights: int, T: int, top_k: int, M: int, out: int,
+                      dtype: int, stream: int = 0) -> None:
     """Enqueue the weighted sum of each token's rows."""
-    _check(library().nvfp4_moe_combine(y, dtype, rows, weights, T, top_k, M, out, stream), "nvfp4_moe_combine")
+    _check(library().nvfp4_moe_combine(y, y_dtype, rows, weights, T, top_k, M, out, dtype, stream),
+           "nvfp4_moe_combine")
 
 
 def nvfp4_moe_ffn_workspace_bytes(T: int, top_k: int, E: int, D: int, F: int) -> int:
@@ -427,18 +428,22 @@ def moe_gated_gemm(a, sfa, b, sfb, order, alpha=None, activation: int = ACT_SILU
     return q, sf
 
 
-def moe_combine(y, order, weights, stream=None):
-    """out [T, M] = sum_j weights[t, j] * y[rows[t, j]] (y fp16 or bf16)."""
+def moe_combine(y, order, weights, dtype=None, stream=None):
+    """out [T, M] = sum_j weights[t, j] * y[rows[t, j]], as dtype (fp16 or bf16; y's own, or y in
+    float32)."""
     torch = _torch or _load()
-    code = _dtype_code(y, "y", fp32=False)
+    y_code = _dtype_code(y, "y")
+    dtype = dtype or y.dtype
+    code = _dtype_code(dtype, "dtype", fp32=False)
     if y.dim() != 2:
         raise ValueError("y must be [row_capacity, M]")
     T, k = order["rows"].shape
     M, dev = y.shape[1], y.device
     yp = _ptr(y, "y", y.dtype, order["row_capacity"] * M, dev)
     wp = _ptr(weights, "weights", torch.float32, T * k, dev)
-    out = torch.empty((T, M), dtype=y.dtype, device=dev)
-    _enqueue("nvfp4_moe_combine", dev, stream, yp, code, order["rows"].data_ptr(), wp, T, k, M, out.data_ptr())
+    out = torch.empty((T, M), dtype=dtype, device=dev)
+    _enqueue("nvfp4_moe_combine", dev, stream, yp, y_code, order["rows"].data_ptr(), wp, T, k, M, out.data_ptr(),
+             code)
     return out
 
 

@@ -505,15 +505,16 @@ def test_moe_gated_gemm_codes(T, k, E, F, K, act):
 
 
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("T,k,M", [(1, 1, 8), (5, 6, 264), (300, 8, 1024), (40, 32, 96)])
-def test_moe_combine(T, k, M, dtype):
+def test_moe_combine(T, k, M, wide, dtype):
     rng = np.random.default_rng(T + M)
     E = 64
     ids = choices(rng, T, k, E, 0.2)
     order = nv.moe_sort(gpu(ids), E)
-    y = torch.randn(order["row_capacity"], M).to(DT[dtype])
+    y = torch.randn(order["row_capacity"], M).to(torch.float32 if wide else DT[dtype])
     w = rng.random((T, k)).astype(np.float32)
-    out = values(nv.moe_combine(y.to(DEV), order, gpu(w)))
+    out = values(nv.moe_combine(y.to(DEV), order, gpu(w), dtype=DT[dtype]))
     rows = host(order["rows"])
     yv = y.double().numpy()
     terms = np.where(rows[..., None] >= 0, yv[rows] * w[..., None], 0.0)
@@ -544,8 +545,9 @@ def test_moe_ffn_is_its_steps_and_near_the_formula(T, k, E, D, F, dtype):
     order = nv.moe_sort(g[6], E)
     xq, xs = nv.quantize_rows(x.to(DEV), order, 1.25)
     hq, hs = nv.moe_gated_gemm(g[0], g[1], xq, xs, order, alpha=g[4], encode_scale=8.0)
-    y = nv.moe_gemm(g[2], g[3], hq, hs, order, alpha=g[5], dtype=DT[dtype])
-    assert torch.equal(out, nv.moe_combine(y, order, g[7]))
+    # (an expert's output is fp32 up to 1024 choices)
+    y = nv.moe_gemm(g[2], g[3], hq, hs, order, alpha=g[5], dtype=torch.float32 if T * k <= 1024 else DT[dtype])
+    assert torch.equal(out, nv.moe_combine(y, order, g[7], dtype=DT[dtype]))
     # against the formula: with the kernel's own codes of h the second product is held to the
     # accuracy contract
     rows = host(order["rows"])

@@ -145,11 +145,11 @@ def test_moe_gated_gemm_refusals(lib, want, kw):
 
 @pytest.mark.parametrize("want,kw", [
     (V, dict(y=None)), (V, dict(rows=None)), (V, dict(w=None)), (V, dict(out=None)), (V, dict(dt=2)),
-    (V, dict(T=-1)), (U, dict(M=12)), (U, dict(k=33)), (A, dict(y=P + 8)), (A, dict(out=P + 8)),
+    (V, dict(ydt=1)), (V, dict(ydt=3)), (V, dict(T=-1)), (U, dict(M=12)), (U, dict(k=33)), (A, dict(y=P + 8)), (A, dict(out=P + 8)),
     (0, dict(T=0, y=None)), (0, dict(M=0, out=None)),
 ])
 def test_moe_combine_refusals(lib, want, kw):
-    a = dict(y=P, dt=0, rows=P, w=P, T=4, k=2, M=64, out=P) | kw
+    a = dict(y=P, ydt=0, rows=P, w=P, T=4, k=2, M=64, out=P, dt=0) | kw
     assert lib.nvfp4_moe_combine(*a.values(), None) == want
 
 
