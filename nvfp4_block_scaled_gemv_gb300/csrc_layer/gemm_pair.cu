@@ -353,20 +353,22 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_pair_kernel(const __grid
       __syncwarp();
       if (lane == 0) arrive_remote_relaxed(release);
       if (ok) {
+        int n[kFirst / 2];
 #pragma unroll
-        for (int i = 0; i < kFirst / 2; ++i)
-          if (column(2 * i + group) < tile.rows) finish_columns<EPI>(p, w, column(2 * i + group), v[i]);
-        // the others, each loaded while the one before it is finished
-        tmem_load_16(d + column(kFirst + group), v[0]);
-        tmem_wait(v[0]);
+        for (int i = 0; i < kFirst / 2; ++i) n[i] = column(2 * i + group);
+        // the others are on their way while these are finished
+        constexpr int kRest = (kUnits - kFirst) / 2;
+        float rest[kRest][kUnit];
+        int rest_n[kRest];
 #pragma unroll
-        for (int i = kFirst; i < kUnits; i += 2) {
-          float(&now)[kUnit] = v[((i - kFirst) / 2) & 1];
-          float(&then)[kUnit] = v[((i - kFirst) / 2 + 1) & 1];
-          if (i + 2 < kUnits) tmem_load_16(d + column(i + 2 + group), then);
-          if (column(i + group) < tile.rows) finish_columns<EPI>(p, w, column(i + group), now);
-          if (i + 2 < kUnits) tmem_wait(then);
+        for (int i = 0; i < kRest; ++i) {
+          rest_n[i] = column(kFirst + 2 * i + group);
+          tmem_load_16(d + rest_n[i], rest[i]);
         }
+        finish_columns<EPI, kFirst / 2>(p, w, n, v);
+#pragma unroll
+        for (int i = 0; i < kRest; ++i) tmem_wait(rest[i]);
+        finish_columns<EPI, kRest>(p, w, rest_n, rest);
       }
     }
   }

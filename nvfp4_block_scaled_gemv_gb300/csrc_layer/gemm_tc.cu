@@ -235,12 +235,22 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
       }
       if constexpr (SPLIT) tc::cluster_sync();  // (one tile per cluster; the other warps meet it below)
       if (rank == 0) {
-        for (int n = 0; ok && n < tile.rows; n += kUnit) {
-          float v[kUnit];
-          tc::tmem_load_cols<kUnit>(tmem + d + n, v);
+        constexpr int U = BN < 32 || EPI == kGatedQuantize ? 1 : 2;
+        for (int n = 0; ok && n < tile.rows; n += U * kUnit) {
+          float v[U][kUnit];
+          int at[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            at[u] = n + u * kUnit;
+            tmem_load_16(tmem + d + at[u], v[u]);
+          }
+#pragma unroll
+          for (int u = 0; u < U; ++u) tmem_wait(v[u]);
           if constexpr (SPLIT)
-            for (int r = 1; r < ks; ++r) add_remote(sums + 512u * n, (uint32_t)r, v);
-          finish_columns<EPI>(p, w, n, v);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+              for (int r = 1; r < ks && at[u] < tile.rows; ++r) add_remote(sums + 512u * at[u], (uint32_t)r, v[u]);
+          finish_columns<EPI, U>(p, w, at, v);
         }
       }
       tc::fence_before();
@@ -387,6 +397,8 @@ cudaError_t launch_gemm(const GemmArgs& g, int sms, cudaStream_t stream) {
   p.c_stride = g.c_stride;
   p.alpha = g.alpha;
   p.encode = g.encode;
+  p.q_stride = g.M / 4;
+  p.q_atom_row = (g.M + 127) / 128 * 512;
   p.c_dtype = g.c_dtype;
   p.activation = g.activation;
   const uintptr_t two = g.c_dtype == kF32 ? 8 : 4;
