@@ -173,6 +173,7 @@ __device__ __forceinline__ void tmem_wait(float (&v)[16]) {
 struct Place {
   int64_t m, row0;   // row of A; row of c or q of the tile's column 0
   int32_t rows;      // columns of the tile
+  bool whole;        // all rows of the warp are below M
   float alpha, bias;
   // quantised output: where column 0's codes (of this lane's 8 outputs) and scale go
   // (null past the last block or atom column), and the warp's transpose buffer
@@ -192,13 +193,20 @@ __device__ __forceinline__ void store_columns(const GemmParams& p, const Place& 
     const bool odd = (threadIdx.x & 1) != 0;  // (m is the lane plus a multiple of 32)
     at += (odd ? p.c_stride : 0) + (w.m & ~int64_t(1));
     const int64_t step = 2 * p.c_stride;
-    const bool whole = n + kUnit <= w.rows && (w.m | 31) < p.M;  // the same for the whole warp
-    const int left = w.m < p.M ? w.rows - n - (odd ? 1 : 0) : 0;
+    if (w.whole && n + kUnit <= w.rows) {  // the same for the whole warp
 #pragma unroll
-    for (int i = 0; i < kUnit; i += 2) {
-      const typename Turned<T>::Store two = Turned<T>::turn(v[i], v[i + 1], odd);
-      if (whole || i < left) *reinterpret_cast<typename Turned<T>::Store*>(at) = two;
-      at += step;
+      for (int i = 0; i < kUnit; i += 2) {
+        *reinterpret_cast<typename Turned<T>::Store*>(at) = Turned<T>::turn(v[i], v[i + 1], odd);
+        at += step;
+      }
+    } else {
+      const int left = w.m < p.M ? w.rows - n - (odd ? 1 : 0) : 0;
+#pragma unroll
+      for (int i = 0; i < kUnit; i += 2) {
+        const typename Turned<T>::Store two = Turned<T>::turn(v[i], v[i + 1], odd);
+        if (i < left) *reinterpret_cast<typename Turned<T>::Store*>(at) = two;
+        at += step;
+      }
     }
   } else if (w.m < p.M) {
     at += w.m;
@@ -329,6 +337,7 @@ __device__ __forceinline__ Place place_of(const GemmParams& p, const Tile& t, in
   w.m = row_tile * 128 + 32 * quarter + (int)(threadIdx.x & 31);
   w.row0 = (GROUPED ? 0 : (int64_t)t.g * p.N) + t.n0;
   w.rows = t.rows;
+  w.whole = row_tile * 128 + 32 * quarter + 32 <= p.M;
   if constexpr (EPI == kGatedQuantize) {
     const int64_t block = row_tile * 4 + quarter, rest = (p.M + 127) / 128;  // atom columns of M/2
     const int half = threadIdx.x & 1;

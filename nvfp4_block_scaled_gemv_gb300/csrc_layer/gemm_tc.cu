@@ -25,6 +25,7 @@
 //
 // Every wait on an mbarrier gives up after tc::kWaitNs, counts a timeout in a
 // device word the host can read, and the thread then skips its remaining work.
+#include <algorithm>
 #include <cstdint>
 #include <cstring>
 
@@ -353,13 +354,15 @@ GemmChoice choose_gemm(int64_t M, int64_t N, int64_t K, int64_t L, int sms) {
   const int64_t stages = (K + 255) / 256, rest_m = (M + 127) / 128;
   struct Kind {
     int bn;
-    double stage, tile;
+    double stage, tile, epilogue;  // (the epilogue runs beside the next tile's stages)
   };
-  static constexpr Kind kKinds[] = {{16, 0.20, 0.3}, {32, 0.21, 0.3}, {64, 0.22, 0.5}, {128, 0.29, 0.4}};
+  static constexpr Kind kKinds[] = {
+      {16, 0.20, 0.3, 0.3}, {32, 0.21, 0.3, 0.5}, {64, 0.22, 0.5, 0.9}, {128, 0.29, 0.4, 1.7}};
   GemmChoice best = {256, 1};
   const int64_t pair_tiles = L * ((rest_m + 1) / 2) * ((N + 255) / 256), pairs = sms / 2;
   const double pair_stage = 0.24 * lines > 0.334 ? 0.24 * lines : 0.334;
-  double least = (double)((pair_tiles + pairs - 1) / pairs) * ((double)stages * pair_stage + 1.5) + 1.5;
+  const double pair_tile = std::max((double)stages * pair_stage + 1.5, 3.3);
+  double least = (double)((pair_tiles + pairs - 1) / pairs) * pair_tile + 1.5;
   for (const Kind& k : kKinds) {
     if (k.bn < 128 && N > k.bn) continue;  // a tile starts on a scale atom
     const int64_t tiles = L * rest_m * ((N + k.bn - 1) / k.bn);
@@ -368,7 +371,7 @@ GemmChoice choose_gemm(int64_t M, int64_t N, int64_t K, int64_t L, int sms) {
       // 8 start late: 2048x16x8192 took 11.3 us with them, 6.4 with 4, 11.3 without)
       if (ks > 1 && (tiles * ks > sms || stages < 2 * ks)) break;
       const int64_t rounds = (tiles * ks + sms - 1) / sms, own = (stages + ks - 1) / ks;
-      const double time = (double)rounds * ((double)own * k.stage * lines + k.tile) +
+      const double time = (double)rounds * std::max((double)own * k.stage * lines + k.tile, k.epilogue) +
                           (ks > 1 ? 0.8 + 0.02 * k.bn * (ks - 1) : 0.0);
       if (time < least) {
         least = time;
