@@ -16,6 +16,10 @@ constexpr int kTransposePitch = 33;       // floats between columns of a warp's 
 constexpr int kUnit = 16;                 // columns an epilogue warp takes at once
 constexpr uint32_t kTransposeBytes = kUnit * kTransposePitch * 4;  // per epilogue warp
 
+// Staging of c, per four epilogue warps: buffers of a unit's columns, 128 rows each (two
+// of 32-bit values, four of 16-bit ones).
+constexpr uint32_t kStageBytesC = 2 * kUnit * 128 * 4;
+
 enum Epilogue { kStore = 0, kGatedQuantize = 1 };
 
 struct GemmParams {
@@ -23,6 +27,7 @@ struct GemmParams {
   CUtensorMap tmap_b;    // uint8 {K/2, N, L}, box {128, rows, 1}, 128-byte swizzle
   CUtensorMap tmap_sfa;  // pair kernel: the atoms as uint64 {rest_k * 64, G * rest_m}, box {256, 1}
   CUtensorMap tmap_sfb;  // pair kernel: {rest_k * 64, L * rest_n}, box {256, 2}
+  CUtensorMap tmap_c;    // c as {M, rows, L}, box {128, kUnit, 1} (if bulk)
   const uint8_t* sfa;    // [G][rest_m][rest_k][512]
   const uint8_t* sfb;    // [L][rest_n][rest_k][512]
   const int4* tiles;     // grouped: {expert, first row, rows, 0}
@@ -37,6 +42,7 @@ struct GemmParams {
   float alpha, encode;
   int32_t c_dtype, activation;
   int32_t paired;        // c takes stores of two adjacent elements
+  int32_t bulk;          // c's rows start on 16 bytes: c is stored by TMA
   int32_t rest_m, rest_n, rest_k, kstages;
   int32_t tiles_m;       // tiles of A per group
   int32_t tiles_n;       // dense: N tiles per batch
@@ -175,6 +181,11 @@ struct Place {
   int32_t rows;      // columns of the tile
   bool whole;        // all rows of the warp are below M
   float alpha, bias;
+  // c by TMA: the four warps' staging (shared address), which buffer is next, their
+  // barrier, this warp's quarter, and the tile's place in the map
+  uint32_t staging;
+  int buffer, barrier, quarter;
+  int m0, n0, batch;
   // quantised output: where column 0's codes (of this lane's 8 outputs) and scale go
   // (null past the last block or atom column), and the warp's transpose buffer
   uint8_t* q_at;
@@ -218,12 +229,76 @@ __device__ __forceinline__ void store_columns(const GemmParams& p, const Place& 
   }
 }
 
+// Whether ok holds for all four warps at a barrier.  (They go on to meet at it for each
+// unit, so one that gave up waiting must not leave the others there.)
+__device__ __forceinline__ bool four_warps_all(int barrier, bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbar.red.and.pred q, %1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"(barrier), "r"((uint32_t)ok)
+      : "memory");
+  return all != 0;
+}
+
+// All but the last N of this thread's bulk stores have read their shared memory.
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+// They are all complete.
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// Columns n..n+kUnit-1 through shared memory: the four warps lay their rows side by
+// side and one lane stores the 128 x kUnit box.  One barrier per unit: before it, that
+// lane has seen that the store from the buffer of the next unit has been read.  Rows of c past the
+// batch's last are not written; a grouped tile's last box may write rows that hold no
+// choice.  (A bulk copy per column in place of the box took three times as long as
+// the plain stores, ~85 cycles each.)
+template <typename T>
+__device__ __forceinline__ void bulk_columns(const GemmParams& p, Place& w, int n, const float (&v)[kUnit]) {
+  const int lane = threadIdx.x & 31;
+  constexpr uint32_t kBytes = kUnit * 128 * (uint32_t)sizeof(T);
+  constexpr int kBuffers = (int)(kStageBytesC / kBytes);
+  const uint32_t buffer = w.staging + (uint32_t)w.buffer * kBytes;
+  w.buffer = w.buffer + 1 == kBuffers ? 0 : w.buffer + 1;
+  const uint32_t at = buffer + (uint32_t)sizeof(T) * (uint32_t)(32 * w.quarter + lane);
+#pragma unroll
+  for (int i = 0; i < kUnit; i += 2) {
+    if constexpr (sizeof(T) == 4) {
+      asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + 512u * i), "f"(v[i]) : "memory");
+      asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + 512u * (i + 1)), "f"(v[i + 1]) : "memory");
+    } else {
+      asm volatile(
+          "{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tst.shared.b16 [%0], lo;\n\t"
+          "st.shared.b16 [%1], hi;\n\t}" ::"r"(at + 256u * i),
+          "r"(at + 256u * (i + 1)), "r"(pack2(T(), v[i], v[i + 1]))
+          : "memory");
+    }
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  const bool sends = w.quarter == 0 && lane == 0;
+  if (sends) bulk_wait_read<kBuffers - 2>();
+  __syncwarp();
+  named_barrier_sync(w.barrier, 128);
+  if (sends) {
+    if (w.m0 < p.M)
+      asm volatile(
+          "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(&p.tmap_c),
+          "r"(w.m0), "r"(w.n0 + n), "r"(w.batch), "r"(buffer)
+          : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
+  __syncwarp();
+}
+
 // The epilogue of U units of columns, starting at n[u], of a warp's 32 rows (sums v).
 // What depends on the call (activation, type) is asked once for all of them: asked
 // for each 16 columns, the branches took longer than the columns' own instructions
 // (8192 x 8192, K 2048: 60 us, and 47 without any epilogue).
-template <int U>
-__device__ __forceinline__ void finish_store(const GemmParams& p, const Place& w, const int (&n)[U],
+template <int U, bool BULK>
+__device__ __forceinline__ void finish_store(const GemmParams& p, Place& w, const int (&n)[U],
                                              float (&v)[U][kUnit]) {
   const uint64_t alpha2 = pack_f32x2(w.alpha, w.alpha), bias2 = pack_f32x2(w.bias, w.bias);
 #pragma unroll
@@ -247,6 +322,14 @@ __device__ __forceinline__ void finish_store(const GemmParams& p, const Place& w
     if (p.activation == 4) each(Act<4>());
   }
   auto store = [&](auto type) {
+    if constexpr (BULK) {
+      if (p.bulk) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (n[u] < w.rows) bulk_columns<decltype(type)>(p, w, n[u], v[u]);
+        return;
+      }
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (n[u] < w.rows) store_columns<decltype(type)>(p, w, n[u], v[u]);
@@ -305,12 +388,12 @@ __device__ __forceinline__ void finish_quantize(const GemmParams& p, const Place
   }
 }
 
-// finish_store or finish_quantize of U units.
-template <int EPI, int U>
-__device__ __forceinline__ void finish_columns(const GemmParams& p, const Place& w, const int (&n)[U],
+// finish_store or finish_quantize of U units.  BULK: the kernel has staging for c.
+template <int EPI, int U, bool BULK>
+__device__ __forceinline__ void finish_columns(const GemmParams& p, Place& w, const int (&n)[U],
                                                float (&v)[U][kUnit]) {
   if constexpr (EPI == kStore) {
-    finish_store<U>(p, w, n, v);
+    finish_store<U, BULK>(p, w, n, v);
   } else {
     auto each = [&](auto act) {
 #pragma unroll
@@ -331,9 +414,8 @@ __device__ __forceinline__ void finish_columns(const GemmParams& p, const Place&
 }
 
 template <int EPI, bool GROUPED>
-__device__ __forceinline__ Place place_of(const GemmParams& p, const Tile& t, int64_t row_tile, int quarter,
-                                          float* transpose) {
-  Place w;
+__device__ __forceinline__ void place_at(Place& w, const GemmParams& p, const Tile& t, int64_t row_tile,
+                                         int quarter) {
   w.m = row_tile * 128 + 32 * quarter + (int)(threadIdx.x & 31);
   w.row0 = (GROUPED ? 0 : (int64_t)t.g * p.N) + t.n0;
   w.rows = t.rows;
@@ -346,8 +428,10 @@ __device__ __forceinline__ Place place_of(const GemmParams& p, const Tile& t, in
   }
   w.alpha = p.alphas ? p.alphas[t.g] : p.alpha;
   w.bias = EPI == kStore && p.bias && w.m < p.M ? p.bias[(int64_t)t.g * p.M + w.m] : 0.f;
-  w.transpose = transpose;
-  return w;
+  w.quarter = quarter;
+  w.m0 = (int)(row_tile * 128);
+  w.n0 = (int)t.n0;
+  w.batch = GROUPED ? 0 : t.g;
 }
 
 }  // namespace gemm

@@ -53,7 +53,7 @@ static_assert(kSecondCol % kUnit == 0 && (kFirst - 1) * kUnit == kBN - (int)kSec
 static_assert(kSecondCol + kBN <= kSfCol && kSfCol + 3 * kSfCols <= 512, "TMEM columns");
 
 constexpr uint32_t pair_smem_bytes(int epi) {
-  return kStages * kStageBytes + 1024u + (epi == kGatedQuantize ? 8u * kTransposeBytes : 0u);
+  return kStages * kStageBytes + 1024u + (epi == kGatedQuantize ? 8u * kTransposeBytes : 2u * kStageBytesC);
 }
 
 // M = 256 over the pair, N = n (see tc::mxf4nvf4_idesc for the fields).
@@ -326,16 +326,21 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_pair_kernel(const __grid
     }
   } else {
     const int quarter = warp & 3, group = (warp - kEpilogueWarp) >> 2;
-    float* const tr = reinterpret_cast<float*>(pair_smem + (tr_s - raw)) +
-                      (warp - kEpilogueWarp) * (int)(kTransposeBytes / 4);
+    Place w;
+    w.transpose = reinterpret_cast<float*>(pair_smem + (tr_s - raw)) +
+                  (warp - kEpilogueWarp) * (int)(kTransposeBytes / 4);
+    w.staging = tr_s + (uint32_t)group * kStageBytesC;
+    w.buffer = 0;
+    w.barrier = 1 + group;
     const uint32_t release = tc::map_rank(dempty_bar, 0);
     int j = 0;
     for (int32_t t = pair; t < total; t += pairs, ++j) {
       const Tile tile = tile_at<kBN, GROUPED>(p, t);
-      const Place w = place_of<EPI, GROUPED>(p, tile, (int64_t)tile.mt * 2 + rank, quarter, tr);
+      place_at<EPI, GROUPED>(w, p, tile, (int64_t)tile.mt * 2 + rank, quarter);
       if (lane == 0) tc::mbar_wait<false>(dfull_bar, (uint32_t)j & 1u, ok, &g_gemm_pair_timeouts);
       __syncwarp();
       ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      if (EPI == kStore) ok = four_warps_all(w.barrier, ok);  // (they meet at it for each unit)
       tc::fence_after();
       const uint32_t d = tmem + ((j & 1) ? kSecondCol : 0u) + ((uint32_t)(32 * quarter) << 16);
       // two groups of four warps take every other unit, the shared columns first:
@@ -365,12 +370,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_pair_kernel(const __grid
           rest_n[i] = column(kFirst + 2 * i + group);
           tmem_load_16(d + rest_n[i], rest[i]);
         }
-        finish_columns<EPI, kFirst / 2>(p, w, n, v);
+        finish_columns<EPI, kFirst / 2, true>(p, w, n, v);
 #pragma unroll
         for (int i = 0; i < kRest; ++i) tmem_wait(rest[i]);
-        finish_columns<EPI, kRest>(p, w, rest_n, rest);
+        finish_columns<EPI, kRest, true>(p, w, rest_n, rest);
       }
     }
+    if (EPI == kStore) bulk_wait();
   }
 
   tc::fence_before();

@@ -211,13 +211,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
     __syncwarp();
   } else {
     const int quarter = warp & 3;
-    float* const tr =
-        reinterpret_cast<float*>(gemm_smem + (tr_s - raw)) + (warp - 2) * (int)(kTransposeBytes / 4);
+    Place w;
+    w.transpose = reinterpret_cast<float*>(gemm_smem + (tr_s - raw)) + (warp - 2) * (int)(kTransposeBytes / 4);
     int j = 0;
     for (int32_t t = first; t < total; t += step, ++j) {
       const int acc = j % kAcc;
       const Tile tile = tile_at<BN, GROUPED>(p, t);
-      const Place w = place_of<EPI, GROUPED>(p, tile, tile.mt, quarter, tr);
+      place_at<EPI, GROUPED>(w, p, tile, tile.mt, quarter);
       if (lane == 0) tc::mbar_wait<false>(dfull_bar(acc), (uint32_t)(j / kAcc) & 1u, ok, &g_gemm_timeouts);
       __syncwarp();
       ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
 #pragma unroll
             for (int u = 0; u < U; ++u)
               for (int r = 1; r < ks && at[u] < tile.rows; ++r) add_remote(sums + 512u * at[u], (uint32_t)r, v[u]);
-          finish_columns<EPI, U>(p, w, at, v);
+          finish_columns<EPI, U, false>(p, w, at, v);
         }
       }
       tc::fence_before();
@@ -429,6 +429,23 @@ cudaError_t launch_gemm(const GemmArgs& g, int sms, cudaStream_t stream) {
   if (pair && (!encode_atoms(encode, &p.tmap_sfa, g.sfa, p.rest_k, g.G * p.rest_m, 1) ||
                !encode_atoms(encode, &p.tmap_sfb, g.sfb, p.rest_k, batches * p.rest_n, 2)))
     return cudaErrorInvalidValue;
+  // the pair kernel stores c by TMA (8192 x 8192, K 2048: 53 us, 58 with plain stores;
+  // the one-SM kernel's four epilogue warps were slower with it, 58 us against 43 at K 256)
+  const int64_t size = g.c_dtype == kF32 ? 4 : 2;
+  p.bulk = pair && g.c != nullptr && reinterpret_cast<uintptr_t>(g.c) % 16 == 0 && g.c_stride * size % 16 == 0 &&
+           g.c_stride * size * g.N < (int64_t(1) << 40);  // (a tensor map's largest stride)
+  if (p.bulk) {
+    const cuuint64_t dims[3] = {(cuuint64_t)g.M, (cuuint64_t)g.N, (cuuint64_t)batches};
+    const cuuint64_t strides[2] = {(cuuint64_t)(g.c_stride * size), (cuuint64_t)(g.c_stride * size * g.N)};
+    const cuuint32_t box[3] = {128, kUnit, 1}, estr[3] = {1, 1, 1};
+    const CUtensorMapDataType type = g.c_dtype == kF32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                     : g.c_dtype == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                          : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    if (encode(&p.tmap_c, type, 3, g.c, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
   p.tiles_m = pair ? (p.rest_m + 1) / 2 : p.rest_m;
   if (grouped) {
     const int64_t max_tiles = g.max_tiles * p.tiles_m;
