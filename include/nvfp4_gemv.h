@@ -473,6 +473,15 @@ nvfp4_status_t nvfp4_gemm(const void* a, const void* b, const void* sfa, const v
                           int64_t M, int64_t N, int64_t K, int64_t L,
                           const nvfp4_gemm_options_t* options, struct CUstream_st* stream);
 
+/*
+ * The tile and K split that nvfp4_gemm uses (host only, no GPU needed), for inspection
+ * and tests: tile_rows rows of b per tile (16, 32, 64 or 128 against 128 rows of a on one
+ * SM, 256 against 256 on a pair of SMs), and k_split CTAs of a cluster that share a
+ * tile's K range (1, 2 or 4).  num_sms: the device's multiprocessors (>= 2).
+ */
+nvfp4_status_t nvfp4_gemm_plan(int64_t M, int64_t N, int64_t K, int64_t L, int num_sms, int* tile_rows,
+                               int* k_split);
+
 typedef enum {
   NVFP4_SCORE_SOFTMAX = 0, /* over all E experts */
   NVFP4_SCORE_SIGMOID = 1
@@ -549,7 +558,8 @@ nvfp4_status_t nvfp4_moe_sort(const int32_t* ids, int64_t T, int64_t top_k, int6
  * input of output f; h = act(alpha gate) * (alpha input) in fp32 is quantised with
  * encode_scale as nvfp4_quantize does: q uint8 [row_capacity][F/2], sf 128x4 scales
  * (both 16-byte aligned).
- * Rows of the buffers that hold no choice are neither read into a result nor written.
+ * Rows of the buffers that hold no choice are not read into a result; what the products
+ * leave in such rows of c, q and sf is not defined.
  * Shapes: K % 32 == 0, K > 0; F % 32 == 0.  Alignment as for nvfp4_gemm.
  */
 nvfp4_status_t nvfp4_moe_gemm(const void* a, const void* sfa, const void* b, const void* sfb,

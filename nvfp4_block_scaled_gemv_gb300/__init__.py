@@ -46,6 +46,7 @@ EXPORTS = (
     "nvfp4_dequantize",
     "nvfp4_fold_scale_signs",
     "nvfp4_gemm",
+    "nvfp4_gemm_plan",
     "nvfp4_route",
     "nvfp4_moe_shape",
     "nvfp4_moe_sort",
@@ -329,6 +330,6 @@ def repack_scales(src, dst=None, stream=None):
 from .layer import (  # noqa: E402
     DTYPE_BF16, DTYPE_FP16, DTYPE_FP32, SCORE_SIGMOID, SCORE_SOFTMAX, dequantize, fold_scale_signs, gemm,
     moe_combine, moe_ffn, moe_gated_gemm, moe_gemm, moe_sort, nvfp4_dequantize, nvfp4_fold_scale_signs,
-    nvfp4_gemm, nvfp4_moe_combine, nvfp4_moe_ffn, nvfp4_moe_ffn_workspace_bytes, nvfp4_moe_gated_gemm,
+    nvfp4_gemm, nvfp4_gemm_plan, nvfp4_moe_combine, nvfp4_moe_ffn, nvfp4_moe_ffn_workspace_bytes, nvfp4_moe_gated_gemm,
     nvfp4_moe_gemm, nvfp4_moe_shape, nvfp4_moe_sort, nvfp4_quantize, nvfp4_route, quantize, quantize_rows,
     route)

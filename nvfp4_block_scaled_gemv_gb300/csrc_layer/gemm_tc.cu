@@ -346,8 +346,8 @@ bool encode_atoms(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, co
 // The dense product's tile and K split, by the time that each would take: rounds of
 // tiles over the SMs (or pairs), each its stages and its epilogue, in us as measured
 // on GB300.  A stage of a 128 x bn tile is bound by its bytes into shared memory; rows
-// that do not start on 128-byte lines (K % 256 != 0) bring 1.6 times as many.  Checked
-// on 14 shapes from 1024x1000x8192 to 8192x1024x1024: the choice was the faster of bn
+// that do not start on 128-byte lines (K % 256 != 0) bring 1.6 times as many lines, which
+// a pair's MMAs nearly hide.  Checked on 14 shapes from 1024x1000x8192 to 8192x1024x1024: the choice was the faster of bn
 // = 128 and 256 on all.
 GemmChoice choose_gemm(int64_t M, int64_t N, int64_t K, int64_t L, int sms) {
   const double lines = K % 256 == 0 ? 1.0 : 1.6;
@@ -360,7 +360,7 @@ GemmChoice choose_gemm(int64_t M, int64_t N, int64_t K, int64_t L, int sms) {
       {16, 0.20, 0.3, 0.3}, {32, 0.21, 0.3, 0.5}, {64, 0.22, 0.5, 0.9}, {128, 0.29, 0.4, 1.7}};
   GemmChoice best = {256, 1};
   const int64_t pair_tiles = L * ((rest_m + 1) / 2) * ((N + 255) / 256), pairs = sms / 2;
-  const double pair_stage = 0.24 * lines > 0.334 ? 0.24 * lines : 0.334;
+  const double pair_stage = K % 256 == 0 ? 0.334 : 0.353;
   const double pair_tile = std::max((double)stages * pair_stage + 1.5, 3.3);
   double least = (double)((pair_tiles + pairs - 1) / pairs) * pair_tile + 1.5;
   for (const Kind& k : kKinds) {

@@ -101,6 +101,8 @@ nvfp4_status_t validate_product(int64_t M, int64_t N, int64_t K, int64_t G) {
   if (K % 32 != 0 || K > kMaxK || M > kMaxDim || N > kMaxDim || G > kMaxDim)
     return NVFP4_ERR_UNSUPPORTED_SHAPE;
   if ((M != 0 && G > kMaxRows / M) || (N != 0 && G > kMaxRows / N)) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  // tiles are counted in 32 bits (the smallest have 128 x 16 outputs)
+  if (M != 0 && N != 0 && G > kMaxDim / ceil_div(M, 128) / ceil_div(N, 16)) return NVFP4_ERR_UNSUPPORTED_SHAPE;
   const int64_t most = M > N ? M : N;
   if (K != 0 && most >= kMaxMapBytes / (K / 2 > 0 ? K / 2 : 1)) return NVFP4_ERR_UNSUPPORTED_SHAPE;
   return NVFP4_OK;
@@ -295,6 +297,17 @@ nvfp4_status_t nvfp4_gemm(const void* a, const void* b, const void* sfa, const v
   g.alpha = opt.alpha;
   g.activation = opt.activation;
   return result(launch_gemm(g, sms, (cudaStream_t)stream));
+}
+
+nvfp4_status_t nvfp4_gemm_plan(int64_t M, int64_t N, int64_t K, int64_t L, int num_sms, int* tile_rows,
+                               int* k_split) {
+  if (tile_rows == nullptr || k_split == nullptr || num_sms < 2) return NVFP4_ERR_INVALID_VALUE;
+  const nvfp4_status_t st = validate_product(M, N, K, L);
+  if (st != NVFP4_OK) return st;
+  const GemmChoice c = choose_gemm(M < 1 ? 1 : M, N < 1 ? 1 : N, K < 1 ? 1 : K, L < 1 ? 1 : L, num_sms);
+  *tile_rows = c.bn;
+  *k_split = c.ks;
+  return NVFP4_OK;
 }
 
 nvfp4_status_t nvfp4_route(const void* logits, int dtype, int64_t row_stride, int64_t T, int64_t E,

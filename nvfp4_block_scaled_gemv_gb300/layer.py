@@ -45,6 +45,7 @@ def declare(lib: ctypes.CDLL) -> None:
             ("nvfp4_dequantize", [P, P, I, I64, I64, I64, F, P, I, I64, P]),
             ("nvfp4_fold_scale_signs", [P, P, I, I64, I64, I64, P]),
             ("nvfp4_gemm", [P, P, P, P, P, I64, I64, I64, I64, R(_GemmOptions), P]),
+            ("nvfp4_gemm_plan", [I64, I64, I64, I64, I, R(I), R(I)]),
             ("nvfp4_route", [P, I, I64, I64, I64, I, R(_RouteOptions), P, P, P]),
             ("nvfp4_moe_shape", [I64, I64, I64, R(_MoeShape)]),
             ("nvfp4_moe_sort", [P, I64, I64, I64, P, P, P, P, P]),
@@ -90,6 +91,14 @@ def nvfp4_gemm(a: int, b: int, sfa: int, sfb: int, c: int, M: int, N: int, K: in
     """Enqueue c [L][N][M] = act(alpha * a b + bias) for quantised a [L][M], b [L][N]."""
     opt = _GemmOptions(alpha, bias or None, activation, c_dtype, c_row_stride)
     _check(library().nvfp4_gemm(a, b, sfa, sfb, c, M, N, K, L, ctypes.byref(opt), stream), "nvfp4_gemm")
+
+
+def nvfp4_gemm_plan(M: int, N: int, K: int, L: int = 1, num_sms: int = 152) -> dict:
+    """The tile and K split that nvfp4_gemm uses (host only)."""
+    rows, split = ctypes.c_int(), ctypes.c_int()
+    _check(library().nvfp4_gemm_plan(M, N, K, L, num_sms, ctypes.byref(rows), ctypes.byref(split)),
+           "nvfp4_gemm_plan")
+    return {"tile_rows": rows.value, "k_split": split.value}
 
 
 def nvfp4_route(logits: int, dtype: int, T: int, E: int, top_k: int, ids: int, weights: int,

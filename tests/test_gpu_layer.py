@@ -223,6 +223,36 @@ def test_gemm_exact_larger():
         assert torch.equal(got, torch.bmm(bt, at.transpose(1, 2)))
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("N,M,K,L", [(2300, 4100, 2080, 1), (2304, 4096, 2048, 1), (2300, 4101, 2080, 1),
+                                     (1153, 4224, 4096, 2), (385, 20000, 8192, 1)])
+def test_gemm_exact_on_pairs_of_sms(N, M, K, L, dtype):
+    """256-row tiles: more tiles than pairs, both accumulators, narrow last tiles, rows of c
+    that TMA can store and rows that it cannot."""
+    assert nv.nvfp4_gemm_plan(M, N, K, L, torch.cuda.get_device_properties(0).multi_processor_count) == {
+        "tile_rows": 256, "k_split": 1}
+    rng = np.random.default_rng(N + M)
+    a, sfa = whole_matrix(rng, L, M, K)
+    b, sfb = whole_matrix(rng, L, N, K)
+    got = run_gemm(a, sfa, b, sfb, alpha=2.0 ** -6, dtype=DT[dtype])
+    at, bt = (torch.from_numpy(ol.matrix(*m)).float().to(DEV) for m in ((a, sfa), (b, sfb)))
+    # whole numbers below 2^24 times a power of two: exact in fp32, one rounding to the type
+    assert torch.equal(got, (torch.bmm(bt, at.transpose(1, 2)) * 2.0 ** -6).to(DT[dtype]))
+
+
+@pytest.mark.parametrize("N,M,K,L,split", [(1, 513, 2080, 1, 2), (16, 4096, 4096, 1, 4), (30, 2048, 4128, 2, 4),
+                                           (40, 1000, 8192, 1, 2), (100, 1000, 8192, 1, 2), (7, 640, 4096, 3, 4)])
+def test_gemm_exact_with_split_k(N, M, K, L, split):
+    plan = nv.nvfp4_gemm_plan(M, N, K, L, torch.cuda.get_device_properties(0).multi_processor_count)
+    assert plan["k_split"] == split
+    rng = np.random.default_rng(N + M)
+    a, sfa = whole_matrix(rng, L, M, K)
+    b, sfb = whole_matrix(rng, L, N, K)
+    want, _ = ol.gemm(ol.matrix(a, sfa), ol.matrix(b, sfb))
+    for _ in range(3):
+        assert np.array_equal(values(run_gemm(a, sfa, b, sfb, dtype=torch.float32)), want)
+
+
 @pytest.mark.parametrize("dtype", ["fp16", "bf16", "fp32"])
 @pytest.mark.parametrize("act", range(5))
 def test_gemm_general_values_and_epilogue(act, dtype):

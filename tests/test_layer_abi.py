@@ -59,6 +59,7 @@ def test_fold_scale_signs_refusals(lib, want, kw):
     (V, dict(M=-1), {}), (V, dict(N=-1), {}), (V, dict(K=-32), {}), (V, dict(L=-1), {}),
     (U, dict(K=48), {}), (U, dict(K=(1 << 30) + 32), {}), (U, dict(M=1 << 31), {}), (U, dict(N=1 << 31), {}),
     (U, dict(M=1 << 30, L=1 << 11), {}), (U, dict(M=1 << 22, K=1 << 20), {}),
+    (U, dict(M=1 << 22, N=1 << 21, L=1), {}),
     (V, {}, dict(activation=5)), (V, {}, dict(activation=-1)), (V, {}, dict(c_dtype=3)),
     (V, {}, dict(c_row_stride=7)), (V, dict(c=None), {}), (V, dict(a=None), {}), (V, dict(sfb=None), {}),
     (A, dict(a=P + 8), {}), (A, dict(b=P + 8), {}), (A, dict(sfa=P + 8), {}), (A, dict(sfb=P + 8), {}),
@@ -69,6 +70,27 @@ def test_gemm_refusals(lib, want, kw, opt):
     a = dict(a=P, b=P, sfa=P, sfb=P, c=P, M=8, N=4, K=64, L=1) | kw
     o = layer._GemmOptions(**(dict(alpha=1.0, bias=None, activation=0, c_dtype=0, c_row_stride=0) | opt))
     assert lib.nvfp4_gemm(*a.values(), ctypes.byref(o), None) == want
+
+
+def test_gemm_plan(lib):
+    plan = nv.nvfp4_gemm_plan
+    # one tile of b's rows as long as it holds them, split while SMs are idle
+    assert plan(4096, 1, 4096) == {"tile_rows": 16, "k_split": 4}
+    assert plan(4096, 17, 4096)["tile_rows"] == 32 and plan(4096, 64, 4096)["tile_rows"] == 64
+    assert plan(65536, 16, 4096) == {"tile_rows": 16, "k_split": 1}
+    for M, N, K in ((4096, 1, 256), (100, 7, 32), (128, 100, 500 * 32)):
+        p = plan(M, N, K)
+        stages = -(-K // 256)
+        assert p["k_split"] == 1 or stages >= 2 * p["k_split"]
+        assert -(-M // 128) * -(-N // p["tile_rows"]) * p["k_split"] <= 152
+    # tiles below 128 rows start on no scale atom but the first
+    for N in (129, 200, 333, 1000, 8192):
+        assert plan(4096, N, 2048)["tile_rows"] in (128, 256)
+    assert plan(8192, 8192, 8192) == {"tile_rows": 256, "k_split": 1}
+    r = ctypes.byref(ctypes.c_int())
+    assert lib.nvfp4_gemm_plan(8, 8, 64, 1, 152, None, r) == V
+    assert lib.nvfp4_gemm_plan(8, 8, 64, 1, 1, r, r) == V
+    assert lib.nvfp4_gemm_plan(8, 8, 40, 1, 152, r, r) == U
 
 
 @pytest.mark.parametrize("want,kw,opt", [
