@@ -101,11 +101,19 @@ nvfp4_status_t validate_product(int64_t M, int64_t N, int64_t K, int64_t G) {
   if (K % 32 != 0 || K > kMaxK || M > kMaxDim || N > kMaxDim || G > kMaxDim)
     return NVFP4_ERR_UNSUPPORTED_SHAPE;
   if ((M != 0 && G > kMaxRows / M) || (N != 0 && G > kMaxRows / N)) return NVFP4_ERR_UNSUPPORTED_SHAPE;
-  // tiles are counted in 32 bits (the smallest have 128 x 16 outputs)
-  if (M != 0 && N != 0 && G > kMaxDim / ceil_div(M, 128) / ceil_div(N, 16)) return NVFP4_ERR_UNSUPPORTED_SHAPE;
   const int64_t most = M > N ? M : N;
   if (K != 0 && most >= kMaxMapBytes / (K / 2 > 0 ? K / 2 : 1)) return NVFP4_ERR_UNSUPPORTED_SHAPE;
   return NVFP4_OK;
+}
+
+// Tiles are counted in 32 bits (the dense product's smallest have 128 x 16 outputs).
+bool dense_tiles_fit(int64_t M, int64_t N, int64_t L) {
+  return M == 0 || N == 0 || L <= kMaxDim / ceil_div(M, 128) / ceil_div(N, 16);
+}
+nvfp4_status_t validate_grouped(const MoeShape& s, int64_t M, int64_t K, int64_t E) {
+  const nvfp4_status_t st = validate_product(M, s.rows, K, E);
+  if (st != NVFP4_OK) return st;
+  return s.tiles * ceil_div(M, 128) > kMaxDim ? NVFP4_ERR_UNSUPPORTED_SHAPE : NVFP4_OK;
 }
 
 SortParams sort_params(const int32_t* ids, const MoeShape& s, int64_t E, int32_t* rows, int32_t* counts,
@@ -269,6 +277,7 @@ nvfp4_status_t nvfp4_gemm(const void* a, const void* b, const void* sfa, const v
   const nvfp4_gemm_options_t& opt = options ? *options : kDefaults;
   nvfp4_status_t st = validate_product(M, N, K, L);
   if (st != NVFP4_OK) return st;
+  if (!dense_tiles_fit(M, N, L)) return NVFP4_ERR_UNSUPPORTED_SHAPE;
   if (!valid_dtype(opt.c_dtype) || !valid_activation(opt.activation) ||
       (opt.c_row_stride != 0 && opt.c_row_stride < M))
     return NVFP4_ERR_INVALID_VALUE;
@@ -304,6 +313,7 @@ nvfp4_status_t nvfp4_gemm_plan(int64_t M, int64_t N, int64_t K, int64_t L, int n
   if (tile_rows == nullptr || k_split == nullptr || num_sms < 2) return NVFP4_ERR_INVALID_VALUE;
   const nvfp4_status_t st = validate_product(M, N, K, L);
   if (st != NVFP4_OK) return st;
+  if (!dense_tiles_fit(M, N, L)) return NVFP4_ERR_UNSUPPORTED_SHAPE;
   const GemmChoice c = choose_gemm(M < 1 ? 1 : M, N < 1 ? 1 : N, K < 1 ? 1 : K, L < 1 ? 1 : L, num_sms);
   *tile_rows = c.bn;
   *k_split = c.ks;
@@ -379,7 +389,7 @@ nvfp4_status_t nvfp4_moe_gemm(const void* a, const void* sfa, const void* b, con
   nvfp4_status_t st = validate_moe(T, top_k, E);
   if (st != NVFP4_OK) return st;
   const MoeShape s = moe_shape(T, top_k, E);
-  st = validate_product(M, s.rows, K, E);
+  st = validate_grouped(s, M, K, E);
   if (st != NVFP4_OK) return st;
   if (!valid_dtype(c_dtype) || !valid_activation(activation)) return NVFP4_ERR_INVALID_VALUE;
   if (K == 0) return NVFP4_ERR_UNSUPPORTED_SHAPE;
@@ -409,7 +419,7 @@ nvfp4_status_t nvfp4_moe_gated_gemm(const void* a, const void* sfa, const void* 
   if (st != NVFP4_OK) return st;
   if (F < 0 || F > kMaxDim / 2) return NVFP4_ERR_INVALID_VALUE;
   const MoeShape s = moe_shape(T, top_k, E);
-  st = validate_product(2 * F, s.rows, K, E);
+  st = validate_grouped(s, 2 * F, K, E);
   if (st != NVFP4_OK) return st;
   if (!valid_activation(activation) || !(encode_scale > 0.f) || !std::isfinite(encode_scale))
     return NVFP4_ERR_INVALID_VALUE;
@@ -479,8 +489,7 @@ nvfp4_status_t nvfp4_moe_ffn(const void* x, int dtype, int64_t x_row_stride, con
     return NVFP4_ERR_INVALID_VALUE;
   if (D % 32 != 0 || F % 32 != 0 || D == 0 || F == 0 || F > kMaxDim / 2) return NVFP4_ERR_UNSUPPORTED_SHAPE;
   const MoeShape s = moe_shape(T, top_k, E);
-  if ((st = validate_product(2 * F, s.rows, D, E)) != NVFP4_OK ||
-      (st = validate_product(D, s.rows, F, E)) != NVFP4_OK ||
+  if ((st = validate_grouped(s, 2 * F, D, E)) != NVFP4_OK || (st = validate_grouped(s, D, F, E)) != NVFP4_OK ||
       (st = validate_rows(dtype, T, D, 1, x_row_stride, NVFP4_SF_PERMUTED_128x4)) != NVFP4_OK)
     return st;
   if (T == 0) return NVFP4_OK;

@@ -64,7 +64,8 @@ def rows_of(rng, rows, K, dtype):
 @pytest.mark.parametrize("layout", [nv.SF_PLAIN, nv.SF_PERMUTED_128x4])
 @pytest.mark.parametrize("dtype", ["fp16", "bf16", "fp32"])
 @pytest.mark.parametrize("rows,K,encode", [(1, 16, 1.0), (1, 4096, 0.7), (3, 80, 1.0), (129, 208, 3.3),
-                                           (128, 64, 1.0), (257, 1024, 0.011), (40, 8192, 1.0)])
+                                           (128, 64, 1.0), (257, 1024, 0.011), (40, 8192, 1.0),
+                                           (2500, 8272, 1.7)])
 def test_quantize_bit_exact(rows, K, encode, dtype, layout):
     rng = np.random.default_rng(rows * 7 + K)
     x = rows_of(rng, rows, K, dtype)
@@ -75,6 +76,29 @@ def test_quantize_bit_exact(rows, K, encode, dtype, layout):
     else:
         assert np.array_equal(host(sf), want_sf.reshape(-1))
     assert np.array_equal(host(q), want_q)
+
+
+def test_quantize_every_scale_with_every_tie():
+    """For each scale s: a block whose largest is 6 s, all ties of the codes, and their
+    neighbours in fp32; and the ties between scales, with theirs."""
+    s = ol.e4m3_values(np.arange(1, 0x7F, dtype=np.uint8)).astype(np.float32)
+    ties = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], dtype=np.float32)
+    blocks = []
+    for toward in (None, np.float32(0), np.float32(1e9)):
+        t = ties[None] * s[:, None]
+        t = t if toward is None else np.nextafter(t, toward)
+        blocks.append(np.concatenate((6 * s[:, None], t, -t, np.zeros((len(s), 1), np.float32)), axis=1))
+    mid = 6 * (s[1:] + s[:-1]) / 2
+    for toward in (mid, np.float32(0), np.float32(1e9)):
+        b = np.zeros((len(mid), 16), dtype=np.float32)
+        b[:, 3], b[:, 5] = np.nextafter(mid, toward), 0.3 * mid
+        blocks.append(b)
+    x = np.concatenate(blocks).reshape(-1, 16)
+    x = np.concatenate((x, np.zeros((-len(x) % 4, 16), np.float32))).reshape(-1, 64)
+    q, sf = nv.quantize(gpu(x), sf_layout=nv.SF_PLAIN)
+    want_q, want_sf = ol.quantize(x)
+    assert np.array_equal(host(sf), want_sf.reshape(-1))
+    assert np.array_equal(ol.e2m1_values(host(q)), ol.e2m1_values(want_q))
 
 
 @pytest.mark.parametrize("dtype", ["fp16", "bf16", "fp32"])

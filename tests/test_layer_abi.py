@@ -148,7 +148,7 @@ def test_moe_sort_refusals(lib, want, kw):
     (V, dict(a=None)), (V, dict(sfa=None)), (V, dict(b=None)), (V, dict(sfb=None)), (V, dict(plan=None)),
     (V, dict(c=None)), (V, dict(M=-1)), (V, dict(act=9)), (V, dict(dt=4)), (U, dict(K=0)), (U, dict(K=40)),
     (A, dict(a=P + 8)), (A, dict(plan=P + 4)), (A, dict(c=P + 1)), (A, dict(alpha=P + 2)),
-    (0, dict(M=0, c=None)), (0, dict(T=0, plan=None)),
+    (U, dict(T=1 << 23, M=1 << 23)), (0, dict(M=0, c=None)), (0, dict(T=0, plan=None)),
 ])
 def test_moe_gemm_refusals(lib, want, kw):
     a = dict(a=P, sfa=P, b=P, sfb=P, plan=P, T=4, k=2, E=8, M=128, K=64, alpha=None, act=0, c=P, dt=0) | kw
