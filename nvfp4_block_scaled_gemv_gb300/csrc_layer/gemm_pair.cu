@@ -15,6 +15,13 @@
 // (its 128 rows, 256 columns) is in its own tensor memory, and 8 epilogue warps of
 // each CTA read it.
 //
+// What bounds it.  On this kernel's tiles a K = 64 MMA of N = 256 takes 128 cycles (with
+// no copies at all a stage took 0.275 us, 9.3 PFLOP/s in all), and the scale copies take
+// their turn in the same pipe: 0.33 us per stage, 256 x 256 x 256 per pair.  From one
+// tile to the next ~900 cycles pass between the last MMA's commit and the release of
+// the shared columns.  Measured on GB300: 8192^3 160 us (6.9 PFLOP/s), 8192 x 8192 with
+// K 2048 53 us (5.2), 4096^3 28.7 us (4.8), bf16 c.
+//
 // A tile of at most 128 rows of B (the last of an expert, often) runs MMAs of
 // N = 128, half the time.
 //

@@ -1,5 +1,11 @@
 // The experts' rows (sm_103a): a stable sort of the routed choices by expert,
 // and the weighted sum of a token's expert outputs.
+//
+// The sort is two launches, or one up to 4096 choices: a histogram per chunk, then every
+// chunk adds up the ones before it and ranks its own choices.  Both are latency, a few
+// passes over at most a few hundred KB: 32768 choices among 64 experts 3 + 11 us beside
+// the products' 350.  The sum is one pass over the experts' outputs, bound by their
+// bytes: 4096 tokens of 8 choices, M 4096 in bf16, 53 us (5.7 TB/s).
 #include <cstdint>
 
 #include <cuda_bf16.h>
