@@ -316,7 +316,8 @@ const char* nvfp4_status_string(int status);
  * (0 if none). */
 int nvfp4_last_cuda_error(void);
 
-/* Waits of the tensor-core kernel that gave up: every wait of that kernel on
+/* Waits of the tensor-core kernels (the GEMV's, the block-dot kernel's and the
+ * layer products') that gave up: every wait of those kernels on
  * a pipeline barrier is bounded (2 s), and a wait that runs out is counted
  * here and makes its thread skip the rest of its work (the launch's c is
  * then not valid).  Synchronises the device; reset != 0 clears the count

@@ -189,6 +189,23 @@ def test_dequantize_all_codes(dtype, layout):
 
 
 @pytest.mark.parametrize("layout", [nv.SF_PLAIN, nv.SF_PERMUTED_128x4])
+@pytest.mark.parametrize("stride,offset", [(96, 0), (104, 0), (97, 1), (2080, 16)])
+def test_dequantize_batches_into_strided_rows(stride, offset, layout):
+    rng = np.random.default_rng(stride)
+    L, rows, K = 2, 131, 2064 if stride > 2000 else 96
+    q = rng.integers(0, 256, (L, rows, K // 2), dtype=np.uint8)
+    sf = rng.integers(0, 0x7F, (L, rows, K // 16)).astype(np.uint8)
+    buf = torch.full((L * rows * stride + offset,), -77.0, dtype=torch.float16, device=DEV)
+    qd, sd = gpu(q), gpu(ol.atoms(sf) if layout else sf.reshape(-1))
+    nv.nvfp4_dequantize(qd.data_ptr(), sd.data_ptr(), rows, K, L, buf.data_ptr() + 2 * offset, nv.DTYPE_FP16,
+                        layout, x_row_stride=stride, stream=torch.cuda.current_stream().cuda_stream)
+    got = values(buf)
+    assert (got[:offset] == -77).all()
+    got = got[offset:].reshape(L, rows, stride)
+    assert np.array_equal(got[:, :, :K], ol.matrix(q, sf)) and (got[:, :, K:] == -77).all()
+
+
+@pytest.mark.parametrize("layout", [nv.SF_PLAIN, nv.SF_PERMUTED_128x4])
 def test_fold_scale_signs_keeps_the_values(layout):
     rng = np.random.default_rng(9)
     L, rows, K = 2, 131, 80
