@@ -266,7 +266,8 @@ def test_gemm_exact_larger():
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
 @pytest.mark.parametrize("N,M,K,L", [(2300, 4100, 2080, 1), (2304, 4096, 2048, 1), (2300, 4101, 2080, 1),
-                                     (1153, 4224, 4096, 2), (385, 20000, 8192, 1)])
+                                     (1153, 4224, 4096, 2), (385, 20000, 8192, 1), (449, 20000, 8192, 1),
+                                     (256 + 64, 20000, 8192, 1), (256 + 180, 20000, 8224, 1)])
 def test_gemm_exact_on_pairs_of_sms(N, M, K, L, dtype):
     """256-row tiles: more tiles than pairs, both accumulators, narrow last tiles, rows of c
     that TMA can store and rows that it cannot."""
