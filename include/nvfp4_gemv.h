@@ -475,10 +475,11 @@ nvfp4_status_t nvfp4_gemm(const void* a, const void* b, const void* sfa, const v
                           const nvfp4_gemm_options_t* options, struct CUstream_st* stream);
 
 /*
- * The tile and K split that nvfp4_gemm uses (host only, no GPU needed), for inspection
- * and tests: tile_rows rows of b per tile (16, 32, 64 or 128 against 128 rows of a on one
- * SM, 256 against 256 on a pair of SMs), and k_split CTAs of a cluster that share a
- * tile's K range (1, 2 or 4).  num_sms: the device's multiprocessors (>= 2).
+ * The tile and K split that nvfp4_gemm uses (host only, no GPU needed) for a product
+ * without an activation (with one, others may be faster), for inspection and tests:
+ * tile_rows rows of b per tile (16, 32, 64 or 128 against 128 rows of a on one SM, 256
+ * against 256 on a pair of SMs), and k_split CTAs of a cluster that share a tile's K
+ * range (1, 2 or 4).  num_sms: the device's multiprocessors (>= 2).
  */
 nvfp4_status_t nvfp4_gemm_plan(int64_t M, int64_t N, int64_t K, int64_t L, int num_sms, int* tile_rows,
                                int* k_split);

@@ -350,34 +350,55 @@ bool encode_atoms(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, co
 }  // namespace
 
 // The dense product's tile and K split, by the time that each would take: rounds of
-// tiles over the SMs (or pairs), each its stages and its epilogue, in us as measured
-// on GB300.  A stage of a 128 x bn tile is bound by its bytes into shared memory; rows
-// that do not start on 128-byte lines (K % 256 != 0) bring 1.6 times as many lines, which
-// a pair's MMAs nearly hide.  Checked on 14 shapes from 1024x1000x8192 to 8192x1024x1024: the choice was the faster of bn
-// = 128 and 256 on all.
-GemmChoice choose_gemm(int64_t M, int64_t N, int64_t K, int64_t L, int sms) {
-  const double lines = K % 256 == 0 ? 1.0 : 1.6;
+// tiles over the SMs (or pairs), each its stages or, if longer, the epilogue of the tile
+// before, then the last epilogue, in us as measured on GB300.  A stage of a 128 x bn
+// tile is bound by its bytes into shared memory.  Rows that do not start on 128-byte
+// lines (K % 256 != 0) bring more lines, which costs the more the more SMs ask for them;
+// a pair's MMAs nearly hide it.  A last tile with few rows of b brings fewer bytes, and
+// fewer columns of the pair's MMAs.  An activation that has an exponential takes the pair
+// kernel's epilogue longest.
+// Both tiles measured on 366 shapes, 200x9000x544 to 5000x5000x7168, on a part of which
+// the constants were fitted: the choice takes 0.2% longer than the faster tile on average
+// without an activation, at most 15% (270x2100x5152, 5 batches), and 0.6%, at most 10%,
+// with one.  Nearly level choices are where it errs.
+GemmChoice choose_gemm(int64_t M, int64_t N, int64_t K, int64_t L, int sms, bool activation) {
+  const bool aligned = K % 256 == 0;
   const int64_t stages = (K + 255) / 256, rest_m = (M + 127) / 128;
   struct Kind {
     int bn;
-    double stage, tile, epilogue;  // (the epilogue runs beside the next tile's stages)
+    double stage, tile, epilogue, last_with_activation;
   };
-  static constexpr Kind kKinds[] = {
-      {16, 0.20, 0.3, 0.3}, {32, 0.21, 0.3, 0.5}, {64, 0.22, 0.5, 0.9}, {128, 0.29, 0.4, 1.7}};
+  static constexpr Kind kKinds[] = {{16, 0.20, 0.3, 0.3, 0.7},
+                                    {32, 0.21, 0.3, 0.5, 1.1},
+                                    {64, 0.22, 0.5, 0.9, 2.0},
+                                    {128, 0.30, 0.4, 1.7, 3.8}};
   GemmChoice best = {256, 1};
   const int64_t pair_tiles = L * ((rest_m + 1) / 2) * ((N + 255) / 256), pairs = sms / 2;
-  const double pair_stage = K % 256 == 0 ? 0.334 : 0.353;
-  const double pair_tile = std::max((double)stages * pair_stage + 1.5, 3.3);
-  double least = (double)((pair_tiles + pairs - 1) / pairs) * pair_tile + 1.5;
+  const int64_t pair_rounds = (pair_tiles + pairs - 1) / pairs;
+  const int64_t pair_n = (N + 255) / 256, pair_width = N / 256 * 256 + (N % 256 + 63) / 64 * 64;
+  const double pair_fill = 0.7 + 0.3 * (double)pair_width / (double)(256 * pair_n);
+  const double pair_tile = (double)stages * (aligned ? 0.334 : 0.38) * pair_fill + 1.5;
+  double least = (double)(pair_rounds - 1) * std::max(pair_tile, activation ? 6.5 : 3.3) + pair_tile +
+                 (activation ? 5.5 : 2.9);
   for (const Kind& k : kKinds) {
     if (k.bn < 128 && N > k.bn) continue;  // a tile starts on a scale atom
-    const int64_t tiles = L * rest_m * ((N + k.bn - 1) / k.bn);
+    if (k.bn == 128 && N <= 64) continue;  // (64 was as fast or faster on 25 shapes)
+    const int64_t tiles_n = (N + k.bn - 1) / k.bn, tiles = L * rest_m * tiles_n;
+    const double there = (double)N / (double)(k.bn * tiles_n);
+    const double epilogue = activation ? 1.2 * k.epilogue : k.epilogue;
+    const double last = activation ? k.last_with_activation : k.epilogue;
     for (int ks = 1; ks <= 4; ks *= 2) {
       // a split needs room for all its CTAs at once, and two stages for each (clusters of
       // 8 start late: 2048x16x8192 took 11.3 us with them, 6.4 with 4, 11.3 without)
       if (ks > 1 && (tiles * ks > sms || stages < 2 * ks)) break;
       const int64_t rounds = (tiles * ks + sms - 1) / sms, own = (stages + ks - 1) / ks;
-      const double time = (double)rounds * std::max((double)own * k.stage * lines + k.tile, k.epilogue) +
+      double stage = k.stage;
+      if (k.bn < 128)
+        stage *= aligned ? 1.0 : 1.6;
+      else
+        stage *= (aligned ? 1.0 : 1.0 + 0.5 * std::min(1.0, (double)(tiles * ks) / sms)) * (0.85 + 0.15 * there);
+      const double tile = (double)own * stage + k.tile;
+      const double time = (double)(rounds - 1) * std::max(tile, epilogue) + tile + last +
                           (ks > 1 ? 0.8 + 0.02 * k.bn * (ks - 1) : 0.0);
       if (time < least) {
         least = time;
@@ -422,7 +443,8 @@ cudaError_t launch_gemm(const GemmArgs& g, int sms, cudaStream_t stream) {
     return launch_pdl(gemm_no_k_kernel, dim3((unsigned)(ctas < 16 * sms ? ctas : 16 * sms)), dim3(256),
                       0, stream, p);
   }
-  const GemmChoice choice = grouped ? GemmChoice{g.tile_rows, 1} : choose_gemm(g.M, g.N, g.K, g.G, sms);
+  const GemmChoice choice = grouped ? GemmChoice{g.tile_rows, 1}
+                                    : choose_gemm(g.M, g.N, g.K, g.G, sms, g.activation > 1);  // (ReLU costs nothing)
   const int bn = choice.bn;
   const bool pair = bn == 256;
   const int64_t batches = grouped ? 1 : g.G;

@@ -123,7 +123,7 @@ cudaError_t gemm_wait_timeouts(int reset, int* out);
 struct GemmChoice {
   int bn, ks;
 };
-GemmChoice choose_gemm(int64_t M, int64_t N, int64_t K, int64_t L, int sms);
+GemmChoice choose_gemm(int64_t M, int64_t N, int64_t K, int64_t L, int sms, bool activation);
 
 // ---- routing and the experts' rows (route.cu, moe.cu) ----
 

@@ -314,7 +314,7 @@ nvfp4_status_t nvfp4_gemm_plan(int64_t M, int64_t N, int64_t K, int64_t L, int n
   const nvfp4_status_t st = validate_product(M, N, K, L);
   if (st != NVFP4_OK) return st;
   if (!dense_tiles_fit(M, N, L)) return NVFP4_ERR_UNSUPPORTED_SHAPE;
-  const GemmChoice c = choose_gemm(M < 1 ? 1 : M, N < 1 ? 1 : N, K < 1 ? 1 : K, L < 1 ? 1 : L, num_sms);
+  const GemmChoice c = choose_gemm(M < 1 ? 1 : M, N < 1 ? 1 : N, K < 1 ? 1 : K, L < 1 ? 1 : L, num_sms, false);
   *tile_rows = c.bn;
   *k_split = c.ks;
   return NVFP4_OK;

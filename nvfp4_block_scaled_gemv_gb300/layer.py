@@ -94,7 +94,7 @@ def nvfp4_gemm(a: int, b: int, sfa: int, sfb: int, c: int, M: int, N: int, K: in
 
 
 def nvfp4_gemm_plan(M: int, N: int, K: int, L: int = 1, num_sms: int = 152) -> dict:
-    """The tile and K split that nvfp4_gemm uses (host only)."""
+    """The tile and K split that nvfp4_gemm uses without an activation (host only)."""
     rows, split = ctypes.c_int(), ctypes.c_int()
     _check(library().nvfp4_gemm_plan(M, N, K, L, num_sms, ctypes.byref(rows), ctypes.byref(split)),
            "nvfp4_gemm_plan")
