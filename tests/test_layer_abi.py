@@ -93,6 +93,15 @@ def test_gemm_plan(lib):
     assert lib.nvfp4_gemm_plan(8, 8, 40, 1, 152, r, r) == U
 
 
+@pytest.mark.parametrize("N,M,K,L,rows,split", [
+    (320, 20000, 8192, 1, 256, 1), (560, 12000, 8224, 1, 256, 1),  # narrow last tiles of pairs
+    (320, 4096, 1024, 3, 128, 1), (310, 9000, 1024, 1, 128, 1),    # too little K for a pair's epilogue
+    (40, 3000, 4128, 1, 64, 2), (128, 9000, 4128, 1, 128, 1), (500, 1000, 4128, 1, 128, 1)])
+def test_gemm_plan_takes_the_faster_tile(lib, N, M, K, L, rows, split):
+    """Shapes on which another tile or split measured 2 to 60% slower."""
+    assert nv.nvfp4_gemm_plan(M, N, K, L) == {"tile_rows": rows, "k_split": split}
+
+
 @pytest.mark.parametrize("want,kw,opt", [
     (V, dict(dt=3), {}), (V, dict(T=-1), {}), (V, dict(E=0), {}), (V, dict(k=0), {}), (V, dict(stride=31), {}),
     (U, dict(E=1025, k=4), {}), (U, dict(k=33, E=64), {}), (U, dict(k=33), {}), (U, {}, dict(groups=5)),
