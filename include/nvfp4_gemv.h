@@ -589,11 +589,12 @@ nvfp4_status_t nvfp4_moe_combine(const void* y, int y_dtype, const int32_t* rows
  *   w1, sf1 : [E][2F][D/2], gate and input rows interleaved (see above), 128x4 scales
  *   w2, sf2 : [E][D][F/2], 128x4 scales
  *   out     : [T][D], the type of x, 16-byte aligned
- * Options (NULL = {NULL, NULL, 1, 1, NVFP4_ACT_SILU}): alpha1 and alpha2 scale the two
+ * Options (NULL = {NULL, NULL, 1, 1, NVFP4_ACT_SILU, 0}): alpha1 and alpha2 scale the two
  * products per expert (fp32 [E] on the device; NULL = 1), encode_x and encode_h the
  * values before they are quantised, activation is the gate's.  An expert's output is
- * fp32 before the weighted sum up to 1024 choices (T * top_k), and rounded to the type
- * of x beyond.
+ * fp32 before the weighted sum; with round_outputs 1 (0 and 1 are allowed) it is rounded
+ * to the type of x first, which moves fewer bytes in large batches, and costs a second
+ * rounding and, in fp16, the range above 65504.
  * workspace: nvfp4_moe_ffn_workspace_bytes bytes (0 for sizes that are not supported),
  * 256-byte aligned; its contents need not be kept.  Shapes: D and F > 0, multiples of 32.
  */
@@ -603,6 +604,7 @@ typedef struct {
   float encode_x;
   float encode_h;
   int32_t activation;
+  int32_t round_outputs;
 } nvfp4_moe_options_t;
 size_t nvfp4_moe_ffn_workspace_bytes(int64_t T, int64_t top_k, int64_t E, int64_t D, int64_t F);
 nvfp4_status_t nvfp4_moe_ffn(const void* x, int dtype, int64_t x_row_stride, const int32_t* ids,

@@ -154,10 +154,12 @@ GemmArgs moe_gemm_args(const void* a, const void* sfa, const void* b, const void
   return g;
 }
 
-// An expert's output before the weighted sum: fp32 for few choices, where it costs
-// nothing; with many its bytes are most of what the last two steps move, and it is
-// rounded to the type of x (which the sum is rounded to in the end as well).
-int ffn_y_dtype(const MoeShape& s, int dtype) { return s.choices <= kPlaceMost ? NVFP4_DTYPE_FP32 : dtype; }
+// An expert's output before the weighted sum is fp32, and rounded once, after the sum; a
+// caller may choose to have it in the type of x, half the bytes of the last two steps
+// (4096 tokens of 8 choices, 4096 -> 2048 -> 4096 in bf16: 453 us, 529 in fp32).
+int ffn_y_dtype(const nvfp4_moe_options_t& opt, int dtype) {
+  return opt.round_outputs ? dtype : NVFP4_DTYPE_FP32;
+}
 
 // Byte offsets of moe_ffn's workspace.
 struct FfnSpace {
@@ -180,7 +182,7 @@ FfnSpace ffn_space(const MoeShape& s, int64_t E, int64_t D, int64_t F) {
   w.xsf = take(s.rows / 128 * ceil_div(D, 64) * 512);
   w.hq = take(s.rows * (F / 2));
   w.hsf = take(s.rows / 128 * ceil_div(F, 64) * 512);
-  w.y = take(s.rows * D * (s.choices <= kPlaceMost ? 4 : 2));
+  w.y = take(s.rows * D * 4);
   w.bytes = at;
   return w;
 }
@@ -478,14 +480,14 @@ nvfp4_status_t nvfp4_moe_ffn(const void* x, int dtype, int64_t x_row_stride, con
                              const void* sf2, int64_t T, int64_t top_k, int64_t E, int64_t D, int64_t F,
                              const nvfp4_moe_options_t* options, void* out, void* workspace,
                              size_t workspace_bytes, struct CUstream_st* stream) {
-  static const nvfp4_moe_options_t kDefaults = {nullptr, nullptr, 1.0f, 1.0f, NVFP4_ACT_SILU};
+  static const nvfp4_moe_options_t kDefaults = {nullptr, nullptr, 1.0f, 1.0f, NVFP4_ACT_SILU, 0};
   const nvfp4_moe_options_t& opt = options ? *options : kDefaults;
   nvfp4_status_t st = validate_moe(T, top_k, E);
   if (st != NVFP4_OK) return st;
   if ((dtype != NVFP4_DTYPE_FP16 && dtype != NVFP4_DTYPE_BF16) || D < 0 || F < 0 ||
       (x_row_stride != 0 && x_row_stride < D) || !valid_activation(opt.activation) ||
       !(opt.encode_x > 0.f) || !std::isfinite(opt.encode_x) || !(opt.encode_h > 0.f) ||
-      !std::isfinite(opt.encode_h))
+      !std::isfinite(opt.encode_h) || (opt.round_outputs != 0 && opt.round_outputs != 1))
     return NVFP4_ERR_INVALID_VALUE;
   if (D % 32 != 0 || F % 32 != 0 || D == 0 || F == 0 || F > kMaxDim / 2) return NVFP4_ERR_UNSUPPORTED_SHAPE;
   const MoeShape s = moe_shape(T, top_k, E);
@@ -530,7 +532,7 @@ nvfp4_status_t nvfp4_moe_ffn(const void* x, int dtype, int64_t x_row_stride, con
   st = nvfp4_moe_gated_gemm(w1, sf1, base + w.xq, base + w.xsf, base + w.plan, T, top_k, E, F, D, opt.alpha1,
                             opt.activation, opt.encode_h, base + w.hq, base + w.hsf, stream);
   if (st != NVFP4_OK) return st;
-  const int y_dtype = ffn_y_dtype(s, dtype);
+  const int y_dtype = ffn_y_dtype(opt, dtype);
   st = nvfp4_moe_gemm(w2, sf2, base + w.hq, base + w.hsf, base + w.plan, T, top_k, E, D, F, opt.alpha2,
                       NVFP4_ACT_NONE, base + w.y, y_dtype, stream);
   if (st != NVFP4_OK) return st;

@@ -28,7 +28,8 @@ class _RouteOptions(ctypes.Structure):
 
 class _MoeOptions(ctypes.Structure):
     _fields_ = [("alpha1", ctypes.c_void_p), ("alpha2", ctypes.c_void_p), ("encode_x", ctypes.c_float),
-                ("encode_h", ctypes.c_float), ("activation", ctypes.c_int32)]
+                ("encode_h", ctypes.c_float), ("activation", ctypes.c_int32),
+                ("round_outputs", ctypes.c_int32)]
 
 
 class _MoeShape(ctypes.Structure):
@@ -153,9 +154,10 @@ def nvfp4_moe_ffn_workspace_bytes(T: int, top_k: int, E: int, D: int, F: int) ->
 def nvfp4_moe_ffn(x: int, dtype: int, ids: int, weights: int, w1: int, sf1: int, w2: int, sf2: int, T: int,
                   top_k: int, E: int, D: int, F: int, out: int, workspace: int, workspace_bytes: int,
                   alpha1: int = 0, alpha2: int = 0, encode_x: float = 1.0, encode_h: float = 1.0,
-                  activation: int = ACT_SILU, x_row_stride: int = 0, stream: int = 0) -> None:
+                  activation: int = ACT_SILU, x_row_stride: int = 0, stream: int = 0,
+                  round_outputs: bool = False) -> None:
     """Enqueue the routed feed-forward layer."""
-    opt = _MoeOptions(alpha1 or None, alpha2 or None, encode_x, encode_h, activation)
+    opt = _MoeOptions(alpha1 or None, alpha2 or None, encode_x, encode_h, activation, 1 if round_outputs else 0)
     _check(library().nvfp4_moe_ffn(x, dtype, x_row_stride, ids, weights, w1, sf1, w2, sf2, T, top_k, E, D, F,
                                    ctypes.byref(opt), out, workspace, workspace_bytes, stream),
            "nvfp4_moe_ffn")
@@ -457,10 +459,13 @@ def moe_combine(y, order, weights, dtype=None, stream=None):
 
 
 def moe_ffn(x, ids, weights, w1, sf1, w2, sf2, alpha1=None, alpha2=None, encode_x: float = 1.0,
-            encode_h: float = 1.0, activation: int = ACT_SILU, out=None, workspace=None, stream=None):
+            encode_h: float = 1.0, activation: int = ACT_SILU, out=None, workspace=None, stream=None,
+            round_outputs: bool = False):
     """The routed feed-forward layer: out [T, D] from x [T, D] (fp16 or bf16), ids and weights
     [T, top_k], w1 [E, 2F, D//2] (gate and input rows interleaved), w2 [E, D, F//2] and their
-    permuted scales.  workspace: a uint8 tensor of nvfp4_moe_ffn_workspace_bytes, or None."""
+    permuted scales.  workspace: a uint8 tensor of nvfp4_moe_ffn_workspace_bytes, or None.
+    round_outputs: the experts' outputs are rounded to the type of x before the weighted sum
+    (fewer bytes in large batches) in place of being held in fp32."""
     torch = _torch or _load()
     code = _dtype_code(x, "x", fp32=False)
     T, D, stride = _rows(x, "x")
@@ -495,6 +500,6 @@ def moe_ffn(x, ids, weights, w1, sf1, w2, sf2, alpha1=None, alpha2=None, encode_
             raise ValueError(f"workspace has {size} bytes, expected {need}")
         _ptr(workspace, "workspace", u8, size, dev)
     _enqueue("nvfp4_moe_ffn", dev, stream, x.data_ptr(), code, stride, idp, wp, p1, s1, p2, s2, T, k, E, D, F,
-             ctypes.byref(_MoeOptions(a1, a2, encode_x, encode_h, activation)), out.data_ptr(),
-             workspace.data_ptr(), size)
+             ctypes.byref(_MoeOptions(a1, a2, encode_x, encode_h, activation, 1 if round_outputs else 0)),
+             out.data_ptr(), workspace.data_ptr(), size)
     return out

@@ -12,6 +12,16 @@ def pytest_configure(config):
     config.addinivalue_line("markers", "gpu: needs a CUDA GPU (sm_103a) and the built library")
 
 
+# These expect the experts' outputs of more than 1024 choices in the type of x before their
+# weighted sum without having asked for it; moe_ffn holds them in fp32 unless the caller says
+# otherwise, so they do not pass.  They run after everything else, which `-x` then still runs.
+ROUNDED_UNASKED = tuple(f"test_moe_ffn_is_its_steps_and_near_the_formula[1500-2-7-128-64-{t}]" for t in ("fp16", "bf16"))
+
+
+def pytest_collection_modifyitems(items):
+    items.sort(key=lambda item: item.name in ROUNDED_UNASKED)
+
+
 @pytest.fixture(scope="session")
 def golden_dir():
     return os.path.join(ROOT, "tests", "golden")
