@@ -127,15 +127,17 @@ struct Turned<float> {
   }
 };
 
-// y / (1 + exp(-x)) to a few fp32 ulps: the hardware's base-2 exponential of x log2(e),
-// whose product's rounding is put back, and its fast division.
+// y / (1 + exp(-x)) to (16 + |x| / 4) 2^-24 of itself and 2^-119: the hardware's base-2
+// exponential of x log2(e), whose product's rounding is put back (the constant's is not: the
+// |x| / 4), and its fast division, which gives 0 for divisors above 2^126.
 __device__ __forceinline__ float times_sigmoid(float y, float x) {
   constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
   const float t = -x * kLog2e;
-  const float rest = fmaf(-x, kLog2e, -t);  // exact
+  const float rest = fmaf(-x, kLog2e, -t);  // exact (not finite where t is not)
   float e;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
-  if (t < 127.f) e = fmaf(e, rest * kLn2, e);  // (beyond, e may be infinite already)
+  // (beyond, e is 0 or may be infinite already: large x give y, large -x give 0)
+  if (fabsf(t) < 127.f) e = fmaf(e, rest * kLn2, e);
   return __fdividef(y, 1.0f + e);
 }
 

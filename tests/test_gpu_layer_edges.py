@@ -1,5 +1,7 @@
 """The layer operators where a result can leave a type's range or be rounded once too often, on
 the GPU, against formulas in 64 bits."""
+import ctypes
+
 import numpy as np
 import pytest
 
@@ -8,7 +10,7 @@ torch = pytest.importorskip("torch")
 import nvfp4_block_scaled_gemv_gb300 as nv  # noqa: E402
 from nvfp4_block_scaled_gemv_gb300 import build as libbuild  # noqa: E402
 from oracle import layer as ol  # noqa: E402
-from test_gpu_layer import DEV, DT, EPS, TINY, any_matrix, choices, gpu, host, values  # noqa: E402
+from test_gpu_layer import DEV, DT, EPS, TINY, any_matrix, choices, gpu, host, whole_matrix  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -73,3 +75,116 @@ def test_experts_outputs_are_rounded_first_when_the_caller_says_so(T, k, dtype):
     order, y = outputs(x, ids, m, a1, a1, DT[dtype])
     out = nv.moe_ffn(x, ids, w, *m, alpha1=a1, alpha2=a1, encode_h=8.0, round_outputs=True)
     assert torch.equal(out, nv.moe_combine(y, order, w, dtype=DT[dtype]))
+
+
+# ---------------------------------------------------------------------------
+# the product's epilogue
+# ---------------------------------------------------------------------------
+
+U = 2.0 ** -24
+PLAIN, RELU, SILU, GELU_TANH, GELU_ERF = range(5)
+# finite values that overflow on the way (a cube, a product with log2 e) and their neighbours,
+# the type's ends, and what is not finite
+EXTREMES = [s * v for v in (1e4, 1e9, 1e12, 1.4e13, 1.6e13, 1e20, 1e30, 2.3e38, 2.5e38, 3.4028234e38, np.inf)
+            for s in (1, -1)] + [np.nan, 0.0, -0.0, 87.0, -87.0, -87.5, -88.5, -89.0, -104.0]
+
+
+def chosen(N, M, K, L, act):
+    """(rows of b per tile, K split) of a call, by the library's own choice."""
+    fn = nv.library()["_ZN5nvfp411choose_gemmEllllib"]  # choose_gemm(M, N, K, L, sms, activation)
+    fn.argtypes, fn.restype = [ctypes.c_int64] * 4 + [ctypes.c_int, ctypes.c_bool], ctypes.c_uint64
+    both = fn(M, N, K, L, torch.cuda.get_device_properties(0).multi_processor_count, act > RELU)
+    return both & 0xFFFFFFFF, both >> 32
+
+
+def formula(y, act):
+    """(act(y) in 64 bits, a bound of the fp32 evaluation's error)."""
+    y = y.double()
+    if act == SILU or act == GELU_TANH:
+        # a sigmoid of x: 16 units for the exponential, the sum and the quotient, |x| / 4 for log2 e,
+        # 6 |x| for the roundings of x, where it is a polynomial of y; the quotient's end
+        x = y if act == SILU else (8 / np.pi) ** 0.5 * (y + 0.044715 * y ** 3)
+        want = y / (1 + torch.exp(-x))
+        return want, (16 + (0.25 if act == SILU else 6.25) * x.abs().clamp(max=128)) * U * want.abs() + 2.0 ** -119
+    if act == GELU_ERF:  # 1 + erf: absolute to an ulp or two of 1
+        want = 0.5 * y * (1 + torch.erf(y / 2 ** 0.5))
+        return want, 4 * U * (y.abs().clamp(max=1e30) + want.abs())
+    if act == RELU:
+        return torch.where(y > 0, y, torch.where(y.isnan(), y, 0.0)), 0 * y.nan_to_num(0, 0, 0)
+    return y, 0 * y.nan_to_num(0, 0, 0)
+
+
+def assert_epilogue(c, y, act, dtype):
+    want, tol = formula(y, act)
+    top = torch.finfo(DT[dtype]).max
+    # values that round to an infinity of the type, and those that may do either
+    over = want.abs() > top * (1 + EPS[dtype]) + tol
+    edge = ~over & (want.abs() > top)
+    got = c.double()
+    assert torch.equal(got.isnan(), want.isnan())
+    inf = float("inf")
+    assert torch.equal(got[over], torch.where(want[over] > 0, inf, -inf))
+    ok = (got - want).abs() <= tol + EPS[dtype] * want.abs() + TINY[dtype]
+    ok |= over | want.isnan() | (edge & ((got.abs() == inf) | (got.abs() >= top)))
+    assert ok.all(), (y[~ok][:4], c[~ok][:4], want[~ok][:4])
+
+
+def exact_product(N, M, K, L, alpha, bias, act, dtype):
+    """(c, alpha * sum + bias in fp32) of whole-number matrices."""
+    rng = np.random.default_rng(N + M + K)
+    a, sfa = whole_matrix(rng, L, M, K)
+    b, sfb = whole_matrix(rng, L, N, K)
+    at, bt = (torch.from_numpy(ol.matrix(*m)).float().to(DEV) for m in ((a, sfa), (b, sfb)))
+    # whole numbers below 2^24: exact in any order; alpha is a power of two
+    sums = torch.bmm(bt, at.transpose(1, 2)) * alpha
+    y = (sums.double() + bias.double().unsqueeze(1)).float()
+    t = [gpu(a), gpu(b), gpu(ol.atoms(sfa)), gpu(ol.atoms(sfb))]
+    return nv.gemm(*t, alpha=alpha, bias=bias, activation=act, dtype=DT[dtype]), y
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16", "fp32"])
+@pytest.mark.parametrize("act", range(5))
+def test_activations_of_extreme_values(act, dtype):
+    """Through the bias: the one-SM kernel, the pair kernel and the product without K."""
+    for N, M, K, L, tile in ((40, 140, 64, 2, 64), (257, 4096, 4096, 2, 256)):
+        assert chosen(N, M, K, L, act)[0] == tile
+        bias = torch.tensor(EXTREMES, dtype=torch.float32, device=DEV).repeat(-(-L * M // len(EXTREMES)))
+        bias = bias[:L * M].view(L, M)
+        assert_epilogue(*exact_product(N, M, K, L, 2.0 ** -10, bias, act, dtype), act, dtype)
+    e = torch.empty(0, dtype=torch.uint8, device=DEV)
+    y = torch.tensor(EXTREMES, dtype=torch.float32, device=DEV).view(1, -1)
+    c = nv.gemm(e.view(1, y.numel(), 0), e.view(1, 1, 0), e, e, bias=y, activation=act, dtype=DT[dtype])[0]
+    want = formula(y, act)[0].to(DT[dtype])
+    big = y.abs() >= 1e4
+    assert torch.equal(c[big].nan_to_num(-7), want[big].nan_to_num(-7))
+
+
+@pytest.mark.parametrize("act", [nv.ACT_SILU, nv.ACT_GELU_TANH])
+@pytest.mark.parametrize("T,k,E,F,K", [(33, 3, 8, 96, 288), (600, 2, 3, 64, 96)])
+def test_gated_product_of_large_gates(T, k, E, F, K, act):
+    """Gates of 2^36 times whole numbers: the sigmoid is 0 or 1, and the scaled h is within the
+    scales' range."""
+    rng = np.random.default_rng(T)
+    ids = choices(rng, T, k, E)
+    order = nv.moe_sort(gpu(ids), E)
+    x = rng.choice([0, 1, 2, 3, 4, 6], (T, K)) * rng.choice([-1.0, 1.0], (T, K))
+    x[:, ::16] = 6
+    xq, xs = nv.quantize_rows(torch.from_numpy(x).to(DEV).bfloat16(), order)
+    a, sfa = whole_matrix(rng, E, 2 * F, K)
+    alpha, encode = 2.0 ** 36, 2.0 ** -88
+    q, sf = nv.moe_gated_gemm(gpu(a), gpu(ol.atoms(sfa)), xq, xs, order, alpha=torch.full((E,), alpha, device=DEV),
+                              activation=act, encode_scale=encode)
+    rows, w = host(order["rows"]), ol.matrix(a, sfa)
+    sf = ol.from_atoms(host(sf), order["row_capacity"], -(-F // 64) * 4)[0][:, :F // 16]
+    q = host(q)
+    for t in range(T):
+        for j in range(k):
+            u = w[ids[t, j]] @ x[t]
+            # a gate that is 0 gives 0; a quotient by 1 is exact to two ulps
+            h = np.maximum(u[0::2], 0) * u[1::2] * (alpha * alpha * encode)
+            lo, hi = (ol.quantize_values(h[None] * (1 + s * 2.0 ** -21)) for s in (-1, 1))
+            same = lo[1][0] == hi[1][0]
+            assert (sf[rows[t, j]] != 0x7F).all() and np.array_equal(sf[rows[t, j]][same], hi[1][0][same])
+            cl, ch, got = (ol.e2m1_values(v).reshape(-1, 16) for v in (lo[0][0], hi[0][0], q[rows[t, j]]))
+            sure = same[:, None] & (cl == ch)
+            assert np.array_equal(got[sure], ch[sure]) and sure.mean() > 0.5
