@@ -20,6 +20,34 @@ constexpr uint32_t kTransposeBytes = kUnit * kTransposePitch * 4;  // per epilog
 // of 32-bit values, four of 16-bit ones).
 constexpr uint32_t kStageBytesC = 2 * kUnit * 128 * 4;
 
+// An SM's 512 columns of tensor memory are never asked for beyond their number: with
+// clusters on both sides, each could hold on one SM what the other waits for on a second, and
+// neither that wait (tcgen05.alloc) nor a cluster barrier gives up.  Within a stream the wait
+// for the preceding kernels comes before the allocation; between streams shared memory decides
+// which CTAs share an SM (it has 228 KB, 1 KB of it reserved per CTA).  A product that takes
+// 512 columns asks for enough that no CTA of the tensor-core GEMV fits beside it; one that takes
+// 256 leaves room for 256 of theirs at most.  (190 KB for all of them made 53 tokens through 8
+// of 64 experts 125 us, 120 with this rule.)
+constexpr uint32_t kSmSmem = 228 * 1024, kCtaReserve = 1024;
+// What a tensor-core GEMV's CTA needs at least, with its columns: stages of an A tile (128 x
+// 128 bytes), a B tile (16 x 128) and eight scale atoms, and 2 KB beside them.
+constexpr uint32_t gemv_smem(int stages) { return (uint32_t)stages * (128 * 128 + 16 * 128 + 8 * 512) + 2048; }
+constexpr uint32_t gemv_columns(int stages) { return stages == 2 ? 128 : 256; }
+// The columns that can be asked for on an SM with a product of this footprint, at most.
+constexpr uint32_t most_columns(uint32_t smem, uint32_t columns, uint32_t sm_smem = kSmSmem,
+                                uint32_t reserve = kCtaReserve) {
+  uint32_t most = columns;
+  for (uint32_t n2 = 0; n2 <= 4; ++n2)
+    for (uint32_t n4 = 0; n4 <= 2; ++n4)
+      for (uint32_t more = 0; more <= 1; ++more) {  // (another product, taken as no larger)
+        const uint32_t bytes = (1 + more) * (smem + reserve) + n2 * (gemv_smem(2) + reserve) + n4 * (gemv_smem(4) + reserve);
+        const uint32_t all = (1 + more) * columns + n2 * gemv_columns(2) + n4 * gemv_columns(4);
+        if (bytes <= sm_smem && all > most) most = all;
+      }
+  return most;
+}
+constexpr uint32_t kAloneSmem = 183 * 1024;  // for products of 512 columns, at least
+
 enum Epilogue { kStore = 0, kGatedQuantize = 1 };
 
 struct GemmParams {
@@ -443,5 +471,6 @@ __device__ __forceinline__ void place_at(Place& w, const GemmParams& p, const Ti
 cudaError_t launch_gemm_pair(const gemm::GemmParams& p, int epi, bool grouped, int64_t max_tiles, int sms,
                              cudaStream_t stream);
 cudaError_t gemm_pair_wait_timeouts(int reset, int* out);
+Footprint pair_footprint(int epi);
 
 }  // namespace nvfp4

@@ -63,6 +63,8 @@ static_assert(kSecondCol + kBN <= kSfCol && kSfCol + 3 * kSfCols <= 512, "TMEM c
 constexpr uint32_t pair_smem_bytes(int epi) {
   return kStages * kStageBytes + 1024u + (epi == kGatedQuantize ? 8u * kTransposeBytes : 2u * kStageBytesC);
 }
+static_assert(most_columns(pair_smem_bytes(kStore), 512) == 512 && most_columns(pair_smem_bytes(kGatedQuantize), 512) == 512,
+              "tensor memory of an SM");
 
 // M = 256 over the pair, N = n (see tc::mxf4nvf4_idesc for the fields).
 __device__ __forceinline__ uint32_t pair_idesc(uint32_t n) {
@@ -418,6 +420,8 @@ cudaError_t launch_gemm_pair(const GemmParams& p, int epi, bool grouped, int64_t
                                  : launch_variant<kStore, true>(p, max_tiles, sms, stream);
   return launch_variant<kStore, false>(p, max_tiles, sms, stream);
 }
+
+Footprint pair_footprint(int epi) { return {pair_smem_bytes(epi), 512}; }
 
 cudaError_t gemm_pair_wait_timeouts(int reset, int* out) {
   cudaError_t err = cudaMemcpyFromSymbol(out, g_gemm_pair_timeouts, sizeof(int));

@@ -32,6 +32,7 @@
 // Every wait on an mbarrier gives up after tc::kWaitNs, counts a timeout in a
 // device word the host can read, and the thread then skips its remaining work.
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 #include <cstring>
 
@@ -49,10 +50,21 @@ constexpr int kGemmThreads = 192;
 
 __host__ __device__ constexpr uint32_t stage_bytes(int bn) { return kABytes + (uint32_t)bn * 128u + 2 * kAtoms; }
 __host__ __device__ constexpr int stages_for(int bn) { return bn == 128 ? 5 : 6; }
-__host__ __device__ constexpr uint32_t gemm_smem_bytes(int bn, int epi) {
-  return (uint32_t)stages_for(bn) * stage_bytes(bn) + 1024u +
-         (epi == kGatedQuantize ? 4u * kTransposeBytes : 0u);
+constexpr int kAcc = 2;  // accumulators in tensor memory
+// Accumulators, then 16 columns of either operand's scales per stage (allocated as a power of two).
+__host__ __device__ constexpr uint32_t columns_for(int bn) {
+  return (uint32_t)(kAcc * bn + 32 * stages_for(bn)) <= 256u ? 256u : 512u;
 }
+constexpr uint32_t gemm_smem_bytes(int bn, int epi) {
+  const uint32_t bytes = (uint32_t)stages_for(bn) * stage_bytes(bn) + 1024u +
+                         (epi == kGatedQuantize ? 4u * kTransposeBytes : 0u);
+  return columns_for(bn) == 512 && bytes < kAloneSmem ? kAloneSmem : bytes;
+}
+constexpr bool columns_fit(int bn) {
+  return most_columns(gemm_smem_bytes(bn, kStore), columns_for(bn)) <= 512 &&
+         most_columns(gemm_smem_bytes(bn, kGatedQuantize), columns_for(bn)) <= 512;
+}
+static_assert(columns_fit(16) && columns_fit(32) && columns_fit(64) && columns_fit(128), "tensor memory of an SM");
 
 template <typename T>
 __device__ __forceinline__ void store_one(const GemmParams& p, int64_t idx, float v) {
@@ -76,10 +88,10 @@ __device__ __forceinline__ void add_remote(uint32_t saddr, uint32_t rank, float 
 template <int BN, int EPI, bool GROUPED, bool SPLIT>
 __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_constant__ GemmParams p) {
   constexpr int S = stages_for(BN);
-  constexpr int kAcc = 2;  // accumulators in tensor memory
   constexpr uint32_t kSfaCol = kAcc * BN;
   constexpr uint32_t kSfbCol = kSfaCol + 16 * S;
-  static_assert(kSfbCol + 16 * S <= 512, "TMEM columns");
+  constexpr uint32_t kColumns = columns_for(BN);
+  static_assert(kSfbCol + 16 * S <= kColumns, "TMEM columns");
   extern __shared__ uint8_t gemm_smem[];
   __shared__ __align__(8) uint64_t bars[2 * S + 2 * kAcc + 1];
   __shared__ uint32_t tmem_slot;
@@ -114,7 +126,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
   // that this one waits for may not have taken its own yet), and the next one
   // may start only after that
   pdl_wait();
-  if (warp == 1) tc::alloc(smem_u32(&tmem_slot), 512);
+  if (warp == 1) tc::alloc(smem_u32(&tmem_slot), kColumns);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -274,7 +286,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
   __syncthreads();
   if (warp == 1) {
     tc::fence_after();
-    tc::dealloc(tmem, 512);
+    tc::dealloc(tmem, kColumns);
   }
 }
 
@@ -322,6 +334,31 @@ cudaError_t launch_for(int bn, const GemmParams& p, int64_t max_tiles, int ks, i
     case 256: return launch_gemm_pair(p, EPI, GROUPED, max_tiles, sms, stream);
     default: return cudaErrorInvalidValue;
   }
+}
+
+// The assertions on most_columns, on the current device; asked once per device.
+cudaError_t columns_fit_here(bool* fit) {
+  constexpr int kMaxDevices = 128;
+  static std::atomic<int> cached[kMaxDevices];  // 0 unknown, 1 they fit, 2 not
+  int dev = 0, smem = 0, reserve = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  int c = cached[dev].load(std::memory_order_relaxed);
+  if (c == 0) {
+    if ((err = cudaDeviceGetAttribute(&smem, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev)) != cudaSuccess ||
+        (err = cudaDeviceGetAttribute(&reserve, cudaDevAttrReservedSharedMemoryPerBlock, dev)) != cudaSuccess)
+      return err;
+    c = 1;
+    for (int rows = 16; rows <= 256; rows *= 2)
+      for (const bool gated : {false, true}) {
+        const Footprint f = product_footprint(rows, gated);
+        if (most_columns(f.smem, f.columns, (uint32_t)smem, (uint32_t)reserve) > 512) c = 2;
+      }
+    cached[dev].store(c, std::memory_order_relaxed);
+  }
+  *fit = c == 1;
+  return cudaSuccess;
 }
 
 bool encode_rows(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, const uint8_t* base,
@@ -443,6 +480,10 @@ cudaError_t launch_gemm(const GemmArgs& g, int sms, cudaStream_t stream) {
     return launch_pdl(gemm_no_k_kernel, dim3((unsigned)(ctas < 16 * sms ? ctas : 16 * sms)), dim3(256),
                       0, stream, p);
   }
+  bool fit = false;
+  const cudaError_t err = columns_fit_here(&fit);
+  if (err != cudaSuccess) return err;
+  if (!fit) return cudaErrorNotSupported;
   const GemmChoice choice = grouped ? GemmChoice{g.tile_rows, 1}
                                     : choose_gemm(g.M, g.N, g.K, g.G, sms, g.activation > 1);  // (ReLU costs nothing)
   const int bn = choice.bn;
@@ -483,6 +524,11 @@ cudaError_t launch_gemm(const GemmArgs& g, int sms, cudaStream_t stream) {
   p.tiles_n = (int32_t)((g.N + bn - 1) / bn);
   p.total = (int32_t)(g.G * p.tiles_n * p.tiles_m);
   return launch_for<kStore, false>(bn, p, p.total, choice.ks, sms, stream);
+}
+
+Footprint product_footprint(int tile_rows, bool gated) {
+  const int epi = gated ? kGatedQuantize : kStore;
+  return tile_rows == 256 ? pair_footprint(epi) : Footprint{gemm_smem_bytes(tile_rows, epi), columns_for(tile_rows)};
 }
 
 cudaError_t gemm_wait_timeouts(int reset, int* out) {

@@ -119,6 +119,11 @@ struct GemmArgs {
 };
 cudaError_t launch_gemm(const GemmArgs& g, int sms, cudaStream_t stream);
 cudaError_t gemm_wait_timeouts(int reset, int* out);
+// What a product's CTA takes of its SM (see gemm::most_columns).
+struct Footprint {
+  uint32_t smem, columns;  // dynamic shared memory; tensor memory
+};
+Footprint product_footprint(int tile_rows, bool gated);
 // The dense product's rows of b per tile and CTAs that split a tile's K.
 struct GemmChoice {
   int bn, ks;

@@ -32,3 +32,29 @@ def test_moe_ffn_workspace_holds_32_bit_outputs(lib):
         need = nv.nvfp4_moe_ffn_workspace_bytes(T, k, E, D, 64)
         assert need >= 4 * T * k * D
         assert moe_ffn(lib, T, k, E, D, size=need - 1) == nv.ERR_INVALID_VALUE
+
+
+SM_SMEM, RESERVED = 228 * 1024, 1024  # shared memory of an SM, and what every CTA takes beside its own
+
+
+def footprints(lib):
+    """{(rows of a product's tile, gated): (shared memory, columns of tensor memory)}."""
+    fn = lib["_ZN5nvfp417product_footprintEib"]
+    fn.argtypes, fn.restype = [ctypes.c_int, ctypes.c_bool], ctypes.c_uint64
+    both = {(rows, gated): fn(rows, gated) for rows in (16, 32, 64, 128, 256) for gated in (False, True)}
+    return {key: (v & 0xFFFFFFFF, v >> 32) for key, v in both.items()}
+
+
+def test_tensor_memory_is_never_asked_for_beyond_an_sm(lib):
+    """Whatever CTAs of products and of the tensor-core GEMV share an SM between streams: one that
+    waited for columns there could, in a cluster, hold up another SM's for ever."""
+    # the GEMV's stages: an A tile of 128 x 128 bytes, a B tile of 16 x 128 and eight scale atoms
+    kinds = list(footprints(lib).values()) + [(s * (128 * 128 + 16 * 128 + 8 * 512), c) for s, c in ((2, 128), (4, 256))]
+    assert all(smem <= 227 * 1024 for smem, _ in kinds)
+    for first in footprints(lib).values():
+        packed = [(first,)]
+        while packed:
+            ctas = packed.pop()
+            assert sum(columns for _, columns in ctas) <= 512, ctas
+            room = SM_SMEM - sum(smem + RESERVED for smem, _ in ctas)
+            packed += [ctas + (k,) for k in kinds if k[0] + RESERVED <= room]
