@@ -81,6 +81,10 @@ __device__ int g_bd_timeouts;
 namespace {
 
 constexpr int kBdThreads = kBlockDotThreads;  // 6 warps
+// A CTA asks for at least this much shared memory (it has its SM to itself anyway), so that
+// no CTA of the other kernels that take tensor memory fits beside it between streams: with
+// four of the tensor-core GEMV's there, its 256 columns would be asked for beyond the SM's 512.
+constexpr size_t kBdAloneSmem = 183 * 1024;
 constexpr int kBdD = 4;                       // accumulator buffers of 16*CB TMEM columns
 constexpr uint32_t kBdTmemCols = 256;
 // The constant scales: 4 columns of unit scales for A, then 4 x 4 columns of
@@ -491,7 +495,8 @@ int blockdot_slot_rows(int64_t M, int64_t L, bool permuted, int64_t ctas) {
 }
 
 size_t blockdot_smem_bytes(bool permuted, int cb, int slot_rows, int stages) {
-  return (size_t)bd_layout(permuted, cb, slot_rows, stages).total + 1024u;  // + alignment slack
+  const size_t bytes = (size_t)bd_layout(permuted, cb, slot_rows, stages).total + 1024u;  // + alignment slack
+  return bytes < kBdAloneSmem ? kBdAloneSmem : bytes;
 }
 
 int blockdot_max_stages(bool permuted, int cb, int slot_rows, size_t smem_per_cta) {

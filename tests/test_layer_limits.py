@@ -45,13 +45,25 @@ def footprints(lib):
     return {key: (v & 0xFFFFFFFF, v >> 32) for key, v in both.items()}
 
 
+def blockdot_footprint(lib):
+    """The least shared memory of the block-dot kernel's CTA, and its columns."""
+    fn = lib["_ZN5nvfp419blockdot_smem_bytesEbiii"]
+    fn.argtypes, fn.restype = [ctypes.c_bool] + [ctypes.c_int] * 3, ctypes.c_size_t
+    return min(fn(permuted, blocks, 8, stages) for permuted in (False, True) for blocks in (1, 2)
+               for stages in (1, 2, 32)), 256
+
+
 def test_tensor_memory_is_never_asked_for_beyond_an_sm(lib):
-    """Whatever CTAs of products and of the tensor-core GEMV share an SM between streams: one that
-    waited for columns there could, in a cluster, hold up another SM's for ever."""
-    # the GEMV's stages: an A tile of 128 x 128 bytes, a B tile of 16 x 128 and eight scale atoms
-    kinds = list(footprints(lib).values()) + [(s * (128 * 128 + 16 * 128 + 8 * 512), c) for s, c in ((2, 128), (4, 256))]
+    """Whatever CTAs of products, of the tensor-core GEMV and of the block-dot kernel share an SM
+    between streams: one that waited for columns there could, in a cluster, hold up another
+    SM's for ever."""
+    # the GEMV's stages: an A tile of 128 x 128 bytes, a B tile of 16 x 128 and eight scale atoms;
+    # and 2 KB (the ranks' sums of one vector, the alignment)
+    gemv = [(s * (128 * 128 + 16 * 128 + 8 * 512) + 2048, c) for s, c in ((2, 128), (4, 256))]
+    kinds = list(footprints(lib).values()) + gemv
+    kinds.append(blockdot_footprint(lib))
     assert all(smem <= 227 * 1024 for smem, _ in kinds)
-    for first in footprints(lib).values():
+    for first in kinds:
         packed = [(first,)]
         while packed:
             ctas = packed.pop()
