@@ -244,7 +244,9 @@ def nvfp4_gemv_plan(M: int, K: int, L: int, sf_layout: int = SF_PLAIN, num_sms: 
 
 
 # ---------------------------------------------------------------------------
-# torch conveniences: argument marshalling only
+# torch conveniences: argument marshalling only.  With ``stream=`` a call runs on that
+# stream: what it allocates is safe there and on the current stream; ordering the two
+# streams, and keeping the arguments until the call has run, is the caller's part.
 # ---------------------------------------------------------------------------
 
 def _stream_handle(stream, device) -> int:
@@ -253,6 +255,26 @@ def _stream_handle(stream, device) -> int:
     if stream is None:
         stream = torch.cuda.current_stream(device)
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _empty(shape, dtype, device, stream):
+    """An uninitialised tensor for a call on ``stream`` (None: the current one) to write.  Memory
+    belongs to the stream that it is allocated on: allocated on the current one for a call on
+    another, it could be written while work queued before still uses it, and be handed out
+    again, once dropped, while the call is still to run.  So it is the call's stream's, and the
+    current stream, where the result is likely used, is recorded as a user."""
+    import torch
+
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream) > 1
+                  else torch.cuda.default_stream(device))
+    current = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(current)
+    return t
 
 
 def _on_device(device):
@@ -299,7 +321,7 @@ def gemv(a, b, sfa, sfb, c=None, sf_layout: int = SF_PLAIN, stream=None):
         _need(sfa, "sfa", torch.uint8, nvfp4_permuted_scale_bytes(M, K, L), dev)
         _need(sfb, "sfb", torch.uint8, nvfp4_permuted_scale_bytes(1, K, L), dev)
     if c is None:
-        c = torch.empty((L, M), dtype=torch.float16, device=dev)
+        c = _empty((L, M), torch.float16, dev, stream)
     _need(c, "c", torch.float16, L * M, dev)
     with _on_device(dev):
         nvfp4_gemv(a.data_ptr(), b.data_ptr(), sfa.data_ptr(), sfb.data_ptr(), c.data_ptr(), M, K,
@@ -318,7 +340,7 @@ def repack_scales(src, dst=None, stream=None):
     _need(src, "src", torch.uint8, L * rows * blocks, src.device)
     n = nvfp4_permuted_scale_bytes(rows, K, L)
     if dst is None:
-        dst = torch.empty(n, dtype=torch.uint8, device=src.device)
+        dst = _empty(n, torch.uint8, src.device, stream)
     _need(dst, "dst", torch.uint8, n, src.device)
     with _on_device(src.device):
         nvfp4_repack_scales(src.data_ptr(), dst.data_ptr(), rows, K, L,

@@ -4,12 +4,17 @@ The same thin binding as the package's GEMV calls: ``nvfp4_*`` functions take
 device pointers as integers, the functions without the prefix take torch tensors,
 check them and allocate the outputs.  Every step of the computation runs in the
 library's CUDA kernels; ``include/nvfp4_gemv.h`` defines each call.
+
+``stream`` is a torch stream or a handle; None is the current one.  What a call on another
+stream allocates is safe there and on the current stream; ordering the two streams, and
+keeping the arguments until the call has run, is the caller's part.
 """
 from __future__ import annotations
 
 import ctypes
 
-from . import (ACT_NONE, ACT_SILU, SF_PERMUTED_128x4, SF_PLAIN, _check, _need, _stream_handle, library)
+from . import (ACT_NONE, ACT_SILU, SF_PERMUTED_128x4, SF_PLAIN, _check, _empty as _empty_for, _need, _stream_handle,
+               library)
 
 DTYPE_FP16, DTYPE_BF16, DTYPE_FP32 = 0, 1, 2
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
@@ -198,6 +203,12 @@ def _ptr(t, name, dtype, numel, device) -> int:
     return t.data_ptr()
 
 
+def _empty(shape, dtype, device, stream):
+    if stream is None:
+        return _torch.empty(shape, dtype=dtype, device=device)
+    return _empty_for(shape, dtype, device, stream)
+
+
 def _dtype_code(x, name, fp32=True) -> int:
     code = _codes.get(getattr(x, "dtype", x))
     if code is None or (code == DTYPE_FP32 and not fp32):
@@ -255,11 +266,11 @@ def quantize(x, encode_scale: float = 1.0, sf_layout: int = SF_PERMUTED_128x4, q
         raise ValueError(f"x has rows of {K} elements, expected a multiple of 16")
     n, dev, u8 = _scale_bytes(sf_layout, rows, K, L), x.device, torch.uint8
     if q is None:
-        q = torch.empty((rows, K // 2) if x.dim() == 2 else (L, rows, K // 2), dtype=u8, device=dev)
+        q = _empty((rows, K // 2) if x.dim() == 2 else (L, rows, K // 2), u8, dev, stream)
     else:
         _ptr(q, "q", u8, L * rows * (K // 2), dev)
     if sf is None:
-        sf = torch.empty(n, dtype=u8, device=dev)
+        sf = _empty(n, u8, dev, stream)
     else:
         _ptr(sf, "sf", u8, n, dev)
     _enqueue("nvfp4_quantize", dev, stream, x.data_ptr(), code, stride, rows, K, L, encode_scale, q.data_ptr(),
@@ -283,7 +294,7 @@ def dequantize(q, sf, scale: float = 1.0, dtype=None, sf_layout: int = SF_PERMUT
     qp = _ptr(q, "q", u8, L * rows * (K // 2), dev)
     sp = _ptr(sf, "sf", u8, _scale_bytes(sf_layout, rows, K, L), dev)
     if x is None:
-        x = torch.empty((rows, K) if len(shape) == 2 else (L, rows, K), dtype=dtype, device=dev)
+        x = _empty((rows, K) if len(shape) == 2 else (L, rows, K), dtype, dev, stream)
     else:
         _ptr(x, "x", dtype, L * rows * K, dev)
     _enqueue("nvfp4_dequantize", dev, stream, qp, sp, sf_layout, rows, K, L, scale, x.data_ptr(), code, 0)
@@ -323,7 +334,7 @@ def gemm(a, b, sfa, sfb, alpha: float = 1.0, bias=None, activation: int = ACT_NO
         dtype = torch.float16 if c is None else c.dtype
     code = _dtype_code(dtype, "dtype")
     if c is None:
-        c = torch.empty((L, N, M), dtype=dtype, device=dev)
+        c = _empty((L, N, M), dtype, dev, stream)
     else:
         _ptr(c, "c", dtype, L * N * M, dev)
     _enqueue("nvfp4_gemm", dev, stream, ap, bp, sap, sbp, c.data_ptr(), M, N, K, L,
@@ -339,8 +350,8 @@ def route(logits, top_k: int, score: int = SCORE_SOFTMAX, bias=None, groups: int
     T, E, stride = _rows(logits, "logits")
     dev = logits.device
     bias_p = None if bias is None else _ptr(bias, "bias", torch.float32, E, dev)
-    ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
-    weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+    ids = _empty((T, top_k), torch.int32, dev, stream)
+    weights = _empty((T, top_k), torch.float32, dev, stream)
     _enqueue("nvfp4_route", dev, stream, logits.data_ptr(), code, stride, T, E, top_k,
              ctypes.byref(_RouteOptions(score, bias_p, groups, top_groups, 1 if renormalize else 0, weight_scale)),
              ids.data_ptr(), weights.data_ptr())
@@ -356,9 +367,9 @@ def moe_sort(ids, E: int, stream=None) -> dict:
     (T, k), dev, i32 = ids.shape, ids.device, torch.int32
     p = _ptr(ids, "ids", i32, T * k, dev)
     shape = nvfp4_moe_shape(T, k, E)
-    out = {"rows": torch.empty((T, k), dtype=i32, device=dev), "counts": torch.empty(E, dtype=i32, device=dev),
-           "starts": torch.empty(E, dtype=i32, device=dev),
-           "plan": torch.empty(shape["plan_bytes"], dtype=torch.uint8, device=dev),
+    out = {"rows": _empty((T, k), i32, dev, stream), "counts": _empty(E, i32, dev, stream),
+           "starts": _empty(E, i32, dev, stream),
+           "plan": _empty(shape["plan_bytes"], torch.uint8, dev, stream),
            "row_capacity": shape["row_capacity"], "tile_rows": shape["tile_rows"], "experts": E}
     _enqueue("nvfp4_moe_sort", dev, stream, p, T, k, E, out["rows"].data_ptr(), out["counts"].data_ptr(),
              out["starts"].data_ptr(), out["plan"].data_ptr())
@@ -400,8 +411,8 @@ def quantize_rows(x, order, encode_scale: float = 1.0, stream=None):
     if K % 16:
         raise ValueError(f"x has rows of {K} elements, expected a multiple of 16")
     to = _ptr(order["rows"], "rows", torch.int32, T * k, dev)
-    q = torch.empty((rows, K // 2), dtype=torch.uint8, device=dev)
-    sf = torch.empty(_scale_bytes(SF_PERMUTED_128x4, rows, K, 1), dtype=torch.uint8, device=dev)
+    q = _empty((rows, K // 2), torch.uint8, dev, stream)
+    sf = _empty(_scale_bytes(SF_PERMUTED_128x4, rows, K, 1), torch.uint8, dev, stream)
     _enqueue("nvfp4_quantize", dev, stream, x.data_ptr(), code, stride, T, K, 1, encode_scale, q.data_ptr(),
              sf.data_ptr(), SF_PERMUTED_128x4, to, k, rows)
     return q, sf
@@ -415,7 +426,7 @@ def moe_gemm(a, sfa, b, sfb, order, alpha=None, activation: int = ACT_NONE, dtyp
     M, ap, sp, alpha_p = _need_experts(a, sfa, alpha, E, K, dev)
     dtype = dtype or torch.float16
     code = _dtype_code(dtype, "dtype")
-    c = torch.empty((rows, M), dtype=dtype, device=dev)
+    c = _empty((rows, M), dtype, dev, stream)
     _enqueue("nvfp4_moe_gemm", dev, stream, ap, sp, b.data_ptr(), sfb.data_ptr(), order["plan"].data_ptr(), T, k,
              E, M, K, alpha_p, activation, c.data_ptr(), code)
     return c
@@ -432,8 +443,8 @@ def moe_gated_gemm(a, sfa, b, sfb, order, alpha=None, activation: int = ACT_SILU
     if M % 64:
         raise ValueError(f"the weights have {M} rows, expected a multiple of 64")
     F = M // 2
-    q = torch.empty((rows, F // 2), dtype=torch.uint8, device=dev)
-    sf = torch.empty(_scale_bytes(SF_PERMUTED_128x4, rows, F, 1), dtype=torch.uint8, device=dev)
+    q = _empty((rows, F // 2), torch.uint8, dev, stream)
+    sf = _empty(_scale_bytes(SF_PERMUTED_128x4, rows, F, 1), torch.uint8, dev, stream)
     _enqueue("nvfp4_moe_gated_gemm", dev, stream, ap, sp, b.data_ptr(), sfb.data_ptr(), order["plan"].data_ptr(),
              T, k, E, F, K, alpha_p, activation, encode_scale, q.data_ptr(), sf.data_ptr())
     return q, sf
@@ -452,7 +463,7 @@ def moe_combine(y, order, weights, dtype=None, stream=None):
     M, dev = y.shape[1], y.device
     yp = _ptr(y, "y", y.dtype, order["row_capacity"] * M, dev)
     wp = _ptr(weights, "weights", torch.float32, T * k, dev)
-    out = torch.empty((T, M), dtype=dtype, device=dev)
+    out = _empty((T, M), dtype, dev, stream)
     _enqueue("nvfp4_moe_combine", dev, stream, yp, y_code, order["rows"].data_ptr(), wp, T, k, M, out.data_ptr(),
              code)
     return out
@@ -488,12 +499,12 @@ def moe_ffn(x, ids, weights, w1, sf1, w2, sf2, alpha1=None, alpha2=None, encode_
     a1 = None if alpha1 is None else _ptr(alpha1, "alpha1", f32, E, dev)
     a2 = None if alpha2 is None else _ptr(alpha2, "alpha2", f32, E, dev)
     if out is None:
-        out = torch.empty((T, D), dtype=x.dtype, device=dev)
+        out = _empty((T, D), x.dtype, dev, stream)
     else:
         _ptr(out, "out", x.dtype, T * D, dev)
     need = library().nvfp4_moe_ffn_workspace_bytes(T, k, E, D, F)
     if workspace is None:
-        workspace, size = torch.empty(need, dtype=u8, device=dev), need
+        workspace, size = _empty(need, u8, dev, stream), need
     else:
         size = workspace.numel()
         if size < need:
