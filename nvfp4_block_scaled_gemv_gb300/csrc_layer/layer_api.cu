@@ -116,6 +116,17 @@ nvfp4_status_t validate_grouped(const MoeShape& s, int64_t M, int64_t K, int64_t
   return s.tiles * ceil_div(M, 128) > kMaxDim ? NVFP4_ERR_UNSUPPORTED_SHAPE : NVFP4_OK;
 }
 
+// The sizes of the whole layer (those of its steps among them).
+nvfp4_status_t validate_ffn(int64_t T, int64_t k, int64_t E, int64_t D, int64_t F) {
+  nvfp4_status_t st = validate_moe(T, k, E);
+  if (st != NVFP4_OK) return st;
+  if (D < 0 || F < 0) return NVFP4_ERR_INVALID_VALUE;
+  if (D % 32 != 0 || F % 32 != 0 || D == 0 || F == 0 || F > kMaxDim / 2) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  const MoeShape s = moe_shape(T, k, E);
+  st = validate_grouped(s, 2 * F, D, E);
+  return st != NVFP4_OK ? st : validate_grouped(s, D, F, E);
+}
+
 SortParams sort_params(const int32_t* ids, const MoeShape& s, int64_t E, int32_t* rows, int32_t* counts,
                        int32_t* starts, void* plan) {
   uint8_t* const base = static_cast<uint8_t*>(plan);
@@ -471,7 +482,7 @@ nvfp4_status_t nvfp4_moe_combine(const void* y, int y_dtype, const int32_t* rows
 }
 
 size_t nvfp4_moe_ffn_workspace_bytes(int64_t T, int64_t top_k, int64_t E, int64_t D, int64_t F) {
-  if (validate_moe(T, top_k, E) != NVFP4_OK || D < 0 || F < 0 || D > kMaxK || F > kMaxK) return 0;
+  if (validate_ffn(T, top_k, E, D, F) != NVFP4_OK) return 0;
   return (size_t)ffn_space(moe_shape(T, top_k, E), E, D, F).bytes;
 }
 
@@ -489,11 +500,10 @@ nvfp4_status_t nvfp4_moe_ffn(const void* x, int dtype, int64_t x_row_stride, con
       !(opt.encode_x > 0.f) || !std::isfinite(opt.encode_x) || !(opt.encode_h > 0.f) ||
       !std::isfinite(opt.encode_h) || (opt.round_outputs != 0 && opt.round_outputs != 1))
     return NVFP4_ERR_INVALID_VALUE;
-  if (D % 32 != 0 || F % 32 != 0 || D == 0 || F == 0 || F > kMaxDim / 2) return NVFP4_ERR_UNSUPPORTED_SHAPE;
-  const MoeShape s = moe_shape(T, top_k, E);
-  if ((st = validate_grouped(s, 2 * F, D, E)) != NVFP4_OK || (st = validate_grouped(s, D, F, E)) != NVFP4_OK ||
+  if ((st = validate_ffn(T, top_k, E, D, F)) != NVFP4_OK ||
       (st = validate_rows(dtype, T, D, 1, x_row_stride, NVFP4_SF_PERMUTED_128x4)) != NVFP4_OK)
     return st;
+  const MoeShape s = moe_shape(T, top_k, E);
   if (T == 0) return NVFP4_OK;
   const FfnSpace w = ffn_space(s, E, D, F);
   if (x == nullptr || ids == nullptr || weights == nullptr || w1 == nullptr || sf1 == nullptr ||

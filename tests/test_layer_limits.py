@@ -34,6 +34,14 @@ def test_moe_ffn_workspace_holds_32_bit_outputs(lib):
         assert moe_ffn(lib, T, k, E, D, size=need - 1) == nv.ERR_INVALID_VALUE
 
 
+@pytest.mark.parametrize("T,k,E,D,F", [(4, 2, 8, 48, 64), (4, 2, 8, 64, 48), (4, 2, 8, 0, 64), (4, 2, 8, 64, 0),
+                                       (4, 2, 8, -64, 64), (4, 9, 8, 64, 64), (4, 2, 8, 1 << 30, 1 << 30),
+                                       (1 << 22, 4, 64, 1 << 20, 64), (4, 2, 8, 64, 1 << 31)])
+def test_moe_ffn_workspace_of_sizes_that_are_refused_is_0(lib, T, k, E, D, F):
+    assert nv.nvfp4_moe_ffn_workspace_bytes(T, k, E, D, F) == 0
+    assert moe_ffn(lib, T, k, E, D, F) in (nv.ERR_INVALID_VALUE, nv.ERR_UNSUPPORTED_SHAPE)
+
+
 SM_SMEM, RESERVED = 228 * 1024, 1024  # shared memory of an SM, and what every CTA takes beside its own
 
 
