@@ -76,6 +76,7 @@ struct GemmParams {
   int32_t tiles_n;       // dense: N tiles per batch
   int32_t total;         // dense: tiles
   int64_t rows;          // dense: rows of c in all batches
+  int32_t c_tile_rows;   // grouped: 0, or the rows of a tile if c's tiles follow each other
 };
 
 // One output tile: the mt-th tile of group g's A against rows n0..n0+rows-1 of b.
@@ -448,6 +449,7 @@ __device__ __forceinline__ void place_at(Place& w, const GemmParams& p, const Ti
                                          int quarter) {
   w.m = row_tile * 128 + 32 * quarter + (int)(threadIdx.x & 31);
   w.row0 = (GROUPED ? 0 : (int64_t)t.g * p.N) + t.n0;
+  if (GROUPED && EPI == kStore && p.c_tile_rows != 0) w.row0 = (t.n0 >> 7) * p.c_tile_rows;
   w.rows = t.rows;
   w.whole = row_tile * 128 + 32 * quarter + 32 <= p.M;
   if constexpr (EPI == kGatedQuantize) {

@@ -517,6 +517,7 @@ cudaError_t launch_gemm(const GemmArgs& g, int sms, cudaStream_t stream) {
   }
   p.tiles_m = pair ? (p.rest_m + 1) / 2 : p.rest_m;
   if (grouped) {
+    p.c_tile_rows = g.compact && bn < 128 ? bn : 0;
     const int64_t max_tiles = g.max_tiles * p.tiles_m;
     return g.q ? launch_for<kGatedQuantize, true>(bn, p, max_tiles, 1, sms, stream)
                : launch_for<kStore, true>(bn, p, max_tiles, 1, sms, stream);

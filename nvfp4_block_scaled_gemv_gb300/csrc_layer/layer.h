@@ -104,6 +104,7 @@ struct GemmArgs {
   const int32_t* tile_count;
   int64_t max_tiles;   // upper bound of *tile_count
   int tile_rows;       // rows of a grouped tile (the kernel's N tile)
+  bool compact;        // c's tiles of fewer than 128 rows follow each other (see CombineParams)
   // epilogue
   void* c;             // [G or 1][N][c_stride], or null with a quantised output
   int c_dtype;
@@ -172,6 +173,7 @@ constexpr int kPlaceMost = 1024;
 struct PlaceParams {
   SortParams sort;
   QuantizeParams quantize;
+  int32_t skip;  // sort.rows is written for CombineParams with these already left out
 };
 cudaError_t launch_place(const PlaceParams& p, int dtype, int64_t T, cudaStream_t stream);
 
@@ -182,6 +184,10 @@ struct CombineParams {
   void* out;           // [T][M]
   int64_t T, M;
   int32_t k;
+  // rows that y leaves out of each 128 that `rows` counts: 0, or, if y's tiles of fewer rows
+  // follow each other, 128 less a tile's (a scale atom's rows mean nothing to y, and are 8 times
+  // the memory of tiles of 16)
+  int32_t skip;
 };
 cudaError_t launch_combine(const CombineParams& p, int y_dtype, int dtype, int sms, cudaStream_t stream);
 

@@ -193,9 +193,65 @@ FfnSpace ffn_space(const MoeShape& s, int64_t E, int64_t D, int64_t F) {
   w.xsf = take(s.rows / 128 * ceil_div(D, 64) * 512);
   w.hq = take(s.rows * (F / 2));
   w.hsf = take(s.rows / 128 * ceil_div(F, 64) * 512);
-  w.y = take(s.rows * D * 4);
+  w.y = take(s.tiles * s.tile_rows * D * 4);  // (compact tiles)
   w.bytes = at;
   return w;
+}
+
+// compact: c's tiles follow each other, whatever their rows.
+nvfp4_status_t moe_product(const void* a, const void* sfa, const void* b, const void* sfb, const void* plan, int64_t T,
+                           int64_t top_k, int64_t E, int64_t M, int64_t K, const float* alpha, int activation, void* c,
+                           int c_dtype, bool compact, CUstream_st* stream) {
+  nvfp4_status_t st = validate_moe(T, top_k, E);
+  if (st != NVFP4_OK) return st;
+  const MoeShape s = moe_shape(T, top_k, E);
+  st = validate_grouped(s, M, K, E);
+  if (st != NVFP4_OK) return st;
+  if (!valid_dtype(c_dtype) || !valid_activation(activation)) return NVFP4_ERR_INVALID_VALUE;
+  if (K == 0) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  if (T == 0 || M == 0) return NVFP4_OK;
+  if (a == nullptr || sfa == nullptr || b == nullptr || sfb == nullptr || plan == nullptr || c == nullptr)
+    return NVFP4_ERR_INVALID_VALUE;
+  if (!aligned(a, 16) || !aligned(b, 16) || !aligned(sfa, 16) || !aligned(sfb, 16) || !aligned(plan, 16) ||
+      !aligned(alpha, 4) || !aligned(c, dtype_size(c_dtype)))
+    return NVFP4_ERR_MISALIGNED;
+  int sms = 0;
+  const cudaError_t err = sm_count(&sms);
+  if (err != cudaSuccess) return result(err);
+  GemmArgs g = moe_gemm_args(a, sfa, b, sfb, plan, s, E, M, K);
+  g.alphas = alpha;
+  g.activation = activation;
+  g.c = c;
+  g.c_dtype = c_dtype;
+  g.c_stride = M;
+  g.compact = compact;
+  return result(launch_gemm(g, sms, (cudaStream_t)stream));
+}
+
+// skip: see CombineParams.
+nvfp4_status_t combine(const void* y, int y_dtype, const int32_t* rows, const float* weights, int64_t T, int64_t top_k,
+                       int64_t M, void* out, int dtype, int skip, CUstream_st* stream) {
+  if ((dtype != NVFP4_DTYPE_FP16 && dtype != NVFP4_DTYPE_BF16) ||
+      (y_dtype != dtype && y_dtype != NVFP4_DTYPE_FP32) || T < 0 || top_k < 1 || M < 0)
+    return NVFP4_ERR_INVALID_VALUE;
+  if (M % 8 != 0 || M > kMaxK || top_k > kMaxTopK || T > kMaxChoices) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  if (T == 0 || M == 0) return NVFP4_OK;
+  if (y == nullptr || rows == nullptr || weights == nullptr || out == nullptr) return NVFP4_ERR_INVALID_VALUE;
+  if (!aligned(y, 16) || !aligned(rows, 4) || !aligned(weights, 4) || !aligned(out, 16))
+    return NVFP4_ERR_MISALIGNED;
+  int sms = 0;
+  const cudaError_t err = sm_count(&sms);
+  if (err != cudaSuccess) return result(err);
+  CombineParams p = {};
+  p.y = y;
+  p.rows = rows;
+  p.weights = weights;
+  p.out = out;
+  p.T = T;
+  p.M = M;
+  p.k = (int32_t)top_k;
+  p.skip = skip;
+  return result(launch_combine(p, y_dtype, dtype, sms, (cudaStream_t)stream));
 }
 
 }  // namespace
@@ -399,29 +455,7 @@ nvfp4_status_t nvfp4_moe_gemm(const void* a, const void* sfa, const void* b, con
                               const void* plan, int64_t T, int64_t top_k, int64_t E, int64_t M, int64_t K,
                               const float* alpha, int activation, void* c, int c_dtype,
                               struct CUstream_st* stream) {
-  nvfp4_status_t st = validate_moe(T, top_k, E);
-  if (st != NVFP4_OK) return st;
-  const MoeShape s = moe_shape(T, top_k, E);
-  st = validate_grouped(s, M, K, E);
-  if (st != NVFP4_OK) return st;
-  if (!valid_dtype(c_dtype) || !valid_activation(activation)) return NVFP4_ERR_INVALID_VALUE;
-  if (K == 0) return NVFP4_ERR_UNSUPPORTED_SHAPE;
-  if (T == 0 || M == 0) return NVFP4_OK;
-  if (a == nullptr || sfa == nullptr || b == nullptr || sfb == nullptr || plan == nullptr || c == nullptr)
-    return NVFP4_ERR_INVALID_VALUE;
-  if (!aligned(a, 16) || !aligned(b, 16) || !aligned(sfa, 16) || !aligned(sfb, 16) || !aligned(plan, 16) ||
-      !aligned(alpha, 4) || !aligned(c, dtype_size(c_dtype)))
-    return NVFP4_ERR_MISALIGNED;
-  int sms = 0;
-  const cudaError_t err = sm_count(&sms);
-  if (err != cudaSuccess) return result(err);
-  GemmArgs g = moe_gemm_args(a, sfa, b, sfb, plan, s, E, M, K);
-  g.alphas = alpha;
-  g.activation = activation;
-  g.c = c;
-  g.c_dtype = c_dtype;
-  g.c_stride = M;
-  return result(launch_gemm(g, sms, (cudaStream_t)stream));
+  return moe_product(a, sfa, b, sfb, plan, T, top_k, E, M, K, alpha, activation, c, c_dtype, false, stream);
 }
 
 nvfp4_status_t nvfp4_moe_gated_gemm(const void* a, const void* sfa, const void* b, const void* sfb,
@@ -459,26 +493,7 @@ nvfp4_status_t nvfp4_moe_gated_gemm(const void* a, const void* sfa, const void* 
 nvfp4_status_t nvfp4_moe_combine(const void* y, int y_dtype, const int32_t* rows, const float* weights,
                                  int64_t T, int64_t top_k, int64_t M, void* out, int dtype,
                                  struct CUstream_st* stream) {
-  if ((dtype != NVFP4_DTYPE_FP16 && dtype != NVFP4_DTYPE_BF16) ||
-      (y_dtype != dtype && y_dtype != NVFP4_DTYPE_FP32) || T < 0 || top_k < 1 || M < 0)
-    return NVFP4_ERR_INVALID_VALUE;
-  if (M % 8 != 0 || M > kMaxK || top_k > kMaxTopK || T > kMaxChoices) return NVFP4_ERR_UNSUPPORTED_SHAPE;
-  if (T == 0 || M == 0) return NVFP4_OK;
-  if (y == nullptr || rows == nullptr || weights == nullptr || out == nullptr) return NVFP4_ERR_INVALID_VALUE;
-  if (!aligned(y, 16) || !aligned(rows, 4) || !aligned(weights, 4) || !aligned(out, 16))
-    return NVFP4_ERR_MISALIGNED;
-  int sms = 0;
-  const cudaError_t err = sm_count(&sms);
-  if (err != cudaSuccess) return result(err);
-  CombineParams p = {};
-  p.y = y;
-  p.rows = rows;
-  p.weights = weights;
-  p.out = out;
-  p.T = T;
-  p.M = M;
-  p.k = (int32_t)top_k;
-  return result(launch_combine(p, y_dtype, dtype, sms, (cudaStream_t)stream));
+  return combine(y, y_dtype, rows, weights, T, top_k, M, out, dtype, 0, stream);
 }
 
 size_t nvfp4_moe_ffn_workspace_bytes(int64_t T, int64_t top_k, int64_t E, int64_t D, int64_t F) {
@@ -518,8 +533,11 @@ nvfp4_status_t nvfp4_moe_ffn(const void* x, int dtype, int64_t x_row_stride, con
   int32_t* const rows = reinterpret_cast<int32_t*>(base + w.rows);
   int32_t* const counts = reinterpret_cast<int32_t*>(base + w.counts);
   int32_t* const starts = reinterpret_cast<int32_t*>(base + w.starts);
+  int skip = s.pitch > 128 ? 0 : 128 - s.tile_rows;  // (the outputs' tiles follow each other)
   if (s.choices <= kPlaceMost) {
     PlaceParams p = {};
+    p.skip = skip;
+    skip = 0;
     p.sort = sort_params(ids, s, E, rows, counts, starts, base + w.plan);
     p.quantize.x = x;
     p.quantize.q = base + w.xq;
@@ -543,10 +561,10 @@ nvfp4_status_t nvfp4_moe_ffn(const void* x, int dtype, int64_t x_row_stride, con
                             opt.activation, opt.encode_h, base + w.hq, base + w.hsf, stream);
   if (st != NVFP4_OK) return st;
   const int y_dtype = ffn_y_dtype(opt, dtype);
-  st = nvfp4_moe_gemm(w2, sf2, base + w.hq, base + w.hsf, base + w.plan, T, top_k, E, D, F, opt.alpha2,
-                      NVFP4_ACT_NONE, base + w.y, y_dtype, stream);
+  st = moe_product(w2, sf2, base + w.hq, base + w.hsf, base + w.plan, T, top_k, E, D, F, opt.alpha2, NVFP4_ACT_NONE,
+                   base + w.y, y_dtype, true, stream);
   if (st != NVFP4_OK) return st;
-  return nvfp4_moe_combine(base + w.y, y_dtype, rows, weights, T, top_k, D, out, dtype, stream);
+  return combine(base + w.y, y_dtype, rows, weights, T, top_k, D, out, dtype, skip, stream);
 }
 
 }  // extern "C"

@@ -200,7 +200,8 @@ constexpr int kCombineThreads = 256;
 // values per thread.  M % 8 == 0.  B choices' loads go together: 4 for a few tokens,
 // where their latency counts (one token: 6.2 -> 4.2 us), 1 for many (4096 tokens of 8
 // choices, M 4096: 53 us, 72 with 4 at once, which reads the rows in more streams).
-template <typename Y, typename T, int B>
+// SKIP: with p.skip (asked for at run time it made one token's layer 0.1 us longer).
+template <typename Y, typename T, int B, bool SKIP>
 __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineParams p) {
   pdl_launch_dependents();
   pdl_wait();
@@ -217,6 +218,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineP
 #pragma unroll
       for (int j = 0; j < B; ++j) {
         row[j] = j0 + j < p.k ? p.rows[t * p.k + j0 + j] : -1;
+        if (SKIP && row[j] >= 0) row[j] -= (row[j] >> 7) * p.skip;
         w[j] = row[j] >= 0 ? p.weights[t * p.k + j0 + j] : 0.f;
       }
 #pragma unroll
@@ -255,18 +257,19 @@ cudaError_t launch_sort(const SortParams& p, cudaStream_t stream) {
                     dim3((unsigned)(chunks < 1 ? 1 : chunks)), dim3(kSortThreads), smem, stream, p);
 }
 
-template <int B>
+template <int B, bool SKIP>
 void (*combine_for(int y_dtype, int dtype))(const CombineParams) {
   if (y_dtype == kF32)
-    return dtype == kBF16 ? combine_kernel<float, __nv_bfloat16, B> : combine_kernel<float, __half, B>;
-  return dtype == kBF16 ? combine_kernel<__nv_bfloat16, __nv_bfloat16, B> : combine_kernel<__half, __half, B>;
+    return dtype == kBF16 ? combine_kernel<float, __nv_bfloat16, B, SKIP> : combine_kernel<float, __half, B, SKIP>;
+  return dtype == kBF16 ? combine_kernel<__nv_bfloat16, __nv_bfloat16, B, SKIP> : combine_kernel<__half, __half, B, SKIP>;
 }
 
 cudaError_t launch_combine(const CombineParams& p, int y_dtype, int dtype, int sms, cudaStream_t stream) {
   int64_t ctas = (p.T * (p.M / 8) + kCombineThreads - 1) / kCombineThreads;
   if (ctas > 64ll * sms) ctas = 64ll * sms;
   const bool few = ctas < sms;
-  auto kern = few ? combine_for<4>(y_dtype, dtype) : combine_for<1>(y_dtype, dtype);
+  auto kern = p.skip != 0 ? (few ? combine_for<4, true>(y_dtype, dtype) : combine_for<1, true>(y_dtype, dtype))
+                          : (few ? combine_for<4, false>(y_dtype, dtype) : combine_for<1, false>(y_dtype, dtype));
   return launch_pdl(kern, dim3((unsigned)ctas), dim3(kCombineThreads), 0, stream, p);
 }
 

@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kThreads) place_kernel(const PlaceParams p) {
     const int32_t row = e < 0 ? -1 : (first[e] + tile) * s.pitch + before - tile * s.tile_rows;
     if (lane == 0) {
       rows[j] = row;
-      s.rows[i] = row;
+      s.rows[i] = row < 0 ? -1 : row - (row >> 7) * p.skip;
     }
   }
   if (blockIdx.x == 0) {

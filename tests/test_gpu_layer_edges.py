@@ -77,6 +77,23 @@ def test_experts_outputs_are_rounded_first_when_the_caller_says_so(T, k, dtype):
     assert torch.equal(out, nv.moe_combine(y, order, w, dtype=DT[dtype]))
 
 
+
+@pytest.mark.parametrize("T,k,E,tile", [(7, 3, 40, 16), (200, 2, 64, 16), (24, 2, 4, 32), (90, 2, 9, 64), (120, 2, 4, 128),
+                                        (700, 2, 4, 256),
+                                        (260, 4, 200, 16), (340, 8, 300, 32), (1100, 1, 40, 64)])
+@pytest.mark.parametrize("uneven", [False, True])
+def test_experts_rows_of_every_tile(T, k, E, tile, uneven):
+    """The layer is its steps for every tile, one per expert or many (an expert that most choose)."""
+    x, ids, w, m, a1 = experts(T, k, E, 128, 64, "bf16", T + k)
+    if uneven:
+        ids[:, 0] = E - 2
+        ids[ids == 1] = -1
+    assert nv.nvfp4_moe_shape(T, k, E)["tile_rows"] == tile
+    order, y = outputs(x, ids, m, a1, a1, torch.float32)
+    out = nv.moe_ffn(x, ids, w, *m, alpha1=a1, alpha2=a1, encode_h=8.0)
+    assert torch.equal(out, nv.moe_combine(y, order, w, dtype=torch.bfloat16))
+
+
 # ---------------------------------------------------------------------------
 # the product's epilogue
 # ---------------------------------------------------------------------------

@@ -34,6 +34,18 @@ def test_moe_ffn_workspace_holds_32_bit_outputs(lib):
         assert moe_ffn(lib, T, k, E, D, size=need - 1) == nv.ERR_INVALID_VALUE
 
 
+@pytest.mark.parametrize("T,k,E,D,F", [(1, 8, 256, 7168, 2048), (128, 8, 256, 7168, 2048), (64, 16, 1024, 4096, 1024),
+                                       (500, 4, 37, 2048, 512), (4096, 8, 64, 4096, 2048)])
+def test_moe_ffn_workspace_holds_tiles_of_outputs_and_no_scale_atoms_of_them(lib, T, k, E, D, F):
+    """Rows of outputs for the choices and for one tile's rest per expert, not the 128 rows that
+    a tile's scales take."""
+    s = nv.nvfp4_moe_shape(T, k, E)
+    outputs = 4 * D * (T * k + s["tile_rows"] * min(E, T * k))
+    codes = s["row_capacity"] * ((D + F) // 2 + -(-D // 64) * 4 + -(-F // 64) * 4)
+    need = nv.nvfp4_moe_ffn_workspace_bytes(T, k, E, D, F)
+    assert need <= outputs + codes + s["plan_bytes"] + 4 * T * k + 8 * E + 9 * 256
+
+
 @pytest.mark.parametrize("T,k,E,D,F", [(4, 2, 8, 48, 64), (4, 2, 8, 64, 48), (4, 2, 8, 0, 64), (4, 2, 8, 64, 0),
                                        (4, 2, 8, -64, 64), (4, 9, 8, 64, 64), (4, 2, 8, 1 << 30, 1 << 30),
                                        (1 << 22, 4, 64, 1 << 20, 64), (4, 2, 8, 64, 1 << 31)])
