@@ -2,9 +2,11 @@
 // and the weighted sum of a token's expert outputs.
 //
 // The sort is two launches, or one up to 4096 choices: a histogram per chunk, then every
-// chunk adds up the ones before it and ranks its own choices.  Both are latency, a few
-// passes over at most a few hundred KB: 32768 choices among 64 experts 3 + 11 us beside
-// the products' 350.  The sum is one pass over the experts' outputs, bound by their
+// chunk adds up the ones before it and ranks its own choices.  Both are latency up to some
+// hundred thousand choices: 32768 among 64 experts 3 + 11 us beside the products' 350.  As
+// every chunk reads the counts of all, it then grows with their square: among 256 experts
+// 2^20 choices 43 us, 2^22 183 us, the most (2^24) 1.5 ms, or 5.7 ms among 1024, for products
+// of a hundred ms and more.  The sum is one pass over the experts' outputs, bound by their
 // bytes: 4096 tokens of 8 choices, M 4096 in bf16, 53 us (5.7 TB/s).
 #include <cstdint>
 

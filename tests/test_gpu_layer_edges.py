@@ -94,6 +94,28 @@ def test_experts_rows_of_every_tile(T, k, E, tile, uneven):
     assert torch.equal(out, nv.moe_combine(y, order, w, dtype=torch.bfloat16))
 
 
+
+@pytest.mark.parametrize("T,k,E", [(70_000, 4, 100), (131_072, 8, 1024), (300_001, 1, 3)])
+def test_sort_of_many_chunks_with_holes(T, k, E):
+    """69 to 256 chunks of 4096 choices, some of them with no choice at all."""
+    g = torch.Generator(device=DEV).manual_seed(T)
+    ids = torch.randint(-1, E + 1, (T, k), dtype=torch.int32, device=DEV, generator=g)
+    ids[T // 3:T // 3 + 20_000] = -1
+    order = nv.moe_sort(ids, E)
+    flat = ids.flatten().long()
+    real = (flat >= 0) & (flat < E)
+    tile, pitch = order["tile_rows"], max(order["tile_rows"], 128)
+    counts = torch.bincount(flat[real], minlength=E)
+    tiles = (counts + tile - 1) // tile
+    first = tiles.cumsum(0) - tiles
+    assert torch.equal(order["counts"].long(), counts) and torch.equal(order["starts"].long(), first * pitch)
+    e, at = torch.where(real, flat, E).sort(stable=True)
+    rank = torch.arange(T * k, device=DEV) - (counts.cumsum(0) - counts)[e.clamp(max=E - 1)]
+    row = (first[e.clamp(max=E - 1)] + rank // tile) * pitch + rank % tile
+    want = torch.empty_like(flat).scatter_(0, at, torch.where(e < E, row, -1))
+    assert torch.equal(order["rows"].flatten().long(), want)
+
+
 # ---------------------------------------------------------------------------
 # the product's epilogue
 # ---------------------------------------------------------------------------
