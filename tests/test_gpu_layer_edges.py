@@ -168,17 +168,18 @@ def assert_epilogue(c, y, act, dtype):
     assert ok.all(), (y[~ok][:4], c[~ok][:4], want[~ok][:4])
 
 
-def exact_product(N, M, K, L, alpha, bias, act, dtype):
-    """(c, alpha * sum + bias in fp32) of whole-number matrices."""
+def exact_case(N, M, K, L, alpha=2.0 ** -6, bias=None):
+    """(a, b and their scales, bias, alpha * sums + bias in fp32) of whole-number matrices, alpha a power
+    of two and the bias, if it is not given, in 64ths: exact but for a given bias's sum."""
     rng = np.random.default_rng(N + M + K)
     a, sfa = whole_matrix(rng, L, M, K)
     b, sfb = whole_matrix(rng, L, N, K)
+    if bias is None:
+        bias = gpu(rng.integers(-512, 513, (L, M)).astype(np.float32) / 64)
     at, bt = (torch.from_numpy(ol.matrix(*m)).float().to(DEV) for m in ((a, sfa), (b, sfb)))
-    # whole numbers below 2^24: exact in any order; alpha is a power of two
-    sums = torch.bmm(bt, at.transpose(1, 2)) * alpha
-    y = (sums.double() + bias.double().unsqueeze(1)).float()
-    t = [gpu(a), gpu(b), gpu(ol.atoms(sfa)), gpu(ol.atoms(sfb))]
-    return nv.gemm(*t, alpha=alpha, bias=bias, activation=act, dtype=DT[dtype]), y
+    # (whole numbers below 2^24: fp32 products are exact in any order)
+    y = (torch.bmm(bt, at.transpose(1, 2)) * alpha).double() + bias.double().unsqueeze(1)
+    return [gpu(a), gpu(b), gpu(ol.atoms(sfa)), gpu(ol.atoms(sfb))], bias, y.float()
 
 
 @pytest.mark.parametrize("dtype", ["fp16", "bf16", "fp32"])
@@ -189,7 +190,8 @@ def test_activations_of_extreme_values(act, dtype):
         assert chosen(N, M, K, L, act)[0] == tile
         bias = torch.tensor(EXTREMES, dtype=torch.float32, device=DEV).repeat(-(-L * M // len(EXTREMES)))
         bias = bias[:L * M].view(L, M)
-        assert_epilogue(*exact_product(N, M, K, L, 2.0 ** -10, bias, act, dtype), act, dtype)
+        t, bias, y = exact_case(N, M, K, L, 2.0 ** -10, bias)
+        assert_epilogue(nv.gemm(*t, alpha=2.0 ** -10, bias=bias, activation=act, dtype=DT[dtype]), y, act, dtype)
     e = torch.empty(0, dtype=torch.uint8, device=DEV)
     y = torch.tensor(EXTREMES, dtype=torch.float32, device=DEV).view(1, -1)
     c = nv.gemm(e.view(1, y.numel(), 0), e.view(1, 1, 0), e, e, bias=y, activation=act, dtype=DT[dtype])[0]
@@ -227,3 +229,41 @@ def test_gated_product_of_large_gates(T, k, E, F, K, act):
             cl, ch, got = (ol.e2m1_values(v).reshape(-1, 16) for v in (lo[0][0], hi[0][0], q[rows[t, j]]))
             sure = same[:, None] & (cl == ch)
             assert np.array_equal(got[sure], ch[sure]) and sure.mean() > 0.5
+
+
+# (N, M, K, L): rows per tile and K split, without an activation and with one that has an exponential
+PATHS = {(1, 513, 2080, 1): ((16, 2), (16, 4)), (16, 4096, 4096, 1): ((16, 4),) * 2,
+         (30, 2048, 4128, 2): ((32, 4),) * 2, (40, 1000, 8192, 1): ((64, 2),) * 2,
+         (100, 1000, 8192, 1): ((128, 2),) * 2, (9, 20000, 544, 1): ((16, 1),) * 2,
+         (20, 20000, 544, 1): ((32, 1),) * 2, (40, 20000, 544, 1): ((64, 1),) * 2,
+         (100, 7000, 2048, 1): ((128, 1),) * 2,
+         # pairs of SMs: rows of c that TMA can store, and rows that it cannot
+         (257, 4096, 4096, 2): ((256, 1),) * 2, (257, 4101, 4096, 2): ((256, 1),) * 2,
+         (1153, 4224, 4096, 2): ((256, 1),) * 2}
+
+
+@pytest.mark.parametrize("path", PATHS, ids=lambda p: "x".join(map(str, p)))
+def test_epilogue_of_every_kernel(path):
+    """Scaling, bias, each activation and each type where K is split, where it is not, and on pairs."""
+    t, bias, y = exact_case(*path)
+    for act in range(5):
+        assert chosen(*path, act) == PATHS[path][act > RELU]
+        for dtype in DT:
+            c = nv.gemm(*t, alpha=2.0 ** -6, bias=bias, activation=act, dtype=DT[dtype])
+            assert_epilogue(c, y, act, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16", "fp32"])
+@pytest.mark.parametrize("gap", [8, 2, 1])
+@pytest.mark.parametrize("path", [(257, 4096, 4096, 2), (16, 4096, 4096, 1), (100, 7000, 2048, 1)],
+                         ids=lambda p: "x".join(map(str, p)))
+def test_epilogue_into_rows_with_gaps(path, gap, dtype):
+    """Rows of c that start on 16 bytes (TMA stores them on pairs), on two elements, on one."""
+    N, M, K, L = path
+    t, bias, y = exact_case(*path)
+    out = torch.full((L, N, M + gap), -77.0, dtype=DT[dtype], device=DEV)
+    nv.nvfp4_gemm(*[x.data_ptr() for x in t], out.data_ptr(), M, N, K, L, alpha=2.0 ** -6, bias=bias.data_ptr(),
+                  activation=GELU_TANH, c_dtype={"fp16": nv.DTYPE_FP16, "bf16": nv.DTYPE_BF16, "fp32": nv.DTYPE_FP32}[dtype],
+                  c_row_stride=M + gap, stream=torch.cuda.current_stream().cuda_stream)
+    assert_epilogue(out[..., :M], y, GELU_TANH, dtype)
+    assert (out[..., M:] == -77).all()
