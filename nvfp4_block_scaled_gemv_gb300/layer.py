@@ -94,7 +94,8 @@ def nvfp4_fold_scale_signs(a: int, sf: int, rows: int, K: int, L: int, sf_layout
 def nvfp4_gemm(a: int, b: int, sfa: int, sfb: int, c: int, M: int, N: int, K: int, L: int, alpha: float = 1.0,
                bias: int = 0, activation: int = ACT_NONE, c_dtype: int = DTYPE_FP16, c_row_stride: int = 0,
                stream: int = 0) -> None:
-    """Enqueue c [L][N][M] = act(alpha * a b + bias) for quantised a [L][M], b [L][N]."""
+    """Enqueue c [L][N][M] = act(alpha * a b + bias) for quantised a [L][M], b [L][N]; the scales'
+    signs are ignored."""
     opt = _GemmOptions(alpha, bias or None, activation, c_dtype, c_row_stride)
     _check(library().nvfp4_gemm(a, b, sfa, sfb, c, M, N, K, L, ctypes.byref(opt), stream), "nvfp4_gemm")
 
@@ -317,7 +318,10 @@ def fold_scale_signs(a, sf, sf_layout: int = SF_PERMUTED_128x4, stream=None):
 def gemm(a, b, sfa, sfb, alpha: float = 1.0, bias=None, activation: int = ACT_NONE, dtype=None, c=None,
          stream=None):
     """c [L, N, M] = act(alpha * b a^T + bias) from a [L, M, K//2], b [L, N, K//2] (uint8) and their
-    permuted scales (flat uint8); bias fp32 [L, M]; dtype float16 (default), bfloat16 or float32."""
+    permuted scales (flat uint8); bias fp32 [L, M]; dtype float16 (default), bfloat16 or float32.
+    The scales are read as magnitudes, their signs ignored, unlike gemv() and nvfp4_gemm_small_n():
+    fold_scale_signs() makes signed ones unsigned, once.  For a single row nvfp4_gemm_small_n() is
+    the faster call, for 2 to 16 this one."""
     torch = _torch or _load()
     ashape, bshape = a.shape, b.shape
     if len(ashape) != 3 or len(bshape) != 3 or ashape[0] != bshape[0] or ashape[2] != bshape[2]:

@@ -267,3 +267,22 @@ def test_epilogue_into_rows_with_gaps(path, gap, dtype):
                   c_row_stride=M + gap, stream=torch.cuda.current_stream().cuda_stream)
     assert_epilogue(out[..., :M], y, GELU_TANH, dtype)
     assert (out[..., M:] == -77).all()
+
+
+@pytest.mark.parametrize("N", [1, 2, 16])
+def test_gemm_of_folded_scales_is_the_small_product_of_signed_ones(N):
+    """The two products for up to 16 rows: one takes signed scales, the other magnitudes."""
+    M, K, L = 300, 512, 2
+    rng = np.random.default_rng(N)
+    a, sfa = whole_matrix(rng, L, M, K)
+    b, sfb = whole_matrix(rng, L, N, K)
+    sfa, sfb = (s | (rng.integers(0, 2, s.shape) << 7).astype(np.uint8) for s in (sfa, sfb))
+    t = [gpu(a), gpu(b), gpu(ol.atoms(sfa)), gpu(ol.atoms(sfb))]
+    small = torch.empty((L, N, M), dtype=torch.float16, device=DEV)
+    nv.nvfp4_gemm_small_n(*[x.data_ptr() for x in t], small.data_ptr(), M, N, K, L, alpha=2.0 ** -2,
+                          stream=torch.cuda.current_stream().cuda_stream)
+    assert not torch.equal(nv.gemm(*t, alpha=2.0 ** -2), small)  # (the signs are ignored)
+    for m, s in ((0, 2), (1, 3)):
+        nv.fold_scale_signs(t[m], t[s])
+    # whole numbers below 2^24, a power of two, one rounding
+    assert torch.equal(nv.gemm(*t, alpha=2.0 ** -2), small)

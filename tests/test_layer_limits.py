@@ -90,3 +90,8 @@ def test_tensor_memory_is_never_asked_for_beyond_an_sm(lib):
             assert sum(columns for _, columns in ctas) <= 512, ctas
             room = SM_SMEM - sum(smem + RESERVED for smem, _ in ctas)
             packed += [ctas + (k,) for k in kinds if k[0] + RESERVED <= room]
+
+
+def test_calls_say_what_they_do_with_signs():
+    for call in (nv.gemm, nv.nvfp4_gemm):
+        assert "signs" in call.__doc__ and "ignored" in call.__doc__
