@@ -129,3 +129,56 @@ def test_results_used_and_dropped_on_the_current_stream_are_not_overwritten(ops)
         other = torch.zeros_like(want)
     torch.cuda.synchronize()
     assert torch.equal(used, want) and not other.any()
+
+
+@pytest.mark.parametrize("offset", [0, 8, 1])
+def test_every_call_sees_what_the_one_before_it_wrote(offset):
+    """A chain of small calls that overwrite the same buffers, in a graph: each kernel may be launched
+    before the one before it has ended, and reads only after that.  (Rows of 32-, 16- and 2-byte
+    alignment take different loads.)  The values grow until the scales saturate, and stay there."""
+    rng = np.random.default_rng(offset)
+    N, K, steps = 40, 512, 60
+    a, sfa = any_matrix(rng, 1, K, K)
+    a, sfa = gpu(a), gpu(ol.atoms(sfa))
+    wide = torch.zeros((N, K + 16), dtype=torch.bfloat16, device=DEV)
+    x, c = wide[:, offset:offset + K], torch.empty((1, N, K), dtype=torch.bfloat16, device=DEV)
+    q = torch.empty((N, K // 2), dtype=torch.uint8, device=DEV)
+    sf = torch.empty(nv.nvfp4_permuted_scale_bytes(N, K, 1), dtype=torch.uint8, device=DEV)
+    back = torch.empty((N, K), dtype=torch.float32, device=DEV)
+    stride = x.stride(0)
+    start = torch.randn(N, K, device=DEV, generator=torch.Generator(device=DEV).manual_seed(offset)).bfloat16()
+
+    def chain(wait):
+        out = []
+
+        def call(fn, *args, **kw):
+            r = fn(*args, **kw)
+            if wait:
+                torch.cuda.synchronize()
+            return r
+
+        s = torch.cuda.current_stream().cuda_stream
+        for _ in range(steps):
+            call(nv.quantize, x, q=q, sf=sf)
+            call(nv.dequantize, q, sf, x=back)
+            call(nv.gemm, a, q.unsqueeze(0), sfa, sf, alpha=2.0 ** -6, c=c)
+            # the rows of the next step, by the library's own kernels
+            call(nv.quantize, c[0], encode_scale=0.5, q=q, sf=sf)
+            call(nv.nvfp4_dequantize, q.data_ptr(), sf.data_ptr(), N, K, 1, x.data_ptr(), nv.DTYPE_BF16,
+                 nv.SF_PERMUTED_128x4, 2.0, stride, s)
+            i, v = call(nv.route, c[0, :, :64], 4)
+            out += [back.clone(), c.clone(), i, v]
+        return out
+
+    x.copy_(start)
+    want = chain(True)
+    assert want[-3].isfinite().all() and want[-3].abs().max() > 0
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        got = chain(False)
+    for _ in range(5):
+        x.copy_(start)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(g, t) for g, t in zip(got, want))
