@@ -22,8 +22,8 @@
 // Tiles of 256 rows of B run on pairs of SMs instead (gemm_pair.cu).
 //
 // What bounds it: with few rows per expert the weights' bytes (53 tokens through 8 of 64
-// experts, 4096 -> 2048 -> 4096: 108 us for the layer, the weights of the experts in use at
-// the measured copy rate); for one small matrix the latency of a CTA's stages, one
+// experts, 4096 -> 2048 -> 4096: 107 to 125 us for the layer, the weights of the 39 to 49
+// experts in use at the measured copy rate); for one small matrix the latency of a CTA's stages, one
 // after another, which is why idle SMs split a tile's K (1 x 4096 x 4096: 5.6 us, 7.0 without);
 // with 128 rows the bytes of a stage into shared memory, 36 KB at ~64 bytes per cycle and SM.
 //

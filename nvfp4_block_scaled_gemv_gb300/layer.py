@@ -5,6 +5,9 @@ device pointers as integers, the functions without the prefix take torch tensors
 check them and allocate the outputs.  Every step of the computation runs in the
 library's CUDA kernels; ``include/nvfp4_gemv.h`` defines each call.
 
+There are no gradients (the weights are 4-bit codes): results are cut off from tensors that
+require them, as under ``torch.no_grad()``.
+
 ``stream`` is a torch stream or a handle; None is the current one.  What a call on another
 stream allocates is safe there and on the current stream; ordering the two streams, and
 keeping the arguments until the call has run, is the caller's part.
@@ -348,7 +351,7 @@ def gemm(a, b, sfa, sfb, alpha: float = 1.0, bias=None, activation: int = ACT_NO
 
 def route(logits, top_k: int, score: int = SCORE_SOFTMAX, bias=None, groups: int = 1, top_groups: int = 1,
           renormalize: bool = True, weight_scale: float = 1.0, stream=None):
-    """(ids int32 [T, top_k], weights fp32 [T, top_k]) of logits [T, E]."""
+    """(ids int32 [T, top_k], weights fp32 [T, top_k]) of logits [T, E]; no gradients."""
     torch = _torch or _load()
     code = _dtype_code(logits, "logits")
     T, E, stride = _rows(logits, "logits")
@@ -480,7 +483,7 @@ def moe_ffn(x, ids, weights, w1, sf1, w2, sf2, alpha1=None, alpha2=None, encode_
     [T, top_k], w1 [E, 2F, D//2] (gate and input rows interleaved), w2 [E, D, F//2] and their
     permuted scales.  workspace: a uint8 tensor of nvfp4_moe_ffn_workspace_bytes, or None.
     round_outputs: the experts' outputs are rounded to the type of x before the weighted sum
-    (fewer bytes in large batches) in place of being held in fp32."""
+    (fewer bytes in large batches) in place of being held in fp32.  No gradients."""
     torch = _torch or _load()
     code = _dtype_code(x, "x", fp32=False)
     T, D, stride = _rows(x, "x")
