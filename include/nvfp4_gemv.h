@@ -620,6 +620,134 @@ nvfp4_status_t nvfp4_moe_ffn(const void* x, int dtype, int64_t x_row_stride, con
                              const nvfp4_moe_options_t* options, void* out, void* workspace,
                              size_t workspace_bytes, struct CUstream_st* stream);
 
+/* ------------------------------------------------------------------------
+ * Attention on a 4-bit cache: rotary positions, keys and values quantised into pages as
+ * they are written, and attention that reads them there.  The rules of the layer operators
+ * hold (results bitwise reproducible, nothing allocated, stream-capturable, no gradients but
+ * the rotation's own).  examples/attention_layer.py runs them together.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Rotary positions.  Pair i of a head, the elements (2i, 2i+1) interleaved or (i, pairs + i)
+ * in halves, is turned by positions[t] * f_i:
+ *   (a, b) -> factor * (a cos - b sin, b cos + a sin)
+ * in fp32, rounded once; the elements past 2 * pairs are copied.
+ *   x, y      : [T][H][D] of dtype (nvfp4_dtype_t), element aligned (16-byte aligned rows go
+ *               faster).  y may be x with the same strides, and must not overlap it otherwise
+ *   positions : int32 [T], of either sign
+ *   table     : int64 [pairs], f_i in 2^-64 turns per position (f / (2 pi) * 2^64 modulo 2^64):
+ *               the angle is exact modulo a turn at any position
+ * Options (NULL = {0, 0, 1, 0, 0, 0, 0}): interleaved 0 or 1; inverse 1 turns the other way
+ * (the gradient of the rotation, from y's to x's); factor scales the turned elements (what
+ * long contexts multiply their scores by, as its root); strides in elements, 0 = dense.
+ * Limits: 1 <= pairs <= 512, 2 * pairs <= D <= 65536, H <= 65536.
+ */
+typedef struct {
+  int32_t interleaved;
+  int32_t inverse;
+  float factor;
+  int64_t x_token_stride;
+  int64_t x_head_stride;
+  int64_t y_token_stride;
+  int64_t y_head_stride;
+} nvfp4_rope_options_t;
+nvfp4_status_t nvfp4_rope(const void* x, int dtype, int64_t T, int64_t H, int64_t D, const int32_t* positions,
+                          const int64_t* table, int64_t pairs, const nvfp4_rope_options_t* options, void* y,
+                          struct CUstream_st* stream);
+
+/*
+ * The cache: uint8 [pages][heads][page_size/16][2][D/64][576], 16-byte aligned.  A granule of
+ * 16 tokens holds K and then V, each as planes of 64 elements: 16 rows of 32 bytes of codes
+ * (two a byte, low nibble first), then 16 rows of 4 scale bytes, quantised as nvfp4_quantize
+ * does: blocks of 16 elements along the head.  Slot s is token s % page_size of page
+ * s / page_size.  page_size is a multiple of 16, D 64, 128 or 256.  Attention reads the
+ * scales as signed codes.
+ */
+size_t nvfp4_kv_cache_bytes(int64_t pages, int64_t heads, int64_t D, int64_t page_size);
+
+/*
+ * Rows of keys and values: [T][heads][D] each, strides in elements (0 = dense), and the
+ * encode scales (fp32 [heads] on the device, finite and > 0; NULL = 1).
+ */
+typedef struct {
+  void* k;
+  void* v;
+  const float* encode_k;
+  const float* encode_v;
+  int64_t k_token_stride;
+  int64_t k_head_stride;
+  int64_t v_token_stride;
+  int64_t v_head_stride;
+} nvfp4_kv_rows_t;
+
+/*
+ * Write: the rows of token t, times their head's encode scale, are quantised into slot
+ * slots[t] (int64 [T]).  Slots outside the cache are skipped (a negative one marks a padding
+ * row); other slots' bytes stay as they are.  No slot may be named twice in a call.
+ * Rows are element aligned (16- or 32-byte aligned rows load faster).
+ */
+nvfp4_status_t nvfp4_kv_write(const nvfp4_kv_rows_t* rows, int dtype, int64_t T, int64_t heads, int64_t D,
+                              const int64_t* slots, void* cache, int64_t pages, int64_t page_size,
+                              struct CUstream_st* stream);
+
+/*
+ * Read back: k and v (either may be NULL) get dtype(fp32(code * scale) * fp32(1 / encode)) of
+ * slot slots[t], zeros for a slot outside the cache.
+ */
+nvfp4_status_t nvfp4_kv_read(const nvfp4_kv_rows_t* rows, int dtype, int64_t T, int64_t heads, int64_t D,
+                             const int64_t* slots, const void* cache, int64_t pages, int64_t page_size,
+                             struct CUstream_st* stream);
+
+/*
+ * Attention of query tokens on the cache.  Sequence b has lengths[b] cached tokens, token t in
+ * page page_table[b][t / page_size], and its query tokens are its last ones (they are written
+ * to the cache before the call).  For the query at position j of the sequence and query head h,
+ * which reads key head h / (Hq / Hkv):
+ *   out = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale * q . k_t - max),  over the tokens t <= j,
+ *   with a window also t > j - window, or, without causal, over all lengths[b] tokens.
+ *   q, out     : [T][Hq][D] fp16 or bf16; out 16-byte aligned, q too (and its strides)
+ *   page_table : int32 [B][max_pages], the pages of a sequence's length
+ *   lengths    : int32 [B]
+ * Options (NULL = {0, 1, 0, 0, NULL, NULL, NULL, NULL, 0, 0}):
+ *   scale      : > 0; 0 = 1 / sqrt(D)
+ *   causal     : 0 or 1
+ *   window     : 0 = none (needs causal)
+ *   max_q      : with q_starts, the most query tokens of a sequence (0 = T); a bound for the
+ *                choice of kernels, results are right for sequences beyond it too
+ *   q_starts   : NULL (T / B query tokens each), or int32 [B + 1]: rows q_starts[b] to
+ *                q_starts[b + 1] - 1 of q are sequence b's; rows behind the last stay as they are
+ *   encode_k, encode_v : as nvfp4_kv_write had them
+ *   lse        : NULL, or fp32 [T][Hq]: log sum_t exp(scale * q . k_t)
+ *   q_token_stride, q_head_stride : elements, 0 = dense
+ * A query that sees no token has out 0 and lse -inf.  What masked places hold does not matter,
+ * infinities and NaN (a NaN scale code) among them.  A page outside [0, pages) makes the
+ * queries that see it NaN, a length beyond max_pages * page_size those of the sequence; both
+ * read nothing outside the cache.
+ * workspace: nvfp4_attention_workspace_bytes bytes, 256-byte aligned; need not be kept, but no
+ * two calls that may run at once can share it.
+ * Accuracy: scores and sums in fp32, the p to fp16 before the product with v, out rounded once.
+ * Limits: Hq % Hkv == 0, T * Hq < 2^31, max_pages * page_size < 2^31 - 64, B <= 2^20.
+ */
+typedef struct {
+  float scale;
+  int32_t causal;
+  int32_t window;
+  int32_t max_q;
+  const int32_t* q_starts;
+  const float* encode_k;
+  const float* encode_v;
+  float* lse;
+  int64_t q_token_stride;
+  int64_t q_head_stride;
+} nvfp4_attention_options_t;
+size_t nvfp4_attention_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t page_size,
+                                       int64_t max_pages, int ragged, int64_t max_q);
+nvfp4_status_t nvfp4_attention(const void* q, int dtype, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                               const void* cache, int64_t pages, int64_t page_size, const int32_t* page_table,
+                               int64_t max_pages, const int32_t* lengths, int64_t B,
+                               const nvfp4_attention_options_t* options, void* out, void* workspace,
+                               size_t workspace_bytes, struct CUstream_st* stream);
+
 #ifdef __cplusplus
 }
 #endif

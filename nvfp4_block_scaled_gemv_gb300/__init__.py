@@ -55,6 +55,12 @@ EXPORTS = (
     "nvfp4_moe_combine",
     "nvfp4_moe_ffn",
     "nvfp4_moe_ffn_workspace_bytes",
+    "nvfp4_rope",
+    "nvfp4_kv_cache_bytes",
+    "nvfp4_kv_write",
+    "nvfp4_kv_read",
+    "nvfp4_attention",
+    "nvfp4_attention_workspace_bytes",
 )
 
 
@@ -133,8 +139,9 @@ def library() -> ctypes.CDLL:
     lib.nvfp4_selftest_bounded_wait.argtypes = [ctypes.POINTER(I), ctypes.POINTER(I),
                                                 ctypes.POINTER(I), ctypes.POINTER(I64), P]
     lib.nvfp4_selftest_bounded_wait.restype = I
-    from . import layer
+    from . import attention_ops, layer
     layer.declare(lib)
+    attention_ops.declare(lib)
     _lib = lib
     return lib
 
@@ -355,3 +362,8 @@ from .layer import (  # noqa: E402
     nvfp4_gemm, nvfp4_gemm_plan, nvfp4_moe_combine, nvfp4_moe_ffn, nvfp4_moe_ffn_workspace_bytes, nvfp4_moe_gated_gemm,
     nvfp4_moe_gemm, nvfp4_moe_shape, nvfp4_moe_sort, nvfp4_quantize, nvfp4_route, quantize, quantize_rows,
     route)
+
+# Attention on a 4-bit cache (rotary positions, the cache, attention).
+from .attention_ops import (  # noqa: E402
+    attention, kv_cache, kv_read, kv_write, nvfp4_attention, nvfp4_attention_workspace_bytes, nvfp4_kv_cache_bytes,
+    nvfp4_kv_read, nvfp4_kv_write, nvfp4_rope, rope, rope_frequencies, rope_table)

@@ -1,0 +1,795 @@
+// Attention of a few query tokens per sequence on the 4-bit cache (sm_103a).
+//
+//   s[t] = scale * q . k[t],  p = exp(s - max s),  out = sum_t p[t] v[t] / sum_t p[t]
+//
+// over the tokens that a query sees, in one pass over the cache with a running maximum.
+//
+// Its floor is the cache's bytes: K and V of a token and head are 9/8 D bytes, and the C
+// = query tokens x heads of the group columns that share them are few.  So a column
+// tile is the N side (8 columns) of the matrix instruction and the cache's tokens the M
+// side of S^T = K Q^T, the head's elements the M side of O^T = V^T P^T, which wastes
+// nothing on rows that do not exist.  Codes become fp16 in registers: code * scale has 6
+// significant bits and is exact, so the only roundings before the fp32 sums are p to fp16
+// (2^-11 of itself; below 2^-14 of the row's largest p, 2^-25 of that) and the result's.
+//
+// A warp works by itself: 32 tokens at a time in a ring of stages that it fills with bulk
+// copies, a copy per 16 tokens (a granule of the cache, K and V in one run of bytes).  All
+// tiles of all sequences and heads, one after another, are cut into equal runs, one per
+// warp, whatever the lengths are; the lengths are read on the device.  A warp that has all
+// of an item (a head's columns of one sequence) writes its result; of an item that is
+// shared, every warp leaves its piece (maximum, sum, unnormalised result) in the workspace, and a
+// second small kernel adds the pieces in the order of the tokens.
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "attention.h"
+#include "layer.h"
+#include "ptx.cuh"
+#include "tc_ptx.cuh"
+
+namespace nvfp4 {
+
+namespace {
+
+constexpr int kTileTokens = 32;  // a stage: two granules
+constexpr int kMostWarps = 16;
+
+__device__ int g_attention_timeouts;
+
+template <int D, int NT>
+struct Shape {
+  static constexpr int kColumns = 8 * NT;
+  static constexpr int kPlanes = D / 64;
+  static constexpr int kGranule = 2 * kPlanes * kPlaneBytes;  // bytes of K and V of 16 tokens
+  static constexpr int kStage = 2 * kGranule;
+  // (registers: D * NT / 4 of results, D * NT / 8 of queries, ~60 beside them)
+  static constexpr int kWarps = D * NT <= 128 ? 16 : 8;
+  static constexpr int kStagesFit = (220 * 1024 / kWarps - 64) / kStage;
+  static constexpr int kStages = kStagesFit < 6 ? kStagesFit : 6;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kScanBytes = (kThreads + 1) * 8;
+  static constexpr size_t kSmem = (size_t)kWarps * kStages * (kStage + 8) + kScanBytes + 256;
+  static constexpr int kPiece = kColumns * (D + 2);  // floats: columns of D, then (maximum, sum)
+  static_assert(kStages >= 2, "two stages at least");
+};
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+  return d;
+}
+__device__ __forceinline__ uint32_t mul_h2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float d;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(x));
+  return d;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+// Bits of a where mask, bits of b elsewhere.
+__device__ __forceinline__ uint32_t merge_bits(uint32_t a, uint32_t b, uint32_t mask) {
+  return (a & mask) | (b & ~mask);
+}
+
+// What a sequence asks for: its query tokens, length and tiles.
+struct Sequence {
+  int32_t n, q0, length;   // query tokens, the first's row, cached tokens (those of the queries among them)
+  int32_t first_tile, tiles;
+  bool beyond;             // the length is beyond the page table
+};
+
+__device__ __forceinline__ Sequence sequence_of(const AttentionParams& p, int b) {
+  Sequence s;
+  if (p.q_starts != nullptr) {
+    const int32_t from = max(__ldg(p.q_starts + b), 0), to = min(__ldg(p.q_starts + b + 1), p.T);
+    s.q0 = from;
+    s.n = max(to - from, 0);
+  } else {
+    s.q0 = b * p.uniform_n;
+    s.n = p.uniform_n;
+  }
+  const int32_t length = __ldg(p.lengths + b);
+  s.beyond = (int64_t)length > p.capacity;
+  s.length = s.beyond ? (int32_t)p.capacity : max(length, 0);
+  int32_t lo = 0;
+  if (p.window > 0) lo = (int32_t)max((int64_t)s.length - s.n + 1 - p.window, (int64_t)0);
+  s.first_tile = lo / kTileTokens;
+  // (one tile at least, so that somebody writes the result of an empty row)
+  s.tiles = s.n == 0 ? 0 : max((s.length + kTileTokens - 1) / kTileTokens - s.first_tile, 1);
+  return s;
+}
+
+__device__ __forceinline__ int32_t column_tiles(const AttentionParams& p, int32_t n, int columns) {
+  return (int32_t)(((int64_t)n * p.group + columns - 1) / columns);
+}
+
+// The warps' runs: warp w of `warps` takes the tiles [total w / warps, total (w + 1) / warps).
+__device__ __forceinline__ int64_t run_start(int64_t total, int warps, int w) { return total * w / warps; }
+__device__ __forceinline__ int run_of(int64_t total, int warps, int64_t tile) {
+  return (int)(((tile + 1) * warps - 1) / total);
+}
+
+// The token of a row (0..7) of a matrix instruction's half: the loads of K (rows 0-3 and 4-7
+// of a half-warp together) and of V (rows 0, 2, 4, 6 and 1, 3, 5, 7 together) then each touch
+// four tokens that are different modulo 4, that is, different banks.
+__device__ __forceinline__ int token_of(int row) { return row ^ (row >> 2 & 1); }
+
+// The range of tokens that a column sees.
+__device__ __forceinline__ void seen_by(const AttentionParams& p, const Sequence& s, int column, int32_t& lo, int32_t& hi) {
+  const int32_t i = column / p.group;  // query token
+  lo = 0;
+  hi = s.length;
+  if (i >= s.n) {
+    hi = 0;
+  } else if (p.causal) {
+    const int32_t position = s.length - s.n + i;
+    hi = position + 1;  // (0 or less: an empty row)
+    if (p.window > 0) lo = max(position + 1 - p.window, 0);
+  }
+}
+
+template <int D, int NT>
+__device__ __forceinline__ void write_columns(const AttentionParams& p, const Sequence& s, int head, int first_column,
+                                              const float (&o)[D / 16][NT][4], const float (&m)[NT][2],
+                                              const float (&l)[NT][2]) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const float decode = p.encode_v ? 1.f / __ldg(p.encode_v + head) : 1.f;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int column = first_column + nt * 8 + 2 * q + e;
+      const int i = column / p.group;
+      if (i >= s.n) continue;
+      const int64_t row = (int64_t)(s.q0 + i) * p.Hq + (int64_t)head * p.group + (column - i * p.group);
+      const float sum = l[nt][e];
+      float f = sum == 0.f ? 0.f : decode / sum;
+      if (s.beyond) f = __int_as_float(0x7fc00000);
+      if (p.lse != nullptr && g == 0)
+        p.lse[row] = s.beyond ? f : sum == 0.f ? -INFINITY : (m[nt][e] + log2f(sum)) * 0.69314718055994531f;
+      constexpr int kPer = D == 64 ? 8 : 16;  // elements of a lane in a run
+#pragma unroll
+      for (int r = 0; r < (D + 127) / 128; ++r) {
+        const int64_t at = row * D + r * 128 + g * kPer;
+        uint32_t w[kPer / 2];
+#pragma unroll
+        for (int j = 0; j < kPer / 2; ++j) {
+          const float x = o[r * 8 + j][nt][e] * f, y = o[r * 8 + j][nt][2 + e] * f;
+          if (p.bf16) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+            w[j] = *reinterpret_cast<const uint32_t*>(&h);
+          } else {
+            w[j] = pack_h2(x, y);
+          }
+        }
+        uint4* const to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at);
+#pragma unroll
+        for (int j = 0; j < kPer / 8; ++j) to[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+      }
+    }
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(const AttentionParams p) {
+  using S = Shape<D, NT>;
+  constexpr int C = S::kColumns, kWarps = S::kWarps, kStages = S::kStages;
+  constexpr int kRuns = (D + 127) / 128;           // two planes of V at a time (one, if there is one)
+  constexpr int kTilesV = D == 64 ? 4 : 8;         // matrix tiles of a run
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
+  const int g = lane >> 2, q = lane & 3;
+  const uint32_t ring = smem_u32(smem) + warp * kStages * S::kStage;
+  const uint32_t bars = smem_u32(smem) + kWarps * kStages * S::kStage + warp * kStages * 8;
+  int64_t* const scan = reinterpret_cast<int64_t*>(smem + kWarps * kStages * (S::kStage + 8));
+  __shared__ int64_t warp_sums[kMostWarps];
+
+  pdl_launch_dependents();
+  if (lane == 0) {
+    for (int i = 0; i < kStages; ++i) tc::mbar_init(bars + 8 * i, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  pdl_wait();
+
+  // tiles of all sequences before each thread's share of them
+  const int share = (p.B + S::kThreads - 1) / S::kThreads;
+  {
+    int64_t mine = 0;
+    for (int b = threadIdx.x * share; b < min((int)(threadIdx.x + 1) * share, p.B); ++b) {
+      const Sequence s = sequence_of(p, b);
+      mine += (int64_t)s.tiles * column_tiles(p, s.n, C);
+    }
+    int64_t upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t o = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += o;
+    }
+    if (lane == 31) warp_sums[warp] = upto;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) upto += warp_sums[w];
+    scan[threadIdx.x + 1] = upto * p.Hkv;
+    if (threadIdx.x == 0) scan[0] = 0;
+    __syncthreads();
+  }
+  const int64_t total = scan[S::kThreads];
+  // warps in use: those of a CTA that are needed for every CTA to have as many
+  const int64_t even = (total + gridDim.x - 1) / gridDim.x;
+  const int per_cta = (int)(even < kWarps ? even : kWarps);
+  const int64_t all = (int64_t)per_cta * gridDim.x;
+  const int warps = (int)(all < total ? all : total);
+  const int rank = (int)blockIdx.x * per_cta + warp;
+  const int slot = (int)blockIdx.x * kWarps + warp;  // of the piece list
+  if (warp >= per_cta || rank >= warps) {
+    if (lane == 0) p.pieces[slot] = make_int4(-1, 0, 0, 0);
+    return;
+  }
+  const int64_t begin = run_start(total, warps, rank), end = run_start(total, warps, rank + 1);
+
+  // the sequence, head, column tile and tile at `begin`
+  int b = 0;
+  {
+    int lo = 0, hi = S::kThreads;  // the last share that starts at or before it
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (scan[mid] <= begin) lo = mid; else hi = mid;
+    }
+    b = lo * share;
+  }
+  int64_t before = scan[b / share];
+  Sequence seq = sequence_of(p, b);
+  int32_t cts = column_tiles(p, seq.n, C);
+  for (;;) {
+    const int64_t here = (int64_t)seq.tiles * cts * p.Hkv;
+    if (before + here > begin) break;
+    before += here;
+    seq = sequence_of(p, ++b);
+    cts = column_tiles(p, seq.n, C);
+  }
+  int32_t item = (int32_t)((begin - before) / seq.tiles);  // head * cts + column tile
+  int32_t tile = (int32_t)((begin - before) - (int64_t)item * seq.tiles);
+
+  // the loader: the same walk, some stages ahead
+  Sequence ahead = seq;
+  int lb = b;
+  int32_t litem = item, ltile = tile, lcts = cts;
+  int64_t to_load = end - begin;
+  int32_t ids = 0, ids_tile = -1;  // a lane's page of granule ids_tile * 2 + lane
+  uint32_t load_stage = 0;
+  uint32_t bad_bits = 0;           // two bits a stage: granules whose page does not exist
+  auto load_next = [&]() {
+    if (to_load == 0) return;
+    const int32_t at = ahead.first_tile + ltile;  // tile of the sequence
+    if (ids_tile < 0 || at >= ids_tile + 16) {
+      ids_tile = at;
+      const int64_t page = (int64_t)(at * 2 + lane) / p.granules;
+      ids = page < p.max_pages && (at * 2 + lane) * (int64_t)kGranuleTokens < ahead.length
+                ? __ldg(p.page_table + (int64_t)lb * p.max_pages + page)
+                : 0;
+    }
+    const int head = litem / lcts;
+    const int32_t granules = (ahead.length + kGranuleTokens - 1) / kGranuleTokens;
+    uint32_t bad = 0, bytes = 0;
+    const uint32_t bar = bars + 8 * load_stage, dst = ring + load_stage * S::kStage;
+    int32_t id[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      id[i] = __shfl_sync(0xffffffffu, ids, (at - ids_tile) * 2 + i);
+      if (at * 2 + i >= granules) {
+        id[i] = -1;
+      } else if (id[i] < 0 || id[i] >= p.pages) {
+        id[i] = -1;
+        bad |= 1u << i;
+      } else {
+        bytes += S::kGranule;
+      }
+    }
+    if (lane == 0) {
+      tc::mbar_expect_tx(bar, bytes);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (id[i] >= 0) {
+          const int64_t granule = ((int64_t)id[i] * p.Hkv + head) * p.granules + (at * 2 + i) % p.granules;
+          tc::bulk_load(dst + i * S::kGranule, p.cache + granule * S::kGranule, S::kGranule, bar);
+        }
+    }
+    bad_bits = (bad_bits & ~(3u << (2 * load_stage))) | bad << (2 * load_stage);
+    load_stage = load_stage + 1 == kStages ? 0 : load_stage + 1;
+    if (--to_load == 0) return;
+    if (++ltile == ahead.tiles) {
+      ltile = 0;
+      ids_tile = -1;
+      if (++litem == lcts * p.Hkv) {
+        litem = 0;
+        do {
+          ahead = sequence_of(p, ++lb);
+        } while (ahead.tiles == 0);
+        lcts = column_tiles(p, ahead.n, C);
+      }
+    }
+  };
+  __syncwarp();
+#pragma unroll 1
+  for (int i = 0; i < kStages; ++i) load_next();
+
+  int64_t left = end - begin;
+  uint32_t stage = 0, parity = 0;
+  bool ok = true;
+  int4 first_piece = make_int4(-1, 0, 0, 0);
+  while (left > 0) {
+    // an item, or the part of it in this run
+    const int head = item / cts, first_column = (item - head * cts) * C;
+    const int32_t from = tile;
+    const int32_t to = (int32_t)((int64_t)(seq.tiles - tile) < left ? seq.tiles : tile + left);
+
+    // its queries: column 8 nt + g, a lane's 16 elements of every plane, as fp16.  bf16
+    // values go over in a power of two of the row's own (its largest between 2^14 and 2^15),
+    // so that fp16's range is enough; what is then below 2^-39 of the largest is lost.
+    uint32_t qf[S::kPlanes][4][2][NT];
+    float cs[NT][2];  // score scale of the columns 8 nt + 2 q + e
+    const float scale = p.scale_log2 * (p.encode_k ? 1.f / __ldg(p.encode_k + head) : 1.f);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int column = first_column + nt * 8 + g;
+      const int i = column / p.group;
+      const bool real = i < seq.n;
+      uint32_t w[S::kPlanes][8];
+      float largest = 0.f;
+      if (real) {
+        const uint16_t* const src = static_cast<const uint16_t*>(p.q) + (int64_t)(seq.q0 + i) * p.q_token +
+                                    (int64_t)(head * p.group + column - i * p.group) * p.q_head + q * 16;
+#pragma unroll
+        for (int c = 0; c < S::kPlanes; ++c) {
+          const uint4 u = *reinterpret_cast<const uint4*>(src + c * 64), v = *reinterpret_cast<const uint4*>(src + c * 64 + 8);
+          w[c][0] = u.x, w[c][1] = u.y, w[c][2] = u.z, w[c][3] = u.w;
+          w[c][4] = v.x, w[c][5] = v.y, w[c][6] = v.z, w[c][7] = v.w;
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < S::kPlanes; ++c)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) w[c][j] = 0u;
+      }
+      float back = 1.f;
+      if (p.bf16) {
+#pragma unroll
+        for (int c = 0; c < S::kPlanes; ++c)
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            largest = fmaxf(largest, fmaxf(fabsf(__uint_as_float(w[c][j] << 16)),
+                                           fabsf(__uint_as_float(w[c][j] & 0xffff0000u))));
+        largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, 1));
+        largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, 2));
+        // (zero, infinities and NaN keep an exponent of their own range, and their values)
+        const int e = min(max(14 - ((int)(__float_as_uint(largest) >> 23) - 127), -113), 113);
+        const float by = __uint_as_float((uint32_t)(e + 127) << 23);
+        back = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+        for (int c = 0; c < S::kPlanes; ++c)
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            w[c][j] = pack_h2(__uint_as_float(w[c][j] << 16) * by, __uint_as_float(w[c][j] & 0xffff0000u) * by);
+      }
+#pragma unroll
+      for (int c = 0; c < S::kPlanes; ++c)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          qf[c][j][0][nt] = w[c][2 * j];
+          qf[c][j][1][nt] = w[c][2 * j + 1];
+        }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) cs[nt][e] = scale * __shfl_sync(0xffffffffu, back, (2 * q + e) * 4);
+    }
+    // what the columns see; tiles from full_from to full_to are seen by all of them whole
+    int32_t lo[NT][2], hi[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) seen_by(p, seq, first_column + nt * 8 + 2 * q + e, lo[nt][e], hi[nt][e]);
+    int32_t full_from, full_to;
+    {
+      int32_t l0, h0, l1, h1;
+      const int last = min(first_column + C, seq.n * p.group) - 1;
+      seen_by(p, seq, first_column, l0, h0);
+      seen_by(p, seq, last, l1, h1);
+      full_from = l1;
+      full_to = h0;
+    }
+
+    float o[D / 16][NT][4];
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[i][nt][j] = 0.f;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) m[nt][e] = -INFINITY, l[nt][e] = 0.f;
+
+#pragma unroll 1
+    for (; tile < to; ++tile) {
+      const uint32_t bar = bars + 8 * stage, base = ring + stage * S::kStage;
+      if (lane == 0) tc::mbar_wait<false>(bar, parity, ok, &g_attention_timeouts);
+      ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+      if (!ok) break;
+      const int32_t t0 = (seq.first_tile + tile) * kTileTokens;
+      const uint32_t bad = bad_bits >> (2 * stage) & 3u;
+      const bool whole = t0 >= full_from && t0 + kTileTokens <= full_to && bad == 0;  // (the same in all lanes)
+
+      // S^T, 16 tokens x 8 columns at a time
+      float s[2][NT][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[i][nt][j] = 0.f;
+#pragma unroll
+        for (int c = 0; c < S::kPlanes; ++c) {
+          const uint32_t plane = base + i * S::kGranule + c * kPlaneBytes;
+          const uint32_t row = plane + token_of(g) * 32 + q * 8;
+          const uint32_t scale_at = plane + kPlaneScales + token_of(g) * 4 + q;
+          const uint2 c0 = lds64(row), c1 = lds64(row + 8 * 32);
+          const uint32_t s0 = e4m3x2_to_f16x2(lds8(scale_at) * 0x101u), s1 = e4m3x2_to_f16x2(lds8(scale_at + 8 * 4) * 0x101u);
+          uint32_t a[8], d[8];
+          e2m1x8_to_f16x2x4(c0.x, *reinterpret_cast<uint32_t(*)[4]>(&a[0]));
+          e2m1x8_to_f16x2x4(c0.y, *reinterpret_cast<uint32_t(*)[4]>(&a[4]));
+          e2m1x8_to_f16x2x4(c1.x, *reinterpret_cast<uint32_t(*)[4]>(&d[0]));
+          e2m1x8_to_f16x2x4(c1.y, *reinterpret_cast<uint32_t(*)[4]>(&d[4]));
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            a[j] = mul_h2(a[j], s0);
+            d[j] = mul_h2(d[j], s1);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_f16(s[i][nt], a[2 * j], d[2 * j], a[2 * j + 1], d[2 * j + 1], qf[c][j][0][nt], qf[c][j][1][nt]);
+        }
+      }
+      // scores in base 2, masked
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[i][nt][j] *= cs[nt][j & 1];
+      if (!whole) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int32_t t = t0 + i * 16 + r * 8 + token_of(g);
+            const bool absent = (bad >> i & 1u) != 0;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float& v = s[i][nt][2 * r + e];
+                if (t < lo[nt][e] || t >= hi[nt][e])
+                  v = -INFINITY;
+                else if (absent)
+                  v = __int_as_float(0x7fc00000);
+              }
+          }
+      }
+      // the running maximum and what it does to sums and results
+      float keep[NT][2];
+      bool moved = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float top = fmaxf(fmaxf(s[0][nt][e], s[0][nt][2 + e]), fmaxf(s[1][nt][e], s[1][nt][2 + e]));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+          const bool up = top > m[nt][e];
+          const float now = up ? top : m[nt][e];
+          keep[nt][e] = up ? exp2_fast(m[nt][e] - now) : 1.f;
+          moved |= up;
+          m[nt][e] = now;
+        }
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            l[nt][e] *= keep[nt][e];
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              o[i][nt][e] *= keep[nt][e];
+              o[i][nt][2 + e] *= keep[nt][e];
+            }
+          }
+      }
+      // P, and its transposition to the second product's operand
+      uint32_t pf[2][NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float p0 = exp2_fast(s[i][nt][2 * r] - m0), p1 = exp2_fast(s[i][nt][2 * r + 1] - m1);
+            l[nt][0] += p0;
+            l[nt][1] += p1;
+            pf[i][nt][r] = transpose_8x8(pack_h2(p0, p1));
+          }
+      }
+      // O^T += V^T P^T
+      const int t_a = token_of(2 * q), t_b = token_of(2 * q + 1);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int r = 0; r < kRuns; ++r) {
+          // a lane's block: 16 elements of a plane (D = 64: half of one)
+          const uint32_t plane = base + i * S::kGranule + (S::kPlanes + 2 * r + (D == 64 ? 0 : g >> 2)) * kPlaneBytes;
+          const uint32_t row = plane + (D == 64 ? g * 4 : (g & 3) * 8);
+          const uint32_t scale_at = plane + kPlaneScales + (D == 64 ? g >> 1 : g & 3);
+          uint32_t sb[4] = {lds8(scale_at + t_a * 4), lds8(scale_at + t_b * 4), lds8(scale_at + (t_a + 8) * 4),
+                            lds8(scale_at + (t_b + 8) * 4)};
+          if (!whole) {
+            // A masked place adds 0 whatever it holds: tokens past the length and NaN scales
+            // become 0, and a NaN goes to the columns that do see its token.
+            uint32_t nan = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int32_t t = t0 + i * 16 + (j & 1 ? t_b : t_a) + (j >> 1) * 8;
+              if (t >= seq.length || (bad >> i & 1u)) {
+                sb[j] = 0;
+              } else if ((sb[j] & 0x7Fu) == 0x7Fu) {
+                sb[j] = 0;
+                nan |= 1u << j;
+              }
+            }
+            if (__any_sync(0xffffffffu, nan != 0)) {
+#pragma unroll 1
+              for (int other = 0; other < 4; ++other) {
+                const uint32_t theirs = __shfl_sync(0xffffffffu, nan, (lane & ~3) | other);
+#pragma unroll 1
+                for (int j = 0; j < 4; ++j) {
+                  const int32_t t = t0 + i * 16 + token_of(2 * other + (j & 1)) + (j >> 1) * 8;
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                      if ((theirs >> j & 1u) && t >= lo[nt][e] && t < hi[nt][e]) {
+#pragma unroll
+                        for (int x = 0; x < kTilesV; ++x) {
+                          o[r * 8 + x][nt][e] = __int_as_float(0x7fc00000);
+                          o[r * 8 + x][nt][2 + e] = __int_as_float(0x7fc00000);
+                        }
+                      }
+                }
+              }
+            }
+          }
+          const uint32_t s_ab = e4m3x2_to_f16x2(sb[0] | sb[1] << 8), s_cd = e4m3x2_to_f16x2(sb[2] | sb[3] << 8);
+          uint32_t codes[4][2];  // the four tokens' codes
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t at = row + ((j & 1 ? t_b : t_a) + (j >> 1) * 8) * 32;
+            if constexpr (D == 64) {
+              codes[j][0] = lds32(at);
+            } else {
+              const uint2 v = lds64(at);
+              codes[j][0] = v.x;
+              codes[j][1] = v.y;
+            }
+          }
+#pragma unroll
+          for (int w = 0; w < kTilesV / 4; ++w) {
+            constexpr uint32_t kLow = 0x0F0F0F0Fu;
+            // a byte of two tokens' codes of one element: even elements, odd elements
+            uint32_t even_ab[4], odd_ab[4], even_cd[4], odd_cd[4];
+            e2m1x8_to_f16x2x4(merge_bits(codes[0][w], codes[1][w] << 4, kLow), even_ab);
+            e2m1x8_to_f16x2x4(merge_bits(codes[0][w] >> 4, codes[1][w], kLow), odd_ab);
+            e2m1x8_to_f16x2x4(merge_bits(codes[2][w], codes[3][w] << 4, kLow), even_cd);
+            e2m1x8_to_f16x2x4(merge_bits(codes[2][w] >> 4, codes[3][w], kLow), odd_cd);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const uint32_t a0 = mul_h2(even_ab[x], s_ab), a1 = mul_h2(odd_ab[x], s_ab);
+              const uint32_t a2 = mul_h2(even_cd[x], s_cd), a3 = mul_h2(odd_cd[x], s_cd);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma_f16(o[r * 8 + w * 4 + x][nt], a0, a1, a2, a3, pf[i][nt][0], pf[i][nt][1]);
+            }
+          }
+        }
+      __syncwarp();  // the stage has been read
+      load_next();
+      if (++stage == kStages) stage = 0, parity ^= 1;
+    }
+    if (!ok) break;
+    left -= to - from;
+
+    // sums over the lanes that have a column's tokens
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 4);
+        l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 8);
+        l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 16);
+      }
+    if (from == 0 && to == seq.tiles) {
+      write_columns<D, NT>(p, seq, head, first_column, o, m, l);
+    } else {
+      // a piece: the second place is for one that begins the item, the first for one that
+      // goes on with it (a run that does neither begin nor end it is one that goes on)
+      float* const piece = p.partial + ((int64_t)rank * 2 + (from == 0 ? 1 : 0)) * S::kPiece;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int column = nt * 8 + 2 * q + e;
+          constexpr int kPer = D == 64 ? 8 : 16;
+#pragma unroll
+          for (int r = 0; r < kRuns; ++r) {
+            float* const at = piece + column * D + r * 128 + g * kPer;
+#pragma unroll
+            for (int j = 0; j < kPer / 4; ++j)
+              reinterpret_cast<float4*>(at)[j] = make_float4(o[r * 8 + 2 * j][nt][e], o[r * 8 + 2 * j][nt][2 + e],
+                                                             o[r * 8 + 2 * j + 1][nt][e], o[r * 8 + 2 * j + 1][nt][2 + e]);
+          }
+          if (g == 0) *reinterpret_cast<float2*>(piece + C * D + column * 2) = make_float2(m[nt][e], l[nt][e]);
+        }
+      if (from == 0) {
+        const int64_t item_end = before + ((int64_t)item + 1) * seq.tiles;
+        first_piece = make_int4(b, item, rank, run_of(total, warps, item_end - 1));
+      }
+    }
+    // on to the next item
+    tile = 0;
+    if (left > 0 && ++item == cts * p.Hkv) {
+      item = 0;
+      do {
+        before += (int64_t)seq.tiles * cts * p.Hkv;
+        seq = sequence_of(p, ++b);
+        cts = column_tiles(p, seq.n, C);
+      } while (seq.tiles == 0);
+    }
+  }
+  if (lane == 0) p.pieces[slot] = first_piece;
+}
+
+// The pieces of an item added up: a CTA per warp of the first kernel, for the item that its
+// run began and others go on with, if there is one.
+template <int D, int NT>
+__global__ void __launch_bounds__(128) attention_sum_kernel(const AttentionParams p) {
+  using S = Shape<D, NT>;
+  constexpr int C = S::kColumns;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int4 piece = p.pieces[blockIdx.x];
+  if (piece.x < 0) return;
+  const Sequence seq = sequence_of(p, piece.x);
+  const int32_t cts = column_tiles(p, seq.n, C);
+  const int head = piece.y / cts, first_column = (piece.y - head * cts) * C;
+  const float decode = p.encode_v ? 1.f / __ldg(p.encode_v + head) : 1.f;
+  constexpr int kLanes = D / 4;  // threads of a column
+  const int d = threadIdx.x % kLanes * 4;
+  for (int c = threadIdx.x / kLanes; c < C; c += 128 / kLanes) {
+    const int column = first_column + c;
+    const int i = column / p.group;
+    if (i >= seq.n) break;
+    const float* const first = p.partial + ((int64_t)piece.z * 2 + 1) * S::kPiece;
+    const float2 ml0 = *reinterpret_cast<const float2*>(first + C * D + 2 * c);
+    float4 o = *reinterpret_cast<const float4*>(first + c * D + d);
+    float m = ml0.x, l = ml0.y;
+#pragma unroll 4
+    for (int w = piece.z + 1; w <= piece.w; ++w) {
+      const float* const next = p.partial + (int64_t)w * 2 * S::kPiece;
+      const float2 ml = *reinterpret_cast<const float2*>(next + C * D + 2 * c);
+      const float4 v = *reinterpret_cast<const float4*>(next + c * D + d);
+      const float top = fmaxf(m, ml.x);
+      const float fa = m == top ? 1.f : exp2_fast(m - top), fb = ml.x == top ? 1.f : exp2_fast(ml.x - top);
+      o.x = o.x * fa + v.x * fb;
+      o.y = o.y * fa + v.y * fb;
+      o.z = o.z * fa + v.z * fb;
+      o.w = o.w * fa + v.w * fb;
+      l = l * fa + ml.y * fb;
+      m = top;
+    }
+    const int64_t row = (int64_t)(seq.q0 + i) * p.Hq + (int64_t)head * p.group + (column - i * p.group);
+    float f = l == 0.f ? 0.f : decode / l;
+    if (seq.beyond) f = __int_as_float(0x7fc00000);
+    if (p.lse != nullptr && d == 0) p.lse[row] = seq.beyond ? f : l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+    uint2 w;
+    if (p.bf16) {
+      const __nv_bfloat162 x = __floats2bfloat162_rn(o.x * f, o.y * f), y = __floats2bfloat162_rn(o.z * f, o.w * f);
+      w = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+    } else {
+      w = make_uint2(pack_h2(o.x * f, o.y * f), pack_h2(o.z * f, o.w * f));
+    }
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * D + d) = w;
+  }
+}
+
+template <int D, int NT>
+cudaError_t launch_with(AttentionParams p, void* workspace, int sms, cudaStream_t stream) {
+  using S = Shape<D, NT>;
+  const int ctas = sms < kAttentionCtas ? sms : kAttentionCtas;
+  const cudaError_t err = allow_smem<attention_kernel<D, NT>>(S::kSmem);
+  if (err != cudaSuccess) return err;
+  p.pieces = static_cast<int4*>(workspace);
+  p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kAttentionCtas * kMostWarps * sizeof(int4));
+  const cudaError_t ran = launch_pdl(attention_kernel<D, NT>, dim3((unsigned)ctas), dim3(S::kThreads), S::kSmem, stream, p);
+  if (ran != cudaSuccess) return ran;
+  return launch_pdl(attention_sum_kernel<D, NT>, dim3((unsigned)(ctas * S::kWarps)), dim3(128), 0, stream, p);
+}
+
+}  // namespace
+
+int attention_columns(int D, int64_t most) {
+  // the fewest columns of a pass that hold a sequence's (the cache is read once), as far as
+  // results and queries fit the registers
+  const int largest = D == 256 ? 16 : 32;
+  return most <= 8 ? 8 : most <= 16 || largest == 16 ? 16 : 32;
+}
+
+int64_t attention_workspace(int D, int columns) {
+  const int warps = D * (columns / 8) <= 128 ? 16 : 8;
+  return (int64_t)kAttentionCtas * kMostWarps * (int64_t)sizeof(int4) +
+         (int64_t)kAttentionCtas * warps * 2 * columns * (D + 2) * 4;
+}
+
+cudaError_t launch_attention(AttentionParams p, int D, int columns, void* workspace, int sms, cudaStream_t stream) {
+  switch (D * 100 + columns) {
+    case 6408: return launch_with<64, 1>(p, workspace, sms, stream);
+    case 6416: return launch_with<64, 2>(p, workspace, sms, stream);
+    case 6432: return launch_with<64, 4>(p, workspace, sms, stream);
+    case 12808: return launch_with<128, 1>(p, workspace, sms, stream);
+    case 12816: return launch_with<128, 2>(p, workspace, sms, stream);
+    case 12832: return launch_with<128, 4>(p, workspace, sms, stream);
+    case 25608: return launch_with<256, 1>(p, workspace, sms, stream);
+    case 25616: return launch_with<256, 2>(p, workspace, sms, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+cudaError_t attention_wait_timeouts(int reset, int* out) {
+  cudaError_t err = cudaMemcpyFromSymbol(out, g_attention_timeouts, sizeof(int));
+  const int zero = 0;
+  if (err == cudaSuccess && reset) err = cudaMemcpyToSymbol(g_attention_timeouts, &zero, sizeof(int));
+  return err;
+}
+
+}  // namespace nvfp4

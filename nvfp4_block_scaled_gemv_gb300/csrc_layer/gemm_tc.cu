@@ -36,6 +36,7 @@
 #include <cstdint>
 #include <cstring>
 
+#include "attention.h"
 #include "gemm_common.cuh"
 
 namespace nvfp4 {
@@ -533,10 +534,11 @@ Footprint product_footprint(int tile_rows, bool gated) {
 }
 
 cudaError_t gemm_wait_timeouts(int reset, int* out) {
-  int own = 0, pairs = 0;
+  int own = 0, pairs = 0, cache = 0;
   cudaError_t err = cudaMemcpyFromSymbol(&own, g_gemm_timeouts, sizeof(int));
   if (err == cudaSuccess) err = gemm_pair_wait_timeouts(reset, &pairs);
-  *out = own + pairs;
+  if (err == cudaSuccess) err = attention_wait_timeouts(reset, &cache);  // (counted with the layer's)
+  *out = own + pairs + cache;
   if (err != cudaSuccess || !reset) return err;
   const int zero = 0;
   return cudaMemcpyToSymbol(g_gemm_timeouts, &zero, sizeof(int));
