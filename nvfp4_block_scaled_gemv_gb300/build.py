@@ -24,7 +24,7 @@ SOURCES = ["api.cu", "gemv_plain.cu", "gemv_permuted.cu", "gemv_async_plain.cu",
            "gemv_async_permuted.cu", "repack.cu", "gemv_tc.cu", "gemv_blockdot.cu",
            "gemv_blockwise.cu", "selftest.cu"]
 LAYER_SOURCES = ["quantize.cu", "gemm_tc.cu", "gemm_pair.cu", "route.cu", "moe.cu", "layer_api.cu", "rope.cu",
-                 "kv_cache.cu", "attention.cu", "attention_api.cu"]
+                 "kv_cache.cu", "attention.cu", "attention_prompt.cu", "attention_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr"]

@@ -126,7 +126,7 @@ __device__ __forceinline__ Sequence sequence_of(const AttentionParams& p, int b)
   if (p.window > 0) lo = (int32_t)max((int64_t)s.length - s.n + 1 - p.window, (int64_t)0);
   s.first_tile = lo / kTileTokens;
   // (one tile at least, so that somebody writes the result of an empty row)
-  s.tiles = s.n == 0 ? 0 : max((s.length + kTileTokens - 1) / kTileTokens - s.first_tile, 1);
+  s.tiles = s.n == 0 || (int64_t)s.n * p.group > p.few_columns ? 0 : max((s.length + kTileTokens - 1) / kTileTokens - s.first_tile, 1);
   return s;
 }
 
@@ -789,6 +789,9 @@ cudaError_t attention_wait_timeouts(int reset, int* out) {
   cudaError_t err = cudaMemcpyFromSymbol(out, g_attention_timeouts, sizeof(int));
   const int zero = 0;
   if (err == cudaSuccess && reset) err = cudaMemcpyToSymbol(g_attention_timeouts, &zero, sizeof(int));
+  int prompt = 0;
+  if (err == cudaSuccess) err = prompt_wait_timeouts(reset, &prompt);
+  *out += prompt;
   return err;
 }
 

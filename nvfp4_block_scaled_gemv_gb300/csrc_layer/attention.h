@@ -63,6 +63,7 @@ struct AttentionParams {
   int64_t q_token, q_head;
   int64_t pages, capacity;    // capacity: max_pages * page_size
   int32_t T, B, Hq, Hkv, group, uniform_n, max_pages, granules, window, causal;
+  int32_t few_columns;        // sequences of more columns are the prompt kernel's
   int32_t bf16;
   float scale_log2;           // scale * log2(e)
   // split of the work (set by the launcher)
@@ -75,6 +76,9 @@ constexpr int kAttentionCtas = 152;  // most CTAs of a launch, which the workspa
 int attention_columns(int D, int64_t most);
 int64_t attention_workspace(int D, int columns);
 cudaError_t launch_attention(AttentionParams p, int D, int columns, void* workspace, int sms, cudaStream_t stream);
+// Sequences of more than p.few_columns columns (attention_prompt.cu).
+cudaError_t launch_attention_prompt(const AttentionParams& p, int D, cudaStream_t stream);
+cudaError_t prompt_wait_timeouts(int reset, int* out);
 cudaError_t attention_wait_timeouts(int reset, int* out);
 
 }  // namespace nvfp4

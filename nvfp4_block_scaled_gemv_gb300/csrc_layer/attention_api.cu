@@ -16,6 +16,8 @@ constexpr int64_t kMaxStride = int64_t(1) << 40;
 constexpr int64_t kMaxBatch = int64_t(1) << 20;
 constexpr int64_t kMaxPage = int64_t(1) << 20;
 constexpr int64_t kMaxPairs = 512;
+// Sequences of more columns (query tokens x heads of a group) go to the kernel for prompts.
+constexpr int64_t kFewColumns = 64;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -94,6 +96,11 @@ nvfp4_status_t validate_attention(int64_t T, int64_t B, int64_t Hq, int64_t Hkv,
   return NVFP4_OK;
 }
 
+// Columns of a pass of the kernel for few query tokens.
+int few_pass(int64_t D, int64_t columns) {
+  return attention_columns((int)D, columns < kFewColumns ? columns : kFewColumns);
+}
+
 }  // namespace
 
 extern "C" {
@@ -166,7 +173,7 @@ size_t nvfp4_attention_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t
   int64_t most_q = 0;
   if (validate_attention(T, B, Hq, Hkv, D, 0, page_size, max_pages, ragged != 0, max_q, &most_q) != NVFP4_OK) return 0;
   if (T == 0) return 0;
-  return (size_t)attention_workspace((int)D, attention_columns((int)D, most_q * (Hq / Hkv)));
+  return (size_t)attention_workspace((int)D, few_pass(D, most_q * (Hq / Hkv)));
 }
 
 nvfp4_status_t nvfp4_attention(const void* q, int dtype, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
@@ -185,7 +192,8 @@ nvfp4_status_t nvfp4_attention(const void* q, int dtype, int64_t T, int64_t Hq, 
       !valid_stride(opt.q_token_stride) || !valid_stride(opt.q_head_stride))
     return NVFP4_ERR_INVALID_VALUE;
   if (T == 0 || B == 0) return NVFP4_OK;
-  const size_t need = (size_t)attention_workspace((int)D, attention_columns((int)D, most_q * (Hq / Hkv)));
+  const int64_t columns = most_q * (Hq / Hkv);
+  const size_t need = (size_t)attention_workspace((int)D, few_pass(D, columns));
   if (q == nullptr || out == nullptr || lengths == nullptr || (max_pages > 0 && page_table == nullptr) ||
       (pages > 0 && cache == nullptr) || workspace == nullptr || workspace_bytes < need)
     return NVFP4_ERR_INVALID_VALUE;
@@ -225,8 +233,14 @@ nvfp4_status_t nvfp4_attention(const void* q, int dtype, int64_t T, int64_t Hq, 
   int sms = 0;
   const cudaError_t err = device_sms(&sms);
   if (err != cudaSuccess) return result(err);
-  return result(launch_attention(p, (int)D, attention_columns((int)D, most_q * p.group), workspace, sms,
-                                 (cudaStream_t)stream));
+  // (a sequence beyond max_q is the other kernel's all the same, if no prompts are expected)
+  p.few_columns = INT32_MAX;
+  if (columns > kFewColumns) {
+    p.few_columns = (int32_t)kFewColumns;
+    const cudaError_t ran = launch_attention_prompt(p, (int)D, (cudaStream_t)stream);
+    if (ran != cudaSuccess || opt.q_starts == nullptr) return result(ran);
+  }
+  return result(launch_attention(p, (int)D, few_pass(D, columns), workspace, sms, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,705 @@
+// Attention of many query tokens per sequence on the 4-bit cache, on the tensor cores
+// (sm_103a, tcgen05): the same operator as attention.cu, for sequences whose queries and
+// heads of a group make more rows than that kernel takes at once.
+//
+// Its floor is the two products' operations, 4 D per row and token.  A CTA takes 128 NQ rows (query
+// tokens x heads of a group, which share the keys) of one sequence and key head, and walks the
+// tokens they see in tiles of BN.  The products are tcgen05.mma kind::f16, M = 128:
+//
+//   S = Q K^T   Q and K in shared memory; S in tensor memory, two buffers
+//   O += P V    P over S's columns in tensor memory, V in shared memory as it is laid out (its
+//               rows are the contraction); O in tensor memory
+//
+// Four warps turn raw granules into K and V tiles in fp16 (code * scale is exact) in the
+// 128-byte swizzled layout that the MMAs read, so that nothing but the 4-bit cache is read from
+// memory and nothing dequantised is written there.  Eight warps, a thread per row, do the
+// softmax: while one half's rows are worked on, the MMAs of the other half run.  A running
+// maximum is raised only where a score passes it by 8 (in base 2): p then stays
+// below 2^8, and the rows of O are seldom rescaled.  p is rounded to fp16 (2^-11 of itself),
+// sums are fp32 before that rounding.
+//
+// Warps: 0-3 and 4-7 softmax of rows 0-127 and 128-255 (NQ = 1: only the first four), 8-11 raw
+// tiles to fp16, 12 issues MMAs, 13 copies granules.
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "attention.h"
+#include "gemm_common.cuh"
+#include "layer.h"
+#include "ptx.cuh"
+#include "quantize.cuh"
+#include "tc_ptx.cuh"
+
+namespace nvfp4 {
+
+namespace {
+
+constexpr int kPromptThreads = 512;
+constexpr uint32_t kPromptColumns = 512;
+constexpr int kNanTiles = 4;  // tiles whose NaN marks are kept (more than are in flight)
+
+__device__ int g_prompt_timeouts;
+
+template <int D, int BN, int NQ>
+struct Prompt {
+  static constexpr int kPlanes = D / 64;
+  static constexpr int kRows = 128 * NQ;
+  static constexpr uint32_t kPanel = 128 * 128;                 // a plane of 128 rows of Q
+  static constexpr uint32_t kQBytes = (uint32_t)NQ * kPlanes * kPanel;
+  static constexpr uint32_t kTilePanel = BN * 128;              // a plane of a K or V tile
+  static constexpr uint32_t kSlot = kPlanes * kTilePanel;
+  static constexpr uint32_t kGranule = 2 * kPlanes * kPlaneBytes;
+  static constexpr int kGranules = BN / kGranuleTokens;
+  static constexpr uint32_t kRaw = kGranules * kGranule;
+  static constexpr int kSlots = D == 64 ? 6 : 3;
+  static constexpr int kRaws = D == 64 ? 4 : 2;
+  static constexpr uint32_t kUsed = 1024 + kQBytes + kSlots * kSlot + kRaws * kRaw + kNanTiles * (BN * 2 + 4);
+  static constexpr uint32_t kSmem = kUsed > gemm::kAloneSmem ? kUsed : gemm::kAloneSmem;
+  static_assert(kUsed <= 227 * 1024 - 4096, "shared memory");
+  static_assert(2 * kNanTiles >= kSlots + 1, "marks of tiles in flight");
+};
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
+}
+// kind::f16 with fp16 operands and fp32 results, M = 128; B's rows are the contraction (bit 16).
+__host__ __device__ constexpr uint32_t f16_idesc(uint32_t n, bool b_rows) {
+  return (1u << 4) | ((b_rows ? 1u : 0u) << 16) | ((n >> 3) << 17) | ((128u >> 4) << 24);
+}
+// A tile whose rows are the contraction: 128-byte rows of 64 elements, 8-row groups 1024 bytes
+// apart, the next 64 elements `panel` bytes on.
+__device__ __forceinline__ uint64_t desc_rows(uint32_t saddr, uint32_t panel) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(panel >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+#define NVFP4_R32(f) \
+  f(0), f(1), f(2), f(3), f(4), f(5), f(6), f(7), f(8), f(9), f(10), f(11), f(12), f(13), f(14), f(15), f(16), \
+  f(17), f(18), f(19), f(20), f(21), f(22), f(23), f(24), f(25), f(26), f(27), f(28), f(29), f(30), f(31)
+
+// 32 columns of this warp's lanes, without waiting for them.
+__device__ __forceinline__ void tmem_ld_32(uint32_t taddr, uint32_t* v) {
+#define NVFP4_OUT(i) "=r"(v[i])
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : NVFP4_R32(NVFP4_OUT)
+      : "r"(taddr));
+#undef NVFP4_OUT
+}
+// What was loaded is there (the registers pass through, so that nothing reads them earlier).
+__device__ __forceinline__ void tmem_ld_wait(uint32_t* v) {
+#define NVFP4_INOUT(i) "+r"(v[i])
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : NVFP4_R32(NVFP4_INOUT)::"memory");
+#undef NVFP4_INOUT
+}
+__device__ __forceinline__ void tmem_st_32(uint32_t taddr, const uint32_t* v) {
+#define NVFP4_IN(i) "r"(v[i])
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::NVFP4_R32(NVFP4_IN),
+      "r"(taddr)
+      : "memory");
+#undef NVFP4_IN
+}
+__device__ __forceinline__ void tmem_st_16(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15};" ::"r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+      "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void async_proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ float ex2(float x) {
+  float d;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(x));
+  return d;
+}
+__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// What a CTA works on; the same in all its threads.
+struct Work {
+  int32_t q0, n, length, head, first_row;  // rows: query token * group + head of the group
+  int32_t rows;                            // of the sequence
+  int32_t first_token, tiles;              // tokens from first_token, BN at a time
+  int32_t full_from, full_to;              // tokens that all its rows see
+  int32_t b;
+  bool beyond;
+};
+
+__device__ __forceinline__ void row_sees(const AttentionParams& p, int32_t length, int32_t n, int32_t row, int32_t& lo,
+                                         int32_t& hi) {
+  const int32_t i = row / p.group;
+  lo = 0;
+  hi = length;
+  if (p.causal) {
+    const int32_t position = length - n + i;
+    hi = position + 1;
+    if (p.window > 0) lo = max(position + 1 - p.window, 0);
+  }
+}
+
+// Scores of the tokens t to t + 31 outside [lo, hi) do not count.
+__device__ __forceinline__ void mask_32(uint32_t* v, int32_t t, int32_t lo, int32_t hi) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    if (t + i < lo || t + i >= hi) v[i] = 0xff800000u;
+}
+
+template <int BN>
+__device__ __forceinline__ bool tile_whole(const Work& w, int32_t t0) {
+  return t0 >= w.full_from && t0 + BN <= w.full_to;
+}
+
+// Query tokens of a sequence and its first row of q, and the tiles of rows it has here (none,
+// if the other kernel takes it).
+template <int ROWS>
+__device__ __forceinline__ int32_t row_tiles(const AttentionParams& p, int b, int32_t& q0, int32_t& n) {
+  if (p.q_starts != nullptr) {
+    const int32_t from = max(__ldg(p.q_starts + b), 0), to = min(__ldg(p.q_starts + b + 1), p.T);
+    q0 = from;
+    n = max(to - from, 0);
+  } else {
+    q0 = b * p.uniform_n;
+    n = p.uniform_n;
+  }
+  const int64_t rows = (int64_t)n * p.group;
+  return rows > p.few_columns ? (int32_t)((rows + ROWS - 1) / ROWS) : 0;
+}
+
+template <int D, int BN, int NQ>
+__global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(const AttentionParams p) {
+  using S = Prompt<D, BN, NQ>;
+  constexpr int kPlanes = S::kPlanes, kSlots = S::kSlots, kRaws = S::kRaws;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bars[2 * kRaws + 2 * kSlots + 8];
+  __shared__ uint32_t tmem_slot;
+  __shared__ uint32_t raw_bad[kRaws];      // granules of a raw tile whose page does not exist
+  __shared__ uint32_t warp_sums[16];
+  __shared__ Work shared_work;
+
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t q_s = base, slot_s = q_s + S::kQBytes, raw_s = slot_s + kSlots * S::kSlot;
+  uint8_t* const generic = smem_raw + (base - smem_u32(smem_raw));
+  uint16_t* const nan_marks = reinterpret_cast<uint16_t*>(generic + S::kQBytes + kSlots * S::kSlot + kRaws * S::kRaw);
+  uint32_t* const nan_any = reinterpret_cast<uint32_t*>(nan_marks + kNanTiles * BN);
+
+  const uint32_t bar0 = smem_u32(bars);
+  auto raw_full = [&](int i) { return bar0 + 8u * i; };
+  auto raw_empty = [&](int i) { return bar0 + 8u * (kRaws + i); };
+  auto slot_full = [&](int i) { return bar0 + 8u * (2 * kRaws + i); };
+  auto slot_empty = [&](int i) { return bar0 + 8u * (2 * kRaws + kSlots + i); };
+  const uint32_t more = bar0 + 8u * (2 * kRaws + 2 * kSlots);
+  const uint32_t q_full = more, drain = more + 8;
+  auto s_full = [&](int i) { return more + 16 + 8u * i; };
+  auto p_ready = [&](int i) { return more + 32 + 8u * i; };
+  auto o_done = [&](int i) { return more + 48 + 8u * i; };
+
+  const int lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kRaws; ++i) {
+      tc::mbar_init(raw_full(i), 1);
+      tc::mbar_init(raw_empty(i), 4);
+    }
+    for (int i = 0; i < kSlots; ++i) {
+      tc::mbar_init(slot_full(i), 4);
+      tc::mbar_init(slot_empty(i), 1);
+    }
+    tc::mbar_init(q_full, 4 * NQ);
+    tc::mbar_init(drain, 1);
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(s_full(i), 1);
+      tc::mbar_init(p_ready(i), 4);
+      tc::mbar_init(o_done(i), 1);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  pdl_wait();
+
+  // The CTA's work: row tiles are numbered over the sequences, the last (which sees most) of a
+  // sequence first, and the key heads of a row tile follow each other.
+  const int32_t rank = (int32_t)blockIdx.x / p.Hkv, head = (int32_t)blockIdx.x % p.Hkv;
+  {
+    const int share = (p.B + kPromptThreads - 1) / kPromptThreads;
+    const int b0 = threadIdx.x * share;
+    uint32_t mine = 0;
+    for (int b = b0; b < min(b0 + share, p.B); ++b) {
+      int32_t q0, n;
+      mine += (uint32_t)row_tiles<S::kRows>(p, b, q0, n);
+    }
+    uint32_t upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t o = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += o;
+    }
+    if (lane == 31) warp_sums[warp] = upto;
+    if (threadIdx.x == 0) shared_work.tiles = 0;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) upto += warp_sums[w];
+    uint32_t before = upto - mine;
+    if ((uint32_t)rank >= before && (uint32_t)rank < upto) {
+      for (int b = b0;; ++b) {
+        Work w;
+        const int32_t tiles = row_tiles<S::kRows>(p, b, w.q0, w.n);
+        if ((uint32_t)rank >= before + (uint32_t)tiles) {
+          before += (uint32_t)tiles;
+          continue;
+        }
+        w.b = b;
+        w.head = head;
+        w.rows = w.n * p.group;
+        w.first_row = (tiles - 1 - (rank - (int32_t)before)) * S::kRows;
+        const int32_t length = __ldg(p.lengths + b);
+        w.beyond = (int64_t)length > p.capacity;
+        w.length = w.beyond ? (int32_t)p.capacity : max(length, 0);
+        const int32_t last_row = min(w.first_row + S::kRows, w.rows) - 1;
+        int32_t l0, h0, l1, h1;
+        row_sees(p, w.length, w.n, w.first_row, l0, h0);
+        row_sees(p, w.length, w.n, last_row, l1, h1);
+        w.full_from = l1;
+        w.full_to = h0;
+        w.first_token = min(l0, max(h1, 0)) / BN * BN;
+        w.tiles = max((h1 - w.first_token + BN - 1) / BN, 1);
+        shared_work = w;
+        break;
+      }
+    }
+  }
+  __syncthreads();
+  if (shared_work.tiles == 0) return;  // (more CTAs than row tiles)
+  if (warp == 12) tc::alloc(smem_u32(&tmem_slot), kPromptColumns);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  pdl_launch_dependents();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
+  const Work work = shared_work;
+  const int32_t tiles = work.tiles;
+  bool ok = true;
+
+  // Fills of the slots: K of tile j is fill 2 j, V fill 2 j + 1.  Steps x of the products: with two
+  // halves tile x / 2 of half x & 1, otherwise tile x; S of a step is buffer x & 1.
+  const int32_t steps = tiles * NQ;
+  if (warp >= 12) {
+    if (warp == 13) {
+      // granules, a lane each
+      const int32_t have = (work.length + kGranuleTokens - 1) / kGranuleTokens;
+      int issued = 0;
+      auto page_of = [&](int32_t j) {
+        const int32_t granule = work.first_token / kGranuleTokens + j * S::kGranules + lane;
+        if (lane >= S::kGranules || j >= tiles || granule >= have) return INT32_MIN;
+        const int32_t id = __ldg(p.page_table + (int64_t)work.b * p.max_pages + granule / p.granules);
+        return id >= 0 && id < p.pages ? id : -1;
+      };
+      int32_t next = page_of(0);
+      for (int32_t j = 0; j < tiles && ok; ++j) {
+        const int i = j % kRaws;
+        const int32_t id = next;
+        next = page_of(j + 1);
+        tc::mbar_wait<false>(raw_empty(i), ((uint32_t)(j / kRaws) & 1u) ^ 1u, ok, &g_prompt_timeouts);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t valid = __ballot_sync(0xffffffffu, id >= 0);
+        const uint32_t bad = __ballot_sync(0xffffffffu, id == -1);
+        if (lane == 0) {
+          raw_bad[i] = bad;
+          tc::mbar_expect_tx(raw_full(i), (uint32_t)__popc(valid) * S::kGranule);
+        }
+        __syncwarp();
+        if (id >= 0) {
+          const int32_t granule = work.first_token / kGranuleTokens + j * S::kGranules + lane;
+          const int64_t at = ((int64_t)id * p.Hkv + work.head) * p.granules + granule % p.granules;
+          tc::bulk_load(raw_s + i * S::kRaw + lane * S::kGranule, p.cache + at * S::kGranule, S::kGranule, raw_full(i));
+        }
+        ++issued;
+      }
+      // copies still in flight land before the CTA can exit
+      bool landed = true;
+      for (int k = 0; k < kRaws && k < issued; ++k) {
+        const int i = issued - 1 - k;
+        tc::mbar_wait<false>(raw_full(i % kRaws), (uint32_t)((i / kRaws) & 1), landed, &g_prompt_timeouts);
+      }
+      __syncwarp();
+    } else if (warp == 12) {
+      constexpr uint32_t qk = f16_idesc(BN, false), pv = f16_idesc(D, true);
+      const uint64_t q_desc = tc::desc_sw128(q_s);
+      tc::mbar_wait<false>(q_full, 0, ok, &g_prompt_timeouts);
+      auto scores = [&](int32_t x) {
+        const int32_t j = NQ == 2 ? x >> 1 : x;
+        const int u = NQ == 2 ? x & 1 : 0;
+        const int fill = 2 * j, i = fill % kSlots;
+        tc::mbar_wait<false>(slot_full(i), (uint32_t)(fill / kSlots) & 1u, ok, &g_prompt_timeouts);
+        ok = __all_sync(0xffffffffu, ok);
+        tc::fence_after();
+        if (!ok) return;
+        const uint64_t a = q_desc + (uint64_t)(u * kPlanes * (S::kPanel >> 4));
+        const uint64_t b = tc::desc_sw128(slot_s + i * S::kSlot);
+        const uint32_t d = tmem + 128u * (x & 1);
+        if (gemm::elect_one()) {
+#pragma unroll
+          for (int c = 0; c < kPlanes; ++c)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_ss(d, a + c * (S::kPanel >> 4) + 2 * k, b + c * (S::kTilePanel >> 4) + 2 * k, qk, c + k > 0);
+          tc::commit(s_full(x & 1));
+          if (u == NQ - 1) tc::commit(slot_empty(i));
+        }
+        __syncwarp();
+      };
+      scores(0);
+      if (steps > 1) scores(1);
+      for (int32_t x = 0; x < steps && ok; ++x) {
+        const int32_t j = NQ == 2 ? x >> 1 : x;
+        const int u = NQ == 2 ? x & 1 : 0;
+        const int fill = 2 * j + 1, i = fill % kSlots;
+        tc::mbar_wait<false>(slot_full(i), (uint32_t)(fill / kSlots) & 1u, ok, &g_prompt_timeouts);
+        tc::mbar_wait<false>(p_ready(x & 1), (uint32_t)(x >> 1) & 1u, ok, &g_prompt_timeouts);
+        ok = __all_sync(0xffffffffu, ok);
+        tc::fence_after();
+        if (!ok) break;
+        const uint64_t b = desc_rows(slot_s + i * S::kSlot, S::kTilePanel);
+        const uint32_t a = tmem + 128u * (x & 1), d = tmem + 256u + 128u * u;
+        if (gemm::elect_one()) {
+#pragma unroll
+          for (int k = 0; k < BN / 16; ++k) mma_ts(d, a + 8u * k, b + (uint64_t)(k * (16 * 128 >> 4)), pv, j > 0 || k > 0);
+          tc::commit(o_done(u));
+          if (u == NQ - 1) tc::commit(slot_empty(i));
+        }
+        __syncwarp();
+        if (x + 2 < steps) scores(x + 2);
+      }
+      // every MMA has finished before tensor memory is released
+      if (gemm::elect_one()) tc::commit(drain);
+      bool drained = true;
+      tc::mbar_wait<false>(drain, 0, drained, &g_prompt_timeouts);
+      __syncwarp();
+    }
+  } else if (warp >= 8) {
+    // raw granules to fp16 tiles: a warp takes 8 tokens of a plane, a lane a block
+    const int w = warp - 8, row8 = lane >> 2, block = lane & 3;
+    constexpr int kUnits = BN / 8 * kPlanes / 4;  // per warp
+    for (int32_t j = 0; j < tiles && ok; ++j) {
+      const int ri = j % kRaws;
+      const int32_t t0 = work.first_token + j * BN;
+      const bool whole = tile_whole<BN>(work, t0);
+      if (lane == 0) tc::mbar_wait<false>(raw_full(ri), (uint32_t)(j / kRaws) & 1u, ok, &g_prompt_timeouts);
+      ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+      __syncwarp();
+      const uint32_t bad = raw_bad[ri];
+      const int marks = j % kNanTiles;
+#pragma unroll 1
+      for (int side = 0; side < 2 && ok; ++side) {
+        const int fill = 2 * j + side, si = fill % kSlots;
+        if (lane == 0)
+          tc::mbar_wait<false>(slot_empty(si), ((uint32_t)(fill / kSlots) & 1u) ^ 1u, ok, &g_prompt_timeouts);
+        ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+      __syncwarp();
+        if (!ok) break;
+        if (side == 1 && !whole) {
+          const int t = threadIdx.x - 256;
+          if (t < BN) nan_marks[marks * BN + t] = 0;
+          if (t == 0) nan_any[marks] = 0;
+          named_barrier_sync(1, 128);
+        }
+        const uint32_t from = raw_s + ri * S::kRaw + side * kPlanes * kPlaneBytes;
+        const uint32_t to = slot_s + si * S::kSlot;
+#pragma unroll 4
+        for (int k = 0; k < kUnits; ++k) {
+          const int unit = w + 4 * k;
+          const int group = unit / kPlanes, plane = unit % kPlanes;
+          const int t = group * 8 + row8;  // token of the tile
+          const uint32_t at = from + (group >> 1) * S::kGranule + plane * kPlaneBytes;
+          const int row = (group & 1) * 8 + row8;
+          uint2 codes;
+          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(codes.x), "=r"(codes.y) : "r"(at + row * 32 + block * 8));
+          uint32_t sb;
+          asm volatile("ld.shared.u8 %0, [%1];" : "=r"(sb) : "r"(at + kPlaneScales + row * 4 + block));
+          if (!whole || bad) {
+            const bool absent = (bad >> (group >> 1) & 1u) != 0;
+            if (t0 + t >= work.length || absent) sb = 0;
+            if (absent && side == 0) {
+              sb = 0x7Fu;  // its scores are NaN
+            } else if (side == 1 && !whole && (sb & 0x7Fu) == 0x7Fu) {
+              // rows that do not see the token must not get its NaN: the block is 0 here, and
+              // marked for the rows that do
+              sb = 0;
+              const int bit = plane * 4 + block;
+              const uint32_t word = smem_u32(nan_marks + marks * BN + (t & ~1));
+              const uint32_t mark = 1u << (bit + 16 * (t & 1));
+              asm volatile("red.shared.or.b32 [%0], %1;" ::"r"(word), "r"(mark) : "memory");
+              asm volatile("st.shared.b32 [%0], %1;" ::"r"(smem_u32(nan_any + marks)), "r"(1u) : "memory");
+            }
+          }
+          const uint32_t s2 = e4m3x2_to_f16x2(sb * 0x101u);
+          uint32_t h[8];
+          e2m1x8_to_f16x2x4(codes.x, *reinterpret_cast<uint32_t(*)[4]>(&h[0]));
+          e2m1x8_to_f16x2x4(codes.y, *reinterpret_cast<uint32_t(*)[4]>(&h[4]));
+#pragma unroll
+          for (int i = 0; i < 8; ++i) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h[i]) : "r"(s2));
+          // two 16-byte chunks of the token's row, swizzled by the row
+          const uint32_t line = to + plane * S::kTilePanel + t * 128;
+          const uint32_t c0 = (uint32_t)((2 * block) ^ (t & 7)) * 16u;
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(line + c0), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
+                       : "memory");
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(line + (c0 ^ 16u)), "r"(h[4]), "r"(h[5]), "r"(h[6]),
+                       "r"(h[7])
+                       : "memory");
+        }
+        async_proxy_fence();
+        __syncwarp();
+        if (lane == 0) {
+          tc::mbar_arrive(slot_full(si));
+          if (side == 1) tc::mbar_arrive(raw_empty(ri));
+        }
+      }
+    }
+  } else {
+    const int u = warp >> 2;
+    if (u < NQ) {
+      const int r = threadIdx.x & 127;          // row of the half, and lane of tensor memory
+      const int32_t row = work.first_row + u * 128 + r;
+      const bool real = row < work.rows;
+      const int32_t token = row / p.group, member = row - token * p.group;
+      const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+      // the row of Q, as fp16 (bf16: in a power of two of its own, see attention.cu)
+      float back = 1.f;
+      {
+        const uint16_t* const src = static_cast<const uint16_t*>(p.q) +
+                                    (real ? (int64_t)(work.q0 + token) * p.q_token +
+                                                (int64_t)(work.head * p.group + member) * p.q_head
+                                          : 0);
+        float by = 1.f;
+        if (p.bf16 && real) {
+          float largest = 0.f;
+#pragma unroll 4
+          for (int c = 0; c < D / 8; ++c) {
+            const uint4 v = reinterpret_cast<const uint4*>(src)[c];
+            const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              largest = fmaxf(largest, fmaxf(fabsf(__uint_as_float(words[i] << 16)),
+                                             fabsf(__uint_as_float(words[i] & 0xffff0000u))));
+          }
+          const int e = min(max(14 - ((int)(__float_as_uint(largest) >> 23) - 127), -113), 113);
+          by = __uint_as_float((uint32_t)(e + 127) << 23);
+          back = __uint_as_float((uint32_t)(127 - e) << 23);
+        }
+        const uint32_t line = q_s + u * kPlanes * S::kPanel + r * 128;
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (real) v = reinterpret_cast<const uint4*>(src)[c];
+          uint32_t words[4] = {v.x, v.y, v.z, v.w};
+          if (p.bf16) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              words[i] = half2_of(__uint_as_float(words[i] << 16) * by, __uint_as_float(words[i] & 0xffff0000u) * by);
+          }
+          const uint32_t at = line + (c >> 3) * S::kPanel + (uint32_t)((c & 7) ^ (r & 7)) * 16u;
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(words[0]), "r"(words[1]), "r"(words[2]),
+                       "r"(words[3])
+                       : "memory");
+        }
+      }
+      async_proxy_fence();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(q_full);
+
+      const float c = p.scale_log2 * (p.encode_k ? 1.f / __ldg(p.encode_k + work.head) : 1.f) * back;
+      int32_t lo, hi;
+      row_sees(p, work.length, work.n, real ? row : work.rows - 1, lo, hi);
+      float m = -INFINITY;       // the row's reference score, before c
+      uint64_t sum = 0;          // two partial sums
+      uint32_t nan_blocks = 0;   // blocks of 16 whose V is NaN in a token that the row sees
+      const uint32_t o_at = tmem + lanes + 256u + 128u * u;
+#pragma unroll 1
+      for (int32_t j = 0; j < tiles; ++j) {
+        const int32_t x = NQ == 2 ? 2 * j + u : j;
+        const uint32_t s_at = tmem + lanes + 128u * (x & 1);
+        const int32_t t0 = work.first_token + j * BN;
+        if (lane == 0) tc::mbar_wait<false>(s_full(x & 1), (uint32_t)(x >> 1) & 1u, ok, &g_prompt_timeouts);
+        ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+      __syncwarp();
+        if (!ok) break;
+        tc::fence_after();
+        const bool whole = tile_whole<BN>(work, t0);
+        // Two passes over S, 32 columns at a time with the next ones on their way: its 128 values,
+        // held from the maximum to the exponentials, are more than the registers take.
+        uint32_t s[2][32];
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        tmem_ld_32(s_at, s[0]);
+        tmem_ld_wait(s[0]);
+#pragma unroll
+        for (int h = 0; h < BN / 32; ++h) {
+          uint32_t* const v = s[h & 1];
+          tmem_ld_32(s_at + (h + 1 < BN / 32 ? 32 * (h + 1) : 0), s[(h + 1) & 1]);
+          if (!whole) mask_32(v, t0 + 32 * h, lo, hi);
+#pragma unroll
+          for (int i = 0; i < 32; i += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              top[k] = fmaxf(fmaxf(top[k], __uint_as_float(v[i + 2 * k])), __uint_as_float(v[i + 2 * k + 1]));
+          tmem_ld_wait(s[(h + 1) & 1]);
+        }
+        const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        // (from -inf any score passes)
+        const bool up = (now - m) * c > 8.f || (m == -INFINITY && now > m);
+        if (__any_sync(0xffffffffu, up)) {
+          const float f = up ? (m == -INFINITY ? 0.f : ex2((m - now) * c)) : 1.f;
+          if (up) m = now;
+          const float2 two = unpack_f32x2(sum);
+          sum = pack_f32x2(two.x * f, two.y * f);
+          if (j > 0) {
+            if (lane == 0) tc::mbar_wait<false>(o_done(u), (uint32_t)(j - 1) & 1u, ok, &g_prompt_timeouts);
+            ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+      __syncwarp();
+            if (!ok) break;
+            tc::fence_after();
+#pragma unroll 1
+            for (int i = 0; i < D; i += 32) {
+              uint32_t o[32];
+              tmem_ld_32(o_at + i, o);
+              tmem_ld_wait(o);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              tmem_st_32(o_at + i, o);
+            }
+          }
+        }
+        const float base2 = m == -INFINITY ? 0.f : -m * c;
+        const uint64_t c2 = pack_f32x2(c, c), b2 = pack_f32x2(base2, base2), one2 = pack_f32x2(1.f, 1.f);
+        uint64_t other = 0;
+        // (the first 32 columns are there again; P's columns 16 h lie over S's that have been read)
+#pragma unroll
+        for (int h = 0; h < BN / 32; ++h) {
+          uint32_t* const v = s[h & 1];
+          if (h + 1 < BN / 32) tmem_ld_32(s_at + 32 * (h + 1), s[(h + 1) & 1]);
+          if (!whole) mask_32(v, t0 + 32 * h, lo, hi);
+          uint32_t packed[16];
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            float2 a = unpack_f32x2(fma2(pack_f32x2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), c2, b2));
+            float2 b = unpack_f32x2(fma2(pack_f32x2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])), c2, b2));
+            a.x = ex2(a.x), a.y = ex2(a.y), b.x = ex2(b.x), b.y = ex2(b.y);
+            sum = fma2(pack_f32x2(a.x, a.y), one2, sum);
+            other = fma2(pack_f32x2(b.x, b.y), one2, other);
+            packed[i / 2] = half2_of(a.x, a.y);
+            packed[i / 2 + 1] = half2_of(b.x, b.y);
+          }
+          if (h + 1 < BN / 32) tmem_ld_wait(s[(h + 1) & 1]);
+          tmem_st_16(s_at + 16 * h, packed);
+        }
+        sum = fma2(other, one2, sum);
+        if (!whole) {
+          // (before P is handed over: V's slot and marks are not used again until then)
+          const int fill = 2 * j + 1;
+          if (lane == 0) tc::mbar_wait<false>(slot_full(fill % kSlots), (uint32_t)(fill / kSlots) & 1u, ok, &g_prompt_timeouts);
+          ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+      __syncwarp();
+          if (!ok) break;
+          const int marks = j % kNanTiles;
+          if (nan_any[marks] != 0)
+            for (int i = 0; i < BN; ++i)
+              if (t0 + i >= lo && t0 + i < hi) nan_blocks |= nan_marks[marks * BN + i];
+        }
+        tmem_st_wait();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(p_ready(x & 1));
+      }
+      if (lane == 0) tc::mbar_wait<false>(o_done(u), (uint32_t)(tiles - 1) & 1u, ok, &g_prompt_timeouts);
+      ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+      __syncwarp();
+      tc::fence_after();
+      const float2 two = unpack_f32x2(sum);
+      const float l = two.x + two.y;
+      const float decode = p.encode_v ? 1.f / __ldg(p.encode_v + work.head) : 1.f;
+      float f = l == 0.f ? 0.f : decode / l;
+      if (work.beyond) f = __int_as_float(0x7fc00000);
+      const int64_t out_row = (int64_t)(work.q0 + token) * p.Hq + (int64_t)work.head * p.group + member;
+      if (ok && real && p.lse != nullptr)
+        p.lse[out_row] = work.beyond ? f : l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.69314718055994531f;
+#pragma unroll 1
+      for (int i = 0; i < D && ok; i += 32) {
+        uint32_t o[32];
+        tmem_ld_32(o_at + i, o);
+        tmem_ld_wait(o);
+        uint32_t words[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const float g = nan_blocks >> (i / 16 + k / 8) & 1u ? __int_as_float(0x7fc00000) : f;
+          const float a = __uint_as_float(o[2 * k]) * g, b = __uint_as_float(o[2 * k + 1]) * g;
+          if (p.bf16) {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+            words[k] = *reinterpret_cast<const uint32_t*>(&v);
+          } else {
+            words[k] = half2_of(a, b);
+          }
+        }
+        if (real) {
+          uint4* const to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + out_row * D + i);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) to[k] = make_uint4(words[4 * k], words[4 * k + 1], words[4 * k + 2], words[4 * k + 3]);
+        }
+      }
+    }
+  }
+  tc::fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc::fence_after();
+    tc::dealloc(tmem, kPromptColumns);
+  }
+}
+
+template <int D, int BN, int NQ>
+cudaError_t launch_with(const AttentionParams& p, cudaStream_t stream) {
+  using S = Prompt<D, BN, NQ>;
+  const cudaError_t err = allow_smem<attention_prompt_kernel<D, BN, NQ>>(S::kSmem);
+  if (err != cudaSuccess) return err;
+  // row tiles, at most: every sequence that has some begins one more than its rows fill
+  const int64_t rows = (int64_t)p.T * p.group;
+  const int64_t sequences = rows / (p.few_columns + 1);
+  const int64_t tiles = rows / S::kRows + (sequences < p.B ? sequences : p.B);
+  return launch_pdl(attention_prompt_kernel<D, BN, NQ>, dim3((unsigned)(tiles * p.Hkv)), dim3(kPromptThreads), S::kSmem,
+                    stream, p);
+}
+
+}  // namespace
+
+cudaError_t launch_attention_prompt(const AttentionParams& p, int D, cudaStream_t stream) {
+  return D == 64    ? launch_with<64, 128, 2>(p, stream)
+         : D == 128 ? launch_with<128, 128, 2>(p, stream)
+                    : launch_with<256, 64, 1>(p, stream);
+}
+
+cudaError_t prompt_wait_timeouts(int reset, int* out) {
+  cudaError_t err = cudaMemcpyFromSymbol(out, g_prompt_timeouts, sizeof(int));
+  const int zero = 0;
+  if (err == cudaSuccess && reset) err = cudaMemcpyToSymbol(g_prompt_timeouts, &zero, sizeof(int));
+  return err;
+}
+
+}  // namespace nvfp4

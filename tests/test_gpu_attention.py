@@ -288,6 +288,91 @@ def test_attention(lens, n, Hq, Hkv, D, page, dtype):
     assert torch.equal(out, again)
 
 
+PROMPTS = [
+    # more rows than the kernel for few query tokens takes: one, two and many row tiles, lengths
+    # around the tiles' ends, queries without a prefix and behind one, rows before the sequence
+    ([130], 130, 1, 1, 64, 16), ([300, 129], 128, 4, 2, 128, 64), ([70, 700], 65, 3, 3, 128, 48),
+    ([513], 300, 8, 2, 64, 32), ([200, 128, 127], 100, 2, 1, 256, 16), ([256], 256, 6, 6, 256, 64),
+    ([1030], 17, 40, 4, 128, 16), ([20, 0, 90], 80, 4, 4, 128, 16), ([1500], 3, 64, 1, 128, 64),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("lens,n,Hq,Hkv,D,page", PROMPTS)
+def test_attention_of_prompts(lens, n, Hq, Hkv, D, page, dtype):
+    rng = np.random.default_rng(sum(lens) + Hq + D)
+    z = problem(rng, lens, [n] * len(lens), Hq, Hkv, D, page, dtype)
+    out, lse = nv.attention(z["q"].to(DEV), **on_gpu(z), return_lse=True)
+    check(z, out, lse, dtype)
+    assert torch.equal(out, nv.attention(z["q"].to(DEV), **on_gpu(z)))
+
+
+@pytest.mark.parametrize("window,causal,scale", [(1, True, None), (16, True, 0.3), (150, True, None), (0, False, None)])
+@pytest.mark.parametrize("n,Hq,Hkv,D", [(70, 8, 8, 64), (130, 4, 2, 128), (90, 3, 3, 256)])
+def test_attention_of_prompts_masks(n, Hq, Hkv, D, window, causal, scale):
+    rng = np.random.default_rng(window + n)
+    z = problem(rng, [400, 131, 2, 140], [n] * 4, Hq, Hkv, D, 16, "fp16")
+    out, lse = nv.attention(z["q"].to(DEV), **on_gpu(z), return_lse=True, window=window, causal=causal, scale=scale or 0.0)
+    check(z, out, lse, "fp16", scale=scale, window=window, causal=causal)
+
+
+def test_attention_of_prompts_and_single_tokens_together():
+    """Both kernels in one call, sequences of no queries among them."""
+    rng = np.random.default_rng(21)
+    lens, counts = [900, 333, 64, 0, 512, 40, 700], [1, 200, 64, 0, 8, 33, 300]
+    z = problem(rng, lens, counts, 8, 2, 128, 32, "bf16")
+    out = torch.full((sum(counts) + 9, 8, 128), 3.0, dtype=torch.bfloat16, device=DEV)
+    q = torch.cat((z["q"], torch.full((9, 8, 128), float("nan"), dtype=torch.bfloat16))).to(DEV)
+    for max_q in (0, 300, 2):  # (2 is wrong: the results are right all the same)
+        out.fill_(3.0)
+        _, lse = nv.attention(q, **on_gpu(z), q_starts=gpu(z["starts"]), max_q=max_q, return_lse=True, out=out)
+        check(z, out[:-9], lse[:-9], "bf16")
+        assert (out[-9:] == 3).all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_of_prompts_does_not_see_masked_nan(D):
+    rng = np.random.default_rng(22)
+    z = problem(rng, [300], [140], 2, 2, D, 16, "fp16")
+    full = z["cache"].copy()
+    clean = nv.attention(z["q"].to(DEV), **on_gpu(z))
+    for t in (299, 230, 161, 160, 100):
+        page, at = int(z["table"][0, t // 16]), t % 16
+        first = max(0, t - 160)  # the first query that sees the token
+        z["cache"] = full.copy()
+        z["cache"][page, 1, 0, 1, 0, 512 + at * 4 + 2] = 0x7F
+        out = nv.attention(z["q"].to(DEV), **on_gpu(z))
+        bad = torch.zeros(140, 2, D, dtype=torch.bool, device=DEV)
+        bad[first:, 1, 32:48] = True
+        assert torch.equal(out.isnan(), bad) and torch.equal(out[~bad], clean[~bad]), t
+        z["cache"] = full.copy()
+        z["cache"][page, 1, 0, 0, D // 64 - 1, 512 + at * 4] = 0x7F
+        out, lse = nv.attention(z["q"].to(DEV), **on_gpu(z), return_lse=True)
+        bad[:] = False
+        bad[first:, 1] = True
+        assert torch.equal(out.isnan(), bad) and torch.equal(out[~bad], clean[~bad]), t
+        assert torch.equal(lse.isnan(), bad[..., 0])
+
+
+def test_attention_of_prompts_pages_that_are_not_there():
+    rng = np.random.default_rng(23)
+    z = problem(rng, [300, 200], [140, 140], 2, 1, 128, 16, "bf16")
+    good = nv.attention(z["q"].to(DEV), **on_gpu(z))
+    for wrong in (-1, z["cache"].shape[0], 2 ** 31 - 1):
+        t = z["table"].copy()
+        t[0, 14] = wrong  # tokens 224 to 239: queries from 224 - 160 on
+        out, lse = nv.attention(z["q"].to(DEV), **on_gpu(z | {"table": t}), return_lse=True)
+        assert out[64:140].isnan().all() and lse[64:140].isnan().all()
+        assert torch.equal(out[:64], good[:64]) and torch.equal(out[140:], good[140:])
+        t[0, 14], t[0, 1] = z["table"][0, 14], wrong
+        assert nv.attention(z["q"].to(DEV), **on_gpu(z | {"table": t}))[:140].isnan().all()
+    lens = np.array([z["table"].shape[1] * 16 + 1, 200], dtype=np.int32)
+    table = np.where(np.arange(z["table"].shape[1]) < 13, z["table"], z["table"][1, 0])
+    out, lse = nv.attention(z["q"].to(DEV), **on_gpu(z | {"lens": lens, "table": np.abs(table) % z["cache"].shape[0]}),
+                            return_lse=True)
+    assert out[:140].isnan().all() and lse[:140].isnan().all()
+
+
 @pytest.mark.parametrize("window,causal,scale", [(1, True, None), (16, True, 0.3), (33, True, None), (100, True, None),
                                                  (100000, True, None), (0, False, None), (0, False, 0.02)])
 @pytest.mark.parametrize("n,Hq,Hkv,D", [(1, 8, 2, 128), (5, 6, 2, 64), (3, 4, 1, 256)])
