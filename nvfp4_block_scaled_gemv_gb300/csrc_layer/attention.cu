@@ -16,9 +16,9 @@
 // copies, a copy per 16 tokens (a granule of the cache, K and V in one run of bytes).  All
 // tiles of all sequences and heads, one after another, are cut into equal runs, one per
 // warp, whatever the lengths are; the lengths are read on the device.  A warp that has all
-// of an item (a head's columns of one sequence) writes its result; of an item that is
-// shared, every warp leaves its piece (maximum, sum, unnormalised result) in the workspace, and a
-// second small kernel adds the pieces in the order of the tokens.
+// of an item (a head's columns of one sequence) writes its result.  Of an item that is
+// shared, every warp leaves its piece (maximum, sum, unnormalised result); a CTA adds up its warps'
+// pieces, and a second small kernel those of CTAs that share an item, in the order of the tokens.
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -35,6 +35,7 @@ namespace {
 
 constexpr int kTileTokens = 32;  // a stage: two granules
 constexpr int kMostWarps = 16;
+constexpr int64_t kPieceList = (kAttentionCtas * (int64_t)sizeof(int4) + 255) / 256 * 256;
 
 __device__ int g_attention_timeouts;
 
@@ -200,6 +201,47 @@ __device__ __forceinline__ void write_columns(const AttentionParams& p, const Se
     }
 }
 
+// What a warp has of an item that is not all its own: `columns` rows of D unnormalised results,
+// and the columns' maxima and sums behind them.
+struct Piece {
+  float* at;      // null: none
+  int32_t b, item;
+  int64_t end;    // the item's end among all tiles
+};
+
+// One more piece of a column: (maximum, sum) and four results.
+__device__ __forceinline__ void add_piece(float& m, float& l, float4& o, float2 ml, float4 v) {
+  const float top = fmaxf(m, ml.x);
+  const float fa = m == top ? 1.f : exp2_fast(m - top), fb = ml.x == top ? 1.f : exp2_fast(ml.x - top);
+  o.x = o.x * fa + v.x * fb;
+  o.y = o.y * fa + v.y * fb;
+  o.z = o.z * fa + v.z * fb;
+  o.w = o.w * fa + v.w * fb;
+  l = l * fa + ml.y * fb;
+  m = top;
+}
+
+// Four results of a column that is all there.
+template <int D>
+__device__ __forceinline__ void write_four(const AttentionParams& p, const Sequence& s, int head, int column, int d,
+                                           float4 o, float m, float l) {
+  const int i = column / p.group;
+  if (i >= s.n) return;
+  const int64_t row = (int64_t)(s.q0 + i) * p.Hq + (int64_t)head * p.group + (column - i * p.group);
+  float f = l == 0.f ? 0.f : (p.encode_v ? 1.f / __ldg(p.encode_v + head) : 1.f) / l;
+  if (s.beyond) f = __int_as_float(0x7fc00000);
+  if (p.lse != nullptr && d == 0)
+    p.lse[row] = s.beyond ? f : l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+  uint2 w;
+  if (p.bf16) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(o.x * f, o.y * f), y = __floats2bfloat162_rn(o.z * f, o.w * f);
+    w = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+  } else {
+    w = make_uint2(pack_h2(o.x * f, o.y * f), pack_h2(o.z * f, o.w * f));
+  }
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * D + d) = w;
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(const AttentionParams p) {
   using S = Shape<D, NT>;
@@ -214,6 +256,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
   const uint32_t bars = smem_u32(smem) + kWarps * kStages * S::kStage + warp * kStages * 8;
   int64_t* const scan = reinterpret_cast<int64_t*>(smem + kWarps * kStages * (S::kStage + 8));
   __shared__ int64_t warp_sums[kMostWarps];
+  __shared__ Piece piece_of[kMostWarps][2];  // that goes on with an item, that begins one
+  __shared__ int chain_of[2 * kMostWarps + 1];
 
   pdl_launch_dependents();
   if (lane == 0) {
@@ -250,11 +294,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
   const int64_t all = (int64_t)per_cta * gridDim.x;
   const int warps = (int)(all < total ? all : total);
   const int rank = (int)blockIdx.x * per_cta + warp;
-  const int slot = (int)blockIdx.x * kWarps + warp;  // of the piece list
-  if (warp >= per_cta || rank >= warps) {
-    if (lane == 0) p.pieces[slot] = make_int4(-1, 0, 0, 0);
-    return;
-  }
+  const bool works = warp < per_cta && rank < warps;
+  if (lane == 0) piece_of[warp][0].at = piece_of[warp][1].at = nullptr;
+  if (threadIdx.x == 0) p.pieces[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  __syncwarp();
+  if (works) {
   const int64_t begin = run_start(total, warps, rank), end = run_start(total, warps, rank + 1);
 
   // the sequence, head, column tile and tile at `begin`
@@ -346,7 +390,6 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
   int64_t left = end - begin;
   uint32_t stage = 0, parity = 0;
   bool ok = true;
-  int4 first_piece = make_int4(-1, 0, 0, 0);
   while (left > 0) {
     // an item, or the part of it in this run
     const int head = item / cts, first_column = (item - head * cts) * C;
@@ -652,9 +695,10 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
     if (from == 0 && to == seq.tiles) {
       write_columns<D, NT>(p, seq, head, first_column, o, m, l);
     } else {
-      // a piece: the second place is for one that begins the item, the first for one that
-      // goes on with it (a run that does neither begin nor end it is one that goes on)
-      float* const piece = p.partial + ((int64_t)rank * 2 + (from == 0 ? 1 : 0)) * S::kPiece;
+      // A piece.  The run's last one goes where its ring was; one before that, which the ring is
+      // still in use beside, to the workspace.
+      float* const piece = left == 0 ? reinterpret_cast<float*>(smem + warp * kStages * S::kStage)
+                                     : p.partial + ((int64_t)2 * kAttentionCtas + (int64_t)blockIdx.x * kWarps + warp) * S::kPiece;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -671,9 +715,12 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
           }
           if (g == 0) *reinterpret_cast<float2*>(piece + C * D + column * 2) = make_float2(m[nt][e], l[nt][e]);
         }
-      if (from == 0) {
-        const int64_t item_end = before + ((int64_t)item + 1) * seq.tiles;
-        first_piece = make_int4(b, item, rank, run_of(total, warps, item_end - 1));
+      if (lane == 0) {
+        Piece& to_merge = piece_of[warp][from == 0 ? 1 : 0];
+        to_merge.at = piece;
+        to_merge.b = b;
+        to_merge.item = item;
+        to_merge.end = before + ((int64_t)item + 1) * seq.tiles;
       }
     }
     // on to the next item
@@ -687,11 +734,60 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
       } while (seq.tiles == 0);
     }
   }
-  if (lane == 0) p.pieces[slot] = first_piece;
-}
+  }
 
-// The pieces of an item added up: a CTA per warp of the first kernel, for the item that its
-// run began and others go on with, if there is one.
+  // The CTA's pieces, in the order of its warps: chains of one item each.  Every chain is added up
+  // by some warps, into the item's result if it is all there, otherwise into one of the CTA's two
+  // places of the workspace: for an item that goes on from the CTA before, and for one that begins
+  // here and goes on in the next.
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int chains = 0;
+    for (int i = 0; i < 2 * kWarps; ++i) {
+      if (piece_of[i >> 1][i & 1].at == nullptr) continue;
+      if (chains == 0 || (i & 1)) chain_of[++chains] = i;
+    }
+    chain_of[0] = chains;
+  }
+  __syncthreads();
+  const int chains = chain_of[0];
+  if (chains == 0) return;
+  const int64_t cta_end = run_start(total, warps, min(((int)blockIdx.x + 1) * per_cta, warps));
+  const int each = chains < kWarps ? kWarps / chains : 1;  // warps per chain
+  for (int chain = warp / each; chain < chains; chain += kWarps / each) {
+    const int first = chain_of[chain + 1], last = chain + 1 < chains ? chain_of[chain + 2] : 2 * kWarps;
+    const Piece head_piece = piece_of[first >> 1][first & 1];
+    const bool begins = (first & 1) != 0, ends = head_piece.end <= cta_end;
+    const Sequence seq = sequence_of(p, head_piece.b);
+    const int32_t cts = column_tiles(p, seq.n, C);
+    const int head = head_piece.item / cts, first_column = (head_piece.item - head * cts) * C;
+    float* const sum_at = p.partial + ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * S::kPiece;
+    for (int e = (warp % each) * 32 + lane; e < C * D / 4; e += each * 32) {
+      const int c = e / (D / 4), d = e % (D / 4) * 4;
+      float m = -INFINITY, l = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+      for (int i = first; i < last; ++i) {
+        const float* const at = piece_of[i >> 1][i & 1].at;
+        if (at == nullptr) continue;
+        const float2 ml = *reinterpret_cast<const float2*>(at + C * D + 2 * c);
+        const float4 v = *reinterpret_cast<const float4*>(at + c * D + d);
+        add_piece(m, l, o, ml, v);
+      }
+      if (begins && ends) {
+        write_four<D>(p, seq, head, first_column + c, d, o, m, l);
+      } else {
+        *reinterpret_cast<float4*>(sum_at + c * D + d) = o;
+        if (d == 0) *reinterpret_cast<float2*>(sum_at + C * D + 2 * c) = make_float2(m, l);
+      }
+    }
+    if (begins && !ends && warp % each == 0 && lane == 0)
+      p.pieces[blockIdx.x] = make_int4(head_piece.b, head_piece.item, run_of(total, warps, head_piece.end - 1) / per_cta, 0);
+  }
+  }
+
+// The pieces of an item that several CTAs share added up: some CTAs for each CTA of the first
+// kernel, for the item that begins in it and goes on in the next, if there is one.
 template <int D, int NT>
 __global__ void __launch_bounds__(128) attention_sum_kernel(const AttentionParams p) {
   using S = Shape<D, NT>;
@@ -703,44 +799,18 @@ __global__ void __launch_bounds__(128) attention_sum_kernel(const AttentionParam
   const Sequence seq = sequence_of(p, piece.x);
   const int32_t cts = column_tiles(p, seq.n, C);
   const int head = piece.y / cts, first_column = (piece.y - head * cts) * C;
-  const float decode = p.encode_v ? 1.f / __ldg(p.encode_v + head) : 1.f;
-  constexpr int kLanes = D / 4;  // threads of a column
-  const int d = threadIdx.x % kLanes * 4;
-  for (int c = threadIdx.x / kLanes; c < C; c += 128 / kLanes) {
-    const int column = first_column + c;
-    const int i = column / p.group;
-    if (i >= seq.n) break;
-    const float* const first = p.partial + ((int64_t)piece.z * 2 + 1) * S::kPiece;
-    const float2 ml0 = *reinterpret_cast<const float2*>(first + C * D + 2 * c);
-    float4 o = *reinterpret_cast<const float4*>(first + c * D + d);
-    float m = ml0.x, l = ml0.y;
+  const int e = (int)blockIdx.y * 128 + threadIdx.x;
+  const int c = e / (D / 4), d = e % (D / 4) * 4;
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int w = piece.z + 1; w <= piece.w; ++w) {
-      const float* const next = p.partial + (int64_t)w * 2 * S::kPiece;
-      const float2 ml = *reinterpret_cast<const float2*>(next + C * D + 2 * c);
-      const float4 v = *reinterpret_cast<const float4*>(next + c * D + d);
-      const float top = fmaxf(m, ml.x);
-      const float fa = m == top ? 1.f : exp2_fast(m - top), fb = ml.x == top ? 1.f : exp2_fast(ml.x - top);
-      o.x = o.x * fa + v.x * fb;
-      o.y = o.y * fa + v.y * fb;
-      o.z = o.z * fa + v.z * fb;
-      o.w = o.w * fa + v.w * fb;
-      l = l * fa + ml.y * fb;
-      m = top;
-    }
-    const int64_t row = (int64_t)(seq.q0 + i) * p.Hq + (int64_t)head * p.group + (column - i * p.group);
-    float f = l == 0.f ? 0.f : decode / l;
-    if (seq.beyond) f = __int_as_float(0x7fc00000);
-    if (p.lse != nullptr && d == 0) p.lse[row] = seq.beyond ? f : l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
-    uint2 w;
-    if (p.bf16) {
-      const __nv_bfloat162 x = __floats2bfloat162_rn(o.x * f, o.y * f), y = __floats2bfloat162_rn(o.z * f, o.w * f);
-      w = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
-    } else {
-      w = make_uint2(pack_h2(o.x * f, o.y * f), pack_h2(o.z * f, o.w * f));
-    }
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * D + d) = w;
+  for (int w = blockIdx.x; w <= piece.z; ++w) {
+    const float* const at = p.partial + ((int64_t)w * 2 + (w == (int)blockIdx.x ? 1 : 0)) * S::kPiece;
+    const float2 ml = *reinterpret_cast<const float2*>(at + C * D + 2 * c);
+    const float4 v = *reinterpret_cast<const float4*>(at + c * D + d);
+    add_piece(m, l, o, ml, v);
   }
+  write_four<D>(p, seq, head, first_column + c, d, o, m, l);
 }
 
 template <int D, int NT>
@@ -750,10 +820,10 @@ cudaError_t launch_with(AttentionParams p, void* workspace, int sms, cudaStream_
   const cudaError_t err = allow_smem<attention_kernel<D, NT>>(S::kSmem);
   if (err != cudaSuccess) return err;
   p.pieces = static_cast<int4*>(workspace);
-  p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kAttentionCtas * kMostWarps * sizeof(int4));
+  p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kPieceList);
   const cudaError_t ran = launch_pdl(attention_kernel<D, NT>, dim3((unsigned)ctas), dim3(S::kThreads), S::kSmem, stream, p);
   if (ran != cudaSuccess) return ran;
-  return launch_pdl(attention_sum_kernel<D, NT>, dim3((unsigned)(ctas * S::kWarps)), dim3(128), 0, stream, p);
+  return launch_pdl(attention_sum_kernel<D, NT>, dim3((unsigned)ctas, S::kColumns * D / 512), dim3(128), 0, stream, p);
 }
 
 }  // namespace
@@ -767,8 +837,7 @@ int attention_columns(int D, int64_t most) {
 
 int64_t attention_workspace(int D, int columns) {
   const int warps = D * (columns / 8) <= 128 ? 16 : 8;
-  return (int64_t)kAttentionCtas * kMostWarps * (int64_t)sizeof(int4) +
-         (int64_t)kAttentionCtas * warps * 2 * columns * (D + 2) * 4;
+  return kPieceList + (int64_t)kAttentionCtas * (2 + warps) * columns * (D + 2) * 4;
 }
 
 cudaError_t launch_attention(AttentionParams p, int D, int columns, void* workspace, int sms, cudaStream_t stream) {

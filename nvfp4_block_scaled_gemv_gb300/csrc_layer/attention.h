@@ -67,8 +67,8 @@ struct AttentionParams {
   int32_t bf16;
   float scale_log2;           // scale * log2(e)
   // split of the work (set by the launcher)
-  float* partial;             // [warps][2] pieces
-  int4* pieces;               // [warps]: the item whose first piece a warp has
+  float* partial;             // pieces: [CTAs][2] and [CTAs][warps]
+  int4* pieces;               // [CTAs]: {sequence, item, last CTA, 0} of the item that goes on in the next
 };
 constexpr int kAttentionCtas = 152;  // most CTAs of a launch, which the workspace is made for
 // Columns (query token and head of a group, together) that one pass over the cache takes
