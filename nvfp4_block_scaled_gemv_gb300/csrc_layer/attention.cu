@@ -2,7 +2,8 @@
 //
 //   s[t] = scale * q . k[t],  p = exp(s - max s),  out = sum_t p[t] v[t] / sum_t p[t]
 //
-// over the tokens that a query sees, in one pass over the cache with a running maximum.
+// over the tokens that a query sees, in one pass over the cache with a running reference for the
+// maximum.
 //
 // Its floor is the cache's bytes: K and V of a token and head are 9/8 D bytes, and the C
 // = query tokens x heads of the group columns that share them are few.  So a column
@@ -19,6 +20,7 @@
 // of an item (a head's columns of one sequence) writes its result.  Of an item that is
 // shared, every warp leaves its piece (maximum, sum, unnormalised result); a CTA adds up its warps'
 // pieces, and a second small kernel those of CTAs that share an item, in the order of the tokens.
+#include <cfloat>
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -327,53 +329,40 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
   // the loader: the same walk, some stages ahead
   Sequence ahead = seq;
   int lb = b;
-  int32_t litem = item, ltile = tile, lcts = cts;
+  int32_t litem = item, lcts = cts;
+  int32_t ltile = seq.first_tile + tile, ltile_end = seq.first_tile + seq.tiles;  // of the sequence
   int64_t to_load = end - begin;
-  int32_t ids = 0, ids_tile = -1;  // a lane's page of granule ids_tile * 2 + lane
+  // a lane's granule of the next 16 tiles, as its number in the cache, or kAbsent (past the
+  // length) or kBad (its page does not exist)
+  constexpr int64_t kAbsent = -1, kBad = -2;
+  int64_t source = kAbsent;
+  int32_t source_tile = ltile - 16;
   uint32_t load_stage = 0;
   uint32_t bad_bits = 0;           // two bits a stage: granules whose page does not exist
   auto load_next = [&]() {
     if (to_load == 0) return;
-    const int32_t at = ahead.first_tile + ltile;  // tile of the sequence
-    if (ids_tile < 0 || at >= ids_tile + 16) {
-      ids_tile = at;
-      const int64_t page = (int64_t)(at * 2 + lane) / p.granules;
-      ids = page < p.max_pages && (at * 2 + lane) * (int64_t)kGranuleTokens < ahead.length
-                ? __ldg(p.page_table + (int64_t)lb * p.max_pages + page)
-                : 0;
-    }
-    const int head = litem / lcts;
-    const int32_t granules = (ahead.length + kGranuleTokens - 1) / kGranuleTokens;
-    uint32_t bad = 0, bytes = 0;
-    const uint32_t bar = bars + 8 * load_stage, dst = ring + load_stage * S::kStage;
-    int32_t id[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      id[i] = __shfl_sync(0xffffffffu, ids, (at - ids_tile) * 2 + i);
-      if (at * 2 + i >= granules) {
-        id[i] = -1;
-      } else if (id[i] < 0 || id[i] >= p.pages) {
-        id[i] = -1;
-        bad |= 1u << i;
-      } else {
-        bytes += S::kGranule;
+    if (ltile >= source_tile + 16) {
+      source_tile = ltile;
+      const int32_t granule = ltile * 2 + lane;
+      source = kAbsent;
+      if (granule < (ahead.length + kGranuleTokens - 1) / kGranuleTokens) {
+        const int32_t page = granule / p.granules;
+        const int32_t id = __ldg(p.page_table + (int64_t)lb * p.max_pages + page);
+        source = id < 0 || id >= p.pages ? kBad
+                                         : ((int64_t)id * p.Hkv + litem / lcts) * p.granules + (granule - page * p.granules);
       }
     }
-    if (lane == 0) {
-      tc::mbar_expect_tx(bar, bytes);
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (id[i] >= 0) {
-          const int64_t granule = ((int64_t)id[i] * p.Hkv + head) * p.granules + (at * 2 + i) % p.granules;
-          tc::bulk_load(dst + i * S::kGranule, p.cache + granule * S::kGranule, S::kGranule, bar);
-        }
-    }
+    const uint32_t bar = bars + 8 * load_stage, dst = ring + load_stage * S::kStage;
+    const int64_t mine = __shfl_sync(0xffffffffu, source, (ltile - source_tile) * 2 + (lane & 1));
+    const uint32_t valid = __ballot_sync(0xffffffffu, mine >= 0) & 3u;
+    const uint32_t bad = __ballot_sync(0xffffffffu, mine == kBad) & 3u;
+    if (lane == 0) tc::mbar_expect_tx(bar, (uint32_t)__popc(valid) * S::kGranule);
+    __syncwarp();
+    if (valid >> lane & 1u) tc::bulk_load(dst + lane * S::kGranule, p.cache + mine * S::kGranule, S::kGranule, bar);
     bad_bits = (bad_bits & ~(3u << (2 * load_stage))) | bad << (2 * load_stage);
     load_stage = load_stage + 1 == kStages ? 0 : load_stage + 1;
-    if (--to_load == 0) return;
-    if (++ltile == ahead.tiles) {
-      ltile = 0;
-      ids_tile = -1;
+    --to_load;
+    if (++ltile == ltile_end && to_load != 0) {
       if (++litem == lcts * p.Hkv) {
         litem = 0;
         do {
@@ -381,6 +370,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
         } while (ahead.tiles == 0);
         lcts = column_tiles(p, ahead.n, C);
       }
+      ltile = ahead.first_tile;
+      ltile_end = ltile + ahead.tiles;
+      source_tile = ltile - 16;
     }
   };
   __syncwarp();
@@ -400,7 +392,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
     // values go over in a power of two of the row's own (its largest between 2^14 and 2^15),
     // so that fp16's range is enough; what is then below 2^-39 of the largest is lost.
     uint32_t qf[S::kPlanes][4][2][NT];
-    float cs[NT][2];  // score scale of the columns 8 nt + 2 q + e
+    float cs[NT][2];  // score scale of the columns 8 nt + 2 q + e (not 0 or infinite: those times 0 or
+                      // an infinity would be NaN)
     const float scale = p.scale_log2 * (p.encode_k ? 1.f / __ldg(p.encode_k + head) : 1.f);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -452,7 +445,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
           qf[c][j][1][nt] = w[c][2 * j + 1];
         }
 #pragma unroll
-      for (int e = 0; e < 2; ++e) cs[nt][e] = scale * __shfl_sync(0xffffffffu, back, (2 * q + e) * 4);
+      for (int e = 0; e < 2; ++e)
+        cs[nt][e] = fminf(fmaxf(scale * __shfl_sync(0xffffffffu, back, (2 * q + e) * 4), FLT_MIN), FLT_MAX);
     }
     // what the columns see; tiles from full_from to full_to are seen by all of them whole
     int32_t lo[NT][2], hi[NT][2];
@@ -486,9 +480,12 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
 #pragma unroll 1
     for (; tile < to; ++tile) {
       const uint32_t bar = bars + 8 * stage, base = ring + stage * S::kStage;
-      if (lane == 0) tc::mbar_wait<false>(bar, parity, ok, &g_attention_timeouts);
-      ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-      if (!ok) break;
+      if (!__all_sync(0xffffffffu, tc::mbar_try(bar, parity))) {
+        if (lane == 0) tc::mbar_wait<false>(bar, parity, ok, &g_attention_timeouts);
+        ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+        if (!ok) break;
+        __syncwarp();
+      }
       const int32_t t0 = (seq.first_tile + tile) * kTileTokens;
       const uint32_t bad = bad_bits >> (2 * stage) & 3u;
       const bool whole = t0 >= full_from && t0 + kTileTokens <= full_to && bad == 0;  // (the same in all lanes)
@@ -525,13 +522,6 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
               mma_f16(s[i][nt], a[2 * j], d[2 * j], a[2 * j + 1], d[2 * j + 1], qf[c][j][0][nt], qf[c][j][1][nt]);
         }
       }
-      // scores in base 2, masked
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) s[i][nt][j] *= cs[nt][j & 1];
       if (!whole) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -551,33 +541,36 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
               }
           }
       }
-      // the running maximum and what it does to sums and results
-      float keep[NT][2];
-      bool moved = false;
+      // The reference that p is taken from is raised only where a score passes it by 8 (in base
+      // 2): p stays below 2^8, results are seldom rescaled, and most tiles ask a vote of the lanes
+      // in place of the maximum over them.
+      bool passed = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float top = fmaxf(fmaxf(s[0][nt][e], s[0][nt][2 + e]), fmaxf(s[1][nt][e], s[1][nt][2 + e]));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-          const bool up = top > m[nt][e];
-          const float now = up ? top : m[nt][e];
-          keep[nt][e] = up ? exp2_fast(m[nt][e] - now) : 1.f;
-          moved |= up;
-          m[nt][e] = now;
+          const float top = fmaxf(fmaxf(s[0][nt][e], s[0][nt][2 + e]), fmaxf(s[1][nt][e], s[1][nt][2 + e]));
+          // (from -inf any score passes; -inf - -inf is NaN and does not)
+          passed |= (top - m[nt][e]) * cs[nt][e] > 8.f;
         }
-      if (__any_sync(0xffffffffu, moved)) {
+      if (__any_sync(0xffffffffu, passed)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            l[nt][e] *= keep[nt][e];
+            float top = fmaxf(fmaxf(s[0][nt][e], s[0][nt][2 + e]), fmaxf(s[1][nt][e], s[1][nt][2 + e]));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+            if (top > m[nt][e]) {  // (the same in all lanes of a column)
+              const float keep = exp2_fast((m[nt][e] - top) * cs[nt][e]);
+              m[nt][e] = top;
+              l[nt][e] *= keep;
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-              o[i][nt][e] *= keep[nt][e];
-              o[i][nt][2 + e] *= keep[nt][e];
+              for (int i = 0; i < D / 16; ++i) {
+                o[i][nt][e] *= keep;
+                o[i][nt][2 + e] *= keep;
+              }
             }
           }
       }
@@ -585,12 +578,14 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
       uint32_t pf[2][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+        // (an empty row's maximum stays -inf: all its p are 0)
+        const float m0 = m[nt][0] == -INFINITY ? 0.f : -m[nt][0] * cs[nt][0], m1 = m[nt][1] == -INFINITY ? 0.f : -m[nt][1] * cs[nt][1];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const float p0 = exp2_fast(s[i][nt][2 * r] - m0), p1 = exp2_fast(s[i][nt][2 * r + 1] - m1);
+            const float p0 = exp2_fast(fmaf(s[i][nt][2 * r], cs[nt][0], m0));
+            const float p1 = exp2_fast(fmaf(s[i][nt][2 * r + 1], cs[nt][1], m1));
             l[nt][0] += p0;
             l[nt][1] += p1;
             pf[i][nt][r] = transpose_8x8(pack_h2(p0, p1));
@@ -683,7 +678,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
     if (!ok) break;
     left -= to - from;
 
-    // sums over the lanes that have a column's tokens
+    // sums over the lanes that have a column's tokens, and the maxima in base 2
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -691,6 +686,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
         l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 4);
         l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 8);
         l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 16);
+        m[nt][e] *= cs[nt][e];
       }
     if (from == 0 && to == seq.tiles) {
       write_columns<D, NT>(p, seq, head, first_column, o, m, l);

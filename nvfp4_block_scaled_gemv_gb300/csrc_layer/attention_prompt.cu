@@ -20,6 +20,7 @@
 //
 // Warps: 0-3 and 4-7 softmax of rows 0-127 and 128-255 (NQ = 1: only the first four), 8-11 raw
 // tiles to fp16, 12 issues MMAs, 13 copies granules.
+#include <cfloat>
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -527,7 +528,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(q_full);
 
-      const float c = p.scale_log2 * (p.encode_k ? 1.f / __ldg(p.encode_k + work.head) : 1.f) * back;
+      // (not 0 or infinite: those times 0 or an infinity would be NaN)
+      const float c = fminf(fmaxf(p.scale_log2 * (p.encode_k ? 1.f / __ldg(p.encode_k + work.head) : 1.f) * back, FLT_MIN), FLT_MAX);
       int32_t lo, hi;
       row_sees(p, work.length, work.n, real ? row : work.rows - 1, lo, hi);
       float m = -INFINITY;       // the row's reference score, before c
