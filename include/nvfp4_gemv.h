@@ -712,8 +712,8 @@ nvfp4_status_t nvfp4_kv_read(const nvfp4_kv_rows_t* rows, int dtype, int64_t T, 
  *   scale      : > 0; 0 = 1 / sqrt(D)
  *   causal     : 0 or 1
  *   window     : 0 = none (needs causal)
- *   max_q      : with q_starts, the most query tokens of a sequence (0 = T); a bound for the
- *                choice of kernels, results are right for sequences beyond it too
+ *   max_q      : with q_starts, the most query tokens of a sequence (0 = T), for the choice of
+ *                kernels; the rows of a sequence with more may be left as they are
  *   q_starts   : NULL (T / B query tokens each), or int32 [B + 1]: rows q_starts[b] to
  *                q_starts[b + 1] - 1 of q are sequence b's; rows behind the last stay as they are
  *   encode_k, encode_v : as nvfp4_kv_write had them
@@ -726,7 +726,9 @@ nvfp4_status_t nvfp4_kv_read(const nvfp4_kv_rows_t* rows, int dtype, int64_t T, 
  * workspace: nvfp4_attention_workspace_bytes bytes, 256-byte aligned; need not be kept, but no
  * two calls that may run at once can share it.
  * Accuracy: scores and sums in fp32, the p to fp16 before the product with v, out rounded once.
- * Limits: Hq % Hkv == 0, T * Hq < 2^31, max_pages * page_size < 2^31 - 64, B <= 2^20.
+ * Limits: Hq % Hkv == 0, T * Hq < 2^31, max_pages * page_size < 2^31 - 64, B <= 2^20, and
+ * B * Hkv * max_pages * page_size < 2^36, less by the passes that more than 8 query tokens x heads of
+ * a group take (up to 8).
  */
 typedef struct {
   float scale;

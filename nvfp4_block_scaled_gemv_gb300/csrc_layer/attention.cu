@@ -52,8 +52,7 @@ struct Shape {
   static constexpr int kStagesFit = (220 * 1024 / kWarps - 64) / kStage;
   static constexpr int kStages = kStagesFit < 6 ? kStagesFit : 6;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kScanBytes = (kThreads + 1) * 8;
-  static constexpr size_t kSmem = (size_t)kWarps * kStages * (kStage + 8) + kScanBytes + 256;
+  static constexpr size_t kSmem = (size_t)kWarps * kStages * (kStage + 8);
   static constexpr int kPiece = kColumns * (D + 2);  // floats: columns of D, then (maximum, sum)
   static_assert(kStages >= 2, "two stages at least");
 };
@@ -125,23 +124,28 @@ __device__ __forceinline__ Sequence sequence_of(const AttentionParams& p, int b)
   const int32_t length = __ldg(p.lengths + b);
   s.beyond = (int64_t)length > p.capacity;
   s.length = s.beyond ? (int32_t)p.capacity : max(length, 0);
-  int32_t lo = 0;
-  if (p.window > 0) lo = (int32_t)max((int64_t)s.length - s.n + 1 - p.window, (int64_t)0);
+  const int32_t next = s.length - s.n + 1;  // tokens up to the first query's
+  const int32_t lo = p.window > 0 && next > p.window ? next - p.window : 0;
   s.first_tile = lo / kTileTokens;
   // (one tile at least, so that somebody writes the result of an empty row)
-  s.tiles = s.n == 0 || (int64_t)s.n * p.group > p.few_columns ? 0 : max((s.length + kTileTokens - 1) / kTileTokens - s.first_tile, 1);
+  s.tiles = s.n == 0 || s.n * p.group > p.few_columns ? 0 : max((s.length + kTileTokens - 1) / kTileTokens - s.first_tile, 1);
   return s;
 }
 
 __device__ __forceinline__ int32_t column_tiles(const AttentionParams& p, int32_t n, int columns) {
-  return (int32_t)(((int64_t)n * p.group + columns - 1) / columns);
+  return (int32_t)((uint32_t)(n * p.group + columns - 1) / (uint32_t)columns);
 }
 
-// The warps' runs: warp w of `warps` takes the tiles [total w / warps, total (w + 1) / warps).
-__device__ __forceinline__ int64_t run_start(int64_t total, int warps, int w) { return total * w / warps; }
-__device__ __forceinline__ int run_of(int64_t total, int warps, int64_t tile) {
-  return (int)(((tile + 1) * warps - 1) / total);
-}
+// The warps' runs of all tiles (fewer than 2^31, the host has seen to that): the first
+// `longer` warps have one more than the others.
+struct Runs {
+  uint32_t each, longer;
+  __device__ __forceinline__ uint32_t start(uint32_t w) const { return each * w + min(w, longer); }
+  __device__ __forceinline__ uint32_t of(uint32_t tile) const {
+    const uint32_t cut = (each + 1) * longer;
+    return tile < cut ? tile / (each + 1) : longer + (tile - cut) / each;
+  }
+};
 
 // The token of a row (0..7) of a matrix instruction's half: the loads of K (rows 0-3 and 4-7
 // of a half-warp together) and of V (rows 0, 2, 4, 6 and 1, 3, 5, 7 together) then each touch
@@ -158,7 +162,7 @@ __device__ __forceinline__ void seen_by(const AttentionParams& p, const Sequence
   } else if (p.causal) {
     const int32_t position = s.length - s.n + i;
     hi = position + 1;  // (0 or less: an empty row)
-    if (p.window > 0) lo = max(position + 1 - p.window, 0);
+    if (p.window > 0 && hi > p.window) lo = hi - p.window;
   }
 }
 
@@ -167,7 +171,7 @@ __device__ __forceinline__ void write_columns(const AttentionParams& p, const Se
                                               const float (&o)[D / 16][NT][4], const float (&m)[NT][2],
                                               const float (&l)[NT][2]) {
   const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-  const float decode = p.encode_v ? 1.f / __ldg(p.encode_v + head) : 1.f;
+  const float decode = p.encode_v ? __frcp_rn(__ldg(p.encode_v + head)) : 1.f;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -206,21 +210,21 @@ __device__ __forceinline__ void write_columns(const AttentionParams& p, const Se
 // What a warp has of an item that is not all its own: `columns` rows of D unnormalised results,
 // and the columns' maxima and sums behind them.
 struct Piece {
-  float* at;      // null: none
-  int32_t b, item;
-  int64_t end;    // the item's end among all tiles
+  const float* at;  // null: none
+  Sequence seq;
+  uint32_t end;     // the item's end among all tiles
+  int32_t b, item, head, first_column;
+  int32_t early;    // in the workspace, not where the warp's ring was
 };
 
-// One more piece of a column: (maximum, sum) and four results.
-__device__ __forceinline__ void add_piece(float& m, float& l, float4& o, float2 ml, float4 v) {
-  const float top = fmaxf(m, ml.x);
-  const float fa = m == top ? 1.f : exp2_fast(m - top), fb = ml.x == top ? 1.f : exp2_fast(ml.x - top);
-  o.x = o.x * fa + v.x * fb;
-  o.y = o.y * fa + v.y * fb;
-  o.z = o.z * fa + v.z * fb;
-  o.w = o.w * fa + v.w * fb;
-  l = l * fa + ml.y * fb;
-  m = top;
+// One more piece of a column, (maximum, sum) and four results, given the maximum of all.
+__device__ __forceinline__ void add_piece(float m, float& l, float4& o, float2 ml, float4 v) {
+  const float f = ml.x == m ? 1.f : exp2_fast(ml.x - m);
+  o.x = fmaf(v.x, f, o.x);
+  o.y = fmaf(v.y, f, o.y);
+  o.z = fmaf(v.z, f, o.z);
+  o.w = fmaf(v.w, f, o.w);
+  l = fmaf(ml.y, f, l);
 }
 
 // Four results of a column that is all there.
@@ -230,7 +234,7 @@ __device__ __forceinline__ void write_four(const AttentionParams& p, const Seque
   const int i = column / p.group;
   if (i >= s.n) return;
   const int64_t row = (int64_t)(s.q0 + i) * p.Hq + (int64_t)head * p.group + (column - i * p.group);
-  float f = l == 0.f ? 0.f : (p.encode_v ? 1.f / __ldg(p.encode_v + head) : 1.f) / l;
+  float f = l == 0.f ? 0.f : (p.encode_v ? __frcp_rn(__ldg(p.encode_v + head)) : 1.f) / l;
   if (s.beyond) f = __int_as_float(0x7fc00000);
   if (p.lse != nullptr && d == 0)
     p.lse[row] = s.beyond ? f : l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
@@ -256,10 +260,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
   const int g = lane >> 2, q = lane & 3;
   const uint32_t ring = smem_u32(smem) + warp * kStages * S::kStage;
   const uint32_t bars = smem_u32(smem) + kWarps * kStages * S::kStage + warp * kStages * 8;
-  int64_t* const scan = reinterpret_cast<int64_t*>(smem + kWarps * kStages * (S::kStage + 8));
-  __shared__ int64_t warp_sums[kMostWarps];
-  __shared__ Piece piece_of[kMostWarps][2];  // that goes on with an item, that begins one
-  __shared__ int chain_of[2 * kMostWarps + 1];
+  __shared__ uint32_t warp_sums[kMostWarps];
+  __shared__ uint32_t share_ends[S::kThreads];  // tiles up to the end of each thread's share, in its warp
+  __shared__ Piece piece_of[kMostWarps][2];     // that goes on with an item, that begins one
 
   pdl_launch_dependents();
   if (lane == 0) {
@@ -268,70 +271,69 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
   }
   pdl_wait();
 
-  // tiles of all sequences before each thread's share of them
+  // The tiles of each thread's share of the sequences, their sum, the cut of it into runs, and the
+  // sequence that each of this CTA's runs starts in.
   const int share = (p.B + S::kThreads - 1) / S::kThreads;
-  {
-    int64_t mine = 0;
-    for (int b = threadIdx.x * share; b < min((int)(threadIdx.x + 1) * share, p.B); ++b) {
-      const Sequence s = sequence_of(p, b);
-      mine += (int64_t)s.tiles * column_tiles(p, s.n, C);
-    }
-    int64_t upto = mine;
+  const int first_b = threadIdx.x * share;
+  uint32_t mine = 0;
+  for (int b = first_b; b < min(first_b + share, p.B); ++b) {
+    const Sequence seq = sequence_of(p, b);
+    mine += (uint32_t)(seq.tiles * column_tiles(p, seq.n, C));
+  }
+  mine *= (uint32_t)p.Hkv;
+  uint32_t upto = mine;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int64_t o = __shfl_up_sync(0xffffffffu, upto, d);
-      if (lane >= d) upto += o;
-    }
-    if (lane == 31) warp_sums[warp] = upto;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) upto += warp_sums[w];
-    scan[threadIdx.x + 1] = upto * p.Hkv;
-    if (threadIdx.x == 0) scan[0] = 0;
-    __syncthreads();
+  for (int d = 1; d < 32; d <<= 1) {
+    const uint32_t o = __shfl_up_sync(0xffffffffu, upto, d);
+    if (lane >= d) upto += o;
   }
-  const int64_t total = scan[S::kThreads];
-  // warps in use: those of a CTA that are needed for every CTA to have as many
-  const int64_t even = (total + gridDim.x - 1) / gridDim.x;
-  const int per_cta = (int)(even < kWarps ? even : kWarps);
-  const int64_t all = (int64_t)per_cta * gridDim.x;
-  const int warps = (int)(all < total ? all : total);
-  const int rank = (int)blockIdx.x * per_cta + warp;
-  const bool works = warp < per_cta && rank < warps;
-  if (lane == 0) piece_of[warp][0].at = piece_of[warp][1].at = nullptr;
+  share_ends[threadIdx.x] = upto;
+  if (lane < 2) piece_of[warp][lane].at = nullptr;
   if (threadIdx.x == 0) p.pieces[blockIdx.x] = make_int4(-1, 0, 0, 0);
-  __syncwarp();
-  if (works) {
-  const int64_t begin = run_start(total, warps, rank), end = run_start(total, warps, rank + 1);
-
-  // the sequence, head, column tile and tile at `begin`
-  int b = 0;
-  {
-    int lo = 0, hi = S::kThreads;  // the last share that starts at or before it
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (scan[mid] <= begin) lo = mid; else hi = mid;
-    }
-    b = lo * share;
+  __syncthreads();
+  // (a lane has the sum of a warp's shares)
+  uint32_t ends = lane < kWarps ? share_ends[lane * 32 + 31] : 0;
+#pragma unroll
+  for (int d = 1; d < kWarps; d <<= 1) {
+    const uint32_t o = __shfl_up_sync(0xffffffffu, ends, d);
+    if (lane >= d) ends += o;
   }
-  int64_t before = scan[b / share];
+  const uint32_t total = __shfl_sync(0xffffffffu, ends, kWarps - 1);
+  if (total == 0) return;
+  // warps in use: those of a CTA that are needed for every CTA to have as many
+  const uint32_t per_cta = min((total + gridDim.x - 1) / gridDim.x, (uint32_t)kWarps);
+  const uint32_t warps = min(per_cta * gridDim.x, total);
+  Runs runs;
+  runs.each = total / warps;
+  runs.longer = total - runs.each * warps;
+  const uint32_t cta_rank = blockIdx.x * per_cta, rank = cta_rank + warp;
+  if (warp < (int)per_cta && rank < warps) {
+  const uint32_t begin = runs.start(rank), end = runs.start(rank + 1);
+  // the sequence that the run starts in: its warp of shares, its share, and the place there
+  const int chunk = __ffs(__ballot_sync(0xffffffffu, lane < kWarps && begin < ends)) - 1;
+  uint32_t before = chunk == 0 ? 0 : __shfl_sync(0xffffffffu, ends, chunk - 1);
+  const uint32_t share_end = before + share_ends[chunk * 32 + lane];
+  const int place = __ffs(__ballot_sync(0xffffffffu, begin < share_end)) - 1;
+  if (place > 0) before = __shfl_sync(0xffffffffu, share_end, place - 1);
+  int b = (chunk * 32 + place) * share;
   Sequence seq = sequence_of(p, b);
-  int32_t cts = column_tiles(p, seq.n, C);
   for (;;) {
-    const int64_t here = (int64_t)seq.tiles * cts * p.Hkv;
+    const uint32_t here = (uint32_t)(seq.tiles * column_tiles(p, seq.n, C)) * (uint32_t)p.Hkv;
     if (before + here > begin) break;
     before += here;
     seq = sequence_of(p, ++b);
-    cts = column_tiles(p, seq.n, C);
   }
-  int32_t item = (int32_t)((begin - before) / seq.tiles);  // head * cts + column tile
-  int32_t tile = (int32_t)((begin - before) - (int64_t)item * seq.tiles);
+  // head, column tile and tile at `begin`
+  int32_t cts = column_tiles(p, seq.n, C);
+  int32_t item = (int32_t)((begin - before) / (uint32_t)seq.tiles);  // head * cts + column tile
+  int32_t tile = (int32_t)(begin - before) - item * seq.tiles;
 
   // the loader: the same walk, some stages ahead
   Sequence ahead = seq;
   int lb = b;
   int32_t litem = item, lcts = cts;
   int32_t ltile = seq.first_tile + tile, ltile_end = seq.first_tile + seq.tiles;  // of the sequence
-  int64_t to_load = end - begin;
+  uint32_t to_load = end - begin;
   // a lane's granule of the next 16 tiles, as its number in the cache, or kAbsent (past the
   // length) or kBad (its page does not exist)
   constexpr int64_t kAbsent = -1, kBad = -2;
@@ -375,18 +377,15 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
       source_tile = ltile - 16;
     }
   };
-  __syncwarp();
-#pragma unroll 1
-  for (int i = 0; i < kStages; ++i) load_next();
-
-  int64_t left = end - begin;
+  uint32_t left = end - begin;
+  bool primed = false;
   uint32_t stage = 0, parity = 0;
   bool ok = true;
   while (left > 0) {
     // an item, or the part of it in this run
     const int head = item / cts, first_column = (item - head * cts) * C;
     const int32_t from = tile;
-    const int32_t to = (int32_t)((int64_t)(seq.tiles - tile) < left ? seq.tiles : tile + left);
+    const int32_t to = (uint32_t)(seq.tiles - tile) < left ? seq.tiles : tile + (int32_t)left;
 
     // its queries: column 8 nt + g, a lane's 16 elements of every plane, as fp16.  bf16
     // values go over in a power of two of the row's own (its largest between 2^14 and 2^15),
@@ -394,7 +393,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
     uint32_t qf[S::kPlanes][4][2][NT];
     float cs[NT][2];  // score scale of the columns 8 nt + 2 q + e (not 0 or infinite: those times 0 or
                       // an infinity would be NaN)
-    const float scale = p.scale_log2 * (p.encode_k ? 1.f / __ldg(p.encode_k + head) : 1.f);
+    const float encode = p.encode_k ? __ldg(p.encode_k + head) : 1.f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int column = first_column + nt * 8 + g;
@@ -416,6 +415,12 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
         for (int c = 0; c < S::kPlanes; ++c)
 #pragma unroll
           for (int j = 0; j < 8; ++j) w[c][j] = 0u;
+      }
+      if (nt == 0 && !primed) {
+        // (the first queries are on their way)
+        primed = true;
+#pragma unroll 1
+        for (int j = 0; j < kStages; ++j) load_next();
       }
       float back = 1.f;
       if (p.bf16) {
@@ -446,7 +451,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
         }
 #pragma unroll
       for (int e = 0; e < 2; ++e)
-        cs[nt][e] = fminf(fmaxf(scale * __shfl_sync(0xffffffffu, back, (2 * q + e) * 4), FLT_MIN), FLT_MAX);
+        cs[nt][e] = fminf(fmaxf(p.scale_log2 * __frcp_rn(encode) * __shfl_sync(0xffffffffu, back, (2 * q + e) * 4), FLT_MIN), FLT_MAX);
     }
     // what the columns see; tiles from full_from to full_to are seen by all of them whole
     int32_t lo[NT][2], hi[NT][2];
@@ -676,7 +681,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
       if (++stage == kStages) stage = 0, parity ^= 1;
     }
     if (!ok) break;
-    left -= to - from;
+    left -= (uint32_t)(to - from);
 
     // sums over the lanes that have a column's tokens, and the maxima in base 2
 #pragma unroll
@@ -716,7 +721,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
         to_merge.at = piece;
         to_merge.b = b;
         to_merge.item = item;
-        to_merge.end = before + ((int64_t)item + 1) * seq.tiles;
+        to_merge.head = head;
+        to_merge.first_column = first_column;
+        to_merge.early = left != 0;
+        to_merge.end = before + (uint32_t)((item + 1) * seq.tiles);
+        to_merge.seq = seq;
       }
     }
     // on to the next item
@@ -724,7 +733,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
     if (left > 0 && ++item == cts * p.Hkv) {
       item = 0;
       do {
-        before += (int64_t)seq.tiles * cts * p.Hkv;
+        before += (uint32_t)(seq.tiles * cts) * (uint32_t)p.Hkv;
         seq = sequence_of(p, ++b);
         cts = column_tiles(p, seq.n, C);
       } while (seq.tiles == 0);
@@ -737,50 +746,54 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
   // places of the workspace: for an item that goes on from the CTA before, and for one that begins
   // here and goes on in the next.
   __syncthreads();
-  if (threadIdx.x == 0) {
-    int chains = 0;
-    for (int i = 0; i < 2 * kWarps; ++i) {
-      if (piece_of[i >> 1][i & 1].at == nullptr) continue;
-      if (chains == 0 || (i & 1)) chain_of[++chains] = i;
-    }
-    chain_of[0] = chains;
-  }
-  __syncthreads();
-  const int chains = chain_of[0];
-  if (chains == 0) return;
-  const int64_t cta_end = run_start(total, warps, min(((int)blockIdx.x + 1) * per_cta, warps));
+  const uint32_t present =
+      __ballot_sync(0xffffffffu, (lane >> 1) < kWarps && piece_of[(lane >> 1) & (kWarps - 1)][lane & 1].at != nullptr);
+  if (present == 0) return;
+  // (an item begins in the second place of its first warp)
+  const uint32_t starts = (present & 0xAAAAAAAAu) | (present & (0u - present));
+  const uint32_t cta_end = runs.start(min(cta_rank + per_cta, warps));
+  const int chains = __popc(starts);
   const int each = chains < kWarps ? kWarps / chains : 1;  // warps per chain
   for (int chain = warp / each; chain < chains; chain += kWarps / each) {
-    const int first = chain_of[chain + 1], last = chain + 1 < chains ? chain_of[chain + 2] : 2 * kWarps;
-    const Piece head_piece = piece_of[first >> 1][first & 1];
-    const bool begins = (first & 1) != 0, ends = head_piece.end <= cta_end;
-    const Sequence seq = sequence_of(p, head_piece.b);
-    const int32_t cts = column_tiles(p, seq.n, C);
-    const int head = head_piece.item / cts, first_column = (head_piece.item - head * cts) * C;
+    uint32_t rest = starts;
+    for (int i = 0; i < chain; ++i) rest &= rest - 1;
+    const int first = __ffs(rest) - 1;
+    rest &= rest - 1;  // of the next chains
+    const uint32_t members = present & (0xffffffffu << first) & ((rest & (0u - rest)) - 1u);  // (none: all above)
+    const Piece& lead = piece_of[first >> 1][first & 1];
+    const bool begins = (first & 1) != 0, ends = lead.end <= cta_end;
     float* const sum_at = p.partial + ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * S::kPiece;
+    // pieces where the rings of warps one after another were, and at most one more behind them
+    const int last = 31 - __clz(members);
+    const bool more = piece_of[last >> 1][last & 1].early != 0;
+    const float* const behind = piece_of[last >> 1][last & 1].at;
+    const int w0 = first >> 1, w1 = (last >> 1) + (more ? 0 : 1);
+    constexpr int kStep = kStages * S::kStage / 4;  // floats from one ring to the next
+    const float* const rings = reinterpret_cast<const float*>(smem);
     for (int e = (warp % each) * 32 + lane; e < C * D / 4; e += each * 32) {
       const int c = e / (D / 4), d = e % (D / 4) * 4;
-      float m = -INFINITY, l = 0.f;
+      float l = 0.f, m = more ? behind[C * D + 2 * c] : -INFINITY;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-      for (int i = first; i < last; ++i) {
-        const float* const at = piece_of[i >> 1][i & 1].at;
-        if (at == nullptr) continue;
-        const float2 ml = *reinterpret_cast<const float2*>(at + C * D + 2 * c);
-        const float4 v = *reinterpret_cast<const float4*>(at + c * D + d);
-        add_piece(m, l, o, ml, v);
-      }
+#pragma unroll 4
+      for (int w = w0; w < w1; ++w) m = fmaxf(m, rings[w * kStep + C * D + 2 * c]);
+#pragma unroll 4
+      for (int w = w0; w < w1; ++w)
+        add_piece(m, l, o, *reinterpret_cast<const float2*>(rings + w * kStep + C * D + 2 * c),
+                  *reinterpret_cast<const float4*>(rings + w * kStep + c * D + d));
+      if (more)
+        add_piece(m, l, o, *reinterpret_cast<const float2*>(behind + C * D + 2 * c),
+                  *reinterpret_cast<const float4*>(behind + c * D + d));
       if (begins && ends) {
-        write_four<D>(p, seq, head, first_column + c, d, o, m, l);
+        write_four<D>(p, lead.seq, lead.head, lead.first_column + c, d, o, m, l);
       } else {
         *reinterpret_cast<float4*>(sum_at + c * D + d) = o;
         if (d == 0) *reinterpret_cast<float2*>(sum_at + C * D + 2 * c) = make_float2(m, l);
       }
     }
     if (begins && !ends && warp % each == 0 && lane == 0)
-      p.pieces[blockIdx.x] = make_int4(head_piece.b, head_piece.item, run_of(total, warps, head_piece.end - 1) / per_cta, 0);
+      p.pieces[blockIdx.x] = make_int4(lead.b, lead.item, (int)(runs.of(lead.end - 1) / per_cta), 0);
   }
-  }
+}
 
 // The pieces of an item that several CTAs share added up: some CTAs for each CTA of the first
 // kernel, for the item that begins in it and goes on in the next, if there is one.
@@ -799,13 +812,13 @@ __global__ void __launch_bounds__(128) attention_sum_kernel(const AttentionParam
   const int c = e / (D / 4), d = e % (D / 4) * 4;
   float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto piece_at = [&](int w) { return p.partial + ((int64_t)w * 2 + (w == (int)blockIdx.x ? 1 : 0)) * S::kPiece; };
 #pragma unroll 4
-  for (int w = blockIdx.x; w <= piece.z; ++w) {
-    const float* const at = p.partial + ((int64_t)w * 2 + (w == (int)blockIdx.x ? 1 : 0)) * S::kPiece;
-    const float2 ml = *reinterpret_cast<const float2*>(at + C * D + 2 * c);
-    const float4 v = *reinterpret_cast<const float4*>(at + c * D + d);
-    add_piece(m, l, o, ml, v);
-  }
+  for (int w = blockIdx.x; w <= piece.z; ++w) m = fmaxf(m, piece_at(w)[C * D + 2 * c]);
+#pragma unroll 4
+  for (int w = blockIdx.x; w <= piece.z; ++w)
+    add_piece(m, l, o, *reinterpret_cast<const float2*>(piece_at(w) + C * D + 2 * c),
+              *reinterpret_cast<const float4*>(piece_at(w) + c * D + d));
   write_four<D>(p, seq, head, first_column + c, d, o, m, l);
 }
 

@@ -93,6 +93,10 @@ nvfp4_status_t validate_attention(int64_t T, int64_t B, int64_t Hq, int64_t Hkv,
   if (!ragged && ((B == 0 && T != 0) || (B != 0 && (T % B != 0 || (max_q != 0 && max_q != T / B)))))
     return NVFP4_ERR_INVALID_VALUE;
   *most_q = !ragged ? (B == 0 ? 0 : T / B) : max_q != 0 ? max_q : T;
+  // tiles of the kernel for few query tokens, over sequences, heads and passes, are counted in 32 bits
+  const int64_t columns = *most_q * (Hq / Hkv) < kFewColumns ? *most_q * (Hq / Hkv) : kFewColumns;
+  const int64_t passes = (columns + 7) / 8;
+  if (B * Hkv * (passes > 0 ? passes : 1) > kMaxDim / (max_pages * page_size / 32 + 1)) return NVFP4_ERR_UNSUPPORTED_SHAPE;
   return NVFP4_OK;
 }
 
@@ -233,10 +237,9 @@ nvfp4_status_t nvfp4_attention(const void* q, int dtype, int64_t T, int64_t Hq, 
   int sms = 0;
   const cudaError_t err = device_sms(&sms);
   if (err != cudaSuccess) return result(err);
-  // (a sequence beyond max_q is the other kernel's all the same, if no prompts are expected)
-  p.few_columns = INT32_MAX;
+  // sequences of more columns are the prompt kernel's, or, if none are to be expected, left out
+  p.few_columns = (int32_t)(columns < kFewColumns ? columns : kFewColumns);
   if (columns > kFewColumns) {
-    p.few_columns = (int32_t)kFewColumns;
     const cudaError_t ran = launch_attention_prompt(p, (int)D, (cudaStream_t)stream);
     if (ran != cudaSuccess || opt.q_starts == nullptr) return result(ran);
   }

@@ -156,7 +156,7 @@ __device__ __forceinline__ void row_sees(const AttentionParams& p, int32_t lengt
   if (p.causal) {
     const int32_t position = length - n + i;
     hi = position + 1;
-    if (p.window > 0) lo = max(position + 1 - p.window, 0);
+    if (p.window > 0 && hi > p.window) lo = hi - p.window;
   }
 }
 

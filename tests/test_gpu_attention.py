@@ -323,11 +323,17 @@ def test_attention_of_prompts_and_single_tokens_together():
     z = problem(rng, lens, counts, 8, 2, 128, 32, "bf16")
     out = torch.full((sum(counts) + 9, 8, 128), 3.0, dtype=torch.bfloat16, device=DEV)
     q = torch.cat((z["q"], torch.full((9, 8, 128), float("nan"), dtype=torch.bfloat16))).to(DEV)
-    for max_q in (0, 300, 2):  # (2 is wrong: the results are right all the same)
+    for max_q in (0, 300):
         out.fill_(3.0)
         _, lse = nv.attention(q, **on_gpu(z), q_starts=gpu(z["starts"]), max_q=max_q, return_lse=True, out=out)
         check(z, out[:-9], lse[:-9], "bf16")
         assert (out[-9:] == 3).all()
+    # sequences with more query tokens than max_q says are left out, others are right
+    right = out.clone()
+    out.fill_(3.0)
+    nv.attention(q, **on_gpu(z), q_starts=gpu(z["starts"]), max_q=8, out=out)
+    few = torch.from_numpy(np.repeat([c <= 8 for c in counts] + [False], counts + [9])).to(DEV)
+    assert torch.equal(out[few], right[few]) and (out[~few] == 3).all()
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
