@@ -68,6 +68,7 @@ struct AttentionParams {
   float scale_log2;           // scale * log2(e)
   // split of the work (set by the launcher)
   float* partial;             // pieces: [CTAs][2] and [CTAs][warps]
+  int32_t splits;             // prompts: parts of a row tile's tokens
   int4* pieces;               // [CTAs]: {sequence, item, last CTA, 0} of the item that goes on in the next
 };
 constexpr int kAttentionCtas = 152;  // most CTAs of a launch, which the workspace is made for
@@ -77,7 +78,9 @@ int attention_columns(int D, int64_t most);
 int64_t attention_workspace(int D, int columns);
 cudaError_t launch_attention(AttentionParams p, int D, int columns, void* workspace, int sms, cudaStream_t stream);
 // Sequences of more than p.few_columns columns (attention_prompt.cu).
-cudaError_t launch_attention_prompt(const AttentionParams& p, int D, cudaStream_t stream);
+cudaError_t launch_attention_prompt(const AttentionParams& p, int D, void* workspace, cudaStream_t stream);
+// Bytes of its workspace, from p's sizes alone.
+int64_t attention_prompt_workspace(AttentionParams p, int D);
 cudaError_t prompt_wait_timeouts(int reset, int* out);
 cudaError_t attention_wait_timeouts(int reset, int* out);
 

@@ -105,6 +105,30 @@ int few_pass(int64_t D, int64_t columns) {
   return attention_columns((int)D, columns < kFewColumns ? columns : kFewColumns);
 }
 
+// The sizes that both kernels work from; with few_columns: sequences of more columns are the
+// prompt kernel's, or, if none are to be expected, left out.
+AttentionParams sizes_of(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t page_size, int64_t max_pages,
+                         int64_t columns) {
+  AttentionParams p = {};
+  p.T = (int32_t)T;
+  p.B = (int32_t)B;
+  p.Hq = (int32_t)Hq;
+  p.Hkv = (int32_t)Hkv;
+  p.group = (int32_t)(Hq / Hkv);
+  p.max_pages = (int32_t)max_pages;
+  p.granules = (int32_t)(page_size / kGranuleTokens);
+  p.capacity = max_pages * page_size;
+  p.few_columns = (int32_t)(columns < kFewColumns ? columns : kFewColumns);
+  return p;
+}
+
+// The kernels of a call use the workspace one after another.
+int64_t workspace_for(const AttentionParams& p, int64_t D, int64_t columns, bool ragged) {
+  const int64_t few = ragged || columns <= kFewColumns ? attention_workspace((int)D, few_pass(D, columns)) : 0;
+  const int64_t prompt = columns > kFewColumns ? attention_prompt_workspace(p, (int)D) : 0;
+  return few > prompt ? few : prompt;
+}
+
 }  // namespace
 
 extern "C" {
@@ -177,7 +201,9 @@ size_t nvfp4_attention_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t
   int64_t most_q = 0;
   if (validate_attention(T, B, Hq, Hkv, D, 0, page_size, max_pages, ragged != 0, max_q, &most_q) != NVFP4_OK) return 0;
   if (T == 0) return 0;
-  return (size_t)attention_workspace((int)D, few_pass(D, most_q * (Hq / Hkv)));
+  const int64_t columns = most_q * (Hq / Hkv);
+  const int64_t bytes = workspace_for(sizes_of(T, B, Hq, Hkv, page_size, max_pages, columns), D, columns, ragged != 0);
+  return (size_t)(bytes > 256 ? bytes : 256);
 }
 
 nvfp4_status_t nvfp4_attention(const void* q, int dtype, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
@@ -197,7 +223,8 @@ nvfp4_status_t nvfp4_attention(const void* q, int dtype, int64_t T, int64_t Hq, 
     return NVFP4_ERR_INVALID_VALUE;
   if (T == 0 || B == 0) return NVFP4_OK;
   const int64_t columns = most_q * (Hq / Hkv);
-  const size_t need = (size_t)attention_workspace((int)D, few_pass(D, columns));
+  AttentionParams p = sizes_of(T, B, Hq, Hkv, page_size, max_pages, columns);
+  const size_t need = (size_t)workspace_for(p, D, columns, opt.q_starts != nullptr);
   if (q == nullptr || out == nullptr || lengths == nullptr || (max_pages > 0 && page_table == nullptr) ||
       (pages > 0 && cache == nullptr) || workspace == nullptr || workspace_bytes < need)
     return NVFP4_ERR_INVALID_VALUE;
@@ -207,7 +234,6 @@ nvfp4_status_t nvfp4_attention(const void* q, int dtype, int64_t T, int64_t Hq, 
       !aligned(workspace, 256) || !aligned(page_table, 4) || !aligned(lengths, 4) || !aligned(opt.q_starts, 4) ||
       !aligned(opt.encode_k, 4) || !aligned(opt.encode_v, 4) || !aligned(opt.lse, 4))
     return NVFP4_ERR_MISALIGNED;
-  AttentionParams p = {};
   p.q = q;
   p.out = out;
   p.lse = opt.lse;
@@ -220,15 +246,7 @@ nvfp4_status_t nvfp4_attention(const void* q, int dtype, int64_t T, int64_t Hq, 
   p.q_token = token_stride;
   p.q_head = head_stride;
   p.pages = pages;
-  p.capacity = max_pages * page_size;
-  p.T = (int32_t)T;
-  p.B = (int32_t)B;
-  p.Hq = (int32_t)Hq;
-  p.Hkv = (int32_t)Hkv;
-  p.group = (int32_t)(Hq / Hkv);
   p.uniform_n = opt.q_starts ? 0 : (int32_t)(T / B);
-  p.max_pages = (int32_t)max_pages;
-  p.granules = (int32_t)(page_size / kGranuleTokens);
   p.window = opt.window;
   p.causal = opt.causal;
   p.bf16 = dtype == NVFP4_DTYPE_BF16;
@@ -237,10 +255,8 @@ nvfp4_status_t nvfp4_attention(const void* q, int dtype, int64_t T, int64_t Hq, 
   int sms = 0;
   const cudaError_t err = device_sms(&sms);
   if (err != cudaSuccess) return result(err);
-  // sequences of more columns are the prompt kernel's, or, if none are to be expected, left out
-  p.few_columns = (int32_t)(columns < kFewColumns ? columns : kFewColumns);
   if (columns > kFewColumns) {
-    const cudaError_t ran = launch_attention_prompt(p, (int)D, (cudaStream_t)stream);
+    const cudaError_t ran = launch_attention_prompt(p, (int)D, workspace, (cudaStream_t)stream);
     if (ran != cudaSuccess || opt.q_starts == nullptr) return result(ran);
   }
   return result(launch_attention(p, (int)D, few_pass(D, columns), workspace, sms, (cudaStream_t)stream));

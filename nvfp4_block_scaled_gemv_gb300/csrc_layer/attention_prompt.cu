@@ -47,6 +47,7 @@ template <int D, int BN, int NQ>
 struct Prompt {
   static constexpr int kPlanes = D / 64;
   static constexpr int kRows = 128 * NQ;
+  static constexpr int64_t kPiece = (int64_t)kRows * (D + 2);  // floats: results, then (reference, sum) of the rows
   static constexpr uint32_t kPanel = 128 * 128;                 // a plane of 128 rows of Q
   static constexpr uint32_t kQBytes = (uint32_t)NQ * kPlanes * kPanel;
   static constexpr uint32_t kTilePanel = BN * 128;              // a plane of a K or V tile
@@ -125,6 +126,26 @@ __device__ __forceinline__ void tmem_st_16(uint32_t taddr, const uint32_t* v) {
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// tc::mbar_wait without its call: one lane waits, in line, so that the warps' registers are
+// split as setmaxnreg says (a call asks for those of its own).
+__device__ __forceinline__ void wait_phase(uint32_t bar, uint32_t parity, bool& ok) {
+  if (!ok || tc::mbar_try(bar, parity)) return;
+  const uint64_t t0 = tc::global_ns();
+  while (!tc::mbar_try(bar, parity))
+    if (tc::global_ns() - t0 > tc::kWaitNs) {
+      atomicAdd(&g_prompt_timeouts, 1);
+      ok = false;
+      return;
+    }
+}
+template <int N>
+__device__ __forceinline__ void registers_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void registers_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 __device__ __forceinline__ void async_proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -138,6 +159,12 @@ __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
   return d;
 }
 
+__device__ __forceinline__ uint32_t rounded_two(bool bf16, float a, float b) {
+  if (!bf16) return half2_of(a, b);
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
 // What a CTA works on; the same in all its threads.
 struct Work {
   int32_t q0, n, length, head, first_row;  // rows: query token * group + head of the group
@@ -146,6 +173,11 @@ struct Work {
   int32_t full_from, full_to;              // tokens that all its rows see
   int32_t b;
   bool beyond;
+};
+
+// What the sum of a row tile's pieces has to know.
+struct PieceHead {
+  int32_t q0, rows, first_row, beyond;  // rows: 0 if there is no such row tile
 };
 
 __device__ __forceinline__ void row_sees(const AttentionParams& p, int32_t length, int32_t n, int32_t row, int32_t& lo,
@@ -239,8 +271,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
   pdl_wait();
 
   // The CTA's work: row tiles are numbered over the sequences, the last (which sees most) of a
-  // sequence first, and the key heads of a row tile follow each other.
-  const int32_t rank = (int32_t)blockIdx.x / p.Hkv, head = (int32_t)blockIdx.x % p.Hkv;
+  // sequence first, the key heads of a row tile follow each other, and the parts of its tokens.
+  const int32_t item = (int32_t)blockIdx.x / p.splits, split = (int32_t)blockIdx.x % p.splits;
+  const int32_t rank = item / p.Hkv, head = item % p.Hkv;
   {
     const int share = (p.B + kPromptThreads - 1) / kPromptThreads;
     const int b0 = threadIdx.x * share;
@@ -256,7 +289,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
       if (lane >= d) upto += o;
     }
     if (lane == 31) warp_sums[warp] = upto;
-    if (threadIdx.x == 0) shared_work.tiles = 0;
+    if (threadIdx.x == 0) shared_work = Work{};  // (no row tile: no tiles, rows or first row)
     __syncthreads();
     for (int w = 0; w < warp; ++w) upto += warp_sums[w];
     uint32_t before = upto - mine;
@@ -283,12 +316,24 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
         w.full_to = h0;
         w.first_token = min(l0, max(h1, 0)) / BN * BN;
         w.tiles = max((h1 - w.first_token + BN - 1) / BN, 1);
+        const int32_t from = (int32_t)((int64_t)w.tiles * split / p.splits);
+        w.tiles = (int32_t)((int64_t)w.tiles * (split + 1) / p.splits) - from;
+        w.first_token += from * BN;
         shared_work = w;
         break;
       }
     }
   }
   __syncthreads();
+  float* const piece = p.partial + (int64_t)blockIdx.x * S::kPiece;
+  if (p.splits > 1) {
+    if (split == 0 && threadIdx.x == 0)
+      reinterpret_cast<PieceHead*>(p.pieces)[item] = {shared_work.q0, shared_work.rows, shared_work.first_row,
+                                                      shared_work.beyond};
+    if (shared_work.tiles == 0 && shared_work.rows > 0)  // (fewer tiles than parts)
+      for (int i = threadIdx.x; i < S::kRows; i += kPromptThreads)
+        reinterpret_cast<float2*>(piece + S::kRows * D)[i] = make_float2(-INFINITY, 0.f);
+  }
   if (shared_work.tiles == 0) return;  // (more CTAs than row tiles)
   if (warp == 12) tc::alloc(smem_u32(&tmem_slot), kPromptColumns);
   tc::fence_before();
@@ -304,6 +349,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
   // halves tile x / 2 of half x & 1, otherwise tile x; S of a step is buffer x & 1.
   const int32_t steps = tiles * NQ;
   if (warp >= 12) {
+    registers_down<56>();
     if (warp == 13) {
       // granules, a lane each
       const int32_t have = (work.length + kGranuleTokens - 1) / kGranuleTokens;
@@ -319,7 +365,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
         const int i = j % kRaws;
         const int32_t id = next;
         next = page_of(j + 1);
-        tc::mbar_wait<false>(raw_empty(i), ((uint32_t)(j / kRaws) & 1u) ^ 1u, ok, &g_prompt_timeouts);
+        wait_phase(raw_empty(i), ((uint32_t)(j / kRaws) & 1u) ^ 1u, ok);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const uint32_t valid = __ballot_sync(0xffffffffu, id >= 0);
@@ -340,18 +386,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
       bool landed = true;
       for (int k = 0; k < kRaws && k < issued; ++k) {
         const int i = issued - 1 - k;
-        tc::mbar_wait<false>(raw_full(i % kRaws), (uint32_t)((i / kRaws) & 1), landed, &g_prompt_timeouts);
+        wait_phase(raw_full(i % kRaws), (uint32_t)((i / kRaws) & 1), landed);
       }
       __syncwarp();
     } else if (warp == 12) {
       constexpr uint32_t qk = f16_idesc(BN, false), pv = f16_idesc(D, true);
       const uint64_t q_desc = tc::desc_sw128(q_s);
-      tc::mbar_wait<false>(q_full, 0, ok, &g_prompt_timeouts);
+      wait_phase(q_full, 0, ok);
       auto scores = [&](int32_t x) {
         const int32_t j = NQ == 2 ? x >> 1 : x;
         const int u = NQ == 2 ? x & 1 : 0;
         const int fill = 2 * j, i = fill % kSlots;
-        tc::mbar_wait<false>(slot_full(i), (uint32_t)(fill / kSlots) & 1u, ok, &g_prompt_timeouts);
+        wait_phase(slot_full(i), (uint32_t)(fill / kSlots) & 1u, ok);
         ok = __all_sync(0xffffffffu, ok);
         tc::fence_after();
         if (!ok) return;
@@ -375,8 +421,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
         const int32_t j = NQ == 2 ? x >> 1 : x;
         const int u = NQ == 2 ? x & 1 : 0;
         const int fill = 2 * j + 1, i = fill % kSlots;
-        tc::mbar_wait<false>(slot_full(i), (uint32_t)(fill / kSlots) & 1u, ok, &g_prompt_timeouts);
-        tc::mbar_wait<false>(p_ready(x & 1), (uint32_t)(x >> 1) & 1u, ok, &g_prompt_timeouts);
+        wait_phase(slot_full(i), (uint32_t)(fill / kSlots) & 1u, ok);
+        wait_phase(p_ready(x & 1), (uint32_t)(x >> 1) & 1u, ok);
         ok = __all_sync(0xffffffffu, ok);
         tc::fence_after();
         if (!ok) break;
@@ -394,10 +440,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
       // every MMA has finished before tensor memory is released
       if (gemm::elect_one()) tc::commit(drain);
       bool drained = true;
-      tc::mbar_wait<false>(drain, 0, drained, &g_prompt_timeouts);
+      wait_phase(drain, 0, drained);
       __syncwarp();
     }
   } else if (warp >= 8) {
+    registers_down<88>();
     // raw granules to fp16 tiles: a warp takes 8 tokens of a plane, a lane a block
     const int w = warp - 8, row8 = lane >> 2, block = lane & 3;
     constexpr int kUnits = BN / 8 * kPlanes / 4;  // per warp
@@ -405,7 +452,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
       const int ri = j % kRaws;
       const int32_t t0 = work.first_token + j * BN;
       const bool whole = tile_whole<BN>(work, t0);
-      if (lane == 0) tc::mbar_wait<false>(raw_full(ri), (uint32_t)(j / kRaws) & 1u, ok, &g_prompt_timeouts);
+      if (lane == 0) wait_phase(raw_full(ri), (uint32_t)(j / kRaws) & 1u, ok);
       ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
       __syncwarp();
       const uint32_t bad = raw_bad[ri];
@@ -414,7 +461,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
       for (int side = 0; side < 2 && ok; ++side) {
         const int fill = 2 * j + side, si = fill % kSlots;
         if (lane == 0)
-          tc::mbar_wait<false>(slot_empty(si), ((uint32_t)(fill / kSlots) & 1u) ^ 1u, ok, &g_prompt_timeouts);
+          wait_phase(slot_empty(si), ((uint32_t)(fill / kSlots) & 1u) ^ 1u, ok);
         ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
       __syncwarp();
         if (!ok) break;
@@ -477,6 +524,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
       }
     }
   } else {
+    registers_up<184>();
     const int u = warp >> 2;
     if (u < NQ) {
       const int r = threadIdx.x & 127;          // row of the half, and lane of tensor memory
@@ -541,29 +589,26 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
         const int32_t x = NQ == 2 ? 2 * j + u : j;
         const uint32_t s_at = tmem + lanes + 128u * (x & 1);
         const int32_t t0 = work.first_token + j * BN;
-        if (lane == 0) tc::mbar_wait<false>(s_full(x & 1), (uint32_t)(x >> 1) & 1u, ok, &g_prompt_timeouts);
+        if (lane == 0) wait_phase(s_full(x & 1), (uint32_t)(x >> 1) & 1u, ok);
         ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
       __syncwarp();
         if (!ok) break;
         tc::fence_after();
         const bool whole = tile_whole<BN>(work, t0);
-        // Two passes over S, 32 columns at a time with the next ones on their way: its 128 values,
-        // held from the maximum to the exponentials, are more than the registers take.
-        uint32_t s[2][32];
+        uint32_t s[BN / 32][32];
         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        tmem_ld_32(s_at, s[0]);
-        tmem_ld_wait(s[0]);
+#pragma unroll
+        for (int h = 0; h < BN / 32; ++h) tmem_ld_32(s_at + 32 * h, s[h]);
 #pragma unroll
         for (int h = 0; h < BN / 32; ++h) {
-          uint32_t* const v = s[h & 1];
-          tmem_ld_32(s_at + (h + 1 < BN / 32 ? 32 * (h + 1) : 0), s[(h + 1) & 1]);
+          uint32_t* const v = s[h];
+          tmem_ld_wait(v);
           if (!whole) mask_32(v, t0 + 32 * h, lo, hi);
 #pragma unroll
           for (int i = 0; i < 32; i += 8)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               top[k] = fmaxf(fmaxf(top[k], __uint_as_float(v[i + 2 * k])), __uint_as_float(v[i + 2 * k + 1]));
-          tmem_ld_wait(s[(h + 1) & 1]);
         }
         const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
         // (from -inf any score passes)
@@ -574,7 +619,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
           const float2 two = unpack_f32x2(sum);
           sum = pack_f32x2(two.x * f, two.y * f);
           if (j > 0) {
-            if (lane == 0) tc::mbar_wait<false>(o_done(u), (uint32_t)(j - 1) & 1u, ok, &g_prompt_timeouts);
+            if (lane == 0) wait_phase(o_done(u), (uint32_t)(j - 1) & 1u, ok);
             ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
       __syncwarp();
             if (!ok) break;
@@ -593,12 +638,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
         const float base2 = m == -INFINITY ? 0.f : -m * c;
         const uint64_t c2 = pack_f32x2(c, c), b2 = pack_f32x2(base2, base2), one2 = pack_f32x2(1.f, 1.f);
         uint64_t other = 0;
-        // (the first 32 columns are there again; P's columns 16 h lie over S's that have been read)
 #pragma unroll
         for (int h = 0; h < BN / 32; ++h) {
-          uint32_t* const v = s[h & 1];
-          if (h + 1 < BN / 32) tmem_ld_32(s_at + 32 * (h + 1), s[(h + 1) & 1]);
-          if (!whole) mask_32(v, t0 + 32 * h, lo, hi);
+          const uint32_t* const v = s[h];
           uint32_t packed[16];
 #pragma unroll
           for (int i = 0; i < 32; i += 4) {
@@ -610,14 +652,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
             packed[i / 2] = half2_of(a.x, a.y);
             packed[i / 2 + 1] = half2_of(b.x, b.y);
           }
-          if (h + 1 < BN / 32) tmem_ld_wait(s[(h + 1) & 1]);
           tmem_st_16(s_at + 16 * h, packed);
         }
         sum = fma2(other, one2, sum);
         if (!whole) {
           // (before P is handed over: V's slot and marks are not used again until then)
           const int fill = 2 * j + 1;
-          if (lane == 0) tc::mbar_wait<false>(slot_full(fill % kSlots), (uint32_t)(fill / kSlots) & 1u, ok, &g_prompt_timeouts);
+          if (lane == 0) wait_phase(slot_full(fill % kSlots), (uint32_t)(fill / kSlots) & 1u, ok);
           ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
       __syncwarp();
           if (!ok) break;
@@ -631,7 +672,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(p_ready(x & 1));
       }
-      if (lane == 0) tc::mbar_wait<false>(o_done(u), (uint32_t)(tiles - 1) & 1u, ok, &g_prompt_timeouts);
+      if (lane == 0) wait_phase(o_done(u), (uint32_t)(tiles - 1) & 1u, ok);
       ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
       __syncwarp();
       tc::fence_after();
@@ -641,26 +682,32 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
       float f = l == 0.f ? 0.f : decode / l;
       if (work.beyond) f = __int_as_float(0x7fc00000);
       const int64_t out_row = (int64_t)(work.q0 + token) * p.Hq + (int64_t)work.head * p.group + member;
-      if (ok && real && p.lse != nullptr)
+      const bool part = p.splits > 1;
+      if (part) {
+        f = 1.f;
+        if (ok) reinterpret_cast<float2*>(piece + S::kRows * D)[u * 128 + r] = make_float2(m == -INFINITY ? m : m * c, l);
+      } else if (ok && real && p.lse != nullptr) {
         p.lse[out_row] = work.beyond ? f : l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.69314718055994531f;
+      }
 #pragma unroll 1
       for (int i = 0; i < D && ok; i += 32) {
         uint32_t o[32];
         tmem_ld_32(o_at + i, o);
         tmem_ld_wait(o);
-        uint32_t words[16];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float g = nan_blocks >> (i / 16 + k / 8) & 1u ? __int_as_float(0x7fc00000) : f;
-          const float a = __uint_as_float(o[2 * k]) * g, b = __uint_as_float(o[2 * k + 1]) * g;
-          if (p.bf16) {
-            const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-            words[k] = *reinterpret_cast<const uint32_t*>(&v);
-          } else {
-            words[k] = half2_of(a, b);
-          }
+        for (int k = 0; k < 32; ++k) {
+          const float g = nan_blocks >> (i / 16 + k / 16) & 1u ? __int_as_float(0x7fc00000) : f;
+          o[k] = __float_as_uint(__uint_as_float(o[k]) * g);
         }
-        if (real) {
+        if (part) {
+          uint4* const to = reinterpret_cast<uint4*>(piece + (int64_t)(u * 128 + r) * D + i);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) to[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        } else if (real) {
+          uint32_t words[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            words[k] = rounded_two(p.bf16, __uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1]));
           uint4* const to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + out_row * D + i);
 #pragma unroll
           for (int k = 0; k < 4; ++k) to[k] = make_uint4(words[4 * k], words[4 * k + 1], words[4 * k + 2], words[4 * k + 3]);
@@ -676,25 +723,100 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
   }
 }
 
+// The parts of a row tile added up, in the order of the tokens: 256 threads, four results each.
 template <int D, int BN, int NQ>
-cudaError_t launch_with(const AttentionParams& p, cudaStream_t stream) {
+__global__ void __launch_bounds__(256) attention_prompt_sum_kernel(const AttentionParams p) {
+  using S = Prompt<D, BN, NQ>;
+  pdl_launch_dependents();
+  pdl_wait();
+  const PieceHead at = reinterpret_cast<const PieceHead*>(p.pieces)[blockIdx.x];
+  const int r = (int)(blockIdx.y * 256 + threadIdx.x) / (D / 4), d = threadIdx.x % (D / 4) * 4;
+  const int32_t row = at.first_row + r;
+  if ((uint32_t)row >= (uint32_t)at.rows) return;
+  const float* const pieces = p.partial + (int64_t)blockIdx.x * p.splits * S::kPiece;
+  float m = -INFINITY, l = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < p.splits; ++i) m = fmaxf(m, pieces[i * S::kPiece + S::kRows * D + 2 * r]);
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = 0; i < p.splits; ++i) {
+    const float* const piece = pieces + i * S::kPiece;
+    const float2 ml = *reinterpret_cast<const float2*>(piece + S::kRows * D + 2 * r);
+    const float4 v = *reinterpret_cast<const float4*>(piece + (int64_t)r * D + d);
+    if (ml.y == 0.f) continue;  // (nothing that the row sees; a part without tiles has no results at all)
+    const float f = ml.x == m ? 1.f : ex2(ml.x - m);
+    o.x = fmaf(v.x, f, o.x);
+    o.y = fmaf(v.y, f, o.y);
+    o.z = fmaf(v.z, f, o.z);
+    o.w = fmaf(v.w, f, o.w);
+    l = fmaf(ml.y, f, l);
+  }
+  const int head = (int)blockIdx.x % p.Hkv;
+  const int32_t token = row / p.group, member = row - token * p.group;
+  const int64_t out_row = (int64_t)(at.q0 + token) * p.Hq + (int64_t)head * p.group + member;
+  float f = l == 0.f ? 0.f : (p.encode_v ? 1.f / __ldg(p.encode_v + head) : 1.f) / l;
+  if (at.beyond) f = __int_as_float(0x7fc00000);
+  if (p.lse != nullptr && d == 0)
+    p.lse[out_row] = at.beyond ? f : l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + out_row * D + d) =
+      make_uint2(rounded_two(p.bf16, o.x * f, o.y * f), rounded_two(p.bf16, o.z * f, o.w * f));
+}
+
+// Row tiles of all sequences, at most: every sequence that has some begins one more than its
+// rows fill.
+int64_t most_row_tiles(int64_t T, int64_t B, int64_t group, int64_t few, int rows_per_tile) {
+  const int64_t rows = T * group, sequences = rows / (few + 1);
+  return rows / rows_per_tile + (sequences < B ? sequences : B);
+}
+
+// Parts that the tokens of a row tile are cut into: as many as bring the row tiles and heads to the
+// SMs, where these are fewer, but at most twice the SMs in all, and 4 tiles of tokens a part.
+int prompt_splits(int64_t items, int64_t most_tokens, int tile) {
+  if (items >= kAttentionCtas) return 1;
+  const int64_t long_enough = most_tokens / (4 * tile);
+  int best = 1;
+  double least = 1e30;
+  for (int64_t s = 1; s * items <= 2 * kAttentionCtas && (s == 1 || s <= long_enough); ++s) {
+    const double rounds = (double)((s * items + kAttentionCtas - 1) / kAttentionCtas) / (double)s + 0.01 * (double)s;
+    if (rounds < least) least = rounds, best = (int)s;
+  }
+  return best;
+}
+
+template <int D, int BN, int NQ>
+int64_t plan_with(AttentionParams& p) {
+  using S = Prompt<D, BN, NQ>;
+  const int64_t items = most_row_tiles(p.T, p.B, p.group, p.few_columns, S::kRows) * p.Hkv;
+  p.splits = prompt_splits(items, p.capacity, BN);
+  return p.splits == 1 ? 0 : (items * (int64_t)sizeof(PieceHead) + 255) / 256 * 256 + items * p.splits * S::kPiece * 4;
+}
+
+template <int D, int BN, int NQ>
+cudaError_t launch_with(AttentionParams p, void* workspace, cudaStream_t stream) {
   using S = Prompt<D, BN, NQ>;
   const cudaError_t err = allow_smem<attention_prompt_kernel<D, BN, NQ>>(S::kSmem);
   if (err != cudaSuccess) return err;
-  // row tiles, at most: every sequence that has some begins one more than its rows fill
-  const int64_t rows = (int64_t)p.T * p.group;
-  const int64_t sequences = rows / (p.few_columns + 1);
-  const int64_t tiles = rows / S::kRows + (sequences < p.B ? sequences : p.B);
-  return launch_pdl(attention_prompt_kernel<D, BN, NQ>, dim3((unsigned)(tiles * p.Hkv)), dim3(kPromptThreads), S::kSmem,
+  plan_with<D, BN, NQ>(p);
+  const int64_t items = most_row_tiles(p.T, p.B, p.group, p.few_columns, S::kRows) * p.Hkv;
+  p.pieces = static_cast<int4*>(workspace);
+  p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + (items * (int64_t)sizeof(PieceHead) + 255) / 256 * 256);
+  const cudaError_t ran = launch_pdl(attention_prompt_kernel<D, BN, NQ>, dim3((unsigned)(items * p.splits)),
+                                     dim3(kPromptThreads), S::kSmem, stream, p);
+  if (ran != cudaSuccess || p.splits == 1) return ran;
+  return launch_pdl(attention_prompt_sum_kernel<D, BN, NQ>, dim3((unsigned)items, S::kRows * D / 1024), dim3(256), 0,
                     stream, p);
 }
 
 }  // namespace
 
-cudaError_t launch_attention_prompt(const AttentionParams& p, int D, cudaStream_t stream) {
-  return D == 64    ? launch_with<64, 128, 2>(p, stream)
-         : D == 128 ? launch_with<128, 128, 2>(p, stream)
-                    : launch_with<256, 64, 1>(p, stream);
+cudaError_t launch_attention_prompt(const AttentionParams& p, int D, void* workspace, cudaStream_t stream) {
+  return D == 64    ? launch_with<64, 128, 2>(p, workspace, stream)
+         : D == 128 ? launch_with<128, 128, 2>(p, workspace, stream)
+                    : launch_with<256, 64, 1>(p, workspace, stream);
+}
+
+int64_t attention_prompt_workspace(AttentionParams p, int D) {
+  return D == 64 ? plan_with<64, 128, 2>(p) : D == 128 ? plan_with<128, 128, 2>(p) : plan_with<256, 64, 1>(p);
 }
 
 cudaError_t prompt_wait_timeouts(int reset, int* out) {

@@ -294,6 +294,10 @@ PROMPTS = [
     ([130], 130, 1, 1, 64, 16), ([300, 129], 128, 4, 2, 128, 64), ([70, 700], 65, 3, 3, 128, 48),
     ([513], 300, 8, 2, 64, 32), ([200, 128, 127], 100, 2, 1, 256, 16), ([256], 256, 6, 6, 256, 64),
     ([1030], 17, 40, 4, 128, 16), ([20, 0, 90], 80, 4, 4, 128, 16), ([1500], 3, 64, 1, 128, 64),
+    # the row tiles are counted from above: one fewer than there is room for
+    ([600], 64, 32, 8, 128, 64), ([400, 300], 64, 8, 1, 64, 16),
+    # as many row tiles and heads as there are SMs and more: their tokens are not cut into parts
+    ([140] * 10, 130, 16, 16, 64, 16), ([150, 131] * 6, 129, 14, 14, 128, 32), ([100, 90] * 8, 66, 12, 12, 256, 16),
 ]
 
 
