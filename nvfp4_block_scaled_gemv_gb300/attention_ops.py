@@ -178,6 +178,10 @@ def rope_table(rotary_dim: int = 0, base: float = 10000.0, scaling: str = "none"
 
 def _heads(x, name, device=None):
     """[T, H, D] with contiguous heads: T, H, D, token stride, head stride."""
+    shape, stride = x.shape, x.stride()
+    if len(shape) == 3 and stride[2] == 1 and stride[1] >= shape[2] and \
+            stride[0] >= (shape[1] - 1) * stride[1] + shape[2] and (device is None or x.device == device):
+        return (*shape, stride[0], stride[1])  # (the usual case in few steps)
     if x.dim() != 3:
         raise ValueError(f"{name} must be [T, H, D]")
     if device is not None and x.device != device:
@@ -203,7 +207,7 @@ def rope(x, positions, table, interleaved: bool = False, factor: float = 1.0, in
     every head turned by positions [T] (int32) times the table's frequencies, in pairs (i, pairs + i) or,
     interleaved, (2i, 2i + 1), and multiplied by factor.  inverse turns back, which is the gradient.
     out: x itself (in place), or a tensor that does not overlap it."""
-    torch = _torch()
+    torch = _layer._torch or _load()
     code = _dtype_code(x, "x")
     T, H, D, token, head = _heads(x, "x")
     dev, pairs = x.device, table.numel()
@@ -317,6 +321,9 @@ def kv_read(cache, slots, dtype=None, encode_k=None, encode_v=None, stream=None)
     return k, v
 
 
+_workspaces = {}  # workspace bytes of sizes
+
+
 def attention(q, cache, page_table, lengths, q_starts=None, max_q: int = 0, scale: float = 0.0, causal: bool = True,
               window: int = 0, encode_k=None, encode_v=None, return_lse: bool = False, out=None, workspace=None,
               stream=None):
@@ -352,8 +359,12 @@ def attention(q, cache, page_table, lengths, q_starts=None, max_q: int = 0, scal
     else:
         _ptr(out, "out", q.dtype, T * Hq * D, dev)
     lse = _empty((T, Hq), torch.float32, dev, stream) if return_lse else None
-    need = library().nvfp4_attention_workspace_bytes(T, B, Hq, Hkv, D, page, max_pages, 0 if starts is None else 1,
-                                                     max_q)
+    sizes = (T, B, Hq, Hkv, D, page, max_pages, 0 if starts is None else 1, max_q)
+    need = _workspaces.get(sizes)
+    if need is None:
+        if len(_workspaces) > 4096:
+            _workspaces.clear()
+        need = _workspaces[sizes] = library().nvfp4_attention_workspace_bytes(*sizes)
     if workspace is None:
         workspace, size = _empty(need, torch.uint8, dev, stream), need
     else:

@@ -1,4 +1,5 @@
 // C ABI of the operators of attention: argument validation and launches.
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -27,10 +28,22 @@ nvfp4_status_t result(cudaError_t err) {
   return NVFP4_ERR_CUDA;
 }
 
+// Multiprocessors of the current device, cached per device.
 cudaError_t device_sms(int* out) {
+  constexpr int kMaxDevices = 128;
+  static std::atomic<int> cached[kMaxDevices];
   int dev = 0;
-  const cudaError_t err = cudaGetDevice(&dev);
-  return err != cudaSuccess ? err : cudaDeviceGetAttribute(out, cudaDevAttrMultiProcessorCount, dev);
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  int n = cached[dev].load(std::memory_order_relaxed);
+  if (n <= 0) {
+    err = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    if (err != cudaSuccess) return err;
+    cached[dev].store(n, std::memory_order_relaxed);
+  }
+  *out = n;
+  return cudaSuccess;
 }
 
 bool valid_dtype(int t) { return t == NVFP4_DTYPE_FP16 || t == NVFP4_DTYPE_BF16 || t == NVFP4_DTYPE_FP32; }
