@@ -64,6 +64,14 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The same from zero.
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
   uint32_t d;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
@@ -79,21 +87,10 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(x));
   return d;
 }
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds8(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
+// Loads of what a bulk copy left in shared memory: through pointers, so that constant distances go
+// into the instruction (the waits on the barriers keep them in their place).
+__device__ __forceinline__ uint32_t load_32(const uint8_t* p) { return *reinterpret_cast<const uint32_t*>(p); }
+__device__ __forceinline__ uint2 load_64(const uint8_t* p) { return *reinterpret_cast<const uint2*>(p); }
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
   uint32_t d;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
@@ -471,6 +468,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
 
     float o[D / 16][NT][4];
     float m[NT][2], l[NT][2];
+    float shift[NT][2];  // -m in base 2, or 0 while a row is empty (all its p are 0)
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -480,11 +478,12 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) m[nt][e] = -INFINITY, l[nt][e] = 0.f;
+      for (int e = 0; e < 2; ++e) m[nt][e] = -INFINITY, l[nt][e] = shift[nt][e] = 0.f;
 
 #pragma unroll 1
     for (; tile < to; ++tile) {
-      const uint32_t bar = bars + 8 * stage, base = ring + stage * S::kStage;
+      const uint32_t bar = bars + 8 * stage;
+      const uint8_t* const base = smem + warp * kStages * S::kStage + stage * S::kStage;
       if (!__all_sync(0xffffffffu, tc::mbar_try(bar, parity))) {
         if (lane == 0) tc::mbar_wait<false>(bar, parity, ok, &g_attention_timeouts);
         ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
@@ -496,20 +495,17 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
       const bool whole = t0 >= full_from && t0 + kTileTokens <= full_to && bad == 0;  // (the same in all lanes)
 
       // S^T, 16 tokens x 8 columns at a time
+      const uint8_t* const k_codes = base + token_of(g) * 32 + q * 8;
+      const uint8_t* const k_scales = base + kPlaneScales + token_of(g) * 4 + q;
       float s[2][NT][4];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) s[i][nt][j] = 0.f;
-#pragma unroll
         for (int c = 0; c < S::kPlanes; ++c) {
-          const uint32_t plane = base + i * S::kGranule + c * kPlaneBytes;
-          const uint32_t row = plane + token_of(g) * 32 + q * 8;
-          const uint32_t scale_at = plane + kPlaneScales + token_of(g) * 4 + q;
-          const uint2 c0 = lds64(row), c1 = lds64(row + 8 * 32);
-          const uint32_t s0 = e4m3x2_to_f16x2(lds8(scale_at) * 0x101u), s1 = e4m3x2_to_f16x2(lds8(scale_at + 8 * 4) * 0x101u);
+          const uint8_t* const row = k_codes + i * S::kGranule + c * kPlaneBytes;
+          const uint8_t* const scale_at = k_scales + i * S::kGranule + c * kPlaneBytes;
+          const uint2 c0 = load_64(row), c1 = load_64(row + 8 * 32);
+          const uint32_t s0 = e4m3x2_to_f16x2(scale_at[0] * 0x101u), s1 = e4m3x2_to_f16x2(scale_at[8 * 4] * 0x101u);
           uint32_t a[8], d[8];
           e2m1x8_to_f16x2x4(c0.x, *reinterpret_cast<uint32_t(*)[4]>(&a[0]));
           e2m1x8_to_f16x2x4(c0.y, *reinterpret_cast<uint32_t(*)[4]>(&a[4]));
@@ -523,8 +519,12 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
 #pragma unroll
           for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma_f16(s[i][nt], a[2 * j], d[2 * j], a[2 * j + 1], d[2 * j + 1], qf[c][j][0][nt], qf[c][j][1][nt]);
+            for (int nt = 0; nt < NT; ++nt) {
+              if (c + j == 0)
+                mma_f16_first(s[i][nt], a[0], d[0], a[1], d[1], qf[0][0][0][nt], qf[0][0][1][nt]);
+              else
+                mma_f16(s[i][nt], a[2 * j], d[2 * j], a[2 * j + 1], d[2 * j + 1], qf[c][j][0][nt], qf[c][j][1][nt]);
+            }
         }
       }
       if (!whole) {
@@ -570,6 +570,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
             if (top > m[nt][e]) {  // (the same in all lanes of a column)
               const float keep = exp2_fast((m[nt][e] - top) * cs[nt][e]);
               m[nt][e] = top;
+              shift[nt][e] = -top * cs[nt][e];
               l[nt][e] *= keep;
 #pragma unroll
               for (int i = 0; i < D / 16; ++i) {
@@ -583,14 +584,12 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
       uint32_t pf[2][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        // (an empty row's maximum stays -inf: all its p are 0)
-        const float m0 = m[nt][0] == -INFINITY ? 0.f : -m[nt][0] * cs[nt][0], m1 = m[nt][1] == -INFINITY ? 0.f : -m[nt][1] * cs[nt][1];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const float p0 = exp2_fast(fmaf(s[i][nt][2 * r], cs[nt][0], m0));
-            const float p1 = exp2_fast(fmaf(s[i][nt][2 * r + 1], cs[nt][1], m1));
+            const float p0 = exp2_fast(fmaf(s[i][nt][2 * r], cs[nt][0], shift[nt][0]));
+            const float p1 = exp2_fast(fmaf(s[i][nt][2 * r + 1], cs[nt][1], shift[nt][1]));
             l[nt][0] += p0;
             l[nt][1] += p1;
             pf[i][nt][r] = transpose_8x8(pack_h2(p0, p1));
@@ -598,16 +597,19 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
       }
       // O^T += V^T P^T
       const int t_a = token_of(2 * q), t_b = token_of(2 * q + 1);
+      // a lane's block: 16 elements of one of two planes (D = 64: half of one)
+      const uint8_t* const v_plane = base + (S::kPlanes + (D == 64 ? 0 : g >> 2)) * kPlaneBytes;
+      const uint8_t* const v_codes_a = v_plane + (D == 64 ? g * 4 : (g & 3) * 8) + t_a * 32;
+      const uint8_t* const v_codes_b = v_codes_a + (t_b - t_a) * 32;
+      const uint8_t* const v_scales_a = v_plane + kPlaneScales + (D == 64 ? g >> 1 : g & 3) + t_a * 4;
+      const uint8_t* const v_scales_b = v_scales_a + (t_b - t_a) * 4;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int r = 0; r < kRuns; ++r) {
-          // a lane's block: 16 elements of a plane (D = 64: half of one)
-          const uint32_t plane = base + i * S::kGranule + (S::kPlanes + 2 * r + (D == 64 ? 0 : g >> 2)) * kPlaneBytes;
-          const uint32_t row = plane + (D == 64 ? g * 4 : (g & 3) * 8);
-          const uint32_t scale_at = plane + kPlaneScales + (D == 64 ? g >> 1 : g & 3);
-          uint32_t sb[4] = {lds8(scale_at + t_a * 4), lds8(scale_at + t_b * 4), lds8(scale_at + (t_a + 8) * 4),
-                            lds8(scale_at + (t_b + 8) * 4)};
+          constexpr int kScaleStep = 8 * 4, kCodeStep = 8 * 32;
+          const int at = i * S::kGranule + 2 * r * kPlaneBytes;
+          uint32_t sb[4] = {v_scales_a[at], v_scales_b[at], v_scales_a[at + kScaleStep], v_scales_b[at + kScaleStep]};
           if (!whole) {
             // A masked place adds 0 whatever it holds: tokens past the length and NaN scales
             // become 0, and a NaN goes to the columns that do see its token.
@@ -648,11 +650,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
           uint32_t codes[4][2];  // the four tokens' codes
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint32_t at = row + ((j & 1 ? t_b : t_a) + (j >> 1) * 8) * 32;
+            const uint8_t* const code = (j & 1 ? v_codes_b : v_codes_a) + at + (j >> 1) * kCodeStep;
             if constexpr (D == 64) {
-              codes[j][0] = lds32(at);
+              codes[j][0] = load_32(code);
             } else {
-              const uint2 v = lds64(at);
+              const uint2 v = load_64(code);
               codes[j][0] = v.x;
               codes[j][1] = v.y;
             }
