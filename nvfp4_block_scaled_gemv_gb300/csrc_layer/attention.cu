@@ -13,7 +13,7 @@
 // significant bits and is exact, so the only roundings before the fp32 sums are p to fp16
 // (2^-11 of itself; below 2^-14 of the row's largest p, 2^-25 of that) and the result's.
 //
-// A warp works by itself: 32 tokens at a time in a ring of stages that it fills with bulk
+// A warp works by itself: 32 tokens (D = 64: 64) at a time in a ring of stages that it fills with bulk
 // copies, a copy per 16 tokens (a granule of the cache, K and V in one run of bytes).  All
 // tiles of all sequences and heads, one after another, are cut into equal runs, one per
 // warp, whatever the lengths are; the lengths are read on the device.  A warp that has all
@@ -35,20 +35,25 @@ namespace nvfp4 {
 
 namespace {
 
-constexpr int kTileTokens = 32;  // a stage: two granules
 constexpr int kMostWarps = 16;
 constexpr int64_t kPieceList = (kAttentionCtas * (int64_t)sizeof(int4) + 255) / 256 * 256;
 
 __device__ int g_attention_timeouts;
+
+// Warps of a CTA, as many as the registers take: D * NT / 4 of results, D * NT / 8 of queries, ~65
+// beside them (D = 64, NT = 4 with 12 warps spills: 57 us in place of 50 for 16 x 8 query tokens on 8192).
+__host__ __device__ constexpr int warps_for(int D, int NT) { return D * NT <= 128 ? 16 : D * NT <= 256 && D != 64 ? 12 : 8; }
 
 template <int D, int NT>
 struct Shape {
   static constexpr int kColumns = 8 * NT;
   static constexpr int kPlanes = D / 64;
   static constexpr int kGranule = 2 * kPlanes * kPlaneBytes;  // bytes of K and V of 16 tokens
-  static constexpr int kStage = 2 * kGranule;
-  // (registers: D * NT / 4 of results, D * NT / 8 of queries, ~60 beside them)
-  static constexpr int kWarps = D * NT <= 128 ? 16 : 8;
+  // granules of a stage (one costs ~240 instructions beside its granules' own)
+  static constexpr int kGranules = D == 64 ? 4 : 2;
+  static constexpr int kTile = kGranules * kGranuleTokens;
+  static constexpr int kStage = kGranules * kGranule;
+  static constexpr int kWarps = warps_for(D, NT);
   static constexpr int kStagesFit = (220 * 1024 / kWarps - 64) / kStage;
   static constexpr int kStages = kStagesFit < 6 ? kStagesFit : 6;
   static constexpr int kThreads = 32 * kWarps;
@@ -108,6 +113,7 @@ struct Sequence {
   bool beyond;             // the length is beyond the page table
 };
 
+template <int TILE>
 __device__ __forceinline__ Sequence sequence_of(const AttentionParams& p, int b) {
   Sequence s;
   if (p.q_starts != nullptr) {
@@ -123,9 +129,9 @@ __device__ __forceinline__ Sequence sequence_of(const AttentionParams& p, int b)
   s.length = s.beyond ? (int32_t)p.capacity : max(length, 0);
   const int32_t next = s.length - s.n + 1;  // tokens up to the first query's
   const int32_t lo = p.window > 0 && next > p.window ? next - p.window : 0;
-  s.first_tile = lo / kTileTokens;
+  s.first_tile = lo / TILE;
   // (one tile at least, so that somebody writes the result of an empty row)
-  s.tiles = s.n == 0 || s.n * p.group > p.few_columns ? 0 : max((s.length + kTileTokens - 1) / kTileTokens - s.first_tile, 1);
+  s.tiles = s.n == 0 || s.n * p.group > p.few_columns ? 0 : max((s.length + TILE - 1) / TILE - s.first_tile, 1);
   return s;
 }
 
@@ -274,7 +280,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
   const int first_b = threadIdx.x * share;
   uint32_t mine = 0;
   for (int b = first_b; b < min(first_b + share, p.B); ++b) {
-    const Sequence seq = sequence_of(p, b);
+    const Sequence seq = sequence_of<S::kTile>(p, b);
     mine += (uint32_t)(seq.tiles * column_tiles(p, seq.n, C));
   }
   mine *= (uint32_t)p.Hkv;
@@ -313,12 +319,12 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
   const int place = __ffs(__ballot_sync(0xffffffffu, begin < share_end)) - 1;
   if (place > 0) before = __shfl_sync(0xffffffffu, share_end, place - 1);
   int b = (chunk * 32 + place) * share;
-  Sequence seq = sequence_of(p, b);
+  Sequence seq = sequence_of<S::kTile>(p, b);
   for (;;) {
     const uint32_t here = (uint32_t)(seq.tiles * column_tiles(p, seq.n, C)) * (uint32_t)p.Hkv;
     if (before + here > begin) break;
     before += here;
-    seq = sequence_of(p, ++b);
+    seq = sequence_of<S::kTile>(p, ++b);
   }
   // head, column tile and tile at `begin`
   int32_t cts = column_tiles(p, seq.n, C);
@@ -331,18 +337,20 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
   int32_t litem = item, lcts = cts;
   int32_t ltile = seq.first_tile + tile, ltile_end = seq.first_tile + seq.tiles;  // of the sequence
   uint32_t to_load = end - begin;
-  // a lane's granule of the next 16 tiles, as its number in the cache, or kAbsent (past the
+  // a lane's granule of the next kWindow tiles, as its number in the cache, or kAbsent (past the
   // length) or kBad (its page does not exist)
   constexpr int64_t kAbsent = -1, kBad = -2;
+  constexpr int kGr = S::kGranules, kWindow = 32 / kGr;
+  constexpr uint32_t kAll = (1u << kGr) - 1;
   int64_t source = kAbsent;
-  int32_t source_tile = ltile - 16;
+  int32_t source_tile = ltile - kWindow;
   uint32_t load_stage = 0;
-  uint32_t bad_bits = 0;           // two bits a stage: granules whose page does not exist
+  uint32_t bad_bits = 0;           // kGr bits a stage: granules whose page does not exist
   auto load_next = [&]() {
     if (to_load == 0) return;
-    if (ltile >= source_tile + 16) {
+    if (ltile >= source_tile + kWindow) {
       source_tile = ltile;
-      const int32_t granule = ltile * 2 + lane;
+      const int32_t granule = ltile * kGr + lane;
       source = kAbsent;
       if (granule < (ahead.length + kGranuleTokens - 1) / kGranuleTokens) {
         const int32_t page = granule / p.granules;
@@ -352,26 +360,26 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
       }
     }
     const uint32_t bar = bars + 8 * load_stage, dst = ring + load_stage * S::kStage;
-    const int64_t mine = __shfl_sync(0xffffffffu, source, (ltile - source_tile) * 2 + (lane & 1));
-    const uint32_t valid = __ballot_sync(0xffffffffu, mine >= 0) & 3u;
-    const uint32_t bad = __ballot_sync(0xffffffffu, mine == kBad) & 3u;
+    const int64_t mine = __shfl_sync(0xffffffffu, source, (ltile - source_tile) * kGr + (lane & (kGr - 1)));
+    const uint32_t valid = __ballot_sync(0xffffffffu, mine >= 0) & kAll;
+    const uint32_t bad = __ballot_sync(0xffffffffu, mine == kBad) & kAll;
     if (lane == 0) tc::mbar_expect_tx(bar, (uint32_t)__popc(valid) * S::kGranule);
     __syncwarp();
     if (valid >> lane & 1u) tc::bulk_load(dst + lane * S::kGranule, p.cache + mine * S::kGranule, S::kGranule, bar);
-    bad_bits = (bad_bits & ~(3u << (2 * load_stage))) | bad << (2 * load_stage);
+    bad_bits = (bad_bits & ~(kAll << (kGr * load_stage))) | bad << (kGr * load_stage);
     load_stage = load_stage + 1 == kStages ? 0 : load_stage + 1;
     --to_load;
     if (++ltile == ltile_end && to_load != 0) {
       if (++litem == lcts * p.Hkv) {
         litem = 0;
         do {
-          ahead = sequence_of(p, ++lb);
+          ahead = sequence_of<S::kTile>(p, ++lb);
         } while (ahead.tiles == 0);
         lcts = column_tiles(p, ahead.n, C);
       }
       ltile = ahead.first_tile;
       ltile_end = ltile + ahead.tiles;
-      source_tile = ltile - 16;
+      source_tile = ltile - kWindow;
     }
   };
   uint32_t left = end - begin;
@@ -490,16 +498,16 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
         if (!ok) break;
         __syncwarp();
       }
-      const int32_t t0 = (seq.first_tile + tile) * kTileTokens;
-      const uint32_t bad = bad_bits >> (2 * stage) & 3u;
-      const bool whole = t0 >= full_from && t0 + kTileTokens <= full_to && bad == 0;  // (the same in all lanes)
+      const int32_t t0 = (seq.first_tile + tile) * S::kTile;
+      const uint32_t bad = bad_bits >> (kGr * stage) & kAll;
+      const bool whole = t0 >= full_from && t0 + S::kTile <= full_to && bad == 0;  // (the same in all lanes)
 
       // S^T, 16 tokens x 8 columns at a time
       const uint8_t* const k_codes = base + token_of(g) * 32 + q * 8;
       const uint8_t* const k_scales = base + kPlaneScales + token_of(g) * 4 + q;
-      float s[2][NT][4];
+      float s[kGr][NT][4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < kGr; ++i) {
 #pragma unroll
         for (int c = 0; c < S::kPlanes; ++c) {
           const uint8_t* const row = k_codes + i * S::kGranule + c * kPlaneBytes;
@@ -529,7 +537,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
       }
       if (!whole) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < kGr; ++i)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             const int32_t t = t0 + i * 16 + r * 8 + token_of(g);
@@ -554,7 +562,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float top = fmaxf(fmaxf(s[0][nt][e], s[0][nt][2 + e]), fmaxf(s[1][nt][e], s[1][nt][2 + e]));
+          float top = fmaxf(s[0][nt][e], s[0][nt][2 + e]);
+#pragma unroll
+          for (int i = 1; i < kGr; ++i) top = fmaxf(fmaxf(top, s[i][nt][e]), s[i][nt][2 + e]);
           // (from -inf any score passes; -inf - -inf is NaN and does not)
           passed |= (top - m[nt][e]) * cs[nt][e] > 8.f;
         }
@@ -563,7 +573,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float top = fmaxf(fmaxf(s[0][nt][e], s[0][nt][2 + e]), fmaxf(s[1][nt][e], s[1][nt][2 + e]));
+            float top = fmaxf(s[0][nt][e], s[0][nt][2 + e]);
+#pragma unroll
+            for (int i = 1; i < kGr; ++i) top = fmaxf(fmaxf(top, s[i][nt][e]), s[i][nt][2 + e]);
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
@@ -581,11 +593,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
           }
       }
       // P, and its transposition to the second product's operand
-      uint32_t pf[2][NT][2];
+      uint32_t pf[kGr][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < kGr; ++i)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             const float p0 = exp2_fast(fmaf(s[i][nt][2 * r], cs[nt][0], shift[nt][0]));
@@ -604,7 +616,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
       const uint8_t* const v_scales_a = v_plane + kPlaneScales + (D == 64 ? g >> 1 : g & 3) + t_a * 4;
       const uint8_t* const v_scales_b = v_scales_a + (t_b - t_a) * 4;
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < kGr; ++i)
 #pragma unroll
         for (int r = 0; r < kRuns; ++r) {
           constexpr int kScaleStep = 8 * 4, kCodeStep = 8 * 32;
@@ -736,7 +748,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
       item = 0;
       do {
         before += (uint32_t)(seq.tiles * cts) * (uint32_t)p.Hkv;
-        seq = sequence_of(p, ++b);
+        seq = sequence_of<S::kTile>(p, ++b);
         cts = column_tiles(p, seq.n, C);
       } while (seq.tiles == 0);
     }
@@ -749,7 +761,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
   // here and goes on in the next.
   __syncthreads();
   const uint32_t present =
-      __ballot_sync(0xffffffffu, (lane >> 1) < kWarps && piece_of[(lane >> 1) & (kWarps - 1)][lane & 1].at != nullptr);
+      __ballot_sync(0xffffffffu, (lane >> 1) < kWarps && piece_of[min(lane >> 1, kWarps - 1)][lane & 1].at != nullptr);
   if (present == 0) return;
   // (an item begins in the second place of its first warp)
   const uint32_t starts = (present & 0xAAAAAAAAu) | (present & (0u - present));
@@ -807,7 +819,7 @@ __global__ void __launch_bounds__(128) attention_sum_kernel(const AttentionParam
   pdl_wait();
   const int4 piece = p.pieces[blockIdx.x];
   if (piece.x < 0) return;
-  const Sequence seq = sequence_of(p, piece.x);
+  const Sequence seq = sequence_of<S::kTile>(p, piece.x);
   const int32_t cts = column_tiles(p, seq.n, C);
   const int head = piece.y / cts, first_column = (piece.y - head * cts) * C;
   const int e = (int)blockIdx.y * 128 + threadIdx.x;
@@ -842,12 +854,12 @@ cudaError_t launch_with(AttentionParams p, void* workspace, int sms, cudaStream_
 int attention_columns(int D, int64_t most) {
   // the fewest columns of a pass that hold a sequence's (the cache is read once), as far as
   // results and queries fit the registers
-  const int largest = D == 256 ? 16 : 32;
+  const int largest = D >= 128 ? 16 : 32;
   return most <= 8 ? 8 : most <= 16 || largest == 16 ? 16 : 32;
 }
 
 int64_t attention_workspace(int D, int columns) {
-  const int warps = D * (columns / 8) <= 128 ? 16 : 8;
+  const int warps = warps_for(D, columns / 8);
   return kPieceList + (int64_t)kAttentionCtas * (2 + warps) * columns * (D + 2) * 4;
 }
 
@@ -858,7 +870,6 @@ cudaError_t launch_attention(AttentionParams p, int D, int columns, void* worksp
     case 6432: return launch_with<64, 4>(p, workspace, sms, stream);
     case 12808: return launch_with<128, 1>(p, workspace, sms, stream);
     case 12816: return launch_with<128, 2>(p, workspace, sms, stream);
-    case 12832: return launch_with<128, 4>(p, workspace, sms, stream);
     case 25608: return launch_with<256, 1>(p, workspace, sms, stream);
     case 25616: return launch_with<256, 2>(p, workspace, sms, stream);
     default: return cudaErrorInvalidValue;
