@@ -63,6 +63,7 @@ struct AttentionParams {
   int64_t q_token, q_head;
   int64_t pages, capacity;    // capacity: max_pages * page_size
   int32_t T, B, Hq, Hkv, group, uniform_n, max_pages, granules, window, causal;
+  int32_t most_columns;       // of a sequence (query tokens x heads of a group), at most
   int32_t few_columns;        // sequences of more columns are the prompt kernel's
   int32_t bf16;
   float scale_log2;           // scale * log2(e)

@@ -131,6 +131,7 @@ AttentionParams sizes_of(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t 
   p.max_pages = (int32_t)max_pages;
   p.granules = (int32_t)(page_size / kGranuleTokens);
   p.capacity = max_pages * page_size;
+  p.most_columns = (int32_t)columns;
   p.few_columns = (int32_t)(columns < kFewColumns ? columns : kFewColumns);
   return p;
 }

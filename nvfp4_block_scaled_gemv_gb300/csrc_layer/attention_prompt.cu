@@ -22,6 +22,7 @@
 // tiles to fp16, 12 issues MMAs, 13 copies granules.
 #include <cfloat>
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -43,43 +44,101 @@ constexpr int kNanTiles = 4;  // tiles whose NaN marks are kept (more than are i
 
 __device__ int g_prompt_timeouts;
 
-template <int D, int BN, int NQ>
+template <int D, int BN, int NQ, int CTAS>
 struct Prompt {
   static constexpr int kPlanes = D / 64;
-  static constexpr int kRows = 128 * NQ;
+  static constexpr int kRows = 128 * NQ * CTAS;
   static constexpr int64_t kPiece = (int64_t)kRows * (D + 2);  // floats: results, then (reference, sum) of the rows
-  static constexpr uint32_t kPanel = 128 * 128;                 // a plane of 128 rows of Q
+  static constexpr uint32_t kPanel = 128 * 128;                // a plane of 128 rows of Q
   static constexpr uint32_t kQBytes = (uint32_t)NQ * kPlanes * kPanel;
-  static constexpr uint32_t kTilePanel = BN * 128;              // a plane of a K or V tile
-  static constexpr uint32_t kSlot = kPlanes * kTilePanel;
-  static constexpr uint32_t kGranule = 2 * kPlanes * kPlaneBytes;
-  static constexpr int kGranules = BN / kGranuleTokens;
-  static constexpr uint32_t kRaw = kGranules * kGranule;
-  static constexpr int kSlots = D == 64 ? 6 : 3;
-  static constexpr int kRaws = D == 64 ? 4 : 2;
-  static constexpr uint32_t kUsed = 1024 + kQBytes + kSlots * kSlot + kRaws * kRaw + kNanTiles * (BN * 2 + 4);
+  // what a CTA has of a tile: some of K's tokens, and some planes of V
+  static constexpr int kKeyTokens = BN / CTAS, kValuePlanes = kPlanes / CTAS;
+  static constexpr uint32_t kKeyPanel = kKeyTokens * 128, kValuePanel = BN * 128;
+  static constexpr uint32_t kSlot = kPlanes * kKeyPanel;
+  // raw tiles: K of those tokens, V of all (its scales are looked at for all planes)
+  static constexpr uint32_t kSide = kPlanes * kPlaneBytes;  // K or V of a granule
+  static constexpr int kKeyGranules = kKeyTokens / kGranuleTokens, kGranules = BN / kGranuleTokens;
+  // (one SM: K and V of a granule in one copy, one after the other, as they are in the cache)
+  static constexpr int kKeyCopies = CTAS == 1 ? 0 : kKeyGranules, kCopies = kKeyCopies + kGranules;
+  static constexpr uint32_t kCopy = CTAS == 1 ? 2 * kSide : kSide, kRaw = kCopies * kCopy;
+  static constexpr uint32_t kRawValues = CTAS == 1 ? kSide : kKeyCopies * kSide;  // where V's begin
+  static constexpr int kSlots = D == 64 ? 6 : D == 128 && CTAS == 2 ? 5 : 3;
+  static constexpr int kRaws = D == 64 ? 4 : D == 128 && CTAS == 2 ? 3 : 2;
+  // Tensor memory: S, two buffers; P of its own where there is room, otherwise over S; O at the end.
+  static constexpr bool kOwnP = NQ == 2 && 3 * BN <= 512 - NQ * D;
+  static constexpr uint32_t kS = BN > 128 || kOwnP ? BN : 128, kP = 2 * BN, kO = 512 - NQ * D;
+  static_assert(!kOwnP || kP + BN <= kO, "tensor memory");
+  static constexpr uint32_t kUsed = 1024 + kQBytes + kSlots * kSlot + kRaws * kRaw + kNanTiles * (BN * 2 + 16);
   static constexpr uint32_t kSmem = kUsed > gemm::kAloneSmem ? kUsed : gemm::kAloneSmem;
-  static_assert(kUsed <= 227 * 1024 - 4096, "shared memory");
-  static_assert(2 * kNanTiles >= kSlots + 1, "marks of tiles in flight");
+  static_assert(kSlot == kValuePlanes * kValuePanel, "a slot holds either");
+  static_assert(kCopies <= 32 && kUsed <= 227 * 1024 - 4096, "shared memory");
+  static_assert(2 * kNanTiles >= kSlots + 2, "marks of tiles in flight");
 };
 
+template <int CTAS>
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
-      : "memory");
+  if constexpr (CTAS == 1)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
 }
+template <int CTAS>
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
-      : "memory");
+  if constexpr (CTAS == 1)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
 }
-// kind::f16 with fp16 operands and fp32 results, M = 128; B's rows are the contraction (bit 16).
-__host__ __device__ constexpr uint32_t f16_idesc(uint32_t n, bool b_rows) {
-  return (1u << 4) | ((b_rows ? 1u : 0u) << 16) | ((n >> 3) << 17) | ((128u >> 4) << 24);
+// Arrives on this barrier (of both CTAs of a pair) once the MMAs issued so far have completed.
+template <int CTAS>
+__device__ __forceinline__ void commit_all(uint32_t bar) {
+  if constexpr (CTAS == 1)
+    tc::commit(bar);
+  else
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+// An arrive of some lanes, by a predicate: a branch around it would split the warp.
+__device__ __forceinline__ void arrive_if(uint32_t bar, bool who) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\t@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar),
+               "r"((uint32_t)who)
+               : "memory");
+}
+// Arrives on the barrier of the CTA that issues the MMAs.  What it announces is in tensor memory, or
+// in this CTA's shared memory and ordered for the MMAs by the writers' own proxy fences: the
+// arrive need not order other memory at cluster scope (which takes it ~1000 cycles).
+template <int CTAS>
+__device__ __forceinline__ void arrive_issuer(uint32_t bar, bool who) {
+  if constexpr (CTAS == 1)
+    arrive_if(bar, who);
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\t@p mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" ::"r"(
+            tc::map_rank(bar, 0)),
+        "r"((uint32_t)who)
+        : "memory");
+}
+// kind::f16 with fp16 operands and fp32 results; B's rows are the contraction (bit 16).
+__host__ __device__ constexpr uint32_t f16_idesc(uint32_t m, uint32_t n, bool b_rows) {
+  return (1u << 4) | ((b_rows ? 1u : 0u) << 16) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
 // A tile whose rows are the contraction: 128-byte rows of 64 elements, 8-row groups 1024 bytes
 // apart, the next 64 elements `panel` bytes on.
@@ -128,11 +187,13 @@ __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.
 
 // tc::mbar_wait without its call: one lane waits, in line, so that the warps' registers are
 // split as setmaxnreg says (a call asks for those of its own).
+template <bool CLUSTER = false>
 __device__ __forceinline__ void wait_phase(uint32_t bar, uint32_t parity, bool& ok) {
-  if (!ok || tc::mbar_try(bar, parity)) return;
+  auto done = [&]() { return CLUSTER ? tc::mbar_try_cluster(bar, parity) : tc::mbar_try(bar, parity); };
+  if (!ok || done()) return;
   const uint64_t t0 = tc::global_ns();
-  while (!tc::mbar_try(bar, parity))
-    if (tc::global_ns() - t0 > tc::kWaitNs) {
+  for (uint32_t i = 1; !done(); ++i)
+    if ((i & 63u) == 0 && tc::global_ns() - t0 > tc::kWaitNs) {
       atomicAdd(&g_prompt_timeouts, 1);
       ok = false;
       return;
@@ -220,12 +281,12 @@ __device__ __forceinline__ int32_t row_tiles(const AttentionParams& p, int b, in
   return rows > p.few_columns ? (int32_t)((rows + ROWS - 1) / ROWS) : 0;
 }
 
-template <int D, int BN, int NQ>
+template <int D, int BN, int NQ, int CTAS>
 __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(const AttentionParams p) {
-  using S = Prompt<D, BN, NQ>;
+  using S = Prompt<D, BN, NQ, CTAS>;
   constexpr int kPlanes = S::kPlanes, kSlots = S::kSlots, kRaws = S::kRaws;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * kRaws + 2 * kSlots + 8];
+  __shared__ __align__(8) uint64_t bars[2 * kRaws + 2 * kSlots + 10 + kNanTiles];
   __shared__ uint32_t tmem_slot;
   __shared__ uint32_t raw_bad[kRaws];      // granules of a raw tile whose page does not exist
   __shared__ uint32_t warp_sums[16];
@@ -247,6 +308,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
   auto s_full = [&](int i) { return more + 16 + 8u * i; };
   auto p_ready = [&](int i) { return more + 32 + 8u * i; };
   auto o_done = [&](int i) { return more + 48 + 8u * i; };
+  auto s_free = [&](int i) { return more + 64 + 8u * i; };
+  auto marks_full = [&](int i) { return more + 80 + 8u * i; };
 
   const int lane = threadIdx.x & 31;
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
@@ -256,23 +319,27 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
       tc::mbar_init(raw_empty(i), 4);
     }
     for (int i = 0; i < kSlots; ++i) {
-      tc::mbar_init(slot_full(i), 4);
+      tc::mbar_init(slot_full(i), 4 * CTAS);  // the issuer's
       tc::mbar_init(slot_empty(i), 1);
     }
-    tc::mbar_init(q_full, 4 * NQ);
+    tc::mbar_init(q_full, 4 * NQ * CTAS);  // the issuer's
     tc::mbar_init(drain, 1);
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(s_full(i), 1);
-      tc::mbar_init(p_ready(i), 4);
+      tc::mbar_init(s_free(i), 4 * CTAS);  // the issuer's
+      tc::mbar_init(p_ready(i), 4 * CTAS);  // the issuer's
       tc::mbar_init(o_done(i), 1);
     }
+    for (int i = 0; i < kNanTiles; ++i) tc::mbar_init(marks_full(i), 4);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   pdl_wait();
 
   // The CTA's work: row tiles are numbered over the sequences, the last (which sees most) of a
   // sequence first, the key heads of a row tile follow each other, and the parts of its tokens.
-  const int32_t item = (int32_t)blockIdx.x / p.splits, split = (int32_t)blockIdx.x % p.splits;
+  const int32_t unit = (int32_t)blockIdx.x / CTAS;
+  const int cta = CTAS == 1 ? 0 : (int)tc::cluster_rank();
+  const int32_t item = unit / p.splits, split = unit % p.splits;
   const int32_t rank = item / p.Hkv, head = item % p.Hkv;
   {
     const int share = (p.B + kPromptThreads - 1) / kPromptThreads;
@@ -325,9 +392,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
     }
   }
   __syncthreads();
-  float* const piece = p.partial + (int64_t)blockIdx.x * S::kPiece;
+  float* const piece = p.partial + (int64_t)unit * S::kPiece;
   if (p.splits > 1) {
-    if (split == 0 && threadIdx.x == 0)
+    if (split == 0 && cta == 0 && threadIdx.x == 0)
       reinterpret_cast<PieceHead*>(p.pieces)[item] = {shared_work.q0, shared_work.rows, shared_work.first_row,
                                                       shared_work.beyond};
     if (shared_work.tiles == 0 && shared_work.rows > 0)  // (fewer tiles than parts)
@@ -335,9 +402,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
         reinterpret_cast<float2*>(piece + S::kRows * D)[i] = make_float2(-INFINITY, 0.f);
   }
   if (shared_work.tiles == 0) return;  // (more CTAs than row tiles)
-  if (warp == 12) tc::alloc(smem_u32(&tmem_slot), kPromptColumns);
+  if constexpr (CTAS == 2) tc::cluster_sync();  // the peer's barriers are initialised, and it is there to allocate
+  if (warp == 12) {
+    if constexpr (CTAS == 1) {
+      tc::alloc(smem_u32(&tmem_slot), kPromptColumns);
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_slot)) : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+  }
   tc::fence_before();
   __syncthreads();
+  if constexpr (CTAS == 2) tc::cluster_sync();
   tc::fence_after();
   pdl_launch_dependents();
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
@@ -351,12 +427,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
   if (warp >= 12) {
     registers_down<56>();
     if (warp == 13) {
-      // granules, a lane each
+      // a lane for K or V of a granule
       const int32_t have = (work.length + kGranuleTokens - 1) / kGranuleTokens;
+      const bool keys = lane < S::kKeyCopies;
+      const int32_t first = work.first_token / kGranuleTokens + (keys ? cta * S::kKeyGranules + lane : lane - S::kKeyCopies);
       int issued = 0;
       auto page_of = [&](int32_t j) {
-        const int32_t granule = work.first_token / kGranuleTokens + j * S::kGranules + lane;
-        if (lane >= S::kGranules || j >= tiles || granule >= have) return INT32_MIN;
+        const int32_t granule = first + j * S::kGranules;
+        if (lane >= S::kCopies || j >= tiles || granule >= have) return INT32_MIN;
         const int32_t id = __ldg(p.page_table + (int64_t)work.b * p.max_pages + granule / p.granules);
         return id >= 0 && id < p.pages ? id : -1;
       };
@@ -372,13 +450,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
         const uint32_t bad = __ballot_sync(0xffffffffu, id == -1);
         if (lane == 0) {
           raw_bad[i] = bad;
-          tc::mbar_expect_tx(raw_full(i), (uint32_t)__popc(valid) * S::kGranule);
+          tc::mbar_expect_tx(raw_full(i), (uint32_t)__popc(valid) * S::kCopy);
         }
         __syncwarp();
         if (id >= 0) {
-          const int32_t granule = work.first_token / kGranuleTokens + j * S::kGranules + lane;
+          const int32_t granule = first + j * S::kGranules;
           const int64_t at = ((int64_t)id * p.Hkv + work.head) * p.granules + granule % p.granules;
-          tc::bulk_load(raw_s + i * S::kRaw + lane * S::kGranule, p.cache + at * S::kGranule, S::kGranule, raw_full(i));
+          tc::bulk_load(raw_s + i * S::kRaw + lane * S::kCopy, p.cache + (2 * at + (keys || CTAS == 1 ? 0 : 1)) * S::kSide,
+                        S::kCopy, raw_full(i));
         }
         ++issued;
       }
@@ -389,56 +468,69 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
         wait_phase(raw_full(i % kRaws), (uint32_t)((i / kRaws) & 1), landed);
       }
       __syncwarp();
-    } else if (warp == 12) {
-      constexpr uint32_t qk = f16_idesc(BN, false), pv = f16_idesc(D, true);
+    } else if (warp == 12 && cta == 0) {
+      constexpr uint32_t qk = f16_idesc(128 * CTAS, BN, false), pv = f16_idesc(128 * CTAS, D, true);
+      constexpr bool kPair = false;
       const uint64_t q_desc = tc::desc_sw128(q_s);
-      wait_phase(q_full, 0, ok);
+      wait_phase<kPair>(q_full, 0, ok);
       auto scores = [&](int32_t x) {
         const int32_t j = NQ == 2 ? x >> 1 : x;
         const int u = NQ == 2 ? x & 1 : 0;
         const int fill = 2 * j, i = fill % kSlots;
-        wait_phase(slot_full(i), (uint32_t)(fill / kSlots) & 1u, ok);
+        wait_phase<kPair>(slot_full(i), (uint32_t)(fill / kSlots) & 1u, ok);
         ok = __all_sync(0xffffffffu, ok);
         tc::fence_after();
         if (!ok) return;
         const uint64_t a = q_desc + (uint64_t)(u * kPlanes * (S::kPanel >> 4));
         const uint64_t b = tc::desc_sw128(slot_s + i * S::kSlot);
-        const uint32_t d = tmem + 128u * (x & 1);
+        const uint32_t d = tmem + S::kS * (x & 1);
         if (gemm::elect_one()) {
 #pragma unroll
           for (int c = 0; c < kPlanes; ++c)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_ss(d, a + c * (S::kPanel >> 4) + 2 * k, b + c * (S::kTilePanel >> 4) + 2 * k, qk, c + k > 0);
-          tc::commit(s_full(x & 1));
-          if (u == NQ - 1) tc::commit(slot_empty(i));
+              mma_ss<CTAS>(d, a + c * (S::kPanel >> 4) + 2 * k, b + c * (S::kKeyPanel >> 4) + 2 * k, qk, c + k > 0);
+          commit_all<CTAS>(s_full(x & 1));
+          if (u == NQ - 1) commit_all<CTAS>(slot_empty(i));
         }
         __syncwarp();
       };
       scores(0);
       if (steps > 1) scores(1);
       for (int32_t x = 0; x < steps && ok; ++x) {
+        if (S::kOwnP && x + 2 < steps) {
+          // S is in registers: the next scores need not wait for P and its product
+          wait_phase<kPair>(s_free(x & 1), (uint32_t)(x >> 1) & 1u, ok);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          scores(x + 2);
+        }
         const int32_t j = NQ == 2 ? x >> 1 : x;
         const int u = NQ == 2 ? x & 1 : 0;
         const int fill = 2 * j + 1, i = fill % kSlots;
-        wait_phase(slot_full(i), (uint32_t)(fill / kSlots) & 1u, ok);
-        wait_phase(p_ready(x & 1), (uint32_t)(x >> 1) & 1u, ok);
+        wait_phase<kPair>(slot_full(i), (uint32_t)(fill / kSlots) & 1u, ok);
+        wait_phase<kPair>(p_ready(x & 1), (uint32_t)(x >> 1) & 1u, ok);
         ok = __all_sync(0xffffffffu, ok);
         tc::fence_after();
         if (!ok) break;
-        const uint64_t b = desc_rows(slot_s + i * S::kSlot, S::kTilePanel);
-        const uint32_t a = tmem + 128u * (x & 1), d = tmem + 256u + 128u * u;
+        const uint64_t b = desc_rows(slot_s + i * S::kSlot, S::kValuePanel);
+        const uint32_t a = tmem + (S::kOwnP ? S::kP + (BN / 2) * u : S::kS * (x & 1)), d = tmem + S::kO + D * u;
         if (gemm::elect_one()) {
 #pragma unroll
-          for (int k = 0; k < BN / 16; ++k) mma_ts(d, a + 8u * k, b + (uint64_t)(k * (16 * 128 >> 4)), pv, j > 0 || k > 0);
-          tc::commit(o_done(u));
-          if (u == NQ - 1) tc::commit(slot_empty(i));
+          for (int k = 0; k < BN / 16; ++k) mma_ts<CTAS>(d, a + 8u * k, b + (uint64_t)(k * (16 * 128 >> 4)), pv, j > 0 || k > 0);
+          commit_all<CTAS>(o_done(u));
+          if (u == NQ - 1) commit_all<CTAS>(slot_empty(i));
         }
         __syncwarp();
-        if (x + 2 < steps) scores(x + 2);
+        if (!S::kOwnP && x + 2 < steps) scores(x + 2);
       }
       // every MMA has finished before tensor memory is released
-      if (gemm::elect_one()) tc::commit(drain);
+      if (gemm::elect_one()) {
+        if constexpr (CTAS == 1)
+          tc::commit(drain);
+        else
+          asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(drain) : "memory");
+      }
       bool drained = true;
       wait_phase(drain, 0, drained);
       __syncwarp();
@@ -447,58 +539,67 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
     registers_down<88>();
     // raw granules to fp16 tiles: a warp takes 8 tokens of a plane, a lane a block
     const int w = warp - 8, row8 = lane >> 2, block = lane & 3;
-    constexpr int kUnits = BN / 8 * kPlanes / 4;  // per warp
+    constexpr int kUnits = S::kKeyTokens / 8 * kPlanes / 4;  // per warp, of either side
     for (int32_t j = 0; j < tiles && ok; ++j) {
       const int ri = j % kRaws;
       const int32_t t0 = work.first_token + j * BN;
       const bool whole = tile_whole<BN>(work, t0);
-      if (lane == 0) wait_phase(raw_full(ri), (uint32_t)(j / kRaws) & 1u, ok);
-      ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+      wait_phase(raw_full(ri), (uint32_t)(j / kRaws) & 1u, ok);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
       __syncwarp();
       const uint32_t bad = raw_bad[ri];
-      const int marks = j % kNanTiles;
-#pragma unroll 1
-      for (int side = 0; side < 2 && ok; ++side) {
-        const int fill = 2 * j + side, si = fill % kSlots;
-        if (lane == 0)
-          wait_phase(slot_empty(si), ((uint32_t)(fill / kSlots) & 1u) ^ 1u, ok);
-        ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-      __syncwarp();
-        if (!ok) break;
-        if (side == 1 && !whole) {
-          const int t = threadIdx.x - 256;
-          if (t < BN) nan_marks[marks * BN + t] = 0;
-          if (t == 0) nan_any[marks] = 0;
-          named_barrier_sync(1, 128);
+      if (!whole) {
+        // Rows that do not see a token must not get a NaN of its V: there the blocks whose scale is
+        // NaN become 0, and are marked for the rows that do see them.
+        const int t = threadIdx.x - 256;
+        uint32_t marks = 0;
+        if (t < BN && t0 + t < work.length && !(bad >> (S::kKeyCopies + t / kGranuleTokens) & 1u)) {
+          const uint32_t at = raw_s + ri * S::kRaw + S::kRawValues + t / kGranuleTokens * S::kCopy + kPlaneScales +
+                              t % kGranuleTokens * 4;
+#pragma unroll
+          for (int c = 0; c < kPlanes; ++c) {
+            uint32_t four;
+            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(four) : "r"(at + c * kPlaneBytes));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) marks |= (four >> (8 * i) & 0x7Fu) == 0x7Fu ? 1u << (4 * c + i) : 0u;
+          }
         }
-        const uint32_t from = raw_s + ri * S::kRaw + side * kPlanes * kPlaneBytes;
+        if (t < BN) nan_marks[j % kNanTiles * BN + t] = (uint16_t)marks;
+        const bool any = __any_sync(0xffffffffu, marks != 0);
+        if (lane == 0) nan_any[j % kNanTiles * 4 + w] = any;
+        __syncwarp();
+      }
+      arrive_if(marks_full(j % kNanTiles), lane == 0);
+      // K, then V: one code for both, with distances that depend on which
+#pragma unroll 1
+      for (int side = 0; side < 2; ++side) {
+        const bool values = side == 1;
+        const int own = values ? S::kValuePlanes : kPlanes;  // planes of this CTA
+        const uint32_t panel = values ? S::kValuePanel : S::kKeyPanel;
+        const int fill = 2 * j + (values ? 1 : 0), si = fill % kSlots;
+        wait_phase(slot_empty(si), ((uint32_t)(fill / kSlots) & 1u) ^ 1u, ok);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        __syncwarp();
+        const uint32_t from = raw_s + ri * S::kRaw + (values ? S::kRawValues + cta * S::kValuePlanes * kPlaneBytes : 0);
         const uint32_t to = slot_s + si * S::kSlot;
-#pragma unroll 4
+#pragma unroll 2
         for (int k = 0; k < kUnits; ++k) {
           const int unit = w + 4 * k;
-          const int group = unit / kPlanes, plane = unit % kPlanes;
-          const int t = group * 8 + row8;  // token of the tile
-          const uint32_t at = from + (group >> 1) * S::kGranule + plane * kPlaneBytes;
+          const int group = unit >> (own == 4 ? 2 : own == 2 ? 1 : 0), plane = unit & (own - 1);
+          const int t = group * 8 + row8;  // token of this CTA's
+          const uint32_t at = from + (group >> 1) * S::kCopy + plane * kPlaneBytes;
           const int row = (group & 1) * 8 + row8;
           uint2 codes;
           asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(codes.x), "=r"(codes.y) : "r"(at + row * 32 + block * 8));
           uint32_t sb;
           asm volatile("ld.shared.u8 %0, [%1];" : "=r"(sb) : "r"(at + kPlaneScales + row * 4 + block));
           if (!whole || bad) {
-            const bool absent = (bad >> (group >> 1) & 1u) != 0;
-            if (t0 + t >= work.length || absent) sb = 0;
-            if (absent && side == 0) {
-              sb = 0x7Fu;  // its scores are NaN
-            } else if (side == 1 && !whole && (sb & 0x7Fu) == 0x7Fu) {
-              // rows that do not see the token must not get its NaN: the block is 0 here, and
-              // marked for the rows that do
-              sb = 0;
-              const int bit = plane * 4 + block;
-              const uint32_t word = smem_u32(nan_marks + marks * BN + (t & ~1));
-              const uint32_t mark = 1u << (bit + 16 * (t & 1));
-              asm volatile("red.shared.or.b32 [%0], %1;" ::"r"(word), "r"(mark) : "memory");
-              asm volatile("st.shared.b32 [%0], %1;" ::"r"(smem_u32(nan_any + marks)), "r"(1u) : "memory");
-            }
+            const bool absent = (bad >> ((group >> 1) + (values ? S::kKeyCopies : 0)) & 1u) != 0;
+            if (t0 + t + (values ? 0 : cta * S::kKeyTokens) >= work.length || absent) sb = 0;
+            if (absent && !values) sb = 0x7Fu;  // its scores are NaN
+            if (values && !whole && (sb & 0x7Fu) == 0x7Fu) sb = 0;
           }
           const uint32_t s2 = e4m3x2_to_f16x2(sb * 0x101u);
           uint32_t h[8];
@@ -507,7 +608,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
 #pragma unroll
           for (int i = 0; i < 8; ++i) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h[i]) : "r"(s2));
           // two 16-byte chunks of the token's row, swizzled by the row
-          const uint32_t line = to + plane * S::kTilePanel + t * 128;
+          const uint32_t line = to + plane * panel + t * 128;
           const uint32_t c0 = (uint32_t)((2 * block) ^ (t & 7)) * 16u;
           asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(line + c0), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
                        : "memory");
@@ -517,10 +618,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
         }
         async_proxy_fence();
         __syncwarp();
-        if (lane == 0) {
-          tc::mbar_arrive(slot_full(si));
-          if (side == 1) tc::mbar_arrive(raw_empty(ri));
-        }
+        arrive_issuer<CTAS>(slot_full(si), lane == 0);
+        if (values) arrive_if(raw_empty(ri), lane == 0);
       }
     }
   } else {
@@ -528,7 +627,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
     const int u = warp >> 2;
     if (u < NQ) {
       const int r = threadIdx.x & 127;          // row of the half, and lane of tensor memory
-      const int32_t row = work.first_row + u * 128 + r;
+      const int in_tile = (u * CTAS + cta) * 128 + r;
+      const int32_t row = work.first_row + in_tile;
       const bool real = row < work.rows;
       const int32_t token = row / p.group, member = row - token * p.group;
       const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
@@ -574,7 +674,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
       }
       async_proxy_fence();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(q_full);
+      arrive_issuer<CTAS>(q_full, lane == 0);
 
       // (not 0 or infinite: those times 0 or an infinity would be NaN)
       const float c = fminf(fmaxf(p.scale_log2 * (p.encode_k ? 1.f / __ldg(p.encode_k + work.head) : 1.f) * back, FLT_MIN), FLT_MAX);
@@ -583,14 +683,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
       float m = -INFINITY;       // the row's reference score, before c
       uint64_t sum = 0;          // two partial sums
       uint32_t nan_blocks = 0;   // blocks of 16 whose V is NaN in a token that the row sees
-      const uint32_t o_at = tmem + lanes + 256u + 128u * u;
+      const uint32_t o_at = tmem + lanes + S::kO + D * u;
 #pragma unroll 1
       for (int32_t j = 0; j < tiles; ++j) {
         const int32_t x = NQ == 2 ? 2 * j + u : j;
-        const uint32_t s_at = tmem + lanes + 128u * (x & 1);
+        const uint32_t s_at = tmem + lanes + S::kS * (x & 1);
+        const uint32_t p_at = S::kOwnP ? tmem + lanes + S::kP + (BN / 2) * u : s_at;
         const int32_t t0 = work.first_token + j * BN;
-        if (lane == 0) wait_phase(s_full(x & 1), (uint32_t)(x >> 1) & 1u, ok);
-        ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+        wait_phase(s_full(x & 1), (uint32_t)(x >> 1) & 1u, ok);
+        ok = __all_sync(0xffffffffu, ok);
       __syncwarp();
         if (!ok) break;
         tc::fence_after();
@@ -610,6 +711,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
             for (int k = 0; k < 4; ++k)
               top[k] = fmaxf(fmaxf(top[k], __uint_as_float(v[i + 2 * k])), __uint_as_float(v[i + 2 * k + 1]));
         }
+        if constexpr (S::kOwnP) {
+          tc::fence_before();
+          __syncwarp();
+          arrive_issuer<CTAS>(s_free(x & 1), lane == 0);
+          // the product before this one has read its P (and O may be rescaled)
+          if (j > 0) {
+            wait_phase(o_done(u), (uint32_t)(j - 1) & 1u, ok);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc::fence_after();
+          }
+        }
         const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
         // (from -inf any score passes)
         const bool up = (now - m) * c > 8.f || (m == -INFINITY && now > m);
@@ -619,11 +732,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
           const float2 two = unpack_f32x2(sum);
           sum = pack_f32x2(two.x * f, two.y * f);
           if (j > 0) {
-            if (lane == 0) wait_phase(o_done(u), (uint32_t)(j - 1) & 1u, ok);
-            ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-      __syncwarp();
-            if (!ok) break;
-            tc::fence_after();
+            if (!S::kOwnP) {
+              wait_phase(o_done(u), (uint32_t)(j - 1) & 1u, ok);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+              tc::fence_after();
+            }
 #pragma unroll 1
             for (int i = 0; i < D; i += 32) {
               uint32_t o[32];
@@ -652,28 +766,27 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
             packed[i / 2] = half2_of(a.x, a.y);
             packed[i / 2 + 1] = half2_of(b.x, b.y);
           }
-          tmem_st_16(s_at + 16 * h, packed);
+          tmem_st_16(p_at + 16 * h, packed);
         }
         sum = fma2(other, one2, sum);
         if (!whole) {
-          // (before P is handed over: V's slot and marks are not used again until then)
-          const int fill = 2 * j + 1;
-          if (lane == 0) wait_phase(slot_full(fill % kSlots), (uint32_t)(fill / kSlots) & 1u, ok);
-          ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-      __syncwarp();
-          if (!ok) break;
+          // (before P is handed over: the marks' place is not used again until then)
           const int marks = j % kNanTiles;
-          if (nan_any[marks] != 0)
+          wait_phase(marks_full(marks), (uint32_t)(j / kNanTiles) & 1u, ok);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          __syncwarp();
+          if ((nan_any[marks * 4] | nan_any[marks * 4 + 1] | nan_any[marks * 4 + 2] | nan_any[marks * 4 + 3]) != 0)
             for (int i = 0; i < BN; ++i)
               if (t0 + i >= lo && t0 + i < hi) nan_blocks |= nan_marks[marks * BN + i];
         }
         tmem_st_wait();
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(p_ready(x & 1));
+        arrive_issuer<CTAS>(p_ready(x & 1), lane == 0);
       }
-      if (lane == 0) wait_phase(o_done(u), (uint32_t)(tiles - 1) & 1u, ok);
-      ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+      wait_phase(o_done(u), (uint32_t)(tiles - 1) & 1u, ok);
+      ok = __all_sync(0xffffffffu, ok);
       __syncwarp();
       tc::fence_after();
       const float2 two = unpack_f32x2(sum);
@@ -685,7 +798,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
       const bool part = p.splits > 1;
       if (part) {
         f = 1.f;
-        if (ok) reinterpret_cast<float2*>(piece + S::kRows * D)[u * 128 + r] = make_float2(m == -INFINITY ? m : m * c, l);
+        if (ok) reinterpret_cast<float2*>(piece + S::kRows * D)[in_tile] = make_float2(m == -INFINITY ? m : m * c, l);
       } else if (ok && real && p.lse != nullptr) {
         p.lse[out_row] = work.beyond ? f : l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.69314718055994531f;
       }
@@ -700,7 +813,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
           o[k] = __float_as_uint(__uint_as_float(o[k]) * g);
         }
         if (part) {
-          uint4* const to = reinterpret_cast<uint4*>(piece + (int64_t)(u * 128 + r) * D + i);
+          uint4* const to = reinterpret_cast<uint4*>(piece + (int64_t)in_tile * D + i);
 #pragma unroll
           for (int k = 0; k < 8; ++k) to[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
         } else if (real) {
@@ -717,16 +830,20 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
   }
   tc::fence_before();
   __syncthreads();
+  if constexpr (CTAS == 2) tc::cluster_sync();  // neither CTA reads or signals the other's memory any more
   if (warp == 12) {
     tc::fence_after();
-    tc::dealloc(tmem, kPromptColumns);
+    if constexpr (CTAS == 1)
+      tc::dealloc(tmem, kPromptColumns);
+    else
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
 }
 
 // The parts of a row tile added up, in the order of the tokens: 256 threads, four results each.
-template <int D, int BN, int NQ>
+template <int D, int BN, int NQ, int CTAS>
 __global__ void __launch_bounds__(256) attention_prompt_sum_kernel(const AttentionParams p) {
-  using S = Prompt<D, BN, NQ>;
+  using S = Prompt<D, BN, NQ, CTAS>;
   pdl_launch_dependents();
   pdl_wait();
   const PieceHead at = reinterpret_cast<const PieceHead*>(p.pieces)[blockIdx.x];
@@ -771,52 +888,57 @@ int64_t most_row_tiles(int64_t T, int64_t B, int64_t group, int64_t few, int row
 
 // Parts that the tokens of a row tile are cut into: as many as bring the row tiles and heads to the
 // SMs, where these are fewer, but at most twice the SMs in all, and 4 tiles of tokens a part.
-int prompt_splits(int64_t items, int64_t most_tokens, int tile) {
-  if (items >= kAttentionCtas) return 1;
+int prompt_splits(int64_t items, int64_t most_tokens, int tile, int ctas) {
+  const int64_t places = kAttentionCtas / ctas;
+  if (items >= places) return 1;
   const int64_t long_enough = most_tokens / (4 * tile);
   int best = 1;
   double least = 1e30;
-  for (int64_t s = 1; s * items <= 2 * kAttentionCtas && (s == 1 || s <= long_enough); ++s) {
-    const double rounds = (double)((s * items + kAttentionCtas - 1) / kAttentionCtas) / (double)s + 0.01 * (double)s;
+  for (int64_t s = 1; s * items <= 2 * places && (s == 1 || s <= long_enough); ++s) {
+    const double rounds = (double)((s * items + places - 1) / places) / (double)s + 0.01 * (double)s;
     if (rounds < least) least = rounds, best = (int)s;
   }
   return best;
 }
 
-template <int D, int BN, int NQ>
+template <int D, int BN, int NQ, int CTAS>
 int64_t plan_with(AttentionParams& p) {
-  using S = Prompt<D, BN, NQ>;
+  using S = Prompt<D, BN, NQ, CTAS>;
   const int64_t items = most_row_tiles(p.T, p.B, p.group, p.few_columns, S::kRows) * p.Hkv;
-  p.splits = prompt_splits(items, p.capacity, BN);
+  p.splits = prompt_splits(items, p.capacity, BN, CTAS);
   return p.splits == 1 ? 0 : (items * (int64_t)sizeof(PieceHead) + 255) / 256 * 256 + items * p.splits * S::kPiece * 4;
 }
 
-template <int D, int BN, int NQ>
+template <int D, int BN, int NQ, int CTAS>
 cudaError_t launch_with(AttentionParams p, void* workspace, cudaStream_t stream) {
-  using S = Prompt<D, BN, NQ>;
-  const cudaError_t err = allow_smem<attention_prompt_kernel<D, BN, NQ>>(S::kSmem);
+  using S = Prompt<D, BN, NQ, CTAS>;
+  const cudaError_t err = allow_smem<attention_prompt_kernel<D, BN, NQ, CTAS>>(S::kSmem);
   if (err != cudaSuccess) return err;
-  plan_with<D, BN, NQ>(p);
+  plan_with<D, BN, NQ, CTAS>(p);
   const int64_t items = most_row_tiles(p.T, p.B, p.group, p.few_columns, S::kRows) * p.Hkv;
   p.pieces = static_cast<int4*>(workspace);
   p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + (items * (int64_t)sizeof(PieceHead) + 255) / 256 * 256);
-  const cudaError_t ran = launch_pdl(attention_prompt_kernel<D, BN, NQ>, dim3((unsigned)(items * p.splits)),
-                                     dim3(kPromptThreads), S::kSmem, stream, p);
+  const cudaError_t ran = launch_pdl(attention_prompt_kernel<D, BN, NQ, CTAS>, dim3((unsigned)(items * p.splits * CTAS)),
+                                     dim3(kPromptThreads), S::kSmem, stream, p, CTAS);
   if (ran != cudaSuccess || p.splits == 1) return ran;
-  return launch_pdl(attention_prompt_sum_kernel<D, BN, NQ>, dim3((unsigned)items, S::kRows * D / 1024), dim3(256), 0,
+  return launch_pdl(attention_prompt_sum_kernel<D, BN, NQ, CTAS>, dim3((unsigned)items, S::kRows * D / 1024), dim3(256), 0,
                     stream, p);
 }
 
 }  // namespace
 
+// On pairs where sequences may have more rows than one SM takes.
 cudaError_t launch_attention_prompt(const AttentionParams& p, int D, void* workspace, cudaStream_t stream) {
-  return D == 64    ? launch_with<64, 128, 2>(p, workspace, stream)
-         : D == 128 ? launch_with<128, 128, 2>(p, workspace, stream)
-                    : launch_with<256, 64, 1>(p, workspace, stream);
+  if (D == 64) return launch_with<64, 128, 2, 1>(p, workspace, stream);
+  if (D == 128) return launch_with<128, 128, 2, 1>(p, workspace, stream);
+  return p.most_columns > 128 ? launch_with<256, 128, 1, 2>(p, workspace, stream)
+                              : launch_with<256, 64, 1, 1>(p, workspace, stream);
 }
 
 int64_t attention_prompt_workspace(AttentionParams p, int D) {
-  return D == 64 ? plan_with<64, 128, 2>(p) : D == 128 ? plan_with<128, 128, 2>(p) : plan_with<256, 64, 1>(p);
+  if (D == 64) return plan_with<64, 128, 2, 1>(p);
+  if (D == 128) return plan_with<128, 128, 2, 1>(p);
+  return p.most_columns > 128 ? plan_with<256, 128, 1, 2>(p) : plan_with<256, 64, 1, 1>(p);
 }
 
 cudaError_t prompt_wait_timeouts(int reset, int* out) {
