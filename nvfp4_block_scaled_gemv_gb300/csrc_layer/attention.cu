@@ -96,6 +96,21 @@ __device__ __forceinline__ float exp2_fast(float x) {
 // into the instruction (the waits on the barriers keep them in their place).
 __device__ __forceinline__ uint32_t load_32(const uint8_t* p) { return *reinterpret_cast<const uint32_t*>(p); }
 __device__ __forceinline__ uint2 load_64(const uint8_t* p) { return *reinterpret_cast<const uint2*>(p); }
+// What one lane or some do to a barrier, by a predicate: a branch around it would split the warp.
+__device__ __forceinline__ void expect_if(uint32_t bar, uint32_t bytes, bool who) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(
+          bar),
+      "r"(bytes), "r"((uint32_t)who)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_load_if(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar, bool who) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@p cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n\t}" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar), "r"((uint32_t)who)
+      : "memory");
+}
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
   uint32_t d;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
@@ -363,9 +378,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
     const int64_t mine = __shfl_sync(0xffffffffu, source, (ltile - source_tile) * kGr + (lane & (kGr - 1)));
     const uint32_t valid = __ballot_sync(0xffffffffu, mine >= 0) & kAll;
     const uint32_t bad = __ballot_sync(0xffffffffu, mine == kBad) & kAll;
-    if (lane == 0) tc::mbar_expect_tx(bar, (uint32_t)__popc(valid) * S::kGranule);
+    expect_if(bar, (uint32_t)__popc(valid) * S::kGranule, lane == 0);
     __syncwarp();
-    if (valid >> lane & 1u) tc::bulk_load(dst + lane * S::kGranule, p.cache + mine * S::kGranule, S::kGranule, bar);
+    bulk_load_if(dst + lane * S::kGranule, p.cache + mine * S::kGranule, S::kGranule, bar, (valid >> lane & 1u) != 0);
     bad_bits = (bad_bits & ~(kAll << (kGr * load_stage))) | bad << (kGr * load_stage);
     load_stage = load_stage + 1 == kStages ? 0 : load_stage + 1;
     --to_load;
@@ -492,11 +507,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
     for (; tile < to; ++tile) {
       const uint32_t bar = bars + 8 * stage;
       const uint8_t* const base = smem + warp * kStages * S::kStage + stage * S::kStage;
+      // (the whole warp waits: one lane's wait under a branch would split it)
       if (!__all_sync(0xffffffffu, tc::mbar_try(bar, parity))) {
-        if (lane == 0) tc::mbar_wait<false>(bar, parity, ok, &g_attention_timeouts);
-        ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+        tc::mbar_wait<false>(bar, parity, ok, &g_attention_timeouts);
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        __syncwarp();
       }
       const int32_t t0 = (seq.first_tile + tile) * S::kTile;
       const uint32_t bad = bad_bits >> (kGr * stage) & kAll;
