@@ -17,8 +17,12 @@ constexpr int64_t kMaxStride = int64_t(1) << 40;
 constexpr int64_t kMaxBatch = int64_t(1) << 20;
 constexpr int64_t kMaxPage = int64_t(1) << 20;
 constexpr int64_t kMaxPairs = 512;
-// Sequences of more columns (query tokens x heads of a group) go to the kernel for prompts.
-constexpr int64_t kFewColumns = 64;
+// Sequences of more columns (query tokens x heads of a group) go to the kernel for prompts, which
+// takes 128 or 256 rows at once; up to here passes of 16 (heads of 64: 32) columns over the cache are
+// as fast or faster.  16 sequences of 8192 tokens, us, passes against prompts: heads of 128: 36
+// columns 124 and 112, 64 columns 160 and 113 (one sequence: 21 and 30, 24 and 30); heads of 64: 64
+// columns 84 and 93; heads of 256: 32 columns 94 and 161, 64 columns 176 and 164.
+int64_t few_columns_for(int64_t D) { return D == 64 ? 64 : 48; }
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -107,7 +111,7 @@ nvfp4_status_t validate_attention(int64_t T, int64_t B, int64_t Hq, int64_t Hkv,
     return NVFP4_ERR_INVALID_VALUE;
   *most_q = !ragged ? (B == 0 ? 0 : T / B) : max_q != 0 ? max_q : T;
   // tiles of the kernel for few query tokens, over sequences, heads and passes, are counted in 32 bits
-  const int64_t columns = *most_q * (Hq / Hkv) < kFewColumns ? *most_q * (Hq / Hkv) : kFewColumns;
+  const int64_t columns = *most_q * (Hq / Hkv) < few_columns_for(D) ? *most_q * (Hq / Hkv) : few_columns_for(D);
   const int64_t passes = (columns + 7) / 8;
   if (B * Hkv * (passes > 0 ? passes : 1) > kMaxDim / (max_pages * page_size / 32 + 1)) return NVFP4_ERR_UNSUPPORTED_SHAPE;
   return NVFP4_OK;
@@ -115,13 +119,13 @@ nvfp4_status_t validate_attention(int64_t T, int64_t B, int64_t Hq, int64_t Hkv,
 
 // Columns of a pass of the kernel for few query tokens.
 int few_pass(int64_t D, int64_t columns) {
-  return attention_columns((int)D, columns < kFewColumns ? columns : kFewColumns);
+  return attention_columns((int)D, columns < few_columns_for(D) ? columns : few_columns_for(D));
 }
 
 // The sizes that both kernels work from; with few_columns: sequences of more columns are the
 // prompt kernel's, or, if none are to be expected, left out.
-AttentionParams sizes_of(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t page_size, int64_t max_pages,
-                         int64_t columns) {
+AttentionParams sizes_of(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t page_size,
+                         int64_t max_pages, int64_t columns) {
   AttentionParams p = {};
   p.T = (int32_t)T;
   p.B = (int32_t)B;
@@ -132,14 +136,14 @@ AttentionParams sizes_of(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t 
   p.granules = (int32_t)(page_size / kGranuleTokens);
   p.capacity = max_pages * page_size;
   p.most_columns = (int32_t)columns;
-  p.few_columns = (int32_t)(columns < kFewColumns ? columns : kFewColumns);
+  p.few_columns = (int32_t)(columns < few_columns_for(D) ? columns : few_columns_for(D));
   return p;
 }
 
 // The kernels of a call use the workspace one after another.
 int64_t workspace_for(const AttentionParams& p, int64_t D, int64_t columns, bool ragged) {
-  const int64_t few = ragged || columns <= kFewColumns ? attention_workspace((int)D, few_pass(D, columns)) : 0;
-  const int64_t prompt = columns > kFewColumns ? attention_prompt_workspace(p, (int)D) : 0;
+  const int64_t few = ragged || columns <= few_columns_for(D) ? attention_workspace((int)D, few_pass(D, columns)) : 0;
+  const int64_t prompt = columns > few_columns_for(D) ? attention_prompt_workspace(p, (int)D) : 0;
   return few > prompt ? few : prompt;
 }
 
@@ -216,7 +220,7 @@ size_t nvfp4_attention_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t
   if (validate_attention(T, B, Hq, Hkv, D, 0, page_size, max_pages, ragged != 0, max_q, &most_q) != NVFP4_OK) return 0;
   if (T == 0) return 0;
   const int64_t columns = most_q * (Hq / Hkv);
-  const int64_t bytes = workspace_for(sizes_of(T, B, Hq, Hkv, page_size, max_pages, columns), D, columns, ragged != 0);
+  const int64_t bytes = workspace_for(sizes_of(T, B, Hq, Hkv, D, page_size, max_pages, columns), D, columns, ragged != 0);
   return (size_t)(bytes > 256 ? bytes : 256);
 }
 
@@ -237,7 +241,7 @@ nvfp4_status_t nvfp4_attention(const void* q, int dtype, int64_t T, int64_t Hq, 
     return NVFP4_ERR_INVALID_VALUE;
   if (T == 0 || B == 0) return NVFP4_OK;
   const int64_t columns = most_q * (Hq / Hkv);
-  AttentionParams p = sizes_of(T, B, Hq, Hkv, page_size, max_pages, columns);
+  AttentionParams p = sizes_of(T, B, Hq, Hkv, D, page_size, max_pages, columns);
   const size_t need = (size_t)workspace_for(p, D, columns, opt.q_starts != nullptr);
   if (q == nullptr || out == nullptr || lengths == nullptr || (max_pages > 0 && page_table == nullptr) ||
       (pages > 0 && cache == nullptr) || workspace == nullptr || workspace_bytes < need)
@@ -269,7 +273,7 @@ nvfp4_status_t nvfp4_attention(const void* q, int dtype, int64_t T, int64_t Hq, 
   int sms = 0;
   const cudaError_t err = device_sms(&sms);
   if (err != cudaSuccess) return result(err);
-  if (columns > kFewColumns) {
+  if (columns > few_columns_for(D)) {
     const cudaError_t ran = launch_attention_prompt(p, (int)D, workspace, (cudaStream_t)stream);
     if (ran != cudaSuccess || opt.q_starts == nullptr) return result(ran);
   }

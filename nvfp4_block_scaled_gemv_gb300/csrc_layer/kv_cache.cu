@@ -20,7 +20,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int64_t kMaxCtas = 1 << 20;
 
-// A lane's block: its token, head and element, and its place in the cache.
+// A lane's block of the first of PLANES planes: its token, head and element, and its place in the
+// cache.  The next planes' blocks are 64 elements and kPlaneBytes on.
 struct Place {
   int64_t token;
   int32_t head, element;
@@ -28,15 +29,16 @@ struct Place {
   int32_t row, block;
 };
 
+template <int PLANES>
 __device__ __forceinline__ Place place_of(const CacheParams& p, int64_t place) {
   const int lane = threadIdx.x & 31;
-  const int per_token = p.heads * p.planes;
-  const int64_t group = place / per_token;
+  const int runs = p.planes / PLANES, per_token = p.heads * runs;
+  const int64_t group = p.places < (int64_t(1) << 32) ? (int64_t)((uint32_t)place / (uint32_t)per_token) : place / per_token;
   const int rest = (int)(place - group * per_token);
   Place at;
   at.token = group * 8 + (lane >> 2);
-  at.head = rest / p.planes;
-  const int plane = rest - at.head * p.planes;
+  at.head = runs == 1 ? rest : rest / runs;
+  const int plane = (rest - at.head * runs) * PLANES;
   at.block = lane & 3;
   at.element = plane * 64 + at.block * 16;
   at.plane = nullptr;
@@ -55,56 +57,78 @@ __device__ __forceinline__ Place place_of(const CacheParams& p, int64_t place) {
   return at;
 }
 
-template <typename T, int ALIGN>
+template <typename T, int ALIGN, int PLANES>
 __global__ void __launch_bounds__(kThreads) kv_write_kernel(const CacheParams p) {
   pdl_launch_dependents();
   pdl_wait();
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
   for (int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + warp; i < p.places;
        i += (int64_t)gridDim.x * (kThreads / 32)) {
-    const Place at = place_of(p, i);
+    const Place at = place_of<PLANES>(p, i);
     if (at.plane == nullptr) continue;
-    RawBlock<T> raw[2];
-    load_raw<T, ALIGN>(static_cast<const T*>(p.k) + at.token * p.k_token + at.head * p.k_head + at.element, raw[0]);
-    load_raw<T, ALIGN>(static_cast<const T*>(p.v) + at.token * p.v_token + at.head * p.v_head + at.element, raw[1]);
+    const T* const x[2] = {static_cast<const T*>(p.k) + at.token * p.k_token + at.head * p.k_head + at.element,
+                           static_cast<const T*>(p.v) + at.token * p.v_token + at.head * p.v_head + at.element};
+    RawBlock<T> raw[2][PLANES];
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int c = 0; c < PLANES; ++c) load_raw<T, ALIGN>(x[s] + 64 * c, raw[s][c]);
     const float encode[2] = {p.encode_k ? __ldg(p.encode_k + at.head) : 1.f,
                              p.encode_v ? __ldg(p.encode_v + at.head) : 1.f};
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      uint2 q;
-      const uint32_t code = quantize_block<T>(raw[s], encode[s], q);
-      uint8_t* const plane = at.plane + s * p.planes * kPlaneBytes;
-      *reinterpret_cast<uint2*>(plane + at.row * 32 + at.block * 8) = q;
-      plane[kPlaneScales + at.row * 4 + at.block] = (uint8_t)code;
+      uint8_t* const to = at.plane + s * p.planes * kPlaneBytes + at.row * 32 + at.block * 8;
+      uint8_t* const scale_to = at.plane + s * p.planes * kPlaneBytes + kPlaneScales + at.row * 4 + at.block;
+#pragma unroll
+      for (int c = 0; c < PLANES; ++c) {
+        uint2 q;
+        const uint32_t code = quantize_block<T>(raw[s][c], encode[s], q);
+        *reinterpret_cast<uint2*>(to + c * kPlaneBytes) = q;
+        scale_to[c * kPlaneBytes] = (uint8_t)code;
+      }
     }
   }
 }
 
-template <typename T, int ALIGN>
+template <typename T, int ALIGN, int PLANES>
 __global__ void __launch_bounds__(kThreads) kv_read_kernel(const CacheParams p) {
   pdl_launch_dependents();
   pdl_wait();
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
   for (int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + warp; i < p.places;
        i += (int64_t)gridDim.x * (kThreads / 32)) {
-    const Place at = place_of(p, i);
+    const Place at = place_of<PLANES>(p, i);
     if (at.token >= p.T) continue;
-    uint2 q[2] = {make_uint2(0u, 0u), make_uint2(0u, 0u)};
-    uint32_t code[2] = {0u, 0u};  // (no slot: zeros)
+    uint2 q[2][PLANES];
+    uint32_t code[2][PLANES];
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int c = 0; c < PLANES; ++c) q[s][c] = make_uint2(0u, 0u), code[s][c] = 0u;  // (no slot: zeros)
     if (at.plane != nullptr) {
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        const uint8_t* const plane = at.plane + s * p.planes * kPlaneBytes;
-        q[s] = *reinterpret_cast<const uint2*>(plane + at.row * 32 + at.block * 8);
-        code[s] = plane[kPlaneScales + at.row * 4 + at.block];
+        const uint8_t* const from = at.plane + s * p.planes * kPlaneBytes + at.row * 32 + at.block * 8;
+        const uint8_t* const scale_at = at.plane + s * p.planes * kPlaneBytes + kPlaneScales + at.row * 4 + at.block;
+#pragma unroll
+        for (int c = 0; c < PLANES; ++c) {
+          q[s][c] = *reinterpret_cast<const uint2*>(from + c * kPlaneBytes);
+          code[s][c] = scale_at[c * kPlaneBytes];
+        }
       }
     }
-    if (p.k != nullptr)
-      dequantize_block<T, ALIGN>(q[0], code[0], p.encode_k ? 1.f / __ldg(p.encode_k + at.head) : 1.f,
-                                 static_cast<T*>(p.k) + at.token * p.k_token + at.head * p.k_head + at.element);
-    if (p.v != nullptr)
-      dequantize_block<T, ALIGN>(q[1], code[1], p.encode_v ? 1.f / __ldg(p.encode_v + at.head) : 1.f,
-                                 static_cast<T*>(p.v) + at.token * p.v_token + at.head * p.v_head + at.element);
+    if (p.k != nullptr) {
+      const float decode = p.encode_k ? __frcp_rn(__ldg(p.encode_k + at.head)) : 1.f;
+      T* const to = static_cast<T*>(p.k) + at.token * p.k_token + at.head * p.k_head + at.element;
+#pragma unroll
+      for (int c = 0; c < PLANES; ++c) dequantize_block<T, ALIGN>(q[0][c], code[0][c], decode, to + 64 * c);
+    }
+    if (p.v != nullptr) {
+      const float decode = p.encode_v ? __frcp_rn(__ldg(p.encode_v + at.head)) : 1.f;
+      T* const to = static_cast<T*>(p.v) + at.token * p.v_token + at.head * p.v_head + at.element;
+#pragma unroll
+      for (int c = 0; c < PLANES; ++c) dequantize_block<T, ALIGN>(q[1][c], code[1][c], decode, to + 64 * c);
+    }
   }
 }
 
@@ -115,17 +139,24 @@ int rows_alignment(const CacheParams& p, int64_t size) {
   return bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : 1;
 }
 
-template <typename T>
-void (*write_for(int align))(const CacheParams) {
-  return align == 32 ? kv_write_kernel<T, 32> : align == 16 ? kv_write_kernel<T, 16> : kv_write_kernel<T, 1>;
+// Two planes a lane share the work on its place, where heads have more than one and every row's
+// loads are the widest (and there are enough of them for every SM all the same).
+int planes_at_once(const CacheParams& p, int align) {
+  return p.planes > 1 && align == 32 && (int64_t)p.T * p.heads * p.planes >= 32768 ? 2 : 1;
 }
 template <typename T>
-void (*read_for(int align))(const CacheParams) {
-  return align == 32 ? kv_read_kernel<T, 32> : align == 16 ? kv_read_kernel<T, 16> : kv_read_kernel<T, 1>;
+void (*write_for(int align, int planes))(const CacheParams) {
+  if (planes == 2) return kv_write_kernel<T, 32, 2>;
+  return align == 32 ? kv_write_kernel<T, 32, 1> : align == 16 ? kv_write_kernel<T, 16, 1> : kv_write_kernel<T, 1, 1>;
+}
+template <typename T>
+void (*read_for(int align, int planes))(const CacheParams) {
+  if (planes == 2) return kv_read_kernel<T, 32, 2>;
+  return align == 32 ? kv_read_kernel<T, 32, 1> : align == 16 ? kv_read_kernel<T, 16, 1> : kv_read_kernel<T, 1, 1>;
 }
 
-cudaError_t launch(void (*kern)(const CacheParams), CacheParams& p, cudaStream_t stream) {
-  p.places = ((int64_t)p.T + 7) / 8 * p.heads * p.planes;
+cudaError_t launch(void (*kern)(const CacheParams), CacheParams& p, int planes, cudaStream_t stream) {
+  p.places = ((int64_t)p.T + 7) / 8 * p.heads * (p.planes / planes);
   const int64_t per_cta = kThreads / 32, need = (p.places + per_cta - 1) / per_cta;
   return launch_pdl(kern, dim3((unsigned)(need < kMaxCtas ? need : kMaxCtas)), dim3(kThreads), 0, stream, p);
 }
@@ -134,18 +165,20 @@ cudaError_t launch(void (*kern)(const CacheParams), CacheParams& p, cudaStream_t
 
 cudaError_t launch_kv_write(CacheParams p, int dtype, cudaStream_t stream) {
   const int align = rows_alignment(p, dtype == kF32 ? 4 : 2);
-  return launch(dtype == kF32    ? write_for<float>(align)
-                : dtype == kBF16 ? write_for<__nv_bfloat16>(align)
-                                 : write_for<__half>(align),
-                p, stream);
+  const int planes = planes_at_once(p, align);
+  return launch(dtype == kF32    ? write_for<float>(align, planes)
+                : dtype == kBF16 ? write_for<__nv_bfloat16>(align, planes)
+                                 : write_for<__half>(align, planes),
+                p, planes, stream);
 }
 
 cudaError_t launch_kv_read(CacheParams p, int dtype, cudaStream_t stream) {
   const int align = rows_alignment(p, dtype == kF32 ? 4 : 2);
-  return launch(dtype == kF32    ? read_for<float>(align)
-                : dtype == kBF16 ? read_for<__nv_bfloat16>(align)
-                                 : read_for<__half>(align),
-                p, stream);
+  const int planes = planes_at_once(p, align);
+  return launch(dtype == kF32    ? read_for<float>(align, planes)
+                : dtype == kBF16 ? read_for<__nv_bfloat16>(align, planes)
+                                 : read_for<__half>(align, planes),
+                p, planes, stream);
 }
 
 }  // namespace nvfp4
