@@ -65,10 +65,12 @@ struct AttentionParams {
   int32_t T, B, Hq, Hkv, group, uniform_n, max_pages, granules, window, causal;
   int32_t most_columns;       // of a sequence (query tokens x heads of a group), at most
   int32_t few_columns;        // sequences of more columns are the prompt kernel's
+  int32_t ragged;             // q_starts are given
   int32_t bf16;
   float scale_log2;           // scale * log2(e)
   // split of the work (set by the launcher)
   float* partial;             // pieces: [CTAs][2] and [CTAs][warps]
+  int32_t* row_tiles;         // prompts in ragged batches: [B + 1] row tiles before each sequence
   int32_t splits;             // prompts: parts of a row tile's tokens
   int4* pieces;               // [CTAs]: {sequence, item, last CTA, 0} of the item that goes on in the next
 };
@@ -81,7 +83,7 @@ cudaError_t launch_attention(AttentionParams p, int D, int columns, void* worksp
 // Sequences of more than p.few_columns columns (attention_prompt.cu).
 cudaError_t launch_attention_prompt(const AttentionParams& p, int D, void* workspace, cudaStream_t stream);
 // Bytes of its workspace, from p's sizes alone.
-int64_t attention_prompt_workspace(AttentionParams p, int D);
+int64_t attention_prompt_workspace(const AttentionParams& p, int D);
 cudaError_t prompt_wait_timeouts(int reset, int* out);
 cudaError_t attention_wait_timeouts(int reset, int* out);
 

@@ -125,8 +125,9 @@ int few_pass(int64_t D, int64_t columns) {
 // The sizes that both kernels work from; with few_columns: sequences of more columns are the
 // prompt kernel's, or, if none are to be expected, left out.
 AttentionParams sizes_of(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t page_size,
-                         int64_t max_pages, int64_t columns) {
+                         int64_t max_pages, int64_t columns, bool ragged) {
   AttentionParams p = {};
+  p.ragged = ragged;
   p.T = (int32_t)T;
   p.B = (int32_t)B;
   p.Hq = (int32_t)Hq;
@@ -141,8 +142,8 @@ AttentionParams sizes_of(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t 
 }
 
 // The kernels of a call use the workspace one after another.
-int64_t workspace_for(const AttentionParams& p, int64_t D, int64_t columns, bool ragged) {
-  const int64_t few = ragged || columns <= few_columns_for(D) ? attention_workspace((int)D, few_pass(D, columns)) : 0;
+int64_t workspace_for(const AttentionParams& p, int64_t D, int64_t columns) {
+  const int64_t few = p.ragged || columns <= few_columns_for(D) ? attention_workspace((int)D, few_pass(D, columns)) : 0;
   const int64_t prompt = columns > few_columns_for(D) ? attention_prompt_workspace(p, (int)D) : 0;
   return few > prompt ? few : prompt;
 }
@@ -220,7 +221,7 @@ size_t nvfp4_attention_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t
   if (validate_attention(T, B, Hq, Hkv, D, 0, page_size, max_pages, ragged != 0, max_q, &most_q) != NVFP4_OK) return 0;
   if (T == 0) return 0;
   const int64_t columns = most_q * (Hq / Hkv);
-  const int64_t bytes = workspace_for(sizes_of(T, B, Hq, Hkv, D, page_size, max_pages, columns), D, columns, ragged != 0);
+  const int64_t bytes = workspace_for(sizes_of(T, B, Hq, Hkv, D, page_size, max_pages, columns, ragged != 0), D, columns);
   return (size_t)(bytes > 256 ? bytes : 256);
 }
 
@@ -241,8 +242,8 @@ nvfp4_status_t nvfp4_attention(const void* q, int dtype, int64_t T, int64_t Hq, 
     return NVFP4_ERR_INVALID_VALUE;
   if (T == 0 || B == 0) return NVFP4_OK;
   const int64_t columns = most_q * (Hq / Hkv);
-  AttentionParams p = sizes_of(T, B, Hq, Hkv, D, page_size, max_pages, columns);
-  const size_t need = (size_t)workspace_for(p, D, columns, opt.q_starts != nullptr);
+  AttentionParams p = sizes_of(T, B, Hq, Hkv, D, page_size, max_pages, columns, opt.q_starts != nullptr);
+  const size_t need = (size_t)workspace_for(p, D, columns);
   if (q == nullptr || out == nullptr || lengths == nullptr || (max_pages > 0 && page_table == nullptr) ||
       (pages > 0 && cache == nullptr) || workspace == nullptr || workspace_bytes < need)
     return NVFP4_ERR_INVALID_VALUE;

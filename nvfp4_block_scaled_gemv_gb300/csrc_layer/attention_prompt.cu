@@ -267,18 +267,53 @@ __device__ __forceinline__ bool tile_whole(const Work& w, int32_t t0) {
 
 // Query tokens of a sequence and its first row of q, and the tiles of rows it has here (none,
 // if the other kernel takes it).
+struct RowTiles {
+  int32_t q0, n, tiles;
+};
 template <int ROWS>
-__device__ __forceinline__ int32_t row_tiles(const AttentionParams& p, int b, int32_t& q0, int32_t& n) {
+__device__ __forceinline__ RowTiles row_tiles(const AttentionParams& p, int b) {
+  RowTiles r;
   if (p.q_starts != nullptr) {
     const int32_t from = max(__ldg(p.q_starts + b), 0), to = min(__ldg(p.q_starts + b + 1), p.T);
-    q0 = from;
-    n = max(to - from, 0);
+    r.q0 = from;
+    r.n = max(to - from, 0);
   } else {
-    q0 = b * p.uniform_n;
-    n = p.uniform_n;
+    r.q0 = b * p.uniform_n;
+    r.n = p.uniform_n;
   }
-  const int64_t rows = (int64_t)n * p.group;
-  return rows > p.few_columns ? (int32_t)((rows + ROWS - 1) / ROWS) : 0;
+  const int32_t rows = r.n * p.group;
+  r.tiles = rows > p.few_columns ? (rows - 1) / ROWS + 1 : 0;
+  return r;
+}
+
+// Ragged batches: row tiles before each sequence, and of all behind them, in one CTA.  (The CTAs
+// that find no row tile are told so by one number; each of them counting for itself took 3 us.)
+constexpr int kPlanThreads = 1024;
+template <int ROWS>
+__global__ void __launch_bounds__(kPlanThreads) attention_prompt_plan_kernel(const AttentionParams p) {
+  __shared__ int32_t warp_sums[kPlanThreads / 32];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int share = (p.B + kPlanThreads - 1) / kPlanThreads;
+  const int first = min((int)threadIdx.x * share, p.B), end = min(first + share, p.B);
+  int32_t mine = 0;
+  for (int b = first; b < end; ++b) mine += row_tiles<ROWS>(p, b).tiles;
+  int32_t upto = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int32_t o = __shfl_up_sync(0xffffffffu, upto, d);
+    if (lane >= d) upto += o;
+  }
+  if (lane == 31) warp_sums[warp] = upto;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) upto += warp_sums[w];
+  if (threadIdx.x == kPlanThreads - 1) p.row_tiles[p.B] = upto;
+  upto -= mine;
+  for (int b = first; b < end; ++b) {
+    p.row_tiles[b] = upto;
+    upto += row_tiles<ROWS>(p, b).tiles;
+  }
 }
 
 template <int D, int BN, int NQ, int CTAS>
@@ -289,7 +324,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
   __shared__ __align__(8) uint64_t bars[2 * kRaws + 2 * kSlots + 10 + kNanTiles];
   __shared__ uint32_t tmem_slot;
   __shared__ uint32_t raw_bad[kRaws];      // granules of a raw tile whose page does not exist
-  __shared__ uint32_t warp_sums[16];
   __shared__ Work shared_work;
 
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -313,6 +347,20 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
 
   const int lane = threadIdx.x & 31;
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
+  pdl_wait();
+
+  // The CTA's work: row tiles are numbered over the sequences, the last (which sees most) of a
+  // sequence first, the key heads of a row tile follow each other, and the parts of its tokens.
+  const int32_t unit = (int32_t)blockIdx.x / CTAS;
+  const int cta = CTAS == 1 ? 0 : (int)tc::cluster_rank();
+  const int32_t item = unit / p.splits, split = unit % p.splits;
+  const int32_t rank = item / p.Hkv, head = item % p.Hkv;
+  if (p.row_tiles != nullptr && rank >= __ldg(p.row_tiles + p.B)) {
+    // (ragged batches: more CTAs than row tiles)
+    if (p.splits > 1 && split == 0 && cta == 0 && threadIdx.x == 0)
+      reinterpret_cast<PieceHead*>(p.pieces)[item] = {0, 0, 0, 0};
+    return;
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < kRaws; ++i) {
       tc::mbar_init(raw_full(i), 1);
@@ -333,62 +381,46 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
     for (int i = 0; i < kNanTiles; ++i) tc::mbar_init(marks_full(i), 4);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  pdl_wait();
-
-  // The CTA's work: row tiles are numbered over the sequences, the last (which sees most) of a
-  // sequence first, the key heads of a row tile follow each other, and the parts of its tokens.
-  const int32_t unit = (int32_t)blockIdx.x / CTAS;
-  const int cta = CTAS == 1 ? 0 : (int)tc::cluster_rank();
-  const int32_t item = unit / p.splits, split = unit % p.splits;
-  const int32_t rank = item / p.Hkv, head = item % p.Hkv;
-  {
-    const int share = (p.B + kPromptThreads - 1) / kPromptThreads;
-    const int b0 = threadIdx.x * share;
-    uint32_t mine = 0;
-    for (int b = b0; b < min(b0 + share, p.B); ++b) {
-      int32_t q0, n;
-      mine += (uint32_t)row_tiles<S::kRows>(p, b, q0, n);
-    }
-    uint32_t upto = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const uint32_t o = __shfl_up_sync(0xffffffffu, upto, d);
-      if (lane >= d) upto += o;
-    }
-    if (lane == 31) warp_sums[warp] = upto;
-    if (threadIdx.x == 0) shared_work = Work{};  // (no row tile: no tiles, rows or first row)
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) upto += warp_sums[w];
-    uint32_t before = upto - mine;
-    if ((uint32_t)rank >= before && (uint32_t)rank < upto) {
-      for (int b = b0;; ++b) {
-        Work w;
-        const int32_t tiles = row_tiles<S::kRows>(p, b, w.q0, w.n);
-        if ((uint32_t)rank >= before + (uint32_t)tiles) {
-          before += (uint32_t)tiles;
-          continue;
-        }
-        w.b = b;
-        w.head = head;
-        w.rows = w.n * p.group;
-        w.first_row = (tiles - 1 - (rank - (int32_t)before)) * S::kRows;
-        const int32_t length = __ldg(p.lengths + b);
-        w.beyond = (int64_t)length > p.capacity;
-        w.length = w.beyond ? (int32_t)p.capacity : max(length, 0);
-        const int32_t last_row = min(w.first_row + S::kRows, w.rows) - 1;
-        int32_t l0, h0, l1, h1;
-        row_sees(p, w.length, w.n, w.first_row, l0, h0);
-        row_sees(p, w.length, w.n, last_row, l1, h1);
-        w.full_from = l1;
-        w.full_to = h0;
-        w.first_token = min(l0, max(h1, 0)) / BN * BN;
-        w.tiles = max((h1 - w.first_token + BN - 1) / BN, 1);
-        const int32_t from = (int32_t)((int64_t)w.tiles * split / p.splits);
-        w.tiles = (int32_t)((int64_t)w.tiles * (split + 1) / p.splits) - from;
-        w.first_token += from * BN;
-        shared_work = w;
-        break;
+  if (warp == 0) {
+    // the last sequence whose row tiles start at or before this one: 32 of them looked at at once
+    int b = 0, before = 0;
+    if (p.row_tiles == nullptr) {
+      const int each = row_tiles<S::kRows>(p, 0).tiles;  // (all alike)
+      b = rank / each;
+      before = b * each;
+    } else {
+      for (int end = p.B; end - b > 1;) {
+        const int step = (end - b + 31) / 32, at = b + lane * step;
+        const bool here = at < end && __ldg(p.row_tiles + at) <= rank;
+        b += (__popc(__ballot_sync(0xffffffffu, here)) - 1) * step;
+        end = min(end, b + step);
       }
+      before = __ldg(p.row_tiles + b);
+    }
+    if (lane == 0) {
+      const RowTiles its = row_tiles<S::kRows>(p, b);
+      Work w = {};
+      w.q0 = its.q0;
+      w.n = its.n;
+      w.b = b;
+      w.head = head;
+      w.rows = w.n * p.group;
+      w.first_row = (its.tiles - 1 - (rank - before)) * S::kRows;
+      const int32_t length = __ldg(p.lengths + b);
+      w.beyond = (int64_t)length > p.capacity;
+      w.length = w.beyond ? (int32_t)p.capacity : max(length, 0);
+      const int32_t last_row = min(w.first_row + S::kRows, w.rows) - 1;
+      int32_t l0, h0, l1, h1;
+      row_sees(p, w.length, w.n, w.first_row, l0, h0);
+      row_sees(p, w.length, w.n, last_row, l1, h1);
+      w.full_from = l1;
+      w.full_to = h0;
+      w.first_token = min(l0, max(h1, 0)) / BN * BN;
+      w.tiles = max((h1 - w.first_token + BN - 1) / BN, 1);
+      const int32_t from = (int32_t)((int64_t)w.tiles * split / p.splits);
+      w.tiles = (int32_t)((int64_t)w.tiles * (split + 1) / p.splits) - from;
+      w.first_token += from * BN;
+      shared_work = w;
     }
   }
   __syncthreads();
@@ -397,11 +429,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
     if (split == 0 && cta == 0 && threadIdx.x == 0)
       reinterpret_cast<PieceHead*>(p.pieces)[item] = {shared_work.q0, shared_work.rows, shared_work.first_row,
                                                       shared_work.beyond};
-    if (shared_work.tiles == 0 && shared_work.rows > 0)  // (fewer tiles than parts)
+    if (shared_work.tiles == 0)  // (fewer tiles than parts)
       for (int i = threadIdx.x; i < S::kRows; i += kPromptThreads)
         reinterpret_cast<float2*>(piece + S::kRows * D)[i] = make_float2(-INFINITY, 0.f);
   }
-  if (shared_work.tiles == 0) return;  // (more CTAs than row tiles)
+  if (shared_work.tiles == 0) return;
   if constexpr (CTAS == 2) tc::cluster_sync();  // the peer's barriers are initialised, and it is there to allocate
   if (warp == 12) {
     if constexpr (CTAS == 1) {
@@ -879,12 +911,15 @@ __global__ void __launch_bounds__(256) attention_prompt_sum_kernel(const Attenti
       make_uint2(rounded_two(p.bf16, o.x * f, o.y * f), rounded_two(p.bf16, o.z * f, o.w * f));
 }
 
-// Row tiles of all sequences, at most: every sequence that has some begins one more than its
-// rows fill.
-int64_t most_row_tiles(int64_t T, int64_t B, int64_t group, int64_t few, int rows_per_tile) {
-  const int64_t rows = T * group, sequences = rows / (few + 1);
-  return rows / rows_per_tile + (sequences < B ? sequences : B);
+// Row tiles of all sequences: in ragged batches at most (every sequence that has some begins one
+// more than its rows fill).
+int64_t most_row_tiles(const AttentionParams& p, int rows_per_tile) {
+  const int64_t rows = (int64_t)p.T * p.group, sequences = rows / (p.few_columns + 1);
+  if (!p.ragged) return (int64_t)p.B * ((rows / p.B + rows_per_tile - 1) / rows_per_tile);
+  return rows / rows_per_tile + (sequences < p.B ? sequences : p.B);
 }
+
+int64_t round_up(int64_t bytes) { return (bytes + 255) / 256 * 256; }
 
 // Parts that the tokens of a row tile are cut into: as many as bring the row tiles and heads to the
 // SMs, where these are fewer, but at most twice the SMs in all, and 4 tiles of tokens a part.
@@ -901,28 +936,44 @@ int prompt_splits(int64_t items, int64_t most_tokens, int tile, int ctas) {
   return best;
 }
 
+// The launch's sizes, and where in the workspace its parts lie: row tiles of sequences (ragged
+// batches), heads of pieces, pieces.
+struct PromptPlan {
+  int64_t items, heads_at, pieces_at, bytes;
+  int splits;
+};
 template <int D, int BN, int NQ, int CTAS>
-int64_t plan_with(AttentionParams& p) {
+PromptPlan plan_with(const AttentionParams& p) {
   using S = Prompt<D, BN, NQ, CTAS>;
-  const int64_t items = most_row_tiles(p.T, p.B, p.group, p.few_columns, S::kRows) * p.Hkv;
-  p.splits = prompt_splits(items, p.capacity, BN, CTAS);
-  return p.splits == 1 ? 0 : (items * (int64_t)sizeof(PieceHead) + 255) / 256 * 256 + items * p.splits * S::kPiece * 4;
+  PromptPlan plan;
+  plan.items = most_row_tiles(p, S::kRows) * p.Hkv;
+  plan.splits = prompt_splits(plan.items, p.capacity, BN, CTAS);
+  plan.heads_at = p.ragged ? round_up(((int64_t)p.B + 1) * 4) : 0;
+  plan.pieces_at = plan.heads_at + (plan.splits > 1 ? round_up(plan.items * (int64_t)sizeof(PieceHead)) : 0);
+  plan.bytes = plan.pieces_at + (plan.splits > 1 ? plan.items * plan.splits * S::kPiece * 4 : 0);
+  return plan;
 }
 
 template <int D, int BN, int NQ, int CTAS>
 cudaError_t launch_with(AttentionParams p, void* workspace, cudaStream_t stream) {
   using S = Prompt<D, BN, NQ, CTAS>;
-  const cudaError_t err = allow_smem<attention_prompt_kernel<D, BN, NQ, CTAS>>(S::kSmem);
+  cudaError_t err = allow_smem<attention_prompt_kernel<D, BN, NQ, CTAS>>(S::kSmem);
   if (err != cudaSuccess) return err;
-  plan_with<D, BN, NQ, CTAS>(p);
-  const int64_t items = most_row_tiles(p.T, p.B, p.group, p.few_columns, S::kRows) * p.Hkv;
-  p.pieces = static_cast<int4*>(workspace);
-  p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + (items * (int64_t)sizeof(PieceHead) + 255) / 256 * 256);
-  const cudaError_t ran = launch_pdl(attention_prompt_kernel<D, BN, NQ, CTAS>, dim3((unsigned)(items * p.splits * CTAS)),
-                                     dim3(kPromptThreads), S::kSmem, stream, p, CTAS);
-  if (ran != cudaSuccess || p.splits == 1) return ran;
-  return launch_pdl(attention_prompt_sum_kernel<D, BN, NQ, CTAS>, dim3((unsigned)items, S::kRows * D / 1024), dim3(256), 0,
-                    stream, p);
+  const PromptPlan plan = plan_with<D, BN, NQ, CTAS>(p);
+  uint8_t* const base = static_cast<uint8_t*>(workspace);
+  p.splits = plan.splits;
+  p.row_tiles = p.ragged ? reinterpret_cast<int32_t*>(base) : nullptr;
+  p.pieces = reinterpret_cast<int4*>(base + plan.heads_at);
+  p.partial = reinterpret_cast<float*>(base + plan.pieces_at);
+  if (p.ragged) {
+    err = launch_pdl(attention_prompt_plan_kernel<S::kRows>, dim3(1), dim3(kPlanThreads), 0, stream, p);
+    if (err != cudaSuccess) return err;
+  }
+  err = launch_pdl(attention_prompt_kernel<D, BN, NQ, CTAS>, dim3((unsigned)(plan.items * plan.splits * CTAS)),
+                   dim3(kPromptThreads), S::kSmem, stream, p, CTAS);
+  if (err != cudaSuccess || plan.splits == 1) return err;
+  return launch_pdl(attention_prompt_sum_kernel<D, BN, NQ, CTAS>, dim3((unsigned)plan.items, S::kRows * D / 1024), dim3(256),
+                    0, stream, p);
 }
 
 }  // namespace
@@ -935,10 +986,10 @@ cudaError_t launch_attention_prompt(const AttentionParams& p, int D, void* works
                               : launch_with<256, 64, 1, 1>(p, workspace, stream);
 }
 
-int64_t attention_prompt_workspace(AttentionParams p, int D) {
-  if (D == 64) return plan_with<64, 128, 2, 1>(p);
-  if (D == 128) return plan_with<128, 128, 2, 1>(p);
-  return p.most_columns > 128 ? plan_with<256, 128, 1, 2>(p) : plan_with<256, 64, 1, 1>(p);
+int64_t attention_prompt_workspace(const AttentionParams& p, int D) {
+  if (D == 64) return plan_with<64, 128, 2, 1>(p).bytes;
+  if (D == 128) return plan_with<128, 128, 2, 1>(p).bytes;
+  return p.most_columns > 128 ? plan_with<256, 128, 1, 2>(p).bytes : plan_with<256, 64, 1, 1>(p).bytes;
 }
 
 cudaError_t prompt_wait_timeouts(int reset, int* out) {
