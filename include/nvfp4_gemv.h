@@ -640,7 +640,7 @@ nvfp4_status_t nvfp4_moe_ffn(const void* x, int dtype, int64_t x_row_stride, con
  * Options (NULL = {0, 0, 1, 0, 0, 0, 0}): interleaved 0 or 1; inverse 1 turns the other way
  * (the gradient of the rotation, from y's to x's); factor scales the turned elements (what
  * long contexts multiply their scores by, as its root); strides in elements, 0 = dense.
- * Limits: 1 <= pairs <= 512, 2 * pairs <= D <= 65536, H <= 65536.
+ * Limits: 1 <= pairs <= 512, 2 * pairs <= D <= 65536, H <= 65536, H * D < 2^31.
  */
 typedef struct {
   int32_t interleaved;
@@ -660,8 +660,9 @@ nvfp4_status_t nvfp4_rope(const void* x, int dtype, int64_t T, int64_t H, int64_
  * 16 tokens holds K and then V, each as planes of 64 elements: 16 rows of 32 bytes of codes
  * (two a byte, low nibble first), then 16 rows of 4 scale bytes, quantised as nvfp4_quantize
  * does: blocks of 16 elements along the head.  Slot s is token s % page_size of page
- * s / page_size.  page_size is a multiple of 16, D 64, 128 or 256.  Attention reads the
- * scales as signed codes.
+ * s / page_size.  page_size is a multiple of 16, D 64, 128 or 256,
+ * heads at most 65535, pages * heads * page_size * D at most 2^48 (bytes: 0 for other sizes).
+ * Attention reads the scales as signed codes.
  */
 size_t nvfp4_kv_cache_bytes(int64_t pages, int64_t heads, int64_t D, int64_t page_size);
 
@@ -705,7 +706,8 @@ nvfp4_status_t nvfp4_kv_read(const nvfp4_kv_rows_t* rows, int dtype, int64_t T, 
  * which reads key head h / (Hq / Hkv):
  *   out = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale * q . k_t - max),  over the tokens t <= j,
  *   with a window also t > j - window, or, without causal, over all lengths[b] tokens.
- *   q, out     : [T][Hq][D] fp16 or bf16; out 16-byte aligned, q too (and its strides)
+ *   q, out     : [T][Hq][D] fp16 or bf16; out 16-byte aligned, q too (and its strides);
+ *                out (and lse, the workspace) must not overlap q or the other arguments
  *   page_table : int32 [B][max_pages], the pages of a sequence's length
  *   lengths    : int32 [B]
  * Options (NULL = {0, 1, 0, 0, NULL, NULL, NULL, NULL, 0, 0}):

@@ -357,7 +357,9 @@ def attention(q, cache, page_table, lengths, q_starts=None, max_q: int = 0, scal
         # rows that belong to no sequence are not written
         out = _empty((T, Hq, D), q.dtype, dev, stream)
     else:
-        _ptr(out, "out", q.dtype, T * Hq * D, dev)
+        a, b, size = q.data_ptr(), _ptr(out, "out", q.dtype, T * Hq * D, dev), 2
+        if T and a < b + T * Hq * D * size and b < a + ((T - 1) * token + (Hq - 1) * head + D) * size:
+            raise ValueError("out must not overlap q")
     lse = _empty((T, Hq), torch.float32, dev, stream) if return_lse else None
     sizes = (T, B, Hq, Hkv, D, page, max_pages, 0 if starts is None else 1, max_q)
     need = _workspaces.get(sizes)

@@ -16,6 +16,7 @@ constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxStride = int64_t(1) << 40;
 constexpr int64_t kMaxBatch = int64_t(1) << 20;
 constexpr int64_t kMaxPage = int64_t(1) << 20;
+constexpr int64_t kMaxCache = int64_t(1) << 48;  // elements of K, or of V
 constexpr int64_t kMaxPairs = 512;
 // Sequences of more columns (query tokens x heads of a group) go to the kernel for prompts, which
 // takes 128 or 256 rows at once; up to here passes of 16 (heads of 64: 32) columns over the cache are
@@ -58,7 +59,7 @@ bool cached_head(int64_t D) { return D == 64 || D == 128 || D == 256; }
 nvfp4_status_t validate_cache(int64_t pages, int64_t heads, int64_t D, int64_t page_size) {
   if (pages < 0 || heads < 1 || D < 1 || page_size < 1) return NVFP4_ERR_INVALID_VALUE;
   if (!cached_head(D) || page_size % kGranuleTokens != 0 || page_size > kMaxPage || pages > kMaxDim ||
-      heads > 65535)
+      heads > 65535 || (pages > 0 && page_size * heads * D > kMaxCache / pages))
     return NVFP4_ERR_UNSUPPORTED_SHAPE;
   return NVFP4_OK;
 }
@@ -162,7 +163,7 @@ nvfp4_status_t nvfp4_rope(const void* x, int dtype, int64_t T, int64_t H, int64_
       !valid_stride(opt.x_head_stride) || !valid_stride(opt.y_token_stride) || !valid_stride(opt.y_head_stride))
     return NVFP4_ERR_INVALID_VALUE;
   if (2 * pairs > D) return NVFP4_ERR_INVALID_VALUE;
-  if (pairs < 1 || pairs > kMaxPairs || T > kMaxDim || D > 65536 || H > 65536) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  if (pairs < 1 || pairs > kMaxPairs || T > kMaxDim || D > 65536 || H > 65536 || H * D > kMaxDim) return NVFP4_ERR_UNSUPPORTED_SHAPE;
   if (T == 0 || H == 0) return NVFP4_OK;
   if (x == nullptr || y == nullptr || positions == nullptr || table == nullptr) return NVFP4_ERR_INVALID_VALUE;
   if (!aligned(x, dtype_size(dtype)) || !aligned(y, dtype_size(dtype)) || !aligned(positions, 4) || !aligned(table, 8))

@@ -7,19 +7,38 @@
 // tokens they see in tiles of BN.  The products are tcgen05.mma kind::f16, M = 128:
 //
 //   S = Q K^T   Q and K in shared memory; S in tensor memory, two buffers
-//   O += P V    P over S's columns in tensor memory, V in shared memory as it is laid out (its
-//               rows are the contraction); O in tensor memory
+//   O += P V    P in tensor memory, over S's columns or beside them; V in shared memory as it is
+//               laid out (its rows are the contraction); O in tensor memory
 //
 // Four warps turn raw granules into K and V tiles in fp16 (code * scale is exact) in the
 // 128-byte swizzled layout that the MMAs read, so that nothing but the 4-bit cache is read from
 // memory and nothing dequantised is written there.  Eight warps, a thread per row, do the
 // softmax: while one half's rows are worked on, the MMAs of the other half run.  A running
-// maximum is raised only where a score passes it by 8 (in base 2): p then stays
-// below 2^8, and the rows of O are seldom rescaled.  p is rounded to fp16 (2^-11 of itself),
-// sums are fp32 before that rounding.
+// reference is raised only where a score passes it by 8 (in base 2): p then stays
+// below 2^8, and the rows of O are seldom rescaled.  p is rounded to fp16 (2^-11 of itself, below
+// 2^-14 of the reference 2^-25 of that), sums are fp32 before that rounding.
 //
 // Warps: 0-3 and 4-7 softmax of rows 0-127 and 128-255 (NQ = 1: only the first four), 8-11 raw
-// tiles to fp16, 12 issues MMAs, 13 copies granules.
+// tiles to fp16, 12 issues MMAs, 13 copies granules.  Registers are split by what they need: a
+// thread of the softmax holds its row's scores of a tile.
+//
+//   heads of 64    two halves, tiles of 128, P beside S: the next scores need not wait for P's product
+//   heads of 128   two halves, tiles of 128, P over S (there is no room beside)
+//   heads of 256   rows in plenty: pairs of SMs (CTAS = 2), 128 rows of each, tiles of 128, of which a CTA
+//                  brings half the tokens of K and half the elements of V; otherwise one SM, tiles of 64
+//
+// Heads of 128 on pairs were no faster (1237 against 1202 us, 4 prompts of 512 to 4096 tokens after
+// prefixes up to 12k, 32 query heads), 64 tokens a tile with P beside S slower (the MMAs of Q K^T read
+// 4 KB of Q for 64 columns).
+//
+// What bounds it.  That case runs at 1.40 PFLOP/s, 73% of the measured bf16 rate, the tensor pipe busy
+// about two thirds of the time: a half's next scores wait for its softmax and P's product.  Heads of
+// 64 run at 0.82 (4 x 2048 queries on 8192 tokens, 583 us): the exponentials alone, 1024 cycles a
+// tile, are as long as its MMAs.  Heads of 256: 1.10 (2 x 2048 on 8192, 16 heads, 436 us).
+// What mattered most: a wait by one lane under a branch splits the warp for hundreds of cycles, so
+// whole warps wait, and single lanes arrive by predicates (1476 -> 1202 us); one SM's warps share
+// 12 KB of the nearest instruction cache with the softmax, so K and V fills are one code, unrolled
+// twice (unrolled four times for each of them: 1884 us).
 #include <cfloat>
 #include <cstdint>
 #include <type_traits>
@@ -185,16 +204,14 @@ __device__ __forceinline__ void tmem_st_16(uint32_t taddr, const uint32_t* v) {
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// tc::mbar_wait without its call: one lane waits, in line, so that the warps' registers are
-// split as setmaxnreg says (a call asks for those of its own).
-template <bool CLUSTER = false>
+// tc::mbar_wait for a whole warp, and in line: with a call in it ptxas could not give the warps
+// the registers that setmaxnreg asks for.
 __device__ __forceinline__ void wait_phase(uint32_t bar, uint32_t parity, bool& ok) {
-  auto done = [&]() { return CLUSTER ? tc::mbar_try_cluster(bar, parity) : tc::mbar_try(bar, parity); };
-  if (!ok || done()) return;
+  if (!ok || tc::mbar_try(bar, parity)) return;
   const uint64_t t0 = tc::global_ns();
-  for (uint32_t i = 1; !done(); ++i)
+  for (uint32_t i = 1; !tc::mbar_try(bar, parity); ++i)
     if ((i & 63u) == 0 && tc::global_ns() - t0 > tc::kWaitNs) {
-      atomicAdd(&g_prompt_timeouts, 1);
+      if ((threadIdx.x & 31) == 0) atomicAdd(&g_prompt_timeouts, 1);
       ok = false;
       return;
     }
@@ -502,14 +519,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
       __syncwarp();
     } else if (warp == 12 && cta == 0) {
       constexpr uint32_t qk = f16_idesc(128 * CTAS, BN, false), pv = f16_idesc(128 * CTAS, D, true);
-      constexpr bool kPair = false;
       const uint64_t q_desc = tc::desc_sw128(q_s);
-      wait_phase<kPair>(q_full, 0, ok);
+      wait_phase(q_full, 0, ok);
       auto scores = [&](int32_t x) {
         const int32_t j = NQ == 2 ? x >> 1 : x;
         const int u = NQ == 2 ? x & 1 : 0;
         const int fill = 2 * j, i = fill % kSlots;
-        wait_phase<kPair>(slot_full(i), (uint32_t)(fill / kSlots) & 1u, ok);
+        wait_phase(slot_full(i), (uint32_t)(fill / kSlots) & 1u, ok);
         ok = __all_sync(0xffffffffu, ok);
         tc::fence_after();
         if (!ok) return;
@@ -532,7 +548,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
       for (int32_t x = 0; x < steps && ok; ++x) {
         if (S::kOwnP && x + 2 < steps) {
           // S is in registers: the next scores need not wait for P and its product
-          wait_phase<kPair>(s_free(x & 1), (uint32_t)(x >> 1) & 1u, ok);
+          wait_phase(s_free(x & 1), (uint32_t)(x >> 1) & 1u, ok);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           scores(x + 2);
@@ -540,8 +556,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
         const int32_t j = NQ == 2 ? x >> 1 : x;
         const int u = NQ == 2 ? x & 1 : 0;
         const int fill = 2 * j + 1, i = fill % kSlots;
-        wait_phase<kPair>(slot_full(i), (uint32_t)(fill / kSlots) & 1u, ok);
-        wait_phase<kPair>(p_ready(x & 1), (uint32_t)(x >> 1) & 1u, ok);
+        wait_phase(slot_full(i), (uint32_t)(fill / kSlots) & 1u, ok);
+        wait_phase(p_ready(x & 1), (uint32_t)(x >> 1) & 1u, ok);
         ok = __all_sync(0xffffffffu, ok);
         tc::fence_after();
         if (!ok) break;
@@ -724,7 +740,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
         const int32_t t0 = work.first_token + j * BN;
         wait_phase(s_full(x & 1), (uint32_t)(x >> 1) & 1u, ok);
         ok = __all_sync(0xffffffffu, ok);
-      __syncwarp();
+        __syncwarp();
         if (!ok) break;
         tc::fence_after();
         const bool whole = tile_whole<BN>(work, t0);

@@ -10,7 +10,9 @@
 // is left, at most an eighth of a turn, is rounded to fp32 once: an error of 2^-25 of
 // that angle.
 //
-// One pass, bound by the bytes of x and y.  A CTA takes a few tokens: its threads first
+// One pass, bound by the bytes of x and y: 16384 tokens x 40 heads of 128 in bf16 take 54.6 us,
+// 6.15 TB/s, 91% of the measured copy; 333 x 27 3.5 us and one token 2.3 us, the time of a launch
+// and of a dependent load of position, table and row.  A CTA takes a few tokens: its threads first
 // work out the cosines and sines of (token, pair), once for all heads, and then rotate 8
 // pairs at a time, the two 16-byte halves of 16-bit pairs.
 #include <cstdint>

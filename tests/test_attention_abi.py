@@ -23,7 +23,7 @@ def lib():
 @pytest.mark.parametrize("want,kw,opt", [
     (V, dict(dt=3), {}), (V, dict(T=-1), {}), (V, dict(H=-1), {}), (V, dict(D=-2), {}), (V, dict(pairs=-1), {}),
     (U, dict(pairs=0), {}), (V, dict(pairs=33), {}), (U, dict(pairs=513, D=2000), {}), (U, dict(D=65537), {}),
-    (U, dict(H=65537), {}), (U, dict(T=1 << 31), {}), (V, {}, dict(interleaved=2)), (V, {}, dict(inverse=-1)),
+    (U, dict(H=65537), {}), (U, dict(H=65536, D=65536), {}), (U, dict(T=1 << 31), {}), (V, {}, dict(interleaved=2)), (V, {}, dict(inverse=-1)),
     (V, {}, dict(factor=math.inf)), (V, {}, dict(factor=math.nan)), (V, {}, dict(x_token_stride=-1)),
     (V, {}, dict(y_head_stride=(1 << 40) + 1)), (V, dict(x=None), {}), (V, dict(y=None), {}), (V, dict(pos=None), {}),
     (V, dict(table=None), {}), (A, dict(x=P + 1), {}), (A, dict(dt=2, y=P + 2), {}), (A, dict(pos=P + 2), {}),
@@ -42,7 +42,8 @@ def test_rope_refusals(lib, want, kw, opt):
     (V, dict(dt=3), {}), (V, dict(T=-1), {}), (V, dict(heads=0), {}), (V, dict(D=0), {}), (U, dict(D=96), {}),
     (U, dict(D=192), {}), (U, dict(D=512), {}), (V, dict(page=0), {}), (U, dict(page=24), {}), (U, dict(page=8), {}),
     (U, dict(page=(1 << 20) + 16), {}), (V, dict(pages=-1), {}), (U, dict(pages=1 << 31), {}),
-    (U, dict(heads=65536), {}), (U, dict(T=1 << 31), {}), (V, {}, dict(k_token_stride=-1)),
+    (U, dict(heads=65536), {}), (U, dict(pages=(1 << 31) - 1, heads=65535, page=1 << 20), {}),
+    (U, dict(T=1 << 31), {}), (V, {}, dict(k_token_stride=-1)),
     (V, {}, dict(v_head_stride=-8)), (V, dict(slots=None), {}), (V, dict(cache=None), {}), (V, {}, dict(k=None, v=None)),
     (A, {}, dict(k=P + 1)), (A, {}, dict(v=P + 1)), (A, dict(slots=P + 4), {}), (A, dict(cache=P + 8), {}),
     (A, {}, dict(encode_k=P + 2)), (A, {}, dict(encode_v=P + 1)), (0, dict(T=0, slots=None, cache=None), dict(k=None)),
@@ -66,6 +67,8 @@ def test_cache_bytes(lib):
     size = nv.nvfp4_kv_cache_bytes
     assert size(3, 2, 128, 32) == oa.empty_cache(3, 2, 128, 32).nbytes
     assert size(1 << 20, 8, 128, 64) == (1 << 20) * 8 * 64 * 144 > 1 << 36
+    assert size((1 << 31) - 1, 65535, 256, 1 << 20) == 0  # (more than 64 bits)
+    assert size((1 << 26), 256, 256, 64) == (1 << 26) * 256 * 64 * 288
     assert size(0, 2, 64, 16) == 0 and size(3, 2, 96, 16) == 0 and size(3, 2, 64, 20) == 0 and size(-1, 2, 64, 16) == 0
 
 
@@ -182,7 +185,7 @@ def test_torch_refusals_on_the_host():
     for bad in (lambda: nv.attention(q[:, :3], cache, t, n), lambda: nv.attention(q[:3], cache, t, n),
                 lambda: nv.attention(q, cache, t[0], n), lambda: nv.attention(q, cache, t, n[:1]),
                 lambda: nv.attention(q, cache, t, n, q_starts=n), lambda: nv.attention(q[..., :32], cache, t, n),
-                lambda: nv.attention(q, cache, t, n, out=q[:2]),
+                lambda: nv.attention(q, cache, t, n, out=q[:2]), lambda: nv.attention(q, cache, t, n, out=q),
                 lambda: nv.attention(q, cache, t, n, workspace=torch.zeros(16, dtype=torch.uint8)),
                 # (a CPU tensor gets as far as the launch)
                 lambda: nv.attention(q, cache, t, n)):

@@ -606,3 +606,111 @@ def test_attention_calls_on_streams_at_once():
         got = [nv.attention(q, **on, stream=s) for q, on, s in zip(qs, ons, streams)]
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_attention_of_a_long_sequence():
+    """131,072 tokens: single tokens, passes of them, and rows for the prompt kernel."""
+    rng = np.random.default_rng(30)
+    z = problem(rng, [131072], [66], 2, 1, 64, 128, "bf16")
+    for n in (66, 33, 1):
+        zz = z | {"q": z["q"][-n:], "starts": np.array([0, n], dtype=np.int32)}
+        out, lse = nv.attention(zz["q"].to(DEV), **on_gpu(zz), return_lse=True)
+        check(zz, out, lse, "bf16")
+
+
+def test_attention_of_many_ragged_sequences():
+    """More sequences than the kernels' CTAs have threads, most without a query, a few with prompts."""
+    rng = np.random.default_rng(31)
+    B = 2300
+    counts = (rng.random(B) < 0.3).astype(int)
+    counts[[0, 1, 700, 1024, 2298, 2299]] = [70, 0, 129, 200, 65, 66]
+    lens = (counts + rng.integers(0, 30, B)).tolist()
+    z = problem(rng, lens, counts.tolist(), 1, 1, 64, 16, "bf16")
+    out, lse = nv.attention(z["q"].to(DEV), **on_gpu(z), q_starts=gpu(z["starts"]), max_q=200, return_lse=True)
+    check(z, out, lse, "bf16")
+
+
+def test_attention_of_identical_pages():
+    """Sequences that share pages (a common prefix) read the same tokens."""
+    rng = np.random.default_rng(32)
+    z = problem(rng, [96, 100], [1, 1], 4, 2, 128, 32, "bf16")
+    z["table"][1, :3] = z["table"][0, :3]
+    q = z["q"][:1].repeat(2, 1, 1)
+    z = z | {"q": q, "lens": np.array([96, 96], dtype=np.int32)}
+    out, lse = nv.attention(q.to(DEV), **on_gpu(z), return_lse=True)
+    check(z, out, lse, "bf16")
+    assert torch.equal(out[0], out[1]) and torch.equal(lse[0], lse[1])
+
+
+LATE = 40_000_000  # clocks of a kernel that only waits, ~20 ms
+
+
+@pytest.mark.parametrize("name", ["rope", "kv_write", "kv_read", "attention", "prompts"])
+def test_calls_on_a_stream_given_by_name(name):
+    """What a call allocates for another stream is neither still in use by the current one, nor handed
+    out again while the call is to run."""
+    rng = np.random.default_rng(33)
+    n = 80 if name == "prompts" else 1
+    z = problem(rng, [900, 700], [n, n], 8, 2, 128, 64, "bf16")
+    on, q = on_gpu(z), z["q"].to(DEV)
+    x = torch.randn(3000, 2, 128, device=DEV).bfloat16()
+    slots = torch.arange(3000, device=DEV)
+    other = nv.kv_cache(47, 2, 128, 64, device=DEV)
+    pos, table = torch.arange(3000, dtype=torch.int32, device=DEV), nv.rope_table(128)
+    call = {"rope": lambda s: [nv.rope(x, pos, table, stream=s)],
+            "kv_write": lambda s: [nv.kv_write(x, x, other, slots, stream=s)],
+            "kv_read": lambda s: list(nv.kv_read(other, slots, stream=s)),
+            "attention": lambda s: list(nv.attention(q, **on, return_lse=True, stream=s)),
+            "prompts": lambda s: list(nv.attention(q, **on, return_lse=True, stream=s))}[name]
+    if name == "kv_read":
+        nv.kv_write(x, -x, other, slots)
+    want = [t.clone() for t in call(None)]
+    other_bytes = other.clone()
+    if name == "kv_write":
+        other.zero_()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(LATE)
+        got = call(side)  # runs late
+        # the current stream allocates and fills memory meanwhile
+        fills = [torch.full_like(t, 7) for t in got for _ in range(3)]
+        torch.cuda.current_stream().wait_stream(side)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert all((f == 7).all() for f in fills)
+        del got, fills
+        torch.cuda.synchronize()
+    if name == "kv_write":
+        assert torch.equal(other, other_bytes)
+
+
+def test_prompts_and_products_on_streams_at_once():
+    """Kernels that take tensor memory side by side: attention of prompts and the quantised product."""
+    rng = np.random.default_rng(34)
+    zs = [problem(rng, [600], [150], 8, 2, D, 64, "bf16") for D in (64, 128, 256)]
+    ons, qs = [on_gpu(z) for z in zs], [z["q"].to(DEV) for z in zs]
+    a = torch.randn(1, 2048, 1024, device=DEV)
+    w, sw = nv.quantize(a)
+    rows = [nv.quantize(torch.randn(1, n, 1024, device=DEV)) for n in (5, 300, 2000)]
+    calls = [lambda s, q=q, on=on: nv.attention(q, **on, stream=s) for q, on in zip(qs, ons)]
+    calls += [lambda s, r=r: nv.gemm(w, r[0], sw, r[1], dtype=torch.float32, stream=s) for r in rows]
+    want = [c(None) for c in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    for _ in range(15):
+        got = [c(s) for c, s in zip(calls, streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(g, w) for g, w in zip(got, want))
+
+
+@pytest.mark.parametrize("steps", [0, 3])
+def test_example_layer(steps):
+    import os
+    import sys
+
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import attention_layer
+
+    # bf16 outputs are off by at most 2^-8 of themselves, p by 2^-11
+    assert attention_layer.main(steps) < 2.0 ** -7
