@@ -318,8 +318,8 @@ const char* nvfp4_status_string(int status);
  * (0 if none). */
 int nvfp4_last_cuda_error(void);
 
-/* Waits of the tensor-core kernels (the GEMV's, the block-dot kernel's and the
- * layer products') that gave up: every wait of those kernels on
+/* Waits of the tensor-core kernels (the GEMV's, the block-dot kernel's, the
+ * layer products' and attention's) that gave up: every wait of those kernels on
  * a pipeline barrier is bounded (2 s), and a wait that runs out is counted
  * here and makes its thread skip the rest of its work (the launch's c is
  * then not valid).  Synchronises the device; reset != 0 clears the count
@@ -728,7 +728,7 @@ nvfp4_status_t nvfp4_kv_read(const nvfp4_kv_rows_t* rows, int dtype, int64_t T, 
  * workspace: nvfp4_attention_workspace_bytes bytes, 256-byte aligned; need not be kept, but no
  * two calls that may run at once can share it.
  * Accuracy: scores and sums in fp32, the p to fp16 before the product with v, out rounded once.
- * Limits: Hq % Hkv == 0, T * Hq < 2^31, max_pages * page_size < 2^31 - 64, B <= 2^20, and
+ * Limits: Hq % Hkv == 0, T * Hq < 2^31, max_pages * page_size <= 2^31 - 256, B <= 2^20, and
  * B * Hkv * max_pages * page_size < 2^36, less by the passes that more than 8 query tokens x heads of
  * a group take (up to 8).
  */

@@ -17,6 +17,7 @@ constexpr int64_t kMaxStride = int64_t(1) << 40;
 constexpr int64_t kMaxBatch = int64_t(1) << 20;
 constexpr int64_t kMaxPage = int64_t(1) << 20;
 constexpr int64_t kMaxCache = int64_t(1) << 48;  // elements of K, or of V
+constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 256;  // of a sequence: ends of tiles stay in 32 bits
 constexpr int64_t kMaxPairs = 512;
 // Sequences of more columns (query tokens x heads of a group) go to the kernel for prompts, which
 // takes 128 or 256 rows at once; up to here passes of 16 (heads of 64: 32) columns over the cache are
@@ -106,7 +107,7 @@ nvfp4_status_t validate_attention(int64_t T, int64_t B, int64_t Hq, int64_t Hkv,
   const nvfp4_status_t st = validate_cache(pages, Hkv, D, page_size);
   if (st != NVFP4_OK) return st;
   if (T < 0 || B < 0 || Hq < 1 || max_pages < 0 || max_q < 0 || max_q > T) return NVFP4_ERR_INVALID_VALUE;
-  if (Hq % Hkv != 0 || B > kMaxBatch || T > kMaxDim / Hq || max_pages > (kMaxDim - 64) / page_size)
+  if (Hq % Hkv != 0 || B > kMaxBatch || T > kMaxDim / Hq || max_pages > kMaxTokens / page_size)
     return NVFP4_ERR_UNSUPPORTED_SHAPE;
   if (!ragged && ((B == 0 && T != 0) || (B != 0 && (T % B != 0 || (max_q != 0 && max_q != T / B)))))
     return NVFP4_ERR_INVALID_VALUE;

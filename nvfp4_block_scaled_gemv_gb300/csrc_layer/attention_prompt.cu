@@ -306,29 +306,31 @@ __device__ __forceinline__ RowTiles row_tiles(const AttentionParams& p, int b) {
 // Ragged batches: row tiles before each sequence, and of all behind them, in one CTA.  (The CTAs
 // that find no row tile are told so by one number; each of them counting for itself took 3 us.)
 constexpr int kPlanThreads = 1024;
+// (Summed in 64 bits: starts that overlap, which nothing forbids the device to hold, then still give
+// numbers that only grow, and every row tile that a CTA finds is its sequence's own.)
 template <int ROWS>
 __global__ void __launch_bounds__(kPlanThreads) attention_prompt_plan_kernel(const AttentionParams p) {
-  __shared__ int32_t warp_sums[kPlanThreads / 32];
+  __shared__ int64_t warp_sums[kPlanThreads / 32];
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int share = (p.B + kPlanThreads - 1) / kPlanThreads;
   const int first = min((int)threadIdx.x * share, p.B), end = min(first + share, p.B);
-  int32_t mine = 0;
+  int64_t mine = 0;
   for (int b = first; b < end; ++b) mine += row_tiles<ROWS>(p, b).tiles;
-  int32_t upto = mine;
+  int64_t upto = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int32_t o = __shfl_up_sync(0xffffffffu, upto, d);
+    const int64_t o = __shfl_up_sync(0xffffffffu, upto, d);
     if (lane >= d) upto += o;
   }
   if (lane == 31) warp_sums[warp] = upto;
   __syncthreads();
   for (int w = 0; w < warp; ++w) upto += warp_sums[w];
-  if (threadIdx.x == kPlanThreads - 1) p.row_tiles[p.B] = upto;
+  if (threadIdx.x == kPlanThreads - 1) p.row_tiles[p.B] = (int32_t)min(upto, (int64_t)INT32_MAX);
   upto -= mine;
   for (int b = first; b < end; ++b) {
-    p.row_tiles[b] = upto;
+    p.row_tiles[b] = (int32_t)min(upto, (int64_t)INT32_MAX);
     upto += row_tiles<ROWS>(p, b).tiles;
   }
 }

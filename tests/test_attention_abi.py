@@ -75,7 +75,8 @@ def test_cache_bytes(lib):
 @pytest.mark.parametrize("want,kw,opt", [
     (V, dict(dt=2), {}), (V, dict(dt=-1), {}), (V, dict(T=-1), {}), (V, dict(Hq=0), {}), (V, dict(Hkv=0), {}),
     (U, dict(Hq=5), {}), (U, dict(D=80), {}), (U, dict(page=40), {}), (V, dict(pages=-1), {}), (V, dict(mp=-1), {}),
-    (U, dict(mp=1 << 27), {}), (U, dict(mp=1 << 26, B=64, T=64), {}), (U, dict(mp=1 << 23, B=32, T=32, Hq=128), {}), (V, dict(B=-1), {}), (V, dict(B=3), {}), (V, dict(B=0), {}),
+    (U, dict(mp=1 << 27), {}), (U, dict(mp=(1 << 27) - 15), {}), (V, dict(mp=(1 << 27) - 16, q=None), {}),
+    (U, dict(mp=1 << 26, B=64, T=64), {}), (U, dict(mp=1 << 23, B=32, T=32, Hq=128), {}), (V, dict(B=-1), {}), (V, dict(B=3), {}), (V, dict(B=0), {}),
     (U, dict(B=(1 << 20) + 1, T=(1 << 20) + 1), {}), (U, dict(T=1 << 30), {}), (V, {}, dict(max_q=3)),
     (V, {}, dict(max_q=-1)), (V, {}, dict(q_starts=P, max_q=5)), (V, {}, dict(scale=-1.0)),
     (V, {}, dict(scale=math.nan)), (V, {}, dict(scale=math.inf)), (V, {}, dict(causal=2)), (V, {}, dict(window=-1)),

@@ -630,6 +630,22 @@ def test_attention_of_many_ragged_sequences():
     check(z, out, lse, "bf16")
 
 
+def test_attention_with_starts_that_overlap():
+    """Starts that are no partition of q's rows: no result is promised for the rows that are named
+    twice or by a sequence that ends before it starts, every other row's is as it should be."""
+    rng = np.random.default_rng(35)
+    z = problem(rng, [300, 250, 200], [100, 90, 1], 4, 2, 64, 16, "bf16")
+    q = z["q"].to(DEV)
+    # the third sequence begins inside the first and ends at its own row; the fourth ends before it starts
+    table = torch.cat((gpu(z["table"]), gpu(z["table"])[:1]))
+    lens = torch.cat((gpu(z["lens"]), gpu(z["lens"])[:1]))
+    on = on_gpu(z)
+    want = nv.attention(q, **on, q_starts=gpu(z["starts"]), max_q=0)
+    starts = torch.tensor([0, 100, 190, 150, 191], dtype=torch.int32, device=DEV)
+    out = nv.attention(q, **(on | dict(page_table=table, lengths=lens)), q_starts=starts, max_q=0)
+    assert torch.equal(out[:150], want[:150])
+
+
 def test_attention_of_identical_pages():
     """Sequences that share pages (a common prefix) read the same tokens."""
     rng = np.random.default_rng(32)
