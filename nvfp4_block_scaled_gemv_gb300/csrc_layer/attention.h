@@ -72,6 +72,7 @@ struct AttentionParams {
   float* partial;             // pieces: [CTAs][2] and [CTAs][warps]
   int32_t* row_tiles;         // prompts in ragged batches: [B + 1] row tiles before each sequence
   int32_t splits;             // prompts: parts of a row tile's tokens
+  int32_t units;              // prompts: row tiles x heads x parts, at most
   int4* pieces;               // [CTAs]: {sequence, item, last CTA, 0} of the item that goes on in the next
 };
 constexpr int kAttentionCtas = 152;  // most CTAs of a launch, which the workspace is made for

@@ -630,6 +630,30 @@ def test_attention_of_many_ragged_sequences():
     check(z, out, lse, "bf16")
 
 
+@pytest.mark.parametrize("D,window", [(64, 0), (128, 0), (128, 40), (256, 0)])
+def test_attention_of_many_short_prompts(D, window):
+    """More row tiles than CTAs are launched for: a CTA takes several, one after the other; NaN in the
+    cache of some, and pages that do not exist, change those alone."""
+    rng = np.random.default_rng(36)
+    B = 700
+    counts = rng.integers(20, 72, B)
+    counts[rng.random(B) < 0.1] = 0
+    lens = np.maximum(counts + rng.integers(-3, 60, B), 1)
+    z = problem(rng, lens.tolist(), counts.tolist(), 4, 2, D, 16, "bf16")
+    q, more = z["q"].to(DEV), dict(q_starts=gpu(z["starts"]), max_q=71, window=window, return_lse=True)
+    out, lse = nv.attention(q, **on_gpu(z), **more)
+    check(z, out, lse, "bf16", window=window)
+    bad, nan = np.arange(3, B, 40), np.arange(7, B, 40)
+    z["cache"][z["table"][nan, 0], :, 0, 0, 0, 512:] = 0x7F  # K
+    z["cache"][z["table"][nan + 1, 0], :, 0, 1, 0, 512:] = 0xFF  # V
+    z["table"][bad, 0] = -1
+    got, got_lse = nv.attention(q, **on_gpu(z), **more)
+    touched = np.isin(np.arange(B), np.concatenate((bad, nan, nan + 1)))
+    rows = torch.from_numpy(np.repeat(touched, counts))
+    assert torch.equal(got[~rows], out[~rows]) and torch.equal(got_lse[~rows], lse[~rows])
+    assert torch.isnan(got[rows]).any()
+
+
 def test_attention_with_starts_that_overlap():
     """Starts that are no partition of q's rows: no result is promised for the rows that are named
     twice or by a sequence that ends before it starts, every other row's is as it should be."""
