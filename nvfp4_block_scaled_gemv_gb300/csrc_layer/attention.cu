@@ -26,8 +26,8 @@
 // its own keys: 420 us, 85%).  A tile of 32 tokens costs a warp ~730 instructions (128 conversions,
 // 128 products with scales, 32 MMAs), of the ~800 issue slots that an SM has in the time of its bytes.
 // 16 columns take 1.55 times the time of 8 (12 warps, for the registers), heads of 64 1.8 times that of
-// their bytes.  Small calls: one sequence of 900 tokens 12.3 us, of which the second kernel, lengths,
-// page numbers and the first bytes are ~10, one after the other.
+// their bytes.  Small calls: one sequence of 900 tokens 10.2 us, of which the second kernel is 4 and lengths,
+// page numbers and the first bytes most of the rest, one after the other.
 #include <cfloat>
 #include <cstdint>
 
@@ -44,7 +44,7 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kMostWarps = 16;
-constexpr int64_t kPieceList = (kAttentionCtas * (int64_t)sizeof(int4) + 255) / 256 * 256;
+constexpr int64_t kPieceList = (2 * kAttentionCtas * (int64_t)sizeof(int4) + 255) / 256 * 256;
 
 __device__ int g_attention_timeouts;
 
@@ -239,7 +239,7 @@ struct Piece {
   const float* at;  // null: none
   Sequence seq;
   uint32_t end;     // the item's end among all tiles
-  int32_t b, item, head, first_column;
+  int32_t head, first_column;
   int32_t early;    // in the workspace, not where the warp's ring was
 };
 
@@ -286,7 +286,6 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
   const int g = lane >> 2, q = lane & 3;
   const uint32_t ring = smem_u32(smem) + warp * kStages * S::kStage;
   const uint32_t bars = smem_u32(smem) + kWarps * kStages * S::kStage + warp * kStages * 8;
-  __shared__ uint32_t warp_sums[kMostWarps];
   __shared__ uint32_t share_ends[S::kThreads];  // tiles up to the end of each thread's share, in its warp
   __shared__ Piece piece_of[kMostWarps][2];     // that goes on with an item, that begins one
 
@@ -315,7 +314,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
   }
   share_ends[threadIdx.x] = upto;
   if (lane < 2) piece_of[warp][lane].at = nullptr;
-  if (threadIdx.x == 0) p.pieces[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (threadIdx.x == 0) p.pieces[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
   __syncthreads();
   // (a lane has the sum of a warp's shares)
   uint32_t ends = lane < kWarps ? share_ends[lane * 32 + 31] : 0;
@@ -756,8 +755,6 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
       if (lane == 0) {
         Piece& to_merge = piece_of[warp][from == 0 ? 1 : 0];
         to_merge.at = piece;
-        to_merge.b = b;
-        to_merge.item = item;
         to_merge.head = head;
         to_merge.first_column = first_column;
         to_merge.early = left != 0;
@@ -827,36 +824,63 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
         if (d == 0) *reinterpret_cast<float2*>(sum_at + C * D + 2 * c) = make_float2(m, l);
       }
     }
-    if (begins && !ends && warp % each == 0 && lane == 0)
-      p.pieces[blockIdx.x] = make_int4(lead.b, lead.item, (int)(runs.of(lead.end - 1) / per_cta), 0);
+    if (begins && !ends && warp % each == 0 && lane == 0) {
+      p.pieces[2 * blockIdx.x] = make_int4((int)(runs.of(lead.end - 1) / per_cta), lead.head, lead.first_column, lead.seq.beyond);
+      p.pieces[2 * blockIdx.x + 1] = make_int4(lead.seq.n, lead.seq.q0, 0, 0);
+    }
   }
 }
 
 // The pieces of an item that several CTAs share added up: some CTAs for each CTA of the first
-// kernel, for the item that begins in it and goes on in the next, if there is one.
+// kernel, for the item that begins in it and goes on in the next, if there is one.  What it takes is
+// trips to memory: with all that it has to know of an item written down by the first kernel, one pass
+// over the pieces, and the first two fetched at once it is 4 us, where reading lengths and maxima
+// first took 6 (4 fetched at once: level).
 template <int D, int NT>
 __global__ void __launch_bounds__(128) attention_sum_kernel(const AttentionParams p) {
   using S = Shape<D, NT>;
   constexpr int C = S::kColumns;
   pdl_launch_dependents();
   pdl_wait();
-  const int4 piece = p.pieces[blockIdx.x];
-  if (piece.x < 0) return;
-  const Sequence seq = sequence_of<S::kTile>(p, piece.x);
-  const int32_t cts = column_tiles(p, seq.n, C);
-  const int head = piece.y / cts, first_column = (piece.y - head * cts) * C;
   const int e = (int)blockIdx.y * 128 + threadIdx.x;
   const int c = e / (D / 4), d = e % (D / 4) * 4;
+  const float* const own = p.partial + (int64_t)blockIdx.x * 2 * S::kPiece;
+  // (pieces that are not this item's, or no longer anyone's, are fetched in vain)
+  constexpr int kFirst = 2;
+  const int4 piece = p.pieces[2 * blockIdx.x], of = p.pieces[2 * blockIdx.x + 1];
+  float2 ml[kFirst];
+  float4 v[kFirst];
+#pragma unroll
+  for (int i = 0; i < kFirst; ++i) {
+    const float* const at = own + (i == 0 ? S::kPiece : min(i, (int)(gridDim.x - 1 - blockIdx.x)) * 2 * S::kPiece);
+    ml[i] = *reinterpret_cast<const float2*>(at + C * D + 2 * c);
+    v[i] = *reinterpret_cast<const float4*>(at + c * D + d);
+  }
+  if (piece.x < 0) return;
+  Sequence seq = {};
+  seq.n = of.x;
+  seq.q0 = of.y;
+  seq.beyond = piece.w != 0;
   float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto piece_at = [&](int w) { return p.partial + ((int64_t)w * 2 + (w == (int)blockIdx.x ? 1 : 0)) * S::kPiece; };
+  auto add = [&](float2 ml, float4 v) {
+    const float top = fmaxf(m, ml.x);
+    const float f = m == top ? 1.f : exp2_fast(m - top);
+    o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+    l *= f;
+    m = top;
+    add_piece(m, l, o, ml, v);
+  };
+  const int count = piece.x - (int)blockIdx.x + 1;
+#pragma unroll
+  for (int i = 0; i < kFirst; ++i)
+    if (i < count) add(ml[i], v[i]);
 #pragma unroll 4
-  for (int w = blockIdx.x; w <= piece.z; ++w) m = fmaxf(m, piece_at(w)[C * D + 2 * c]);
-#pragma unroll 4
-  for (int w = blockIdx.x; w <= piece.z; ++w)
-    add_piece(m, l, o, *reinterpret_cast<const float2*>(piece_at(w) + C * D + 2 * c),
-              *reinterpret_cast<const float4*>(piece_at(w) + c * D + d));
-  write_four<D>(p, seq, head, first_column + c, d, o, m, l);
+  for (int i = kFirst; i < count; ++i) {
+    const float* const at = own + (int64_t)i * 2 * S::kPiece;
+    add(*reinterpret_cast<const float2*>(at + C * D + 2 * c), *reinterpret_cast<const float4*>(at + c * D + d));
+  }
+  write_four<D>(p, seq, piece.y, piece.z + c, d, o, m, l);
 }
 
 template <int D, int NT>

@@ -73,7 +73,7 @@ struct AttentionParams {
   int32_t* row_tiles;         // prompts in ragged batches: [B + 1] row tiles before each sequence
   int32_t splits;             // prompts: parts of a row tile's tokens
   int32_t units;              // prompts: row tiles x heads x parts, at most
-  int4* pieces;               // [CTAs]: {sequence, item, last CTA, 0} of the item that goes on in the next
+  int4* pieces;               // [CTAs][2]: {last CTA or -1, head, first column, beyond}, {n, q0} of the item that goes on in the next
 };
 constexpr int kAttentionCtas = 152;  // most CTAs of a launch, which the workspace is made for
 // Columns (query token and head of a group, together) that one pass over the cache takes
