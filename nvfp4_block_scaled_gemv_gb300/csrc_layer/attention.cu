@@ -26,7 +26,7 @@
 // its own keys: 420 us, 85%).  A tile of 32 tokens costs a warp ~730 instructions (128 conversions,
 // 128 products with scales, 32 MMAs), of the ~800 issue slots that an SM has in the time of its bytes.
 // 16 columns take 1.55 times the time of 8 (12 warps, for the registers), heads of 64 1.8 times that of
-// their bytes.  Small calls: one sequence of 900 tokens 10.2 us, of which the second kernel is 4 and lengths,
+// their bytes.  Small calls: one sequence of 900 tokens 9.4 us, of which the second kernel is 3 to 4 and lengths,
 // page numbers and the first bytes most of the rest, one after the other.
 #include <cfloat>
 #include <cstdint>
@@ -325,8 +325,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
   }
   const uint32_t total = __shfl_sync(0xffffffffu, ends, kWarps - 1);
   if (total == 0) return;
-  // warps in use: those of a CTA that are needed for every CTA to have as many
-  const uint32_t per_cta = min((total + gridDim.x - 1) / gridDim.x, (uint32_t)kWarps);
+  // Warps in use: those of a CTA that are needed for every CTA to have as many, but no fewer than its four
+  // schedulers take: a CTA then has more of an item, and fewer pieces are left for the second kernel (1
+  // sequence of 400 tokens, 32 heads on 8: 10.0 -> 8.4 us; of 900, 16 heads of 256 on 4: 14.5 -> 11.1;
+  // with 6 at least 8.4 and 10.7, but 16 of 100 tokens 9.0 in place of 7.7).
+  const uint32_t per_cta = min(max((total + gridDim.x - 1) / gridDim.x, 4u), (uint32_t)kWarps);
   const uint32_t warps = min(per_cta * gridDim.x, total);
   Runs runs;
   runs.each = total / warps;
