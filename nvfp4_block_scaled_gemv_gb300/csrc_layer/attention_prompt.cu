@@ -722,44 +722,50 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
         const bool real = row < work.rows;
         const int32_t token = row / p.group, member = row - token * p.group;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-        // the row of Q, as fp16 (bf16: in a power of two of its own, see attention.cu)
+        // This warp's rows of Q, as fp16 (bf16: in a power of two of the row's own, see attention.cu), D / 8
+        // lanes to a row and 16 loads under way (a row a lane, four loads at once: 5 us a row tile).
         float back = 1.f;
         {
-          const uint16_t* const src = static_cast<const uint16_t*>(p.q) +
-                                      (real ? (int64_t)(work.q0 + token) * p.q_token +
-                                                  (int64_t)(work.head * p.group + member) * p.q_head
-                                            : 0);
-          float by = 1.f;
-          if (p.bf16 && real) {
-            float largest = 0.f;
-#pragma unroll 4
-            for (int c = 0; c < D / 8; ++c) {
-              const uint4 v = reinterpret_cast<const uint4*>(src)[c];
-              const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+          constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;  // rows of a load
+          const int64_t own = real ? (int64_t)(work.q0 + token) * p.q_token + (int64_t)(work.head * p.group + member) * p.q_head
+                                   : -1;
+          const int piece = lane % kLanes;
+          const uint32_t panel = q_s + (u * kPlanes + (piece >> 3)) * S::kPanel;
+#pragma unroll 1
+          for (int first = 0; first < 32; first += 16 * kAtOnce) {
+            constexpr int kLoads = kLanes < 16 ? kLanes : 16;
+            uint4 v[kLoads];
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                largest = fmaxf(largest, fmaxf(fabsf(__uint_as_float(words[i] << 16)),
-                                               fabsf(__uint_as_float(words[i] & 0xffff0000u))));
+            for (int k = 0; k < kLoads; ++k) {
+              const int64_t from = __shfl_sync(0xffffffffu, own, first + k * kAtOnce + lane / kLanes);
+              v[k] = make_uint4(0u, 0u, 0u, 0u);
+              if (from >= 0) v[k] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + from + piece * 8);
             }
-            const int e = min(max(14 - ((int)(__float_as_uint(largest) >> 23) - 127), -113), 113);
-            by = __uint_as_float((uint32_t)(e + 127) << 23);
-            back = __uint_as_float((uint32_t)(127 - e) << 23);
-          }
-          const uint32_t line = q_s + u * kPlanes * S::kPanel + r * 128;
-#pragma unroll 4
-          for (int c = 0; c < D / 8; ++c) {
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (real) v = reinterpret_cast<const uint4*>(src)[c];
-            uint32_t words[4] = {v.x, v.y, v.z, v.w};
-            if (p.bf16) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                words[i] = half2_of(__uint_as_float(words[i] << 16) * by, __uint_as_float(words[i] & 0xffff0000u) * by);
+            for (int k = 0; k < kLoads; ++k) {
+              uint32_t words[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+              if (p.bf16) {
+                float largest = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  largest = fmaxf(largest, fmaxf(fabsf(__uint_as_float(words[i] << 16)),
+                                                 fabsf(__uint_as_float(words[i] & 0xffff0000u))));
+#pragma unroll
+                for (int d = 1; d < kLanes; d <<= 1) largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, d));
+                const int e = min(max(14 - ((int)(__float_as_uint(largest) >> 23) - 127), -113), 113);
+                const float by = __uint_as_float((uint32_t)(e + 127) << 23);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  words[i] = half2_of(__uint_as_float(words[i] << 16) * by, __uint_as_float(words[i] & 0xffff0000u) * by);
+                const int theirs = __shfl_sync(0xffffffffu, e, lane % kAtOnce * kLanes);
+                if (lane == first + k * kAtOnce + lane % kAtOnce) back = __uint_as_float((uint32_t)(127 - theirs) << 23);
+              }
+              const uint32_t in_half = (uint32_t)(32 * (warp & 3) + first + k * kAtOnce + lane / kLanes);
+              const uint32_t at = panel + in_half * 128 + (uint32_t)((piece & 7) ^ (in_half & 7)) * 16u;
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(words[0]), "r"(words[1]), "r"(words[2]),
+                           "r"(words[3])
+                           : "memory");
             }
-            const uint32_t at = line + (c >> 3) * S::kPanel + (uint32_t)((c & 7) ^ (r & 7)) * 16u;
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(words[0]), "r"(words[1]), "r"(words[2]),
-                         "r"(words[3])
-                         : "memory");
           }
         }
         async_proxy_fence();
