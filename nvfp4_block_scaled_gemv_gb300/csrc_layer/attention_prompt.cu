@@ -468,6 +468,31 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
         reinterpret_cast<float2*>(piece + S::kRows * D)[i] = make_float2(-INFINITY, 0.f);
   }
   if (shared_work.tiles == 0) return;
+  // This warp's rows of Q on their way to shared memory, D / 8 lanes to a row: 16-byte copies that hold no
+  // registers, in a loop of few instructions (16 loads at once to registers, unrolled, took 4.4 us a
+  // row tile for the instructions alone, which are not in the cache when a CTA begins).
+  constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
+  const int half = warp >> 2, piece16 = lane % kLanes;  // (warps 0 to 7)
+  const uint32_t q_panel = q_s + (half * kPlanes + (piece16 >> 3)) * S::kPanel;
+  auto query_at = [&](int k) {  // of the warp's k-th rows
+    const uint32_t r = (uint32_t)(32 * (warp & 3) + k * kAtOnce + lane / kLanes);
+    return q_panel + r * 128 + (uint32_t)((piece16 & 7) ^ (r & 7)) * 16u;
+  };
+  auto fetch_queries = [&]() {
+    const int32_t row = shared_work.first_row + (half * CTAS + cta) * 128 + 32 * (warp & 3) + lane;
+    const int32_t token = row / p.group, member = row - token * p.group;
+    const int64_t own = row < shared_work.rows ? (int64_t)(shared_work.q0 + token) * p.q_token +
+                                                     (int64_t)(shared_work.head * p.group + member) * p.q_head
+                                               : -1;
+#pragma unroll 4
+    for (int k = 0; k < kLanes; ++k) {
+      const int64_t from = __shfl_sync(0xffffffffu, own, k * kAtOnce + lane / kLanes);
+      const uint16_t* const src = static_cast<const uint16_t*>(p.q) + (from < 0 ? 0 : from) + piece16 * 8;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(query_at(k)), "l"(src), "r"(from < 0 ? 0 : 16)
+                   : "memory");
+    }
+  };
+  if (half < NQ) fetch_queries();
   if constexpr (CTAS == 2) tc::cluster_sync();  // the peer's barriers are initialised, and it is there to allocate
   if (warp == 12) {
     if constexpr (CTAS == 1) {
@@ -477,12 +502,20 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
       asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
   }
-  tc::fence_before();
-  __syncthreads();
-  if constexpr (CTAS == 2) tc::cluster_sync();
-  tc::fence_after();
+  // (one SM: the warps that bring tiles begin meanwhile)
+  uint32_t tmem = 0;
+  if (CTAS == 2 || warp < 8 || warp == 12) {
+    tc::fence_before();
+    if constexpr (CTAS == 2) {
+      __syncthreads();
+      tc::cluster_sync();
+    } else {
+      asm volatile("bar.sync 1, 288;" ::: "memory");
+    }
+    tc::fence_after();
+    tmem = __shfl_sync(0xffffffffu, *const_cast<volatile uint32_t*>(&tmem_slot), 0);
+  }
   pdl_launch_dependents();
-  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
   bool ok = true;
   // Ragged batches of many sequences on one SM each: the next unit, if there is one.
   auto another = [&]() {
@@ -711,6 +744,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
     } while (another());
   } else {
     registers_up<184>();
+    bool first = true;  // unit of this CTA
     do {
       const Work work = shared_work;
       const int32_t tiles = work.tiles;
@@ -722,49 +756,47 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
         const bool real = row < work.rows;
         const int32_t token = row / p.group, member = row - token * p.group;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-        // This warp's rows of Q, as fp16 (bf16: in a power of two of the row's own, see attention.cu), D / 8
-        // lanes to a row and 16 loads under way (a row a lane, four loads at once: 5 us a row tile).
+        // Q as fp16; bf16: in a power of two of the row's own, see attention.cu
+        if (!first) fetch_queries();
+        first = false;
+        asm volatile("cp.async.wait_all;" ::: "memory");
         float back = 1.f;
-        {
-          constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;  // rows of a load
-          const int64_t own = real ? (int64_t)(work.q0 + token) * p.q_token + (int64_t)(work.head * p.group + member) * p.q_head
-                                   : -1;
-          const int piece = lane % kLanes;
-          const uint32_t panel = q_s + (u * kPlanes + (piece >> 3)) * S::kPanel;
+        if (p.bf16) {
+          // (8 pieces at once, all of them what this lane brought: one after the other took 300 cycles each)
 #pragma unroll 1
-          for (int first = 0; first < 32; first += 16 * kAtOnce) {
-            constexpr int kLoads = kLanes < 16 ? kLanes : 16;
-            uint4 v[kLoads];
+          for (int k0 = 0; k0 < kLanes; k0 += 8) {
+            uint32_t words[8][4];
+            float largest[8];
 #pragma unroll
-            for (int k = 0; k < kLoads; ++k) {
-              const int64_t from = __shfl_sync(0xffffffffu, own, first + k * kAtOnce + lane / kLanes);
-              v[k] = make_uint4(0u, 0u, 0u, 0u);
-              if (from >= 0) v[k] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + from + piece * 8);
+            for (int k = 0; k < 8; ++k) {
+              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(words[k][0]), "=r"(words[k][1]), "=r"(words[k][2]), "=r"(words[k][3])
+                           : "r"(query_at(k0 + k)));
             }
 #pragma unroll
-            for (int k = 0; k < kLoads; ++k) {
-              uint32_t words[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-              if (p.bf16) {
-                float largest = 0.f;
+            for (int k = 0; k < 8; ++k) {
+              largest[k] = 0.f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  largest = fmaxf(largest, fmaxf(fabsf(__uint_as_float(words[i] << 16)),
-                                                 fabsf(__uint_as_float(words[i] & 0xffff0000u))));
+              for (int i = 0; i < 4; ++i)
+                largest[k] = fmaxf(largest[k], fmaxf(fabsf(__uint_as_float(words[k][i] << 16)),
+                                                     fabsf(__uint_as_float(words[k][i] & 0xffff0000u))));
+            }
 #pragma unroll
-                for (int d = 1; d < kLanes; d <<= 1) largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, d));
-                const int e = min(max(14 - ((int)(__float_as_uint(largest) >> 23) - 127), -113), 113);
-                const float by = __uint_as_float((uint32_t)(e + 127) << 23);
+            for (int d = 1; d < kLanes; d <<= 1)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  words[i] = half2_of(__uint_as_float(words[i] << 16) * by, __uint_as_float(words[i] & 0xffff0000u) * by);
-                const int theirs = __shfl_sync(0xffffffffu, e, lane % kAtOnce * kLanes);
-                if (lane == first + k * kAtOnce + lane % kAtOnce) back = __uint_as_float((uint32_t)(127 - theirs) << 23);
-              }
-              const uint32_t in_half = (uint32_t)(32 * (warp & 3) + first + k * kAtOnce + lane / kLanes);
-              const uint32_t at = panel + in_half * 128 + (uint32_t)((piece & 7) ^ (in_half & 7)) * 16u;
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(words[0]), "r"(words[1]), "r"(words[2]),
-                           "r"(words[3])
+              for (int k = 0; k < 8; ++k) largest[k] = fmaxf(largest[k], __shfl_xor_sync(0xffffffffu, largest[k], d));
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int e = min(max(14 - ((int)(__float_as_uint(largest[k]) >> 23) - 127), -113), 113);
+              const float by = __uint_as_float((uint32_t)(e + 127) << 23);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                words[k][i] = half2_of(__uint_as_float(words[k][i] << 16) * by, __uint_as_float(words[k][i] & 0xffff0000u) * by);
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(query_at(k0 + k)), "r"(words[k][0]),
+                           "r"(words[k][1]), "r"(words[k][2]), "r"(words[k][3])
                            : "memory");
+              const int theirs = __shfl_sync(0xffffffffu, e, lane % kAtOnce * kLanes);
+              if (lane / kAtOnce == k0 + k) back = __uint_as_float((uint32_t)(127 - theirs) << 23);
             }
           }
         }
@@ -913,15 +945,32 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
             uint4* const to = reinterpret_cast<uint4*>(piece + (int64_t)in_tile * D + i);
 #pragma unroll
             for (int k = 0; k < 8; ++k) to[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-          } else if (real) {
-            uint32_t words[16];
+          } else {
+            // to where the row of Q was: its products are through
+            const uint32_t line = q_s + (half * kPlanes + (i >> 6)) * S::kPanel + r * 128;
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
-              words[k] = rounded_two(p.bf16, __uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1]));
-            uint4* const to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + out_row * D + i);
+            for (int k = 0; k < 4; ++k) {
+              uint32_t words[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              to[k] = make_uint4(words[4 * k], words[4 * k + 1], words[4 * k + 2], words[4 * k + 3]);
+              for (int x = 0; x < 4; ++x)
+                words[x] = rounded_two(p.bf16, __uint_as_float(o[8 * k + 2 * x]), __uint_as_float(o[8 * k + 2 * x + 1]));
+              const uint32_t at = line + (uint32_t)((((i & 63) >> 3) + k) ^ (r & 7)) * 16u;
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(words[0]), "r"(words[1]), "r"(words[2]),
+                           "r"(words[3])
+                           : "memory");
+            }
+          }
+        }
+        if (!part && ok) {
+          // whole rows out, D / 8 lanes to each (a row a lane: 32 pieces of 16 bytes a store)
+          __syncwarp();
+          const int64_t own = real ? out_row : -1;
+#pragma unroll 4
+          for (int k = 0; k < kLanes; ++k) {
+            const int64_t to = __shfl_sync(0xffffffffu, own, k * kAtOnce + lane / kLanes);
+            uint4 v;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(query_at(k)));
+            if (to >= 0) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + to * D + piece16 * 8) = v;
           }
         }
       }
