@@ -37,7 +37,7 @@
 // 4 KB of Q for 64 columns).
 //
 // What bounds it.  That case runs at 1.45 PFLOP/s in 1155 us, 76% of the measured bf16 rate, the tensor pipe busy
-// about two thirds of the time: a half's next scores wait for its softmax and P's product.  Heads of
+// about 70% of the time: a half's next scores wait for its softmax and P's product.  Heads of
 // 64 run at 0.85 (4 x 2048 queries on 8192 tokens, 566 us): the exponentials alone, 1024 cycles a
 // tile, are as long as its MMAs.  Heads of 256: 1.11 (2 x 2048 on 8192, 16 heads, 433 us).
 // Short prompts are bound by the beginning and end of a row tile, ~15,000 cycles where 128 tokens are ~2,800: 4 prompts of 2048
