@@ -670,6 +670,19 @@ def test_attention_with_starts_that_overlap():
     assert torch.equal(out[:150], want[:150])
 
 
+@pytest.mark.parametrize("n", [1, 80])
+def test_attention_without_pages(n):
+    """A cache and a page table without pages: empty sequences are 0, longer ones than the table NaN."""
+    cache = nv.kv_cache(0, 2, 128, 16, device=DEV)
+    q = torch.randn(2 * n, 4, 128, device=DEV).bfloat16()
+    table = torch.zeros((2, 0), dtype=torch.int32, device=DEV)
+    lengths = torch.tensor([0, 5], dtype=torch.int32, device=DEV)
+    out, lse = nv.attention(q, cache, table, lengths, return_lse=True)
+    assert not out[:n].any() and (lse[:n] == -float("inf")).all()
+    assert torch.isnan(out[n:]).all() and torch.isnan(lse[n:]).all()
+    assert nv.attention(q[:0], cache, table, lengths).shape == (0, 4, 128)
+
+
 def test_attention_of_identical_pages():
     """Sequences that share pages (a common prefix) read the same tokens."""
     rng = np.random.default_rng(32)
