@@ -124,6 +124,8 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
 }
+// Whether a row's reference m is far from 0 (-inf: there is none yet).
+__device__ __forceinline__ bool is_far(float m, float c) { return fabsf(m * c) > kFarReference && m != -INFINITY; }
 // Bits of a where mask, bits of b elsewhere.
 __device__ __forceinline__ uint32_t merge_bits(uint32_t a, uint32_t b, uint32_t mask) {
   return (a & mask) | (b & ~mask);
@@ -501,7 +503,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
 
     float o[D / 16][NT][4];
     float m[NT][2], l[NT][2];
-    float shift[NT][2];  // -m in base 2, or 0 while a row is empty (all its p are 0)
+    float shift[NT][2];  // -m in base 2, or 0 while a row is empty (all its p are 0) or if m is far from 0
+    bool far = false;    // m of some column is (the same in all lanes)
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -607,7 +610,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
             if (top > m[nt][e]) {  // (the same in all lanes of a column)
               const float keep = exp2_fast((m[nt][e] - top) * cs[nt][e]);
               m[nt][e] = top;
-              shift[nt][e] = -top * cs[nt][e];
+              shift[nt][e] = is_far(top, cs[nt][e]) ? 0.f : -top * cs[nt][e];
               l[nt][e] *= keep;
 #pragma unroll
               for (int i = 0; i < D / 16; ++i) {
@@ -615,6 +618,20 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
                 o[i][nt][2 + e] *= keep;
               }
             }
+          }
+        far = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) far |= is_far(m[nt][0], cs[nt][0]) || is_far(m[nt][1], cs[nt][1]);
+        far = __any_sync(0xffffffffu, far);
+      }
+      if (far) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float less = is_far(m[nt][e], cs[nt][e]) ? m[nt][e] : 0.f;
+#pragma unroll
+            for (int i = 0; i < kGr; ++i) s[i][nt][e] -= less, s[i][nt][2 + e] -= less;
           }
       }
       // P, and its transposition to the second product's operand

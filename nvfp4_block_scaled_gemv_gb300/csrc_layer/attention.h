@@ -75,6 +75,10 @@ struct AttentionParams {
   int32_t units;              // prompts: row tiles x heads x parts, at most
   int4* pieces;               // [CTAs][2]: {last CTA or -1, head, first column, beyond}, {n, q0} of the item that goes on in the next
 };
+// Scores whose row's reference lies further from 0 than this (in base 2) are taken from the reference before they
+// are scaled: score * c - round(reference * c), one fused operation elsewhere, is off by half a step of that product,
+// 2^-4 here, 1 at 2^24, and from 2^28 more than fp16 (and then the exponential) holds.
+constexpr float kFarReference = 1048576.f;
 constexpr int kAttentionCtas = 152;  // most CTAs of a launch, which the workspace is made for
 // Columns (query token and head of a group, together) that one pass over the cache takes
 // for a head size and the most columns of a sequence.

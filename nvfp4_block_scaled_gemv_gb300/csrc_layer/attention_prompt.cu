@@ -238,6 +238,8 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(x));
   return d;
 }
+// Whether a row's reference m is far from 0 (-inf: there is none yet).
+__device__ __forceinline__ bool is_far(float m, float c) { return fabsf(m * c) > kFarReference && m != -INFINITY; }
 __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
   uint32_t d;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
@@ -812,6 +814,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
         int32_t lo, hi;
         row_sees(p, work.length, work.n, real ? row : work.rows - 1, lo, hi);
         float m = -INFINITY;       // the row's reference score, before c
+        bool far = false;          // it is far from 0 in some row of the warp
         uint64_t sum = 0;          // two partial sums
         uint32_t nan_blocks = 0;   // blocks of 16 whose V is NaN in a token that the row sees
         const uint32_t o_at = tmem + lanes + S::kO + D * u;
@@ -862,6 +865,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
             if (up) m = now;
             const float2 two = unpack_f32x2(sum);
             sum = pack_f32x2(two.x * f, two.y * f);
+            far = __any_sync(0xffffffffu, is_far(m, c));
             if (j > 0) {
               if (!S::kOwnP) {
                 wait_phase(o_done(u), (uint32_t)(j - 1) & 1u, ok);
@@ -880,7 +884,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
               }
             }
           }
-          const float base2 = m == -INFINITY ? 0.f : -m * c;
+          float base2 = m == -INFINITY ? 0.f : -m * c;
+          if (far) {
+            const float less = is_far(m, c) ? m : 0.f;
+#pragma unroll
+            for (int h = 0; h < BN / 32; ++h)
+#pragma unroll
+              for (int i = 0; i < 32; ++i) s[h][i] = __float_as_uint(__uint_as_float(s[h][i]) - less);
+            if (is_far(m, c)) base2 = 0.f;
+          }
           const uint64_t c2 = pack_f32x2(c, c), b2 = pack_f32x2(base2, base2), one2 = pack_f32x2(1.f, 1.f);
           uint64_t other = 0;
 #pragma unroll
