@@ -11,7 +11,7 @@
 // side of S^T = K Q^T, the head's elements the M side of O^T = V^T P^T, which wastes
 // nothing on rows that do not exist.  Codes become fp16 in registers: code * scale has 6
 // significant bits and is exact, so the only roundings before the fp32 sums are p to fp16
-// (2^-11 of itself; below 2^-14 of the row's largest p, 2^-25 of that) and the result's.
+// (2^-11 of itself; below 2^-21 of the row's largest p, 2^-32 of that) and the result's.
 //
 // A warp works by itself: 32 tokens (D = 64: 64) at a time in a ring of stages that it fills with bulk
 // copies, a copy per 16 tokens (a granule of the cache, K and V in one run of bytes).  All
@@ -503,7 +503,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
 
     float o[D / 16][NT][4];
     float m[NT][2], l[NT][2];
-    float shift[NT][2];  // -m in base 2, or 0 while a row is empty (all its p are 0) or if m is far from 0
+    float shift[NT][2];  // 7 - m in base 2, 7 if m is far from 0, 0 while a row is empty (all its p are 0)
     bool far = false;    // m of some column is (the same in all lanes)
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
@@ -583,7 +583,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
           }
       }
       // The reference that p is taken from is raised only where a score passes it by 8 (in base
-      // 2): p stays below 2^8, results are seldom rescaled, and most tiles ask a vote of the lanes
+      // 2): p stays below 2^15, results are seldom rescaled, and most tiles ask a vote of the lanes
       // in place of the maximum over them.
       bool passed = false;
 #pragma unroll
@@ -610,7 +610,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
             if (top > m[nt][e]) {  // (the same in all lanes of a column)
               const float keep = exp2_fast((m[nt][e] - top) * cs[nt][e]);
               m[nt][e] = top;
-              shift[nt][e] = is_far(top, cs[nt][e]) ? 0.f : -top * cs[nt][e];
+              shift[nt][e] = is_far(top, cs[nt][e]) ? kReferenceP : fmaf(-top, cs[nt][e], kReferenceP);
               l[nt][e] *= keep;
 #pragma unroll
               for (int i = 0; i < D / 16; ++i) {
@@ -739,7 +739,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
     if (!ok) break;
     left -= (uint32_t)(to - from);
 
-    // sums over the lanes that have a column's tokens, and the maxima in base 2
+    // sums over the lanes that have a column's tokens, and in base 2 what they are relative to
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -747,7 +747,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
         l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 4);
         l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 8);
         l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 16);
-        m[nt][e] *= cs[nt][e];
+        m[nt][e] = fmaf(m[nt][e], cs[nt][e], -kReferenceP);
       }
     if (from == 0 && to == seq.tiles) {
       write_columns<D, NT>(p, seq, head, first_column, o, m, l);

@@ -14,9 +14,9 @@
 // 128-byte swizzled layout that the MMAs read, so that nothing but the 4-bit cache is read from
 // memory and nothing dequantised is written there.  Eight warps, a thread per row, do the
 // softmax: while one half's rows are worked on, the MMAs of the other half run.  A running
-// reference is raised only where a score passes it by 8 (in base 2): p then stays
-// below 2^8, and the rows of O are seldom rescaled.  p is rounded to fp16 (2^-11 of itself, below
-// 2^-14 of the reference 2^-25 of that), sums are fp32 before that rounding.
+// reference is raised only where a score passes it by 8 (in base 2): p, 2^7 at the reference, then
+// stays below 2^15, and the rows of O are seldom rescaled.  p is rounded to fp16 (2^-11 of itself, below
+// 2^-21 of the reference's 2^-32 of that), sums are fp32 before that rounding.
 //
 // Warps: 0-3 and 4-7 softmax of rows 0-127 and 128-255 (NQ = 1: only the first four), 8-11 raw
 // tiles to fp16, 12 issues MMAs, 13 copies granules.  Registers are split by what they need: a
@@ -884,14 +884,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
               }
             }
           }
-          float base2 = m == -INFINITY ? 0.f : -m * c;
+          float base2 = m == -INFINITY ? 0.f : fmaf(-m, c, kReferenceP);
           if (far) {
             const float less = is_far(m, c) ? m : 0.f;
 #pragma unroll
             for (int h = 0; h < BN / 32; ++h)
 #pragma unroll
               for (int i = 0; i < 32; ++i) s[h][i] = __float_as_uint(__uint_as_float(s[h][i]) - less);
-            if (is_far(m, c)) base2 = 0.f;
+            if (is_far(m, c)) base2 = kReferenceP;
           }
           const uint64_t c2 = pack_f32x2(c, c), b2 = pack_f32x2(base2, base2), one2 = pack_f32x2(1.f, 1.f);
           uint64_t other = 0;
@@ -933,7 +933,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
         __syncwarp();
         tc::fence_after();
         const float2 two = unpack_f32x2(sum);
-        const float l = two.x + two.y;
+        const float l = two.x + two.y, relative_to = fmaf(m, c, -kReferenceP);  // (-inf: nothing)
         const float decode = p.encode_v ? 1.f / __ldg(p.encode_v + work.head) : 1.f;
         float f = l == 0.f ? 0.f : decode / l;
         if (work.beyond) f = __int_as_float(0x7fc00000);
@@ -941,9 +941,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
         const bool part = p.splits > 1;
         if (part) {
           f = 1.f;
-          if (ok) reinterpret_cast<float2*>(piece + S::kRows * D)[in_tile] = make_float2(m == -INFINITY ? m : m * c, l);
+          if (ok) reinterpret_cast<float2*>(piece + S::kRows * D)[in_tile] = make_float2(relative_to, l);
         } else if (ok && real && p.lse != nullptr) {
-          p.lse[out_row] = work.beyond ? f : l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.69314718055994531f;
+          p.lse[out_row] = work.beyond ? f : l == 0.f ? -INFINITY : (relative_to + log2f(l)) * 0.69314718055994531f;
         }
 #pragma unroll 1
         for (int i = 0; i < D && ok; i += 32) {

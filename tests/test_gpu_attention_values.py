@@ -1,4 +1,4 @@
-"""Attention on scores far from zero."""
+"""Attention on scores far from zero, and on many tokens of small weight beside one of large."""
 import math
 
 import numpy as np
@@ -60,3 +60,28 @@ def test_attention_of_scores_far_from_zero(n, D, e):
     # rows with more than one token in question hold something between the tokens' values
     low, high = pool.v[:length, 0].amin(0), pool.v[:length, 0].amax(0)
     assert ((out.double() >= low - 2.0 ** -7 * low.abs()) & (out.double() <= high + 2.0 ** -7 * high.abs())).all()
+
+
+@pytest.mark.parametrize("gap", [8, 14, 16, 17, 18])
+@pytest.mark.parametrize("n,D", SHAPES)
+def test_attention_of_many_tokens_of_small_weight(n, D, gap):
+    """The first token, whose value is 0, outweighs each of the 131,071 others by e^gap: what is left of the result
+    is the others', each of which has a weight far below 2^-14."""
+    import attention64 as a64
+
+    rng = np.random.default_rng(gap)
+    page, base, length = 128, 33, 131072
+    k, v = np.zeros((base * page, 1, D), dtype=np.float32), rng.standard_normal((base * page, 1, D)).astype(np.float32) + 3
+    k[:, 0, 0] = -gap / 2
+    k[0, 0, 0] = gap / 2
+    v[0] = 0
+    pool = a64.Pool(a64.pages_of(k, v, page), page)
+    table = rng.integers(1, base, (1, length // page)).astype(np.int32)
+    table[0, 0] = 0
+    q = torch.zeros(n, 8, D, dtype=torch.bfloat16, device=a64.DEV)
+    q[..., 0] = 1
+    call = dict(pool.call(), page_table=a64.gpu(table), lengths=a64.gpu(np.array([length], dtype=np.int32)), scale=1.0)
+    out, lse = nv.attention(q, **call, return_lse=True)
+    few = n * 8 <= (64 if D == 64 else 48)
+    run = 2 * n * length / (8 * 152) + 128 if few else length / 10
+    a64.check(pool, q, table, [length], [n], out, lse, run, scale=1.0)
