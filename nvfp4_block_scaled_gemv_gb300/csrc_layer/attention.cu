@@ -37,6 +37,7 @@
 #include "attention.h"
 #include "layer.h"
 #include "ptx.cuh"
+#include "ring.h"
 #include "tc_ptx.cuh"
 
 namespace nvfp4 {
@@ -337,6 +338,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
   runs.each = total / warps;
   runs.longer = total - runs.each * warps;
   const uint32_t cta_rank = blockIdx.x * per_cta, rank = cta_rank + warp;
+  bool ok = true;
   if (warp < (int)per_cta && rank < warps) {
   const uint32_t begin = runs.start(rank), end = runs.start(rank + 1);
   // the sequence that the run starts in: its warp of shares, its share, and the place there
@@ -412,7 +414,6 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
   uint32_t left = end - begin;
   bool primed = false;
   uint32_t stage = 0, parity = 0;
-  bool ok = true;
   while (left > 0) {
     // an item, or the part of it in this run
     const int head = item / cts, first_column = (item - head * cts) * C;
@@ -736,7 +737,14 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
       load_next();
       if (++stage == kStages) stage = 0, parity ^= 1;
     }
-    if (!ok) break;
+    if (!ok) {
+      // copies still under way land before the CTA can end
+      bool landed = true;
+      await_fills(left - (uint32_t)(tile - from), to_load, stage, parity, kStages, [&](uint32_t s, uint32_t of) {
+        return tc::mbar_wait<false>(bars + 8 * s, of, landed, &g_attention_timeouts);
+      });
+      break;
+    }
     left -= (uint32_t)(to - from);
 
     // sums over the lanes that have a column's tokens, and in base 2 what they are relative to
@@ -798,8 +806,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
   // The CTA's pieces, in the order of its warps: chains of one item each.  Every chain is added up
   // by some warps, into the item's result if it is all there, otherwise into one of the CTA's two
   // places of the workspace: for an item that goes on from the CTA before, and for one that begins
-  // here and goes on in the next.
-  __syncthreads();
+  // here and goes on in the next.  (A CTA with a wait that ran out has none to show.)
+  if (__syncthreads_or(!ok)) return;
   const uint32_t present =
       __ballot_sync(0xffffffffu, (lane >> 1) < kWarps && piece_of[min(lane >> 1, kWarps - 1)][lane & 1].at != nullptr);
   if (present == 0) return;
