@@ -149,19 +149,32 @@ __device__ __forceinline__ void arrive_if(uint32_t bar, bool who) {
                "r"((uint32_t)who)
                : "memory");
 }
-// Arrives on the barrier of the CTA that issues the MMAs.  What it announces is in tensor memory, or
-// in this CTA's shared memory and ordered for the MMAs by the writers' own proxy fences: the
-// arrive need not order other memory at cluster scope (which takes it ~1000 cycles).
+// Arrive on the barrier of the CTA that issues the MMAs.  What was written to tensor memory is ordered by tcgen05's own
+// fences on both sides, so that its arrive need not order anything;
 template <int CTAS>
 __device__ __forceinline__ void arrive_issuer(uint32_t bar, bool who) {
   if constexpr (CTAS == 1)
     arrive_if(bar, who);
   else
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\t@p mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" ::"r"(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\t@p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(
             tc::map_rank(bar, 0)),
         "r"((uint32_t)who)
         : "memory");
+}
+// what the warp wrote to this CTA's shared memory is released to the cluster first, by a fence of that memory alone (2
+// prompts of 2048 on 8192, heads of 256: 441 us; an arrive with a release of its own, of all memory, 541).
+template <int CTAS>
+__device__ __forceinline__ void arrive_issuer_filled(uint32_t bar, bool who) {
+  if constexpr (CTAS == 1) {
+    arrive_if(bar, who);
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\tfence.release.sync_restrict::shared::cta.cluster;\n\t@p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(
+            tc::map_rank(bar, 0)),
+        "r"((uint32_t)who)
+        : "memory");
+  }
 }
 // kind::f16 with fp16 operands and fp32 results; B's rows are the contraction (bit 16).
 __host__ __device__ constexpr uint32_t f16_idesc(uint32_t m, uint32_t n, bool b_rows) {
@@ -213,11 +226,13 @@ __device__ __forceinline__ void tmem_st_16(uint32_t taddr, const uint32_t* v) {
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // tc::mbar_wait for a whole warp, and in line: with a call in it ptxas could not give the warps
-// the registers that setmaxnreg asks for.
+// the registers that setmaxnreg asks for.  CTAS 2: arrivals come from the other CTA of the pair too.
+template <int CTAS = 1>
 __device__ __forceinline__ void wait_phase(uint32_t bar, uint32_t parity, bool& ok) {
-  if (!ok || tc::mbar_try(bar, parity)) return;
+  auto done = [&]() { return CTAS == 1 ? tc::mbar_try(bar, parity) : tc::mbar_try_cluster(bar, parity); };
+  if (!ok || done()) return;
   const uint64_t t0 = tc::global_ns();
-  for (uint32_t i = 1; !tc::mbar_try(bar, parity); ++i)
+  for (uint32_t i = 1; !done(); ++i)
     if ((i & 63u) == 0 && tc::global_ns() - t0 > tc::kWaitNs) {
       ok = false;
       return;
@@ -588,12 +603,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
       } else if (warp == 12 && cta == 0) {
         constexpr uint32_t qk = f16_idesc(128 * CTAS, BN, false), pv = f16_idesc(128 * CTAS, D, true);
         const uint64_t q_desc = tc::desc_sw128(q_s);
-        wait_phase(q_full, 0, ok);
+        wait_phase<CTAS>(q_full, 0, ok);
         auto scores = [&](int32_t x) {
           const int32_t j = NQ == 2 ? x >> 1 : x;
           const int u = NQ == 2 ? x & 1 : 0;
           const int fill = 2 * j, i = fill % kSlots;
-          wait_phase(slot_full(i), (uint32_t)(fill / kSlots) & 1u, ok);
+          wait_phase<CTAS>(slot_full(i), (uint32_t)(fill / kSlots) & 1u, ok);
           ok = __all_sync(0xffffffffu, ok);
           tc::fence_after();
           if (!ok) return;
@@ -616,7 +631,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
         for (int32_t x = 0; x < steps && ok; ++x) {
           if (S::kOwnP && x + 2 < steps) {
             // S is in registers: the next scores need not wait for P and its product
-            wait_phase(s_free(x & 1), (uint32_t)(x >> 1) & 1u, ok);
+            wait_phase<CTAS>(s_free(x & 1), (uint32_t)(x >> 1) & 1u, ok);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             scores(x + 2);
@@ -624,8 +639,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
           const int32_t j = NQ == 2 ? x >> 1 : x;
           const int u = NQ == 2 ? x & 1 : 0;
           const int fill = 2 * j + 1, i = fill % kSlots;
-          wait_phase(slot_full(i), (uint32_t)(fill / kSlots) & 1u, ok);
-          wait_phase(p_ready(x & 1), (uint32_t)(x >> 1) & 1u, ok);
+          wait_phase<CTAS>(slot_full(i), (uint32_t)(fill / kSlots) & 1u, ok);
+          wait_phase<CTAS>(p_ready(x & 1), (uint32_t)(x >> 1) & 1u, ok);
           ok = __all_sync(0xffffffffu, ok);
           tc::fence_after();
           if (!ok) break;
@@ -741,7 +756,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
           }
           async_proxy_fence();
           __syncwarp();
-          arrive_issuer<CTAS>(slot_full(si), lane == 0);
+          arrive_issuer_filled<CTAS>(slot_full(si), lane == 0);
           if (values) arrive_if(raw_empty(ri), lane == 0);
         }
       }
@@ -806,7 +821,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
         }
         async_proxy_fence();
         __syncwarp();
-        arrive_issuer<CTAS>(q_full, lane == 0);
+        arrive_issuer_filled<CTAS>(q_full, lane == 0);
 
         // (not 0 or infinite: those times 0 or an infinity would be NaN)
         const float decode_k = p.encode_k ? 1.f / __ldg(p.encode_k + work.head) : 1.f;

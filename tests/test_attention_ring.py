@@ -1,5 +1,7 @@
-"""Which copies of a warp's ring are under way when it gives up a wait (host code, compiled here)."""
+"""Which copies of a warp's ring are under way when it gives up a wait (host code, compiled here), and what the
+kernels' sources say about orders that a run need not show."""
 import os
+import re
 import shutil
 import subprocess
 
@@ -63,3 +65,29 @@ def test_the_kernel_of_few_tokens_waits_for_them():
     left = left[left.index("if (!ok) {"):]
     assert "await_fills(" in left[: left.index("break;")]
     assert "__syncthreads_or(!ok)" in code
+
+
+def kernel_sources():
+    return {name: open(os.path.join(SOURCE, name)).read() for name in sorted(os.listdir(SOURCE))}
+
+
+def test_arrivals_at_another_cta_name_the_cluster():
+    """An arrive at a barrier of the cluster's shared memory is not at a CTA's scope, the default."""
+    found = 0
+    for name, code in kernel_sources().items():
+        for line in re.findall(r"mbarrier\.arrive[^\"]*shared::cluster", code):
+            found += 1
+            assert ".cluster.shared::cluster" in line, (name, line)
+    assert found >= 3
+
+
+def test_the_pair_releases_what_it_wrote():
+    """The warps that fill shared memory for the pair's MMAs release it to the cluster, and who issues them acquires it
+    there."""
+    code = kernel_sources()["attention_prompt.cu"]
+    for what in ("slot_full(si)", "q_full"):
+        assert f"arrive_issuer_filled<CTAS>({what}, lane == 0)" in code
+    filled = code[code.index("void arrive_issuer_filled"):]
+    assert "fence.release.sync_restrict::shared::cta.cluster" in filled[: filled.index("\n}\n")]
+    for what in ("q_full, 0", "slot_full(i)", "s_free(x & 1)", "p_ready(x & 1)"):
+        assert f"wait_phase<CTAS>({what}" in code and f"wait_phase({what}" not in code
