@@ -25,6 +25,39 @@ __device__ __forceinline__ void ld_shared_2x128(const void* p, uint32_t (&r)[8])
                : "l"(p));
 }
 
+// The same loads, and single values, of what an earlier kernel of the stream may have written: a grid that was launched
+// before that kernel's end must not read it on the read-only path (.nc), whose memory may not change while the grid
+// is there, although it waits (pdl_wait) first.
+__device__ __forceinline__ void ld_stream_now_256(const void* p, uint32_t (&r)[8]) {
+  asm volatile(
+      "ld.global.L1::no_allocate.L2::256B.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "l"(p));
+}
+__device__ __forceinline__ uint32_t ld_now(const uint32_t* p) {
+  uint32_t v;
+  asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ int32_t ld_now(const int32_t* p) { return (int32_t)ld_now(reinterpret_cast<const uint32_t*>(p)); }
+__device__ __forceinline__ float ld_now(const float* p) { return __uint_as_float(ld_now(reinterpret_cast<const uint32_t*>(p))); }
+__device__ __forceinline__ int64_t ld_now(const int64_t* p) {
+  int64_t v;
+  asm volatile("ld.global.b64 %0, [%1];" : "=l"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 ld_now(const uint2* p) {
+  uint2 v;
+  asm volatile("ld.global.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint4 ld_now(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
 // 32-bit load of scale bytes (their 32-byte sectors are shared by
 // neighbouring rows, so L1 allocation is kept).  p must be 4-byte aligned.
 __device__ __forceinline__ uint32_t ld_scale_32(const void* p) {

@@ -143,14 +143,14 @@ template <int TILE>
 __device__ __forceinline__ Sequence sequence_of(const AttentionParams& p, int b) {
   Sequence s;
   if (p.q_starts != nullptr) {
-    const int32_t from = max(__ldg(p.q_starts + b), 0), to = min(__ldg(p.q_starts + b + 1), p.T);
+    const int32_t from = max(ld_now(p.q_starts + b), 0), to = min(ld_now(p.q_starts + b + 1), p.T);
     s.q0 = from;
     s.n = max(to - from, 0);
   } else {
     s.q0 = b * p.uniform_n;
     s.n = p.uniform_n;
   }
-  const int32_t length = __ldg(p.lengths + b);
+  const int32_t length = ld_now(p.lengths + b);
   s.beyond = (int64_t)length > p.capacity;
   s.length = s.beyond ? (int32_t)p.capacity : max(length, 0);
   const int32_t next = s.length - s.n + 1;  // tokens up to the first query's
@@ -200,7 +200,7 @@ __device__ __forceinline__ void write_columns(const AttentionParams& p, const Se
                                               const float (&o)[D / 16][NT][4], const float (&m)[NT][2],
                                               const float (&l)[NT][2]) {
   const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-  const float decode = p.encode_v ? __frcp_rn(__ldg(p.encode_v + head)) : 1.f;
+  const float decode = p.encode_v ? __frcp_rn(ld_now(p.encode_v + head)) : 1.f;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -263,7 +263,7 @@ __device__ __forceinline__ void write_four(const AttentionParams& p, const Seque
   const int i = column / p.group;
   if (i >= s.n) return;
   const int64_t row = (int64_t)(s.q0 + i) * p.Hq + (int64_t)head * p.group + (column - i * p.group);
-  float f = l == 0.f ? 0.f : (p.encode_v ? __frcp_rn(__ldg(p.encode_v + head)) : 1.f) / l;
+  float f = l == 0.f ? 0.f : (p.encode_v ? __frcp_rn(ld_now(p.encode_v + head)) : 1.f) / l;
   if (s.beyond) f = __int_as_float(0x7fc00000);
   if (p.lse != nullptr && d == 0)
     p.lse[row] = s.beyond ? f : l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
       source = kAbsent;
       if (granule < (ahead.length + kGranuleTokens - 1) / kGranuleTokens) {
         const int32_t page = granule / p.granules;
-        const int32_t id = __ldg(p.page_table + (int64_t)lb * p.max_pages + page);
+        const int32_t id = ld_now(p.page_table + (int64_t)lb * p.max_pages + page);
         source = id < 0 || id >= p.pages ? kBad
                                          : ((int64_t)id * p.Hkv + litem / lcts) * p.granules + (granule - page * p.granules);
       }
@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
     uint32_t qf[S::kPlanes][4][2][NT];
     float cs[NT][2];  // score scale of the columns 8 nt + 2 q + e (not 0 or infinite: those times 0 or
                       // an infinity would be NaN)
-    const float encode = p.encode_k ? __ldg(p.encode_k + head) : 1.f;
+    const float encode = p.encode_k ? ld_now(p.encode_k + head) : 1.f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int column = first_column + nt * 8 + g;

@@ -315,7 +315,7 @@ template <int ROWS>
 __device__ __forceinline__ RowTiles row_tiles(const AttentionParams& p, int b) {
   RowTiles r;
   if (p.q_starts != nullptr) {
-    const int32_t from = max(__ldg(p.q_starts + b), 0), to = min(__ldg(p.q_starts + b + 1), p.T);
+    const int32_t from = max(ld_now(p.q_starts + b), 0), to = min(ld_now(p.q_starts + b + 1), p.T);
     r.q0 = from;
     r.n = max(to - from, 0);
   } else {
@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
   const int cta = CTAS == 1 ? 0 : (int)tc::cluster_rank();
   const int32_t split = unit % p.splits;
   // (ragged batches: there may be more CTAs than row tiles)
-  auto exists = [&](int32_t unit) { return p.row_tiles == nullptr || unit / p.splits / p.Hkv < __ldg(p.row_tiles + p.B); };
+  auto exists = [&](int32_t unit) { return p.row_tiles == nullptr || unit / p.splits / p.Hkv < ld_now(p.row_tiles + p.B); };
   if (!exists(unit)) {
     if (p.splits > 1 && split == 0 && cta == 0 && threadIdx.x == 0)
       reinterpret_cast<PieceHead*>(p.pieces)[unit / p.splits] = {0, 0, 0, 0};
@@ -441,11 +441,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
     } else {
       for (int end = p.B; end - b > 1;) {
         const int step = (end - b + 31) / 32, at = b + lane * step;
-        const bool here = at < end && __ldg(p.row_tiles + at) <= rank;
+        const bool here = at < end && ld_now(p.row_tiles + at) <= rank;
         b += (__popc(__ballot_sync(0xffffffffu, here)) - 1) * step;
         end = min(end, b + step);
       }
-      before = __ldg(p.row_tiles + b);
+      before = ld_now(p.row_tiles + b);
     }
     if (lane == 0) {
       const RowTiles its = row_tiles<S::kRows>(p, b);
@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
       w.head = head;
       w.rows = w.n * p.group;
       w.first_row = (its.tiles - 1 - (rank - before)) * S::kRows;
-      const int32_t length = __ldg(p.lengths + b);
+      const int32_t length = ld_now(p.lengths + b);
       w.beyond = (int64_t)length > p.capacity;
       w.length = w.beyond ? (int32_t)p.capacity : max(length, 0);
       const int32_t last_row = min(w.first_row + S::kRows, w.rows) - 1;
@@ -567,7 +567,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
         auto page_of = [&](int32_t j) {
           const int32_t granule = first + j * S::kGranules;
           if (lane >= S::kCopies || j >= tiles || granule >= have) return INT32_MIN;
-          const int32_t id = __ldg(p.page_table + (int64_t)work.b * p.max_pages + granule / p.granules);
+          const int32_t id = ld_now(p.page_table + (int64_t)work.b * p.max_pages + granule / p.granules);
           return id >= 0 && id < p.pages ? id : -1;
         };
         int32_t next = page_of(0);
@@ -824,7 +824,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
         arrive_issuer_filled<CTAS>(q_full, lane == 0);
 
         // (not 0 or infinite: those times 0 or an infinity would be NaN)
-        const float decode_k = p.encode_k ? 1.f / __ldg(p.encode_k + work.head) : 1.f;
+        const float decode_k = p.encode_k ? 1.f / ld_now(p.encode_k + work.head) : 1.f;
         const float c = fminf(fmaxf(p.scale_log2 * decode_k * back, FLT_MIN), FLT_MAX);
         int32_t lo, hi;
         row_sees(p, work.length, work.n, real ? row : work.rows - 1, lo, hi);
@@ -949,7 +949,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
         tc::fence_after();
         const float2 two = unpack_f32x2(sum);
         const float l = two.x + two.y, relative_to = fmaf(m, c, -kReferenceP);  // (-inf: nothing)
-        const float decode = p.encode_v ? 1.f / __ldg(p.encode_v + work.head) : 1.f;
+        const float decode = p.encode_v ? 1.f / ld_now(p.encode_v + work.head) : 1.f;
         float f = l == 0.f ? 0.f : decode / l;
         if (work.beyond) f = __int_as_float(0x7fc00000);
         const int64_t out_row = (int64_t)(work.q0 + token) * p.Hq + (int64_t)work.head * p.group + member;
@@ -1049,7 +1049,7 @@ __global__ void __launch_bounds__(256) attention_prompt_sum_kernel(const Attenti
   const int head = (int)blockIdx.x % p.Hkv;
   const int32_t token = row / p.group, member = row - token * p.group;
   const int64_t out_row = (int64_t)(at.q0 + token) * p.Hq + (int64_t)head * p.group + member;
-  float f = l == 0.f ? 0.f : (p.encode_v ? 1.f / __ldg(p.encode_v + head) : 1.f) / l;
+  float f = l == 0.f ? 0.f : (p.encode_v ? 1.f / ld_now(p.encode_v + head) : 1.f) / l;
   if (at.beyond) f = __int_as_float(0x7fc00000);
   if (p.lse != nullptr && d == 0)
     p.lse[out_row] = at.beyond ? f : l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;

@@ -40,11 +40,14 @@ __device__ __forceinline__ void load_raw(const T* src, RawBlock<T>& b) {
   } else {
 #pragma unroll
     for (int i = 0; i < RawBlock<T>::kWords; i += 8) {
+      const uint32_t* const at = reinterpret_cast<const uint32_t*>(src) + i;
       uint32_t v[8];
-      if constexpr (ALIGN == 32)
-        ld_stream_256(reinterpret_cast<const uint32_t*>(src) + i, v);
-      else
-        ld_shared_2x128(reinterpret_cast<const uint32_t*>(src) + i, v);
+      if constexpr (ALIGN == 32) {
+        ld_stream_now_256(at, v);
+      } else {
+        const uint4 a = ld_now(reinterpret_cast<const uint4*>(at)), c = ld_now(reinterpret_cast<const uint4*>(at + 4));
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = c.x, v[5] = c.y, v[6] = c.z, v[7] = c.w;
+      }
 #pragma unroll
       for (int j = 0; j < 8; ++j) b.w[i + j] = v[j];
     }

@@ -47,7 +47,7 @@ __device__ __forceinline__ Place place_of(const CacheParams& p, int64_t place) {
   at.plane = nullptr;
   at.row = 0;
   if (at.token < p.T) {
-    const int64_t slot = __ldg(p.slots + at.token);
+    const int64_t slot = ld_now(p.slots + at.token);
     if (slot >= 0 && slot < p.capacity) {
       const int64_t page = p.capacity <= 0xffffffffll ? (int64_t)((uint32_t)slot / (uint32_t)p.page_size)
                                                       : slot / p.page_size;
@@ -76,8 +76,8 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const CacheParams p)
     for (int s = 0; s < 2; ++s)
 #pragma unroll
       for (int c = 0; c < PLANES; ++c) load_raw<T, ALIGN>(x[s] + 64 * c, raw[s][c]);
-    const float encode[2] = {p.encode_k ? __ldg(p.encode_k + at.head) : 1.f,
-                             p.encode_v ? __ldg(p.encode_v + at.head) : 1.f};
+    const float encode[2] = {p.encode_k ? ld_now(p.encode_k + at.head) : 1.f,
+                             p.encode_v ? ld_now(p.encode_v + at.head) : 1.f};
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       uint8_t* const to = at.plane + s * p.planes * kPlaneBytes + at.row * 32 + at.block * 8;
@@ -121,13 +121,13 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const CacheParams p) 
       }
     }
     if (p.k != nullptr) {
-      const float decode = p.encode_k ? __frcp_rn(__ldg(p.encode_k + at.head)) : 1.f;
+      const float decode = p.encode_k ? __frcp_rn(ld_now(p.encode_k + at.head)) : 1.f;
       T* const to = static_cast<T*>(p.k) + at.token * p.k_token + at.head * p.k_head + at.element;
 #pragma unroll
       for (int c = 0; c < PLANES; ++c) dequantize_block<T, ALIGN>(q[0][c], code[0][c], decode, to + 64 * c);
     }
     if (p.v != nullptr) {
-      const float decode = p.encode_v ? __frcp_rn(__ldg(p.encode_v + at.head)) : 1.f;
+      const float decode = p.encode_v ? __frcp_rn(ld_now(p.encode_v + at.head)) : 1.f;
       T* const to = static_cast<T*>(p.v) + at.token * p.v_token + at.head * p.v_head + at.element;
 #pragma unroll
       for (int c = 0; c < PLANES; ++c) dequantize_block<T, ALIGN>(q[1][c], code[1][c], decode, to + 64 * c);

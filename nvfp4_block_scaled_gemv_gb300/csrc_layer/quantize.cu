@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const DequantizePa
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (kb0 + 32 * u < p.blocks) {
-        q[u] = __ldg(q_at + 32 * u);
+        q[u] = ld_now(q_at + 32 * u);
         code[u] = sf_at[kSfStep * u];
       }
     T* const x = static_cast<T*>(p.x) + row * p.x_stride + (int64_t)kb0 * 16;

@@ -105,8 +105,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
   const int tokens = min(p.tokens_per_cta, p.T - t0);
   for (int i = threadIdx.x; i < tokens * p.pairs; i += kThreads) {
     const int t = i / p.pairs, pair = i - t * p.pairs;
-    const uint64_t f = (uint64_t)__ldg(p.table + pair);
-    const int64_t pos = __ldg(p.positions + t0 + t);
+    const uint64_t f = (uint64_t)ld_now(p.table + pair);
+    const int64_t pos = ld_now(p.positions + t0 + t);
     float2 cs = turn((int64_t)((uint64_t)pos * f));
     cs.x *= p.factor;
     cs.y *= p.inverse ? -p.factor : p.factor;

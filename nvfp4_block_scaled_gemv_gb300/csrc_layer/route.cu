@@ -71,13 +71,13 @@ __device__ __forceinline__ void load_logits(const RouteParams& p, int64_t t, int
     for (int i = 0; i < kBytes; i += kVec) {
       uint32_t w[4];
       if constexpr (kVec == 16) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(src + i));
+        const uint4 v = ld_now(reinterpret_cast<const uint4*>(src + i));
         w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
       } else if constexpr (kVec == 8) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(src + i));
+        const uint2 v = ld_now(reinterpret_cast<const uint2*>(src + i));
         w[0] = v.x; w[1] = v.y;
       } else if constexpr (kVec == 4) {
-        w[0] = __ldg(reinterpret_cast<const uint32_t*>(src + i));
+        w[0] = ld_now(reinterpret_cast<const uint32_t*>(src + i));
       }
 #pragma unroll
       for (int j = 0; j < kVec / kSize; ++j) {

@@ -91,3 +91,11 @@ def test_the_pair_releases_what_it_wrote():
     assert "fence.release.sync_restrict::shared::cta.cluster" in filled[: filled.index("\n}\n")]
     for what in ("q_full, 0", "slot_full(i)", "s_free(x & 1)", "p_ready(x & 1)"):
         assert f"wait_phase<CTAS>({what}" in code and f"wait_phase({what}" not in code
+
+
+def test_no_read_only_loads():
+    """Kernels of the layer may be launched before those in front of them end; what they read may have been written by
+    one of these, and does not go by the read-only path."""
+    for name, code in kernel_sources().items():
+        for word in ("__ldg(", "global.nc", "ld_stream_256(", "ld_shared_2x128(", "ld_scale_32("):
+            assert word not in code, (name, word)
