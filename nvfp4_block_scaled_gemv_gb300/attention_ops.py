@@ -18,6 +18,7 @@ from . import layer as _layer
 from .layer import _dtype_code, _empty, _enqueue, _load, _ptr
 
 GRANULE_TOKENS = 16
+MOST = (1 << 31) - 1  # the largest number of an option; no sequence has as many tokens
 PLANE_BYTES = 576  # 16 tokens x 64 elements: 32 bytes of codes and 4 of scales a token
 
 
@@ -55,6 +56,13 @@ def declare(lib: ctypes.CDLL) -> None:
                                  P], I)):
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = result
+
+
+def _limit(name: str, value: int) -> int:
+    """A limit on tokens, for a field of 32 bits (which would take others modulo 2^32)."""
+    if value < 0:
+        raise ValueError(f"{name} is {value}, expected 0 or more")
+    return value if value < MOST else MOST
 
 
 # ---------------------------------------------------------------------------
@@ -106,7 +114,8 @@ def nvfp4_attention(q: int, dtype: int, T: int, Hq: int, Hkv: int, D: int, cache
                     q_starts: int = 0, encode_k: int = 0, encode_v: int = 0, lse: int = 0, q_token_stride: int = 0,
                     q_head_stride: int = 0, stream: int = 0) -> None:
     """Enqueue the attention of q [T][Hq][D] on the cache."""
-    opt = _AttentionOptions(scale, 1 if causal else 0, window, max_q, q_starts or None, encode_k or None,
+    opt = _AttentionOptions(scale, 1 if causal else 0, _limit("window", window), _limit("max_q", max_q),
+                            q_starts or None, encode_k or None,
                             encode_v or None, lse or None, q_token_stride, q_head_stride)
     _check(library().nvfp4_attention(q, dtype, T, Hq, Hkv, D, cache, pages, page_size, page_table, max_pages, lengths,
                                      B, ctypes.byref(opt), out, workspace, workspace_bytes, stream),
@@ -350,7 +359,7 @@ def attention(q, cache, page_table, lengths, q_starts=None, max_q: int = 0, scal
             raise ValueError(f"q has {T} tokens for {B} sequences")
         starts, max_q = None, 0
     else:
-        starts, max_q = _ptr(q_starts, "q_starts", i32, B + 1, dev), min(max_q, T)
+        starts, max_q = _ptr(q_starts, "q_starts", i32, B + 1, dev), min(_limit("max_q", max_q), T)
     if token % 8 or head % 8 or q.data_ptr() % 16:
         raise ValueError("q must have 16-byte aligned heads")
     if out is None:
@@ -374,7 +383,7 @@ def attention(q, cache, page_table, lengths, q_starts=None, max_q: int = 0, scal
         if size < need:
             raise ValueError(f"workspace has {size} bytes, expected {need}")
         _ptr(workspace, "workspace", torch.uint8, size, dev)
-    opt = _AttentionOptions(scale, 1 if causal else 0, window, max_q, starts, _encode(encode_k, "encode_k", Hkv, dev),
+    opt = _AttentionOptions(scale, 1 if causal else 0, _limit("window", window), max_q, starts, _encode(encode_k, "encode_k", Hkv, dev),
                             _encode(encode_v, "encode_v", Hkv, dev), None if lse is None else lse.data_ptr(), token,
                             head)
     _enqueue("nvfp4_attention", dev, stream, q.data_ptr(), code, T, Hq, Hkv, D, cp, pages, page, tp, max_pages, lp, B,
