@@ -186,11 +186,14 @@ def rope_table(rotary_dim: int = 0, base: float = 10000.0, scaling: str = "none"
 
 
 def _heads(x, name, device=None):
-    """[T, H, D] with contiguous heads: T, H, D, token stride, head stride."""
+    """[T, H, D] with contiguous heads: T, H, D, token stride, head stride (dense ones where nothing steps by them)."""
     shape, stride = x.shape, x.stride()
     if len(shape) == 3 and stride[2] == 1 and stride[1] >= shape[2] and \
             stride[0] >= (shape[1] - 1) * stride[1] + shape[2] and (device is None or x.device == device):
-        return (*shape, stride[0], stride[1])  # (the usual case in few steps)
+        # (the usual case in few steps)
+        T, H, D = shape
+        head = stride[1] if H > 1 else D
+        return T, H, D, stride[0] if T > 1 else H * head, head
     if x.dim() != 3:
         raise ValueError(f"{name} must be [T, H, D]")
     if device is not None and x.device != device:

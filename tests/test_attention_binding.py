@@ -71,3 +71,49 @@ def test_negative_limits_are_refused(calls, kw):
     with pytest.raises(ValueError):
         nv.nvfp4_attention(256, 1, 4, 4, 2, 64, 256, 2, 16, 256, 2, 256, 2, 256, 256, 1 << 20, q_starts=256, **kw)
     assert not calls
+
+
+def one_of(buffer, T, H, D, at=0):
+    """A view [T, H, D] whose rows lie at odd distances."""
+    return buffer[:T, at: at + H * D].unflatten(1, (H, D))
+
+
+def test_strides_that_nothing_steps_by(calls):
+    """A single token's distance to the next, and a single head's, may be any: the call is not refused for it, and does
+    not take a slower path."""
+    _, cache, table, lengths = problem(B=1)
+    row = torch.zeros(1, 4 * 64 + 3, dtype=torch.bfloat16)
+    out = nv.attention(one_of(row, 1, 4, 64), cache, table, lengths)
+    opt = options(calls[0][1], ao._AttentionOptions)
+    assert out.shape == (1, 4, 64) and opt.q_token_stride % 8 == 0 and opt.q_head_stride == 64
+    cache = nv.kv_cache(2, 1, 64, 16, device="cpu")
+    flat = torch.zeros(3 * 72 + 8, dtype=torch.bfloat16)
+    for head in (65, 1, 67):
+        q = flat.as_strided((3, 1, 64), (72, head, 1))
+        calls.clear()
+        nv.attention(q, cache, torch.zeros(3, 2, dtype=torch.int32), torch.zeros(3, dtype=torch.int32))
+        opt = options(calls[0][1], ao._AttentionOptions)
+        assert opt.q_token_stride == 72 and opt.q_head_stride % 8 == 0
+        calls.clear()
+        nv.kv_write(q, q, cache, torch.zeros(3, dtype=torch.int64))
+        rows = options(calls[0][1], ao._KvRows)
+        assert rows.k_token_stride == rows.v_token_stride == 72 and rows.k_head_stride % 8 == rows.v_head_stride % 8 == 0
+        calls.clear()
+        table64 = nv.rope_table(64, device="cpu")
+        nv.rope(q, torch.zeros(3, dtype=torch.int32), table64)
+        opt = options(calls[0][1], ao._RopeOptions)
+        assert opt.x_token_stride == 72 and opt.x_head_stride % 8 == 0
+    # a stride that is stepped by is still looked at
+    wide = torch.zeros(2, 4 * 64 + 3, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="aligned"):
+        nv.attention(one_of(wide, 2, 4, 64), nv.kv_cache(2, 2, 64, 16, device="cpu"), torch.zeros(2, 2, dtype=torch.int32),
+                     torch.zeros(2, dtype=torch.int32))
+
+
+def test_strides_of_rows_in_place(calls):
+    """A single token turned in place: both sides have the same strides."""
+    row = torch.zeros(1, 3 * 64 + 5)
+    x = one_of(row, 1, 3, 64)
+    assert nv.rope(x, torch.zeros(1, dtype=torch.int32), nv.rope_table(64, device="cpu"), out=x) is x
+    opt = options(calls[0][1], ao._RopeOptions)
+    assert (opt.x_token_stride, opt.x_head_stride) == (opt.y_token_stride, opt.y_head_stride)
