@@ -19,6 +19,7 @@ from .layer import _dtype_code, _empty, _enqueue, _load, _ptr
 
 GRANULE_TOKENS = 16
 MOST = (1 << 31) - 1  # the largest number of an option; no sequence has as many tokens
+LEAST_SCALE = 2.0 ** -149  # fp32's smallest number; what rounds to 0 would be taken for the default
 PLANE_BYTES = 576  # 16 tokens x 64 elements: 32 bytes of codes and 4 of scales a token
 
 
@@ -114,7 +115,8 @@ def nvfp4_attention(q: int, dtype: int, T: int, Hq: int, Hkv: int, D: int, cache
                     q_starts: int = 0, encode_k: int = 0, encode_v: int = 0, lse: int = 0, q_token_stride: int = 0,
                     q_head_stride: int = 0, stream: int = 0) -> None:
     """Enqueue the attention of q [T][Hq][D] on the cache."""
-    opt = _AttentionOptions(scale, 1 if causal else 0, _limit("window", window), _limit("max_q", max_q),
+    opt = _AttentionOptions(LEAST_SCALE if 0 < scale < LEAST_SCALE else scale, 1 if causal else 0,
+                            _limit("window", window), _limit("max_q", max_q),
                             q_starts or None, encode_k or None,
                             encode_v or None, lse or None, q_token_stride, q_head_stride)
     _check(library().nvfp4_attention(q, dtype, T, Hq, Hkv, D, cache, pages, page_size, page_table, max_pages, lengths,
@@ -386,6 +388,8 @@ def attention(q, cache, page_table, lengths, q_starts=None, max_q: int = 0, scal
         if size < need:
             raise ValueError(f"workspace has {size} bytes, expected {need}")
         _ptr(workspace, "workspace", torch.uint8, size, dev)
+    if 0 < scale < LEAST_SCALE:
+        scale = LEAST_SCALE
     opt = _AttentionOptions(scale, 1 if causal else 0, _limit("window", window), max_q, starts, _encode(encode_k, "encode_k", Hkv, dev),
                             _encode(encode_v, "encode_v", Hkv, dev), None if lse is None else lse.data_ptr(), token,
                             head)

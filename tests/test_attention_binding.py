@@ -117,3 +117,10 @@ def test_strides_of_rows_in_place(calls):
     assert nv.rope(x, torch.zeros(1, dtype=torch.int32), nv.rope_table(64, device="cpu"), out=x) is x
     opt = options(calls[0][1], ao._RopeOptions)
     assert (opt.x_token_stride, opt.x_head_stride) == (opt.y_token_stride, opt.y_head_stride)
+
+
+@pytest.mark.parametrize("scale,given", [(0.0, 0.0), (0.125, 0.125), (2.0 ** -140, 2.0 ** -140), (1e-60, 2.0 ** -149)])
+def test_scale_is_not_taken_for_the_default(calls, scale, given):
+    """0 means 1 / sqrt(D); a scale too small for fp32 is the smallest there is, with which no scores differ either."""
+    nv.attention(*problem(), scale=scale)
+    assert options(calls[0][1], ao._AttentionOptions).scale == given
