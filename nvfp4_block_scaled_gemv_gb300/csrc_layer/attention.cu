@@ -35,6 +35,7 @@
 #include <cuda_fp16.h>
 
 #include "attention.h"
+#include "attention_rows.cuh"
 #include "layer.h"
 #include "ptx.cuh"
 #include "ring.h"
@@ -96,11 +97,6 @@ __device__ __forceinline__ uint32_t mul_h2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-__device__ __forceinline__ float exp2_fast(float x) {
-  float d;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(x));
-  return d;
-}
 // Loads of what a bulk copy left in shared memory: through pointers, so that constant distances go
 // into the instruction (the waits on the barriers keep them in their place).
 __device__ __forceinline__ uint32_t load_32(const uint8_t* p) { return *reinterpret_cast<const uint32_t*>(p); }
@@ -120,13 +116,6 @@ __device__ __forceinline__ void bulk_load_if(uint32_t dst, const void* src, uint
       "l"(src), "r"(bytes), "r"(bar), "r"((uint32_t)who)
       : "memory");
 }
-__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
-// Whether a row's reference m is far from 0 (-inf: there is none yet).
-__device__ __forceinline__ bool is_far(float m, float c) { return fabsf(m * c) > kFarReference && m != -INFINITY; }
 // Bits of a where mask, bits of b elsewhere.
 __device__ __forceinline__ uint32_t merge_bits(uint32_t a, uint32_t b, uint32_t mask) {
   return (a & mask) | (b & ~mask);
@@ -142,19 +131,12 @@ struct Sequence {
 template <int TILE>
 __device__ __forceinline__ Sequence sequence_of(const AttentionParams& p, int b) {
   Sequence s;
-  if (p.q_starts != nullptr) {
-    const int32_t from = max(ld_now(p.q_starts + b), 0), to = min(ld_now(p.q_starts + b + 1), p.T);
-    s.q0 = from;
-    s.n = max(to - from, 0);
-  } else {
-    s.q0 = b * p.uniform_n;
-    s.n = p.uniform_n;
-  }
-  const int32_t length = ld_now(p.lengths + b);
-  s.beyond = (int64_t)length > p.capacity;
-  s.length = s.beyond ? (int32_t)p.capacity : max(length, 0);
-  const int32_t next = s.length - s.n + 1;  // tokens up to the first query's
-  const int32_t lo = p.window > 0 && next > p.window ? next - p.window : 0;
+  const QueryRows rows = query_rows(p, b);
+  s.q0 = rows.q0;
+  s.n = rows.n;
+  s.length = cached_tokens(p, b, s.beyond);
+  int32_t lo, hi;
+  token_sees(p, s.length, s.n, 0, lo, hi);
   s.first_tile = lo / TILE;
   // (one tile at least, so that somebody writes the result of an empty row)
   s.tiles = s.n == 0 || s.n * p.group > p.few_columns ? 0 : max((s.length + TILE - 1) / TILE - s.first_tile, 1);
@@ -184,15 +166,8 @@ __device__ __forceinline__ int token_of(int row) { return row ^ (row >> 2 & 1); 
 // The range of tokens that a column sees.
 __device__ __forceinline__ void seen_by(const AttentionParams& p, const Sequence& s, int column, int32_t& lo, int32_t& hi) {
   const int32_t i = column / p.group;  // query token
-  lo = 0;
-  hi = s.length;
-  if (i >= s.n) {
-    hi = 0;
-  } else if (p.causal) {
-    const int32_t position = s.length - s.n + i;
-    hi = position + 1;  // (0 or less: an empty row)
-    if (p.window > 0 && hi > p.window) lo = hi - p.window;
-  }
+  lo = hi = 0;
+  if (i < s.n) token_sees(p, s.length, s.n, i, lo, hi);
 }
 
 template <int D, int NT>
@@ -504,8 +479,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
 
     float o[D / 16][NT][4];
     float m[NT][2], l[NT][2];
-    float shift[NT][2];  // 7 - m in base 2, 7 if m is far from 0, 0 while a row is empty (all its p are 0)
-    bool far = false;    // m of some column is (the same in all lanes)
+    // m, or 0 while a row is empty (all its p are 0).  Scores are taken from it before they are scaled: far from 0
+    // (scores of 2^28) their product's rounding would be more than the exponential holds.
+    float from_m[NT][2];
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -515,7 +491,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) m[nt][e] = -INFINITY, l[nt][e] = shift[nt][e] = 0.f;
+      for (int e = 0; e < 2; ++e) m[nt][e] = -INFINITY, l[nt][e] = from_m[nt][e] = 0.f;
 
 #pragma unroll 1
     for (; tile < to; ++tile) {
@@ -611,7 +587,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
             if (top > m[nt][e]) {  // (the same in all lanes of a column)
               const float keep = exp2_fast((m[nt][e] - top) * cs[nt][e]);
               m[nt][e] = top;
-              shift[nt][e] = is_far(top, cs[nt][e]) ? kReferenceP : fmaf(-top, cs[nt][e], kReferenceP);
+              from_m[nt][e] = top;
               l[nt][e] *= keep;
 #pragma unroll
               for (int i = 0; i < D / 16; ++i) {
@@ -619,20 +595,6 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
                 o[i][nt][2 + e] *= keep;
               }
             }
-          }
-        far = false;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) far |= is_far(m[nt][0], cs[nt][0]) || is_far(m[nt][1], cs[nt][1]);
-        far = __any_sync(0xffffffffu, far);
-      }
-      if (far) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float less = is_far(m[nt][e], cs[nt][e]) ? m[nt][e] : 0.f;
-#pragma unroll
-            for (int i = 0; i < kGr; ++i) s[i][nt][e] -= less, s[i][nt][2 + e] -= less;
           }
       }
       // P, and its transposition to the second product's operand
@@ -643,8 +605,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
         for (int i = 0; i < kGr; ++i)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const float p0 = exp2_fast(fmaf(s[i][nt][2 * r], cs[nt][0], shift[nt][0]));
-            const float p1 = exp2_fast(fmaf(s[i][nt][2 * r + 1], cs[nt][1], shift[nt][1]));
+            const float p0 = exp2_fast(fmaf(s[i][nt][2 * r] - from_m[nt][0], cs[nt][0], kReferenceP));
+            const float p1 = exp2_fast(fmaf(s[i][nt][2 * r + 1] - from_m[nt][1], cs[nt][1], kReferenceP));
             l[nt][0] += p0;
             l[nt][1] += p1;
             pf[i][nt][r] = transpose_8x8(pack_h2(p0, p1));

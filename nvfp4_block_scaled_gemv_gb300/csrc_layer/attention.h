@@ -75,14 +75,6 @@ struct AttentionParams {
   int32_t units;              // prompts: row tiles x heads x parts, at most
   int4* pieces;               // [CTAs][2]: {last CTA or -1, head, first column, beyond}, {n, q0} of the item that goes on in the next
 };
-// Scores whose row's reference lies further from 0 than this (in base 2) are taken from the reference before they
-// are scaled: score * c - round(reference * c), one fused operation elsewhere, is off by half a step of that product,
-// 2^-4 here, 1 at 2^24, and from 2^28 more than fp16 (and then the exponential) holds.
-constexpr float kFarReference = 1048576.f;
-// p of a row's reference in base 2.  Scores pass the reference by 8 at most, so that fp16 holds every p (2^15 and the
-// 2^-4 above), and below its normal numbers are only p's under 2^-21 of the reference's, which are off by 2^-32 of that.
-// (With the reference at 1 these were 2^-14 and 2^-25: 131071 tokens of e^-18 beside one lost a tenth of their sum.)
-constexpr float kReferenceP = 7.f;
 constexpr int kAttentionCtas = 152;  // most CTAs of a launch, which the workspace is made for
 // Columns (query token and head of a group, together) that one pass over the cache takes
 // for a head size and the most columns of a sequence.

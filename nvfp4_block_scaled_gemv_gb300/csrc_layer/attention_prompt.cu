@@ -55,6 +55,7 @@
 #include <cuda_fp16.h>
 
 #include "attention.h"
+#include "attention_rows.cuh"
 #include "gemm_common.cuh"
 #include "layer.h"
 #include "ptx.cuh"
@@ -248,21 +249,16 @@ __device__ __forceinline__ void registers_down() {
 }
 __device__ __forceinline__ void async_proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-__device__ __forceinline__ float ex2(float x) {
-  float d;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(x));
-  return d;
-}
-// Whether a row's reference m is far from 0 (-inf: there is none yet).
+// Scores whose row's reference lies further from 0 than this (in base 2) are taken from the reference before they
+// are scaled: score * c - round(reference * c), one fused operation elsewhere, is off by half a step of that product,
+// 2^-4 here, 1 at 2^24, and from 2^28 more than fp16 (and then the exponential) holds.  (Subtracting first everywhere:
+// 1188 us in place of 1172, 4 prompts of up to 4096.)
+constexpr float kFarReference = 1048576.f;
+// Whether a row's reference m is that far from 0 (-inf: there is none yet).
 __device__ __forceinline__ bool is_far(float m, float c) { return fabsf(m * c) > kFarReference && m != -INFINITY; }
-__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
 
 __device__ __forceinline__ uint32_t rounded_two(bool bf16, float a, float b) {
-  if (!bf16) return half2_of(a, b);
+  if (!bf16) return pack_h2(a, b);
   const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
@@ -284,14 +280,7 @@ struct PieceHead {
 
 __device__ __forceinline__ void row_sees(const AttentionParams& p, int32_t length, int32_t n, int32_t row, int32_t& lo,
                                          int32_t& hi) {
-  const int32_t i = row / p.group;
-  lo = 0;
-  hi = length;
-  if (p.causal) {
-    const int32_t position = length - n + i;
-    hi = position + 1;
-    if (p.window > 0 && hi > p.window) lo = hi - p.window;
-  }
+  token_sees(p, length, n, row / p.group, lo, hi);
 }
 
 // Scores of the tokens t to t + 31 outside [lo, hi) do not count.
@@ -308,23 +297,14 @@ __device__ __forceinline__ bool tile_whole(const Work& w, int32_t t0) {
 
 // Query tokens of a sequence and its first row of q, and the tiles of rows it has here (none,
 // if the other kernel takes it).
-struct RowTiles {
-  int32_t q0, n, tiles;
+struct RowTiles : QueryRows {
+  int32_t tiles;
 };
 template <int ROWS>
 __device__ __forceinline__ RowTiles row_tiles(const AttentionParams& p, int b) {
-  RowTiles r;
-  if (p.q_starts != nullptr) {
-    const int32_t from = max(ld_now(p.q_starts + b), 0), to = min(ld_now(p.q_starts + b + 1), p.T);
-    r.q0 = from;
-    r.n = max(to - from, 0);
-  } else {
-    r.q0 = b * p.uniform_n;
-    r.n = p.uniform_n;
-  }
-  const int32_t rows = r.n * p.group;
-  r.tiles = rows > p.few_columns ? (rows - 1) / ROWS + 1 : 0;
-  return r;
+  const QueryRows its = query_rows(p, b);
+  const int32_t rows = its.n * p.group;
+  return {its, rows > p.few_columns ? (rows - 1) / ROWS + 1 : 0};
 }
 
 // Ragged batches: row tiles before each sequence, and of all behind them, in one CTA.  (The CTAs
@@ -456,9 +436,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
       w.head = head;
       w.rows = w.n * p.group;
       w.first_row = (its.tiles - 1 - (rank - before)) * S::kRows;
-      const int32_t length = ld_now(p.lengths + b);
-      w.beyond = (int64_t)length > p.capacity;
-      w.length = w.beyond ? (int32_t)p.capacity : max(length, 0);
+      w.length = cached_tokens(p, b, w.beyond);
       const int32_t last_row = min(w.first_row + S::kRows, w.rows) - 1;
       int32_t l0, h0, l1, h1;
       row_sees(p, w.length, w.n, w.first_row, l0, h0);
@@ -810,7 +788,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
               const float by = __uint_as_float((uint32_t)(e + 127) << 23);
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                words[k][i] = half2_of(__uint_as_float(words[k][i] << 16) * by, __uint_as_float(words[k][i] & 0xffff0000u) * by);
+                words[k][i] = pack_h2(__uint_as_float(words[k][i] << 16) * by, __uint_as_float(words[k][i] & 0xffff0000u) * by);
               asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(query_at(k0 + k)), "r"(words[k][0]),
                            "r"(words[k][1]), "r"(words[k][2]), "r"(words[k][3])
                            : "memory");
@@ -876,7 +854,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
           // (from -inf any score passes)
           const bool up = (now - m) * c > 8.f || (m == -INFINITY && now > m);
           if (__any_sync(0xffffffffu, up)) {
-            const float f = up ? (m == -INFINITY ? 0.f : ex2((m - now) * c)) : 1.f;
+            const float f = up ? (m == -INFINITY ? 0.f : exp2_fast((m - now) * c)) : 1.f;
             if (up) m = now;
             const float2 two = unpack_f32x2(sum);
             sum = pack_f32x2(two.x * f, two.y * f);
@@ -918,11 +896,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
             for (int i = 0; i < 32; i += 4) {
               float2 a = unpack_f32x2(fma2(pack_f32x2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), c2, b2));
               float2 b = unpack_f32x2(fma2(pack_f32x2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])), c2, b2));
-              a.x = ex2(a.x), a.y = ex2(a.y), b.x = ex2(b.x), b.y = ex2(b.y);
+              a.x = exp2_fast(a.x), a.y = exp2_fast(a.y), b.x = exp2_fast(b.x), b.y = exp2_fast(b.y);
               sum = fma2(pack_f32x2(a.x, a.y), one2, sum);
               other = fma2(pack_f32x2(b.x, b.y), one2, other);
-              packed[i / 2] = half2_of(a.x, a.y);
-              packed[i / 2 + 1] = half2_of(b.x, b.y);
+              packed[i / 2] = pack_h2(a.x, a.y);
+              packed[i / 2 + 1] = pack_h2(b.x, b.y);
             }
             tmem_st_16(p_at + 16 * h, packed);
           }
@@ -1039,7 +1017,7 @@ __global__ void __launch_bounds__(256) attention_prompt_sum_kernel(const Attenti
     const float2 ml = *reinterpret_cast<const float2*>(piece + S::kRows * D + 2 * r);
     const float4 v = *reinterpret_cast<const float4*>(piece + (int64_t)r * D + d);
     if (ml.y == 0.f) continue;  // (nothing that the row sees; a part without tiles has no results at all)
-    const float f = ml.x == m ? 1.f : ex2(ml.x - m);
+    const float f = ml.x == m ? 1.f : exp2_fast(ml.x - m);
     o.x = fmaf(v.x, f, o.x);
     o.y = fmaf(v.y, f, o.y);
     o.z = fmaf(v.z, f, o.z);
