@@ -90,8 +90,8 @@ struct Prompt {
   static constexpr int kKeyCopies = CTAS == 1 ? 0 : kKeyGranules, kCopies = kKeyCopies + kGranules;
   static constexpr uint32_t kCopy = CTAS == 1 ? 2 * kSide : kSide, kRaw = kCopies * kCopy;
   static constexpr uint32_t kRawValues = CTAS == 1 ? kSide : kKeyCopies * kSide;  // where V's begin
-  static constexpr int kSlots = D == 64 ? 6 : D == 128 && CTAS == 2 ? 5 : 3;
-  static constexpr int kRaws = D == 64 ? 4 : D == 128 && CTAS == 2 ? 3 : 2;
+  static constexpr int kSlots = D == 64 ? 6 : 3;
+  static constexpr int kRaws = D == 64 ? 4 : 2;
   // Tensor memory: S, two buffers; P of its own where there is room, otherwise over S; O at the end.
   static constexpr bool kOwnP = NQ == 2 && 3 * BN <= 512 - NQ * D;
   static constexpr uint32_t kS = BN > 128 || kOwnP ? BN : 128, kP = 2 * BN, kO = 512 - NQ * D;
@@ -1046,7 +1046,10 @@ int64_t most_row_tiles(const AttentionParams& p, int rows_per_tile) {
 int64_t round_up(int64_t bytes) { return (bytes + 255) / 256 * 256; }
 
 // Parts that the tokens of a row tile are cut into: as many as bring the row tiles and heads to the
-// SMs, where these are fewer, but at most twice the SMs in all, and 4 tiles of tokens a part.
+// SMs, where these are fewer, but at most twice the SMs in all, and 4 tiles a part of the tokens that the page table
+// has room for.  The lengths are on the device, and a window is not looked at: where the table is wider than the
+// sequences, or a window narrower, parts are shorter than that, and some have no tile (512 tokens of 8 heads on one, in a
+// table for 131072: 8 parts).
 int prompt_splits(int64_t items, int64_t most_tokens, int tile, int ctas) {
   const int64_t places = kAttentionCtas / ctas;
   if (items >= places) return 1;
