@@ -20,10 +20,10 @@ constexpr int64_t kMaxCache = int64_t(1) << 48;  // elements of K, or of V
 constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 256;  // of a sequence: ends of tiles stay in 32 bits
 constexpr int64_t kMaxPairs = 512;
 // Sequences of more columns (query tokens x heads of a group) go to the kernel for prompts, which
-// takes 128 or 256 rows at once; up to here passes of 16 (heads of 64: 32) columns over the cache are
-// as fast or faster.  16 sequences of 8192 tokens, us, passes against prompts: heads of 128: 36
-// columns 124 and 112, 64 columns 160 and 113 (one sequence: 21 and 30, 24 and 30); heads of 64: 64
-// columns 84 and 93; heads of 256: 32 columns 94 and 161, 64 columns 176 and 164.
+// takes 128 or 256 rows at once; fewer take passes of 16 (heads of 64: 32) columns over the cache.  One limit for a
+// head size, between where few sequences and where many of them change over.  16 sequences of 8192 tokens, us, passes
+// against prompts: heads of 128: 36 columns 124 and 112, 64 columns 160 and 113 (one sequence: 21 and 30, 24 and
+// 30); heads of 64: 64 columns 84 and 93; heads of 256: 32 columns 94 and 161, 64 columns 176 and 164.
 int64_t few_columns_for(int64_t D) { return D == 64 ? 64 : 48; }
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
