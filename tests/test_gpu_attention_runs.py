@@ -212,3 +212,48 @@ def test_attention_of_a_long_sequence_finds_single_tokens(n, D):
     q = q.to(a64.DEV)
     out, lse, run, _ = long_call(q, pool, table, length)
     a64.check(pool, q, table, [length], [n], out, lse, run)
+
+
+@pytest.mark.parametrize("n", [1, 3, 70])
+def test_attention_of_one_sequence_in_a_row_of_odd_length(n):
+    """Views of a wider row: what a single token's row is followed by does not matter, nor a window beyond 32 bits."""
+    import attention64 as a64
+
+    pool = pool_of(128, 2, 32, 48, False)
+    table = np.arange(40, dtype=np.int32)[None]
+    wide = 8 * 128 + (3 if n == 1 else 8)
+    row = torch.randn(n, wide, device=a64.DEV, generator=torch.Generator(a64.DEV).manual_seed(4)).bfloat16()
+    q = row[:, : 8 * 128].unflatten(1, (8, 128))
+    call = dict(pool.call(), page_table=a64.gpu(table), lengths=a64.gpu(np.array([1200], dtype=np.int32)))
+    out, lse = nv.attention(q, **call, return_lse=True)
+    a64.check(pool, q, table, [1200], [n], out, lse, 1200)
+    assert torch.equal(out, nv.attention(q.contiguous(), **call))
+    for window in (1 << 31, (1 << 32) + 5, 1 << 50):
+        assert torch.equal(out, nv.attention(q, **call, window=window))
+    assert not torch.equal(out, nv.attention(q, **call, window=5))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_of_prompts_far_in_a_large_cache(D):
+    """Pages beyond 2^32 bytes of the cache, and the places between them."""
+    import attention64 as a64
+
+    Hkv, page, pages = 2, 32, 48
+    pool = pool_of(D, Hkv, page, pages, False)
+    each = pool.cache[0].numel()
+    far = (1 << 32) // each + 7
+    if torch.cuda.mem_get_info()[0] < (far + pages) * each + (2 << 30):
+        pytest.skip("needs 7 GB of free memory")
+    big = torch.empty((far + pages, *pool.cache.shape[1:]), dtype=torch.uint8, device=a64.DEV)
+    big[far:] = pool.cache
+    rng = np.random.default_rng(D)
+    lens, counts = np.array([1500, 300, 33]), np.array([90, 150, 1])
+    table = tables(rng, lens, page, pages)
+    q = torch.randn(int(counts.sum()), 4, D, device=a64.DEV, generator=torch.Generator(a64.DEV).manual_seed(5)).half()
+    starts = a64.gpu(np.concatenate(([0], np.cumsum(counts))).astype(np.int32))
+    call = dict(lengths=a64.gpu(lens.astype(np.int32)), q_starts=starts, max_q=150, encode_k=pool.e[0], encode_v=pool.e[1])
+    want, lse = nv.attention(q, pool.cache, a64.gpu(table), **call, return_lse=True)
+    a64.check(pool, q, table, lens, counts, want, lse, [1500] * 3)
+    assert torch.equal(want, nv.attention(q, big, a64.gpu(table) + far, **call))
+    del big
+    torch.cuda.empty_cache()
