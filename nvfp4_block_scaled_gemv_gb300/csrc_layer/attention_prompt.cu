@@ -861,6 +861,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
             far = __any_sync(0xffffffffu, is_far(m, c));
             if (j > 0) {
               if (!S::kOwnP) {
+                if (NQ == 1 && j > 1) wait_phase(o_done(u), (uint32_t)(j - 2) & 1u, ok);  // (see the end of the tiles)
                 wait_phase(o_done(u), (uint32_t)(j - 1) & 1u, ok);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
@@ -921,6 +922,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
           __syncwarp();
           arrive_issuer<CTAS>(p_ready(x & 1), lane == 0);
         }
+        // One half of rows: the scores of the last tile are there two products before the last one ends, and a warp that
+        // is ahead of others may come here before the last but one has: a phase is waited for only when the one before
+        // it has completed (they have the same parity as those two on).
+        if (NQ == 1 && tiles > 1) wait_phase(o_done(u), (uint32_t)(tiles - 2) & 1u, ok);
         wait_phase(o_done(u), (uint32_t)(tiles - 1) & 1u, ok);
         ok = __all_sync(0xffffffffu, ok);
         __syncwarp();

@@ -257,3 +257,29 @@ def test_attention_of_prompts_far_in_a_large_cache(D):
     assert torch.equal(want, nv.attention(q, big, a64.gpu(table) + far, **call))
     del big
     torch.cuda.empty_cache()
+
+
+# heads of 256: up to 128 rows of a sequence and key head (one SM a row tile), and more (a pair); in parts and whole
+WIDE = [(2, 1, 66, [1131, 1162, 1345, 535, 334]), (2, 4, 17, [779, 545, 1534, 1597, 1566]), (8, 4, 17, [136, 512]),
+        (3, 8, 9, [1149, 1830, 1438, 912, 131]), (1, 8, 66, [1079, 1771, 1749, 910, 459]), (2, 4, 130, [1500, 700]),
+        (1, 1, 300, [1601]), (8, 4, 300, [1700, 300]), (8, 2, 60, [900] * 24)]
+
+
+@pytest.mark.parametrize("window", [0, 1000])
+@pytest.mark.parametrize("Hkv,group,n,lens", WIDE)
+def test_attention_of_prompts_with_wide_heads_waits_for_its_last_products(Hkv, group, n, lens, window):
+    """Few tiles a row tile, whose warps are then far apart: the results are read when the last product is through, call
+    after call."""
+    import attention64 as a64
+
+    rng = np.random.default_rng(n + Hkv)
+    page, pages = 32, 48
+    pool = pool_of(256, Hkv, page, pages, False)
+    lens = np.array(lens)
+    table = tables(rng, lens, page, pages)
+    q = torch.randn(n * len(lens), Hkv * group, 256, device=a64.DEV, generator=torch.Generator(a64.DEV).manual_seed(6)).half()
+    call = dict(pool.call(), page_table=a64.gpu(table), lengths=a64.gpu(lens.astype(np.int32)), window=window)
+    outs = [nv.attention(q, **call, return_lse=True) for _ in range(25)]
+    for out, lse in outs:
+        assert torch.equal(out, outs[0][0]) and torch.equal(lse, outs[0][1])
+    a64.check(pool, q, table, lens, [n] * len(lens), *outs[0], [int(x) for x in lens], window=window)
