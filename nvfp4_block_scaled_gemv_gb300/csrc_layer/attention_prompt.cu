@@ -365,7 +365,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
   const uint32_t q_full = more, drain = more + 8;
   auto s_full = [&](int i) { return more + 16 + 8u * i; };
   auto p_ready = [&](int i) { return more + 32 + 8u * i; };
-  auto o_done = [&](int i) { return more + 48 + 8u * i; };
+  // The product of P and V of tile j in half u is through.  Only some tiles' are waited for, and a wait by parity cannot tell
+  // a phase from the one two before it: the product before it on the same barrier must be through by then.  With two
+  // halves it is, since a half's next scores are asked for after its product; with one half scores are a tile ahead,
+  // two products may be under way, and tiles take two barriers in turn.
+  auto o_done = [&](int u, int32_t j) { return more + 48 + 8u * (NQ == 2 ? (uint32_t)u : (uint32_t)j & 1u); };
+  auto o_phase = [&](int32_t j) { return (uint32_t)(NQ == 2 ? j : j >> 1) & 1u; };
   auto s_free = [&](int i) { return more + 64 + 8u * i; };
   auto marks_full = [&](int i) { return more + 80 + 8u * i; };
 
@@ -405,7 +410,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
         tc::mbar_init(s_full(i), 1);
         tc::mbar_init(s_free(i), 4 * CTAS);  // the issuer's
         tc::mbar_init(p_ready(i), 4 * CTAS);  // the issuer's
-        tc::mbar_init(o_done(i), 1);
+        tc::mbar_init(more + 48 + 8u * i, 1);
       }
       for (int i = 0; i < kNanTiles; ++i) tc::mbar_init(marks_full(i), 4);
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -628,7 +633,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
 #pragma unroll
             for (int k = 0; k < BN / 16; ++k)
               mma_ts<CTAS>(d, a + 8u * k, b + (uint64_t)(k * (16 * 128 >> 4)), pv, j > 0 || k > 0);
-            commit_all<CTAS>(o_done(u));
+            commit_all<CTAS>(o_done(u, j));
             if (u == NQ - 1) commit_all<CTAS>(slot_empty(i));
           }
           __syncwarp();
@@ -844,7 +849,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
             arrive_issuer<CTAS>(s_free(x & 1), lane == 0);
             // the product before this one has read its P (and O may be rescaled)
             if (j > 0) {
-              wait_phase(o_done(u), (uint32_t)(j - 1) & 1u, ok);
+              wait_phase(o_done(u, j - 1), o_phase(j - 1), ok);
               ok = __all_sync(0xffffffffu, ok);
               if (!ok) break;
               tc::fence_after();
@@ -861,8 +866,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
             far = __any_sync(0xffffffffu, is_far(m, c));
             if (j > 0) {
               if (!S::kOwnP) {
-                if (NQ == 1 && j > 1) wait_phase(o_done(u), (uint32_t)(j - 2) & 1u, ok);  // (see the end of the tiles)
-                wait_phase(o_done(u), (uint32_t)(j - 1) & 1u, ok);
+                wait_phase(o_done(u, j - 1), o_phase(j - 1), ok);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc::fence_after();
@@ -922,11 +926,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
           __syncwarp();
           arrive_issuer<CTAS>(p_ready(x & 1), lane == 0);
         }
-        // One half of rows: the scores of the last tile are there two products before the last one ends, and a warp that
-        // is ahead of others may come here before the last but one has: a phase is waited for only when the one before
-        // it has completed (they have the same parity as those two on).
-        if (NQ == 1 && tiles > 1) wait_phase(o_done(u), (uint32_t)(tiles - 2) & 1u, ok);
-        wait_phase(o_done(u), (uint32_t)(tiles - 1) & 1u, ok);
+        wait_phase(o_done(u, tiles - 1), o_phase(tiles - 1), ok);
         ok = __all_sync(0xffffffffu, ok);
         __syncwarp();
         tc::fence_after();
