@@ -708,7 +708,8 @@ nvfp4_status_t nvfp4_kv_read(const nvfp4_kv_rows_t* rows, int dtype, int64_t T, 
  *   with a window also t > j - window, or, without causal, over all lengths[b] tokens.
  *   q, out     : [T][Hq][D] fp16 or bf16; out 16-byte aligned, q too (and its strides);
  *                out (and lse, the workspace) must not overlap q or the other arguments
- *   page_table : int32 [B][max_pages], the pages of a sequence's length
+ *   page_table : int32 [B][max_pages], the pages of a sequence's length (room for more costs little, but
+ *                where few rows meet a wide table a row tile's tokens are cut by its width)
  *   lengths    : int32 [B]
  * Options (NULL = {0, 1, 0, 0, NULL, NULL, NULL, NULL, 0, 0}):
  *   scale      : > 0; 0 = 1 / sqrt(D)
@@ -727,7 +728,9 @@ nvfp4_status_t nvfp4_kv_read(const nvfp4_kv_rows_t* rows, int dtype, int64_t T, 
  * read nothing outside the cache.
  * workspace: nvfp4_attention_workspace_bytes bytes, 256-byte aligned; need not be kept, but no
  * two calls that may run at once can share it.
- * Accuracy: scores and sums in fp32, the p to fp16 before the product with v, out rounded once.
+ * Accuracy: scores and sums in fp32; p to fp16 before the product with v (2^-11 of itself, or 2^-32 of the
+ * row's largest where that is more); out rounded once.  bf16 queries go over to fp16 in a power of two of
+ * their row: elements below 2^-29 of the row's largest lose bits, below 2^-39 they are 0.
  * Limits: Hq % Hkv == 0, T * Hq < 2^31, max_pages * page_size <= 2^31 - 256, B <= 2^20, and
  * B * Hkv * max_pages * page_size < 2^36, less by the passes that more than 8 query tokens x heads of
  * a group take (up to 8).

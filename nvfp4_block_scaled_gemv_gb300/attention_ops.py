@@ -343,7 +343,7 @@ def attention(q, cache, page_table, lengths, q_starts=None, max_q: int = 0, scal
               stream=None):
     """out [T, Hq, D] of q [T, Hq, D] (fp16 or bf16, heads contiguous) on a kv_cache().
 
-    page_table int32 [B, max_pages] and lengths int32 [B] say what each sequence has cached, its query
+    page_table int32 [B, max_pages] and lengths int32 [B] (contiguous) say what each sequence has cached, its query
     tokens (T / B each, or rows q_starts[b] to q_starts[b + 1] - 1, at most max_q, or 0: any number) among
     them as its last ones.  A query sees the tokens up to its own (causal), the last `window` of them, or all.  scale 0 is
     1 / sqrt(D).  return_lse: (out, lse fp32 [T, Hq]).  workspace: a uint8 tensor of

@@ -21,12 +21,12 @@
 // shared, every warp leaves its piece (maximum, sum, unnormalised result); a CTA adds up its warps'
 // pieces, and a second small kernel those of CTAs that share an item, in the order of the tokens.
 //
-// What bounds it.  32 sequences of 16k to 32k tokens, 64 query heads on 8 heads of 128: 158 us, 5.76
-// TB/s, 85% of the measured copy (a step of 64 sequences of 8192: 111 us, 81%; 32 heads each with
-// its own keys: 420 us, 85%).  A tile of 32 tokens costs a warp ~730 instructions (128 conversions,
+// What bounds it.  32 sequences of 16k to 32k tokens, 64 query heads on 8 heads of 128: 160 us, 5.66
+// TB/s, 83% of the measured copy (a step of 64 sequences of 8192: 112 us, 80%; 32 heads each with
+// its own keys: 403 us, 88%).  A tile of 32 tokens costs a warp ~730 instructions (128 conversions,
 // 128 products with scales, 32 MMAs), of the ~800 issue slots that an SM has in the time of its bytes.
 // 16 columns take 1.55 times the time of 8 (12 warps, for the registers), heads of 64 1.8 times that of
-// their bytes.  Small calls: one sequence of 900 tokens 9.4 us, of which the second kernel is 3 to 4 and lengths,
+// their bytes.  Small calls: one sequence of 900 tokens 9.6 us, of which the second kernel is 3 to 4 and lengths,
 // page numbers and the first bytes most of the rest, one after the other.
 #include <cfloat>
 #include <cstdint>

@@ -5,10 +5,10 @@
 // tokens and one plane (64 elements) of a head, or two, a lane one 16-element block of K and the
 // same one of V of each plane, all loads in flight at once.  So it reads 8 pieces of 128 bytes a plane
 // (16-bit rows), and, where the tokens' slots follow each other, writes 256 bytes of codes and
-// 32 of scales in one run each.  16384 tokens x 8 heads of 128 in bf16, slots in any order: 32.4 us
-// for writing and reading back together, 78% of the bytes' time at the measured copy's rate; issue
-// slots are ~70% used (quantising a block is ~100 instructions), and a code row in a random slot is a
-// piece of 32 bytes.  24 tokens: 4.1 us, two launches.
+// 32 of scales in one run each.  16384 tokens x 8 heads of 128 in bf16, writing and reading back together: 29.6 us
+// where slots run on within pages, as a prompt's do (86% of the bytes' time at the measured copy's rate), 32.5
+// in any order (78%): then a code row is a piece of 32 bytes.  Issue slots are ~58% used (quantising a block is
+// ~100 instructions).  24 tokens: 4.3 us, two launches.
 #include <cstdint>
 
 #include "attention.h"
