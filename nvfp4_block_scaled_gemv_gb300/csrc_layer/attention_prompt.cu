@@ -164,7 +164,7 @@ __device__ __forceinline__ void arrive_issuer(uint32_t bar, bool who) {
         "r"((uint32_t)who)
         : "memory");
 }
-// what the warp wrote to this CTA's shared memory is released to the cluster first, by a fence of that memory alone (2
+// what the warp wrote to (and read of) this CTA's shared memory is released to the cluster first, by a fence of that memory alone (2
 // prompts of 2048 on 8192, heads of 256: 441 us; an arrive with a release of its own, of all memory, 541).
 template <int CTAS>
 __device__ __forceinline__ void arrive_issuer_filled(uint32_t bar, bool who) {
@@ -925,7 +925,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attention_prompt_kernel(con
           tmem_st_wait();
           tc::fence_before();
           __syncwarp();
-          arrive_issuer<CTAS>(p_ready(x & 1), lane == 0);
+          if (CTAS == 1 || whole)
+            arrive_issuer<CTAS>(p_ready(x & 1), lane == 0);
+          else  // (the marks have been read)
+            arrive_issuer_filled<CTAS>(p_ready(x & 1), lane == 0);
         }
         wait_phase(o_done(u, tiles - 1), o_phase(tiles - 1), ok);
         ok = __all_sync(0xffffffffu, ok);

@@ -82,10 +82,10 @@ def test_arrivals_at_another_cta_name_the_cluster():
 
 
 def test_the_pair_releases_what_it_wrote():
-    """The warps that fill shared memory for the pair's MMAs release it to the cluster, and who issues them acquires it
-    there."""
+    """The warps that fill shared memory for the pair's MMAs release it to the cluster, those that have read marks too, and
+    who issues the MMAs acquires it there."""
     code = kernel_sources()["attention_prompt.cu"]
-    for what in ("slot_full(si)", "q_full"):
+    for what in ("slot_full(si)", "q_full", "p_ready(x & 1)"):
         assert f"arrive_issuer_filled<CTAS>({what}, lane == 0)" in code
     filled = code[code.index("void arrive_issuer_filled"):]
     assert "fence.release.sync_restrict::shared::cta.cluster" in filled[: filled.index("\n}\n")]
