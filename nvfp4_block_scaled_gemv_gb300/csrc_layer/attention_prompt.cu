@@ -36,13 +36,13 @@
 // prefixes up to 12k, 32 query heads), 64 tokens a tile with P beside S slower (the MMAs of Q K^T read
 // 4 KB of Q for 64 columns).
 //
-// What bounds it.  That case runs at 1.44 PFLOP/s in 1166 us, 75% of the measured bf16 rate, the tensor pipe busy
+// What bounds it.  That case runs at 1.43 PFLOP/s in 1170 us, 75% of the measured bf16 rate, the tensor pipe busy
 // about 70% of the time: a half's next scores wait for its softmax and P's product.  Heads of
 // 64 run at 0.84 (4 x 2048 queries on 8192 tokens, 575 us): the exponentials and the MMAs of a tile are 1024
-// cycles each, and what keeps them from running beside each other is not known.  Heads of 256: 1.10 (2 x 2048 on 8192, 16
-// heads, 437 us), for which no cause is known either.
+// cycles each, and what keeps them from running beside each other is not known.  Heads of 256: 1.09 (2 x 2048 on 8192, 16
+// heads, 440 us), for which no cause is known either.
 // Short prompts are bound by the beginning and end of a row tile, ~15,000 cycles where 128 tokens are ~2,800: 4 prompts of 2048
-// 157 us (189 with rows of Q and results moved a row a lane).
+// 158 us (189 with rows of Q and results moved a row a lane).
 // What mattered most: a wait by one lane under a branch splits the warp for hundreds of cycles, so
 // whole warps wait, and single lanes arrive by predicates (1476 -> 1202 us), and a wait that ran out is counted
 // when the kernel ends, not in the wait (heads of 64: 655 -> 572 us); one SM's warps share
